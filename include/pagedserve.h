@@ -50,7 +50,7 @@ extern "C" {
 
 #define PS_BLOCK_SIZE 16
 
-typedef enum { PS_F16 = 0, PS_BF16 = 1 } ps_dtype;
+typedef enum { PS_F16 = 0, PS_BF16 = 1, PS_F32 = 2 } ps_dtype; /* F32: ps_beam_select's logits */
 
 typedef enum {
   PS_OK = 0,
@@ -66,7 +66,8 @@ typedef enum {
   PS_DEV_OK = 0,
   PS_DEV_BAD_BLOCK_ID = 1,   /* a block-table entry outside [0, num_blocks)            */
   PS_DEV_BAD_SLOT = 2,       /* a slot_mapping entry >= num_blocks * 16                */
-  PS_DEV_BAD_SEQUENCE = 3,   /* query count > context, or context beyond the table     */
+  PS_DEV_BAD_SEQUENCE = 3,   /* query count > context, context beyond the table, or a
+                                parent outside its group (ps_fork_sequences)           */
   PS_DEV_WAIT_TIMEOUT = 4,   /* a kernel's bounded wait ran out (the kernel returned)  */
   PS_DEV_PLAN_OVERFLOW = 5,  /* the work plan did not fit the workspace                */
   PS_DEV_BAD_TOKEN = 6       /* a draft token id outside [0, V)                          */
@@ -160,6 +161,103 @@ int ps_rope_reshape_and_cache(void* q, const void* k, const void* v, const int32
                               int dtype, void* stream);
 
 /*
+ * ps_rotary_reshape_and_cache -- rotary positions in their other forms, fused with the KV
+ * scatter: pairs of neighbours or of halves, over a part of the head, with a table of
+ * frequencies.
+ *
+ * For token t and frequency i < R / 2 (R = rotary_dim), with a = positions[t] * inv_freq[i],
+ * c = magnitude * cos(a), s = magnitude * sin(a), the pair (x, y) of every query and key head
+ * becomes (x c - y s, y c + x s), where
+ *     interleaved != 0:  x = head[2 i],  y = head[2 i + 1]
+ *     interleaved == 0:  x = head[i],    y = head[i + R / 2]
+ * and elements R .. D - 1 pass through. Any scaling of the positions for contexts longer
+ * than the model was trained on (a factor on all frequencies, another base, a factor by
+ * wavelength) is in the table, its gain in `magnitude`. The angle is reduced exactly but for
+ * the table entry's rounding (2^-53 relative); cosine, sine, products and sums are fp32 and
+ * each output is rounded once.
+ *
+ *   q, k, v       [T, heads, D] of dtype, tokens q_stride, k_stride, v_stride ELEMENTS apart
+ *                 (multiples of 8, at least heads * D): views of one projection's output
+ *                 serve as they are. k and v are not modified.
+ *   q_out         [T, H_q, D], tokens q_out_stride apart: the rotated queries. q_out == q
+ *                 (equal strides) rotates in place; otherwise the two must not overlap.
+ *   positions     int32 [T]; negative positions turn backwards.
+ *   slot_mapping, k_pool, v_pool   as for ps_rope_reshape_and_cache.
+ *   inv_freq      double [R / 2], radians per position (finite).
+ *   rotary_dim    R: a positive multiple of 16 (other values: PS_ERR_UNSUPPORTED), at most D.
+ */
+int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const int32_t* positions,
+                                const int32_t* slot_mapping, void* k_pool, void* v_pool,
+                                const double* inv_freq, int rotary_dim, int interleaved,
+                                float magnitude, void* q_out, int64_t q_out_stride, int T,
+                                int H_q, int H_kv, int D, int num_blocks, int dtype,
+                                void* stream);
+
+/*
+ * ps_beam_select -- beam search's selection over beams and vocabulary.
+ *
+ * For each prompt b, beam w and token v the continuation's score is
+ *     score(w, v) = scores[b, w] + (logits[b, w, v] - lse_w),
+ *     lse_w = log sum_v exp(logits[b, w, v]),
+ * and the n_select best of the W * V are returned in falling order, ties to the lowest beam,
+ * then the lowest token. A finished beam has one continuation: pad_token, at its score as it
+ * is. A logit of -inf or NaN is no continuation (and adds nothing to lse_w); nor has a beam
+ * whose score is not finite, or one with a logit of +inf, any. Where fewer than n_select
+ * remain, the rest are parent -1, token -1, score -inf.
+ * lse is summed in fp32 within 8192 logits and in fp64 across them; scores are compared in
+ * fp64 and rounded once to fp32.
+ *
+ *   logits        [B, W, V] of logits_dtype (PS_F16, PS_BF16 or PS_F32), rows row_stride
+ *                 ELEMENTS apart (at least V: a padded vocabulary is left out by it),
+ *                 aligned to an element. Read once; nothing outside the rows is read.
+ *   scores        float [B, W]: the beams' sums of log probabilities.
+ *   finished      uint8 [B, W], nonzero for a finished beam, or NULL.
+ *   pad_token     in [0, V) when finished is given.
+ *   parents, tokens  int32 [B, n_select], out_scores float [B, n_select], written.
+ *   workspace     device scratch of ps_beam_select_workspace_size() bytes, 256-byte aligned;
+ *                 calls that share one must not overlap on the device.
+ * W and n_select up to 32, W * V below 2^31 - 8192; PS_ERR_UNSUPPORTED beyond. B = 0 is a
+ * no-op.
+ */
+size_t ps_beam_select_workspace_size(int B, int W, int V, int n_select);
+int ps_beam_select(const void* logits, int64_t row_stride, const float* scores,
+                   const uint8_t* finished, int pad_token, int B, int W, int V, int n_select,
+                   int logits_dtype, int32_t* parents, int32_t* tokens, float* out_scores,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ps_fork_sequences -- the cache after a selection: n_out children of each group's n_in
+ * sequences, each continuing one parent (the beams of a prompt; a prompt forked into its
+ * first beams with n_in = 1).
+ *
+ * Child c = (g, i) continues sequence r = g * n_in + parents[g, i], of length L =
+ * seq_lens[r]. Its table takes the parent's L / 16 full blocks as they are (shared from now
+ * on); the L % 16 rows of the parent's last, partly filled block are copied, K and V in
+ * every layer, into the child's own tail_blocks[g, i], which becomes the child's last block.
+ * With L % 16 = 0 nothing is copied and the tail block is not used. The caller keeps count
+ * of who holds which block; the blocks of the parents' tails are free again once every
+ * child has one of its own.
+ *
+ *   block_tables  int32 [groups * n_in, max_blocks_per_seq], seq_lens int32 [groups * n_in].
+ *   parents       int32 [groups, n_out], each in [0, n_in), the same one any number of
+ *                 times; negative for a child that is none (length 0, table left as it was);
+ *                 another value records PS_DEV_BAD_SEQUENCE and counts as none.
+ *   tail_blocks   int32 [groups, n_out]: distinct, and in no parent's table.
+ *   k_pool, v_pool [layers, num_blocks, 16, H_kv, D] of dtype, updated in place.
+ *   out_block_tables int32 [groups * n_out, max_blocks_per_seq], out_seq_lens int32
+ *                 [groups * n_out], written; other arrays than the parents'. Entries past a
+ *                 child's last block are left as they were.
+ * A length beyond the table records PS_DEV_BAD_SEQUENCE (length 0); a block outside the pool
+ * records PS_DEV_BAD_BLOCK_ID and its rows are not copied. groups = 0 is a no-op.
+ */
+int ps_fork_sequences(const int32_t* block_tables, int max_blocks_per_seq,
+                      const int32_t* seq_lens, const int32_t* parents,
+                      const int32_t* tail_blocks, int groups, int n_in, int n_out, void* k_pool,
+                      void* v_pool, int layers, int num_blocks, int H_kv, int D, int dtype,
+                      int32_t* out_block_tables, int32_t* out_seq_lens, void* stream);
+
+/*
  * ps_spec_accept -- speculative-decoding acceptance after the verify pass.
  *
  * tinyserve "How it works" (speculative decoding): draft d_i is accepted with probability
@@ -237,6 +335,45 @@ int ps_paged_attention(const void* q, const void* k_pool, const void* v_pool,
                        const int32_t* seq_lens, const int32_t* query_start_loc, int B, int T,
                        int H_q, int H_kv, int D, int num_blocks, float scale, void* out,
                        void* workspace, size_t workspace_bytes, int dtype, void* stream);
+
+/*
+ * ps_paged_attention_masked -- ps_paged_attention with capped scores, a bias by distance,
+ * and masks that are an interval of keys per row.
+ *
+ * For packed row r at position p of sequence b (context L) and query head h:
+ *     x_j = softcap * tanh(scale * q . K_j / softcap)    (softcap > 0; else scale * q . K_j)
+ *           - distance_slopes[h] * |p - j|                (with distance_slopes)
+ *     out[r, h, :] = sum_j softmax_j(x_j) V_j over the keys j that the row sees:
+ *     lo <= j < hi,  hi = max(p + 1, min(prefix_lens[b], L)),
+ *                    lo = max(0, p - window + 1 if window > 0, key_starts[r])
+ * A row that sees no key (lo >= hi) gives zeros. With all of it absent the result is
+ * ps_paged_attention's up to rounding.
+ *
+ *   scale         > 0 and finite.     softcap  >= 0, 0: none.
+ *   distance_slopes float [H_q] (finite) or NULL: the linear distance bias.
+ *   window        keys a row sees, its own included (a sliding window); 0: none. Block-table
+ *                 entries of pages that lie before the first page any row of the sequence
+ *                 sees are not read: those blocks may have been given back.
+ *   prefix_lens   int32 [B] or NULL: keys j < prefix_lens[b] are seen by every row of the
+ *                 sequence, those after it in the prefix included (they must be in the
+ *                 cache: values beyond L count as L, negative ones as 0).
+ *   key_starts    int32 [T] or NULL: first key of the row's document in a sequence packed of
+ *                 several; must not fall from one row of a sequence to the next (else keys
+ *                 that a row should see may be left out). Negative counts as 0.
+ * Other arguments, workspace and errors as for ps_paged_attention. A sequence whose tokens
+ * lie outside [0, T) records PS_DEV_BAD_SEQUENCE and its rows are left unwritten.
+ * K and V at keys that no row of the sequence sees (rows of a block never written, blocks
+ * given back) may hold anything, NaN included. V at a key that one row of the step sees must
+ * be finite for the others' sake: a NaN or infinity there may reach rows of the same
+ * sequence and step that do not see it.
+ */
+int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_pool,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* seq_lens, const int32_t* query_start_loc, int B,
+                              int T, int H_q, int H_kv, int D, int num_blocks, float scale,
+                              float softcap, const float* distance_slopes, int window,
+                              const int32_t* prefix_lens, const int32_t* key_starts, void* out,
+                              void* workspace, size_t workspace_bytes, int dtype, void* stream);
 
 /*
  * ps_paged_attention_noalloc -- ps_paged_attention for callers that cannot allocate.
@@ -373,7 +510,8 @@ const char* ps_status_string(int status);
  * (ps_reshape_and_cache, or the step's scatter ahead of the tile kernel's direct mode),
  * 2 planner (carrying the step's KV scatter when there is one), 3 split attention (decode
  * and verify rows), 4 split combine, 5 tile attention (prefill rows, tcgen05), 6 block
- * copy, 7 speculative acceptance, 8 rotary KV scatter.
+ * copy (and sequence forks), 7 speculative acceptance (and beam selection), 8 rotary KV
+ * scatter (either form). The masked attention's kernels count under 2 to 5.
  */
 int ps_profile_begin(int max_launches_per_kind);
 int ps_profile_end(void);

@@ -14,8 +14,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpagedser
 _lock = threading.Lock()
 _lib = None
 
-c_int, c_float, c_size_t, c_void_p, c_char_p = (ctypes.c_int, ctypes.c_float, ctypes.c_size_t,
-                                                 ctypes.c_void_p, ctypes.c_char_p)
+c_int, c_float, c_size_t, c_void_p, c_char_p, c_i64 = (
+    ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p,
+    ctypes.c_int64)
 _p = c_void_p  # every pointer argument is passed as an address
 
 SIGNATURES = {
@@ -25,12 +26,23 @@ SIGNATURES = {
                                _p]),
     "ps_rope_reshape_and_cache": (c_int, [_p, _p, _p, _p, _p, _p, _p, c_int, c_int, c_int, c_int,
                                           c_int, c_float, c_int, _p]),
+    "ps_rotary_reshape_and_cache": (c_int, [_p, c_i64, _p, c_i64, _p, c_i64, _p, _p, _p, _p, _p,
+                                            c_int, c_int, c_float, _p, c_i64, c_int, c_int,
+                                            c_int, c_int, c_int, c_int, _p]),
+    "ps_beam_select_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "ps_beam_select": (c_int, [_p, c_i64, _p, _p, c_int, c_int, c_int, c_int, c_int, c_int, _p,
+                               _p, _p, _p, c_size_t, _p]),
+    "ps_fork_sequences": (c_int, [_p, c_int, _p, _p, _p, c_int, c_int, c_int, _p, _p, c_int,
+                                  c_int, c_int, c_int, c_int, _p, _p, _p]),
     "ps_spec_accept_workspace_size": (c_size_t, [c_int, c_int, c_int]),
     "ps_spec_accept": (c_int, [_p, _p, _p, _p, c_int, c_int, c_int, c_int, _p, _p, _p, c_size_t,
                                _p]),
     "ps_paged_attention_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
     "ps_paged_attention": (c_int, [_p, _p, _p, _p, c_int, _p, _p, c_int, c_int, c_int, c_int,
                                    c_int, c_int, c_float, _p, _p, c_size_t, c_int, _p]),
+    "ps_paged_attention_masked": (c_int, [_p, _p, _p, _p, c_int, _p, _p, c_int, c_int, c_int,
+                                          c_int, c_int, c_int, c_float, c_float, _p, c_int, _p,
+                                          _p, _p, _p, c_size_t, c_int, _p]),
     "ps_paged_attention_noalloc": (c_int, [_p, _p, _p, _p, c_int, _p, _p, c_int, c_int, c_int,
                                            c_int, c_int, c_int, c_float, _p, c_int, _p]),
     "ps_attention_step": (c_int, [_p, _p, _p, _p, _p, _p, c_int, _p, _p, c_int, c_int, c_int,

@@ -191,6 +191,154 @@ def spec_accept(target_probs, draft_tokens, random_bits=None, draft_probs=None,
     return out, num
 
 
+def _here(device, *tensors) -> None:
+    """The tensors given (None left out) live on `device`, the current CUDA device."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise PagedServeError(f"tensors are on {device}, not on the current CUDA device")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise PagedServeError(f"a tensor is on {t.device}, the others on {device}")
+
+
+def _alloc(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor for use on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _tokens(t: torch.Tensor, name: str, dtype) -> tuple[int, int]:
+    """Address and token stride of a CUDA tensor [T, heads, D] whose tokens are dense rows,
+    at any distance from one another."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise PagedServeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise PagedServeError(f"{name} must have 3 dimensions, has {t.dim()}")
+    if t.dtype != dtype:
+        raise PagedServeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    T, H, D = t.shape
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise PagedServeError(f"{name}: a token's heads must lie together")
+    return t.data_ptr(), st[0] if T > 1 else H * D
+
+
+def rotary_reshape_and_cache(q, k, v, positions, slot_mapping_t, k_pool, v_pool, inv_freq,
+                             interleaved: bool = False, magnitude: float = 1.0, q_out=None,
+                             stream=None) -> torch.Tensor:
+    """Rotate q [T, H_q, D] into q_out (None: in place) and k [T, H_kv, D] into the pools at
+    the slots, copying v too, by a table of frequencies (ps_rotary_reshape_and_cache).
+    inv_freq is float64 [rotary_dim / 2] (see :func:`rotary.frequencies`); pairs are
+    neighbours (interleaved) or halves of the first rotary_dim elements, the rest of a head
+    passes through. q, k, v and q_out may be views whose tokens lie apart. Returns q_out."""
+    if q_out is None:
+        q_out = q
+    if not isinstance(q, torch.Tensor) or q.dtype not in DTYPE_CODE:
+        raise PagedServeError("q must be a float16 or bfloat16 tensor")
+    qp, qs = _tokens(q, "q", q.dtype)
+    kp, ks = _tokens(k, "k", q.dtype)
+    vp, vs = _tokens(v, "v", q.dtype)
+    op, os_ = _tokens(q_out, "q_out", q.dtype)
+    pp = _dev(positions, "positions", torch.int32, 1)
+    sp = _dev(slot_mapping_t, "slot_mapping", torch.int32, 1)
+    kpp = _dev(k_pool, "k_pool", q.dtype, 4)
+    vpp = _dev(v_pool, "v_pool", q.dtype, 4)
+    fp = _dev(inv_freq, "inv_freq", torch.float64, 1)
+    _here(q.device, k, v, q_out, positions, slot_mapping_t, k_pool, v_pool, inv_freq)
+    T, H_q, D = q.shape
+    H_kv = k.shape[1]
+    if k.shape != (T, H_kv, D) or v.shape != k.shape or q_out.shape != q.shape or \
+            positions.shape[0] != T or slot_mapping_t.shape[0] != T or \
+            tuple(k_pool.shape[1:]) != (BLOCK_SIZE, H_kv, D) or k_pool.shape != v_pool.shape:
+        raise PagedServeError("rotary_reshape_and_cache: inconsistent shapes")
+    _check(lib().ps_rotary_reshape_and_cache(qp, qs, kp, ks, vp, vs, pp, sp, kpp, vpp, fp,
+                                             2 * inv_freq.shape[0], 1 if interleaved else 0,
+                                             magnitude, op, os_, T, H_q, H_kv, D,
+                                             k_pool.shape[0], DTYPE_CODE[q.dtype],
+                                             _stream(stream)),
+           "ps_rotary_reshape_and_cache")
+    return q_out
+
+
+LOGITS_CODE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def alloc_beam_workspace(B: int, W: int, V: int, n_select: int, device=None) -> torch.Tensor:
+    n = max(int(lib().ps_beam_select_workspace_size(B, W, V, n_select)), 256)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def beam_select(logits, scores, n_select: int, finished=None, pad_token: int = 0,
+                workspace=None, stream=None):
+    """Beam search's selection (ps_beam_select): the n_select best continuations of each
+    prompt's W beams by scores + log softmax(logits). logits [B, W, V] (float16, bfloat16 or
+    float32; the last dimension of a padded vocabulary may be cut by a view), scores float32
+    [B, W], finished uint8 or bool [B, W] or None. Returns (parents, tokens, scores), each
+    [B, n_select]."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 3 or \
+            logits.dtype not in LOGITS_CODE:
+        raise PagedServeError("logits must be a float CUDA tensor with 3 dimensions")
+    B, W, V = logits.shape
+    st = logits.stride()
+    ld = st[1] if W > 1 else st[0] if B > 1 else V
+    if (V > 1 and st[2] != 1) or (B > 1 and W > 1 and st[0] != W * st[1]):
+        raise PagedServeError("logits: rows must be dense and equally far apart")
+    sp = _dev(scores, "scores", torch.float32, 2)
+    fp = _dev(finished, "finished", (torch.uint8, torch.bool), 2) if finished is not None else None
+    if scores.shape != (B, W) or (finished is not None and finished.shape != (B, W)):
+        raise PagedServeError("beam_select: inconsistent shapes")
+    dev = logits.device
+    _here(dev, scores, finished, workspace)
+    if workspace is None:
+        n = max(int(lib().ps_beam_select_workspace_size(B, W, V, n_select)), 256)
+        workspace = _alloc(n, torch.uint8, dev, stream)
+    wp = _dev(workspace, "workspace", torch.uint8, 1)
+    ints = _alloc((2, B, n_select), torch.int32, dev, stream)
+    best = _alloc((B, n_select), torch.float32, dev, stream)
+    _check(lib().ps_beam_select(logits.data_ptr(), ld, sp, fp, pad_token, B, W, V, n_select,
+                                LOGITS_CODE[logits.dtype], ints.data_ptr(),
+                                ints.data_ptr() + 4 * B * n_select, best.data_ptr(), wp,
+                                workspace.numel(), _stream(stream)),
+           "ps_beam_select")
+    return ints[0], ints[1], best
+
+
+def fork_sequences(block_tables, seq_lens, parents, tail_blocks, k_pool, v_pool,
+                   out_block_tables, out_seq_lens, stream=None) -> None:
+    """The cache after a selection (ps_fork_sequences): child i of group g takes the table of
+    sequence g * n_in + parents[g, i], its partly filled last block copied into the child's
+    own tail_blocks[g, i] in every layer. block_tables [groups * n_in, max_blocks]; parents and
+    tail_blocks int32 [groups, n_out]; pools [layers, num_blocks, 16, H_kv, D] (or one
+    layer's, without the first dimension); out_block_tables [groups * n_out, max_blocks] and
+    out_seq_lens [groups * n_out] are written."""
+    bt = _dev(block_tables, "block_tables", torch.int32, 2)
+    sl = _dev(seq_lens, "seq_lens", torch.int32, 1)
+    pp = _dev(parents, "parents", torch.int32, 2)
+    tp = _dev(tail_blocks, "tail_blocks", torch.int32, 2)
+    ot = _dev(out_block_tables, "out_block_tables", torch.int32, 2)
+    ol = _dev(out_seq_lens, "out_seq_lens", torch.int32, 1)
+    kp = _dev(k_pool, "k_pool", tuple(DTYPE_CODE))
+    vp = _dev(v_pool, "v_pool", k_pool.dtype)
+    _here(k_pool.device, block_tables, seq_lens, parents, tail_blocks, v_pool,
+          out_block_tables, out_seq_lens)
+    groups, n_out = parents.shape
+    n, width = block_tables.shape
+    if k_pool.dim() not in (4, 5) or k_pool.shape != v_pool.shape or \
+            k_pool.shape[-3] != BLOCK_SIZE or seq_lens.shape[0] != n or \
+            tail_blocks.shape != parents.shape or \
+            tuple(out_block_tables.shape) != (groups * n_out, width) or \
+            out_seq_lens.shape[0] != groups * n_out or (groups > 0 and n % groups != 0):
+        raise PagedServeError("fork_sequences: inconsistent shapes")
+    if groups == 0:
+        return
+    layers = k_pool.shape[0] if k_pool.dim() == 5 else 1
+    _check(lib().ps_fork_sequences(bt, width, sl, pp, tp, groups, n // groups, n_out, kp, vp,
+                                   layers, k_pool.shape[-4], k_pool.shape[-2], k_pool.shape[-1],
+                                   DTYPE_CODE[k_pool.dtype], ot, ol, _stream(stream)),
+           "ps_fork_sequences")
+
+
 def workspace_size(T: int, B: int, H_q: int, H_kv: int, D: int, max_seq_len: int) -> int:
     return int(lib().ps_paged_attention_workspace_size(T, B, H_q, H_kv, D, max_seq_len))
 
@@ -225,6 +373,56 @@ def paged_attention(q, k_pool, v_pool, block_tables, seq_lens, query_start_loc, 
                                     float(scale), op, wp, workspace.numel(),
                                     DTYPE_CODE[q.dtype], _stream(stream)),
            "ps_paged_attention")
+    return out
+
+
+def masked_paged_attention(q, k_pool, v_pool, block_tables, seq_lens, query_start_loc,
+                           scale: float, softcap: float = 0.0, distance_slopes=None,
+                           window: int = 0, prefix_lens=None, key_starts=None, out=None,
+                           workspace=None, max_seq_len: int | None = None,
+                           stream=None) -> torch.Tensor:
+    """Paged attention with scores capped by a tanh (softcap), lowered by the distance
+    (distance_slopes float32 [H_q]), a sliding window, a bidirectional prefix (prefix_lens
+    int32 [B]) and documents packed into a sequence (key_starts int32 [T]); see
+    ps_paged_attention_masked. Rows that see no key give zeros."""
+    qp = _dev(q, "q", tuple(DTYPE_CODE), 3)
+    kpp = _dev(k_pool, "k_pool", q.dtype, 4)
+    vpp = _dev(v_pool, "v_pool", q.dtype, 4)
+    bt, sl, qs, B, maxblk = _batch(block_tables, seq_lens, query_start_loc)
+    T, H_q, D = q.shape
+    NB, bs, H_kv, Dk = k_pool.shape
+    if bs != BLOCK_SIZE or Dk != D or v_pool.shape != k_pool.shape:
+        raise PagedServeError("masked_paged_attention: inconsistent pool shape")
+    dp = pp = sp = None
+    if distance_slopes is not None:
+        dp = _dev(distance_slopes, "distance_slopes", torch.float32, 1)
+        if distance_slopes.shape[0] != H_q:
+            raise PagedServeError("distance_slopes: one per query head")
+    if prefix_lens is not None:
+        pp = _dev(prefix_lens, "prefix_lens", torch.int32, 1)
+        if prefix_lens.shape[0] != B:
+            raise PagedServeError("prefix_lens: one per sequence")
+    if key_starts is not None:
+        sp = _dev(key_starts, "key_starts", torch.int32, 1)
+        if key_starts.shape[0] != T:
+            raise PagedServeError("key_starts: one per packed token")
+    _here(q.device, k_pool, v_pool, block_tables, seq_lens, query_start_loc, distance_slopes,
+          prefix_lens, key_starts, out, workspace)
+    if out is None:
+        out = _alloc(q.shape, q.dtype, q.device, stream)
+    op = _dev(out, "out", q.dtype, 3)
+    if out.shape != q.shape:
+        raise PagedServeError("out must have q's shape")
+    if workspace is None:
+        msl = max_seq_len if max_seq_len is not None else maxblk * BLOCK_SIZE
+        workspace = _alloc(max(workspace_size(T, B, H_q, H_kv, D, msl), 256), torch.uint8,
+                           q.device, stream)
+    wp = _dev(workspace, "workspace", torch.uint8, 1)
+    _check(lib().ps_paged_attention_masked(qp, kpp, vpp, bt, maxblk, sl, qs, B, T, H_q, H_kv, D,
+                                           NB, scale, softcap, dp, window, pp, sp, op, wp,
+                                           workspace.numel(), DTYPE_CODE[q.dtype],
+                                           _stream(stream)),
+           "ps_paged_attention_masked")
     return out
 
 

@@ -367,6 +367,71 @@ int encode_pool_map(CUtensorMap* map, const void* pool, int num_blocks, int H_kv
   if (rc) return rc;
   return make_pool_map(map, pool, num_blocks, H_kv, D, bf16);
 }
+
+// The masked attention's chain: as run_attention's without a scatter. A small batch runs on
+// the split or the tile kernel's direct mode alone; otherwise planner, split kernel, tile
+// kernel and combine, chained with programmatic dependent launch.
+int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const void* v_pool,
+                         bool bf16, cudaStream_t s) {
+  MaskedAttnParams p = p0;
+  int num_sms = 0;
+  int* err = nullptr;
+  int rc = current_device(&num_sms, &err);
+  if (rc) return rc;
+  p.err = err;
+  const bool tiles = p.tpt > 0 && (static_cast<int64_t>(p.T) - p.B + 1) * p.G > 16 * kTileMinGroups;
+  if (!tiles) p.tpt = 0;
+  CUtensorMap kmap, vmap, qmap;
+  if ((rc = make_pool_map(&kmap, k_pool, p.num_blocks, p.H_kv, p.D, bf16))) return rc;
+  if ((rc = make_pool_map(&vmap, v_pool, p.num_blocks, p.H_kv, p.D, bf16))) return rc;
+  if (tiles && (rc = make_q_map(&qmap, p.q, p.T, p.H_q, p.D, p.G, p.tpt, bf16))) return rc;
+  cudaError_t e;
+  if (direct_fits(p, num_sms)) {
+    p.direct = 1;
+    const int64_t items = static_cast<int64_t>(p.B) * p.H_kv;
+    const int warps = attention_warps(p.D);
+    const int64_t want = (items + warps - 1) / warps;
+    Timed tm(3, s);
+    if ((e = launch_masked_split(p, bf16, kmap, vmap,
+                                 static_cast<int>(want < num_sms ? want : num_sms), s, true)) !=
+        cudaSuccess)
+      return cuda_fail(e, "masked split attention kernel (direct)");
+    return PS_OK;
+  }
+  if (tiles && direct_tile_fits(p, num_sms)) {
+    Timed tm(5, s);
+    if ((e = launch_masked_tile(p, bf16, kmap, vmap, qmap, direct_tile_ctas(p, num_sms), s,
+                                true)) != cudaSuccess)
+      return cuda_fail(e, "masked tile attention kernel (direct)");
+    return PS_OK;
+  }
+  if (tiles && static_cast<int64_t>(p.B) * p.H_kv * 2 <= num_sms) p.all_tiles = 1;
+  const int split_grid = split_ctas(p, num_sms);
+  {
+    Timed tm(2, s);
+    if ((e = launch_plan_masked(p, split_grid * attention_warps(p.D), num_sms, num_sms, s)) !=
+        cudaSuccess)
+      return cuda_fail(e, "masked plan kernel");
+  }
+  if (!p.all_tiles) {
+    Timed tm(3, s);
+    if ((e = launch_masked_split(p, bf16, kmap, vmap, split_grid, s, true)) != cudaSuccess)
+      return cuda_fail(e, "masked split attention kernel");
+  }
+  if (tiles) {
+    MaskedAttnParams pt = p;
+    pt.after_split = !p.all_tiles;
+    Timed tm(5, s);
+    if ((e = launch_masked_tile(pt, bf16, kmap, vmap, qmap, num_sms, s, false)) != cudaSuccess)
+      return cuda_fail(e, "masked tile attention kernel");
+  }
+  if (p.max_blocks > kMinSplitPages) {
+    Timed tm(4, s);
+    if ((e = launch_combine(p, bf16, num_sms, s, true)) != cudaSuccess)
+      return cuda_fail(e, "combine kernel");
+  }
+  return PS_OK;
+}
 }  // namespace ps
 
 extern "C" {
@@ -464,6 +529,165 @@ int ps_rope_reshape_and_cache(void* q, const void* k, const void* v, const int32
                                                        rope_theta, dtype == PS_BF16, ds->err,
                                                        ds->num_sms, s),
                      "rotary KV scatter kernel");
+}
+
+int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const int32_t* positions,
+                                const int32_t* slot_mapping, void* k_pool, void* v_pool,
+                                const double* inv_freq, int rotary_dim, int interleaved,
+                                float magnitude, void* q_out, int64_t q_out_stride, int T,
+                                int H_q, int H_kv, int D, int num_blocks, int dtype,
+                                void* stream) {
+  int rc = check_shapes(H_q, H_kv, D, dtype);
+  if (rc) return rc;
+  if (T < 0 || num_blocks <= 0 || rotary_dim <= 0 || rotary_dim > D || !std::isfinite(magnitude))
+    return PS_ERR_ARG;
+  if (rotary_dim % 16 != 0) return PS_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_blocks) * PS_BLOCK_SIZE > INT32_MAX) return PS_ERR_ARG;
+  // a pass of 8 tokens and the passes of a step are counted in 32 bits
+  if (static_cast<int64_t>(H_q) + 2 * static_cast<int64_t>(H_kv) > (1 << 24)) return PS_ERR_UNSUPPORTED;
+  const int64_t q_row = static_cast<int64_t>(H_q) * D, kv_row = static_cast<int64_t>(H_kv) * D;
+  if (q_stride < q_row || q_out_stride < q_row || k_stride < kv_row || v_stride < kv_row)
+    return PS_ERR_ARG;
+  if (q_stride % 8 || q_out_stride % 8 || k_stride % 8 || v_stride % 8) return PS_ERR_ALIGN;
+  if (T == 0) return PS_OK;
+  if (!q || !k || !v || !positions || !slot_mapping || !k_pool || !v_pool || !inv_freq || !q_out)
+    return PS_ERR_ARG;
+  if (q == q_out && q_stride != q_out_stride) return PS_ERR_ARG;  // in place means the same rows
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_pool) ||
+      !aligned16(v_pool) || !aligned16(q_out) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+    return PS_ERR_ALIGN;
+  DeviceState* ds;
+  if ((rc = current_device_state(&ds))) return rc;
+  ps::RotaryParams a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.qo_stride = q_out_stride;
+  a.pos = positions;
+  a.slots = slot_mapping;
+  a.k_pool = static_cast<uint16_t*>(k_pool);
+  a.v_pool = static_cast<uint16_t*>(v_pool);
+  a.inv_freq = inv_freq;
+  a.magnitude = magnitude;
+  a.T = T;
+  a.H_q = H_q;
+  a.H_kv = H_kv;
+  a.rot = rotary_dim;
+  a.num_slots = static_cast<int64_t>(num_blocks) * PS_BLOCK_SIZE;
+  a.err = ds->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(8, s);
+  return cuda_status(ps::launch_rotary(a, D, interleaved != 0, dtype == PS_BF16, ds->num_sms, s),
+                     "rotary KV scatter kernel (table of frequencies)");
+}
+
+int ps_fork_sequences(const int32_t* block_tables, int max_blocks_per_seq,
+                      const int32_t* seq_lens, const int32_t* parents,
+                      const int32_t* tail_blocks, int groups, int n_in, int n_out, void* k_pool,
+                      void* v_pool, int layers, int num_blocks, int H_kv, int D, int dtype,
+                      int32_t* out_block_tables, int32_t* out_seq_lens, void* stream) {
+  int rc = check_shapes(H_kv, H_kv, D, dtype);
+  if (rc) return rc;
+  if (groups < 0 || n_in <= 0 || n_out <= 0 || layers <= 0 || num_blocks <= 0 ||
+      max_blocks_per_seq <= 0)
+    return PS_ERR_ARG;
+  if (static_cast<int64_t>(num_blocks) * PS_BLOCK_SIZE > INT32_MAX ||
+      static_cast<int64_t>(groups) * n_in > INT32_MAX ||
+      static_cast<int64_t>(groups) * n_out > INT32_MAX || layers > (1 << 20))
+    return PS_ERR_ARG;
+  if (groups == 0) return PS_OK;
+  if (!block_tables || !seq_lens || !parents || !tail_blocks || !k_pool || !v_pool ||
+      !out_block_tables || !out_seq_lens)
+    return PS_ERR_ARG;
+  // the children's tables are written while the parents' are read
+  if (out_block_tables == block_tables || out_seq_lens == seq_lens) return PS_ERR_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return PS_ERR_ALIGN;
+  DeviceState* ds;
+  if ((rc = current_device_state(&ds))) return rc;
+  ps::ForkParams a = {};
+  a.tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.parents = parents;
+  a.tails = tail_blocks;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.out_tables = out_block_tables;
+  a.out_lens = out_seq_lens;
+  a.max_blocks = max_blocks_per_seq;
+  a.groups = groups;
+  a.n_in = n_in;
+  a.n_out = n_out;
+  a.layers = layers;
+  a.num_blocks = num_blocks;
+  a.H_kv = H_kv;
+  a.D = D;
+  a.err = ds->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(6, s);
+  return cuda_status(ps::launch_fork(a, ds->num_sms, s), "fork kernel");
+}
+
+namespace {
+// Sizes ps_beam_select takes; PS_OK or the status to return.
+int check_beam(int B, int W, int V, int n) {
+  if (B < 0 || W <= 0 || V <= 0 || n <= 0) return PS_ERR_ARG;
+  if (W > ps::kBeamMaxWidth || n > ps::kBeamMaxWidth) return PS_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(W) * V > INT32_MAX - ps::kBeamChunk) return PS_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * W * ps::beam_chunks(V) > INT32_MAX) return PS_ERR_UNSUPPORTED;
+  return PS_OK;
+}
+}  // namespace
+
+size_t ps_beam_select_workspace_size(int B, int W, int V, int n_select) {
+  if (check_beam(B, W, V, n_select)) return 0;
+  const size_t lists = static_cast<size_t>(B) * W * ps::beam_chunks(V);
+  return ps::up256(lists * sizeof(float2)) + ps::up256(lists * n_select * 8);
+}
+
+int ps_beam_select(const void* logits, int64_t row_stride, const float* scores,
+                   const uint8_t* finished, int pad_token, int B, int W, int V, int n_select,
+                   int logits_dtype, int32_t* parents, int32_t* tokens, float* out_scores,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_beam(B, W, V, n_select);
+  if (rc) return rc;
+  if (logits_dtype != PS_F16 && logits_dtype != PS_BF16 && logits_dtype != PS_F32)
+    return PS_ERR_UNSUPPORTED;
+  if (row_stride < V) return PS_ERR_ARG;
+  if (finished && (pad_token < 0 || pad_token >= V)) return PS_ERR_ARG;
+  if (B == 0) return PS_OK;
+  if (!logits || !scores || !parents || !tokens || !out_scores) return PS_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) & (logits_dtype == PS_F32 ? 3u : 1u)) return PS_ERR_ALIGN;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < ps_beam_select_workspace_size(B, W, V, n_select))
+    return PS_ERR_WORKSPACE;
+  DeviceState* ds;
+  if ((rc = current_device_state(&ds))) return rc;
+  ps::BeamParams a = {};
+  a.logits = logits;
+  a.ld = row_stride;
+  a.scores = scores;
+  a.finished = finished;
+  a.B = B;
+  a.W = W;
+  a.V = V;
+  a.n = n_select;
+  a.pad = pad_token;
+  a.chunks = ps::beam_chunks(V);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.stat = reinterpret_cast<float2*>(ws);
+  a.cand = reinterpret_cast<unsigned long long*>(
+      ws + ps::up256(static_cast<size_t>(B) * W * a.chunks * sizeof(float2)));
+  a.parents = parents;
+  a.tokens = tokens;
+  a.out_scores = out_scores;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(7, s);
+  return cuda_status(ps::launch_beam_select(a, logits_dtype, s), "beam selection kernels");
 }
 
 size_t ps_spec_accept_workspace_size(int B, int k, int V) {
@@ -585,6 +809,54 @@ int ps_paged_attention(const void* q, const void* k_pool, const void* v_pool,
     return PS_ERR_WORKSPACE;
   return ps::run_attention(p, const_cast<void*>(k_pool), const_cast<void*>(v_pool),
                            dtype == PS_BF16, static_cast<cudaStream_t>(stream));
+}
+
+int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_pool,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* seq_lens, const int32_t* query_start_loc, int B,
+                              int T, int H_q, int H_kv, int D, int num_blocks, float scale,
+                              float softcap, const float* distance_slopes, int window,
+                              const int32_t* prefix_lens, const int32_t* key_starts, void* out,
+                              void* workspace, size_t workspace_bytes, int dtype, void* stream) {
+  // (the tile kernel takes a row's maximum on the raw scores)
+  if (!(scale > 0.f) || !std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap) ||
+      window < 0)
+    return PS_ERR_ARG;
+  int rc = check_attention(q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens,
+                           query_start_loc, B, T, H_q, H_kv, D, num_blocks, out, workspace,
+                           workspace_bytes, dtype);
+  if (rc) return rc;
+  if (T == 0) return PS_OK;
+  ps::MaskedAttnParams p{};
+  p.q = q;
+  p.out = out;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.qsl = query_start_loc;
+  p.max_blocks = max_blocks_per_seq;
+  p.B = B;
+  p.T = T;
+  p.H_q = H_q;
+  p.H_kv = H_kv;
+  p.D = D;
+  p.G = H_q / H_kv;
+  p.num_blocks = num_blocks;
+  const double log2e = 1.4426950408889634;
+  p.scale_log2 = static_cast<float>(scale * log2e);
+  p.cap_log2 = static_cast<float>(softcap * log2e);
+  p.cap_arg = softcap > 0.f ? static_cast<float>(2.0 * log2e * scale / softcap) : 0.f;
+  // (a scale or cap at the ends of the range)
+  if (!std::isfinite(p.scale_log2) || !std::isfinite(p.cap_log2) || !std::isfinite(p.cap_arg))
+    return PS_ERR_ARG;
+  p.slopes = distance_slopes;
+  p.window = window;
+  p.prefix = prefix_lens;
+  p.starts = key_starts;
+  p.tpt = ps::tile_tokens(p.G);
+  if (!ps::layout_workspace(p, static_cast<uint8_t*>(workspace), workspace_bytes, false))
+    return PS_ERR_WORKSPACE;
+  return ps::run_masked_attention(p, k_pool, v_pool, dtype == PS_BF16,
+                                  static_cast<cudaStream_t>(stream));
 }
 
 namespace {

@@ -27,18 +27,31 @@ namespace ps {
 // ----------------------------------------------------------------------------------
 struct SeqInfo {
   int n, L, valid, groups, pages, tok0, tile, qtiles;
+  // Masked attention only (both 0 for the causal mask alone, and folded away): the first
+  // page any row of the sequence sees, and the length of its bidirectional prefix.
+  int page0, pre;
 };
 
 // groups: 16-row groups of the split kernel; tile / qtiles: the sequence goes to the tile
 // kernel (more than 16 packed rows and a tile size exists) in qtiles 128-row tiles.
-__device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, const int* qsl,
-                                            const int* lens, int b) {
+template <class Params>
+__device__ __forceinline__ SeqInfo seq_info(const Params& p, const int* qsl, const int* lens,
+                                            int b) {
   SeqInfo s;
   s.tok0 = qsl[b];
   s.n = qsl[b + 1] - s.tok0;
   s.L = lens[b];
   s.pages = (s.L + kBlockSize - 1) / kBlockSize;
   s.valid = s.n >= 0 && s.n <= s.L && s.pages <= p.max_blocks;
+  s.page0 = s.pre = 0;
+  if constexpr (Params::kMasked) {
+    s.valid = s.valid && s.tok0 >= 0 && s.tok0 + s.n <= p.T;
+    if (s.valid && s.n > 0) {
+      // the rows' lower bounds do not fall from one row to the next: the first row's holds
+      s.pre = p.prefix_len(b, s.L);
+      s.page0 = min(p.row_lo(s.tok0, s.L - s.n) / kBlockSize, s.pages - 1);
+    }
+  }
   const int rows = s.valid ? s.n * p.G : 0;
   s.groups = (rows + 15) / 16;
   s.tile = p.tpt > 0 && (s.groups > kTileMinGroups || (p.all_tiles && s.groups > 0));
@@ -55,10 +68,29 @@ __device__ __forceinline__ int seq_splits(const SeqInfo& s, int pps_dec, int pps
     if (s.groups > kSplitGroupLimit) return 1;
     pps = pps_dec;
   }
-  int ns = (s.pages + pps - 1) / pps;
+  const int span = s.pages - s.page0;
+  int ns = (span + pps - 1) / pps;
   ns = ns < 1 ? 1 : ns;
   ns = ns > kMaxSplits ? kMaxSplits : ns;
-  return ns > s.pages ? s.pages : ns;
+  return ns > span ? span : ns;
+}
+
+// First page of split k of ns.
+__device__ __forceinline__ int split_page(const SeqInfo& s, int ns, int k) {
+  return s.page0 + (k * (s.pages - s.page0)) / ns;
+}
+
+// The first token that sees a key at or after page `page`: those of the prefix are seen
+// by all.
+__device__ __forceinline__ int first_token_at(const SeqInfo& s, int page) {
+  const int f = page * kBlockSize - (s.L - s.n);
+  return f > 0 && page * kBlockSize >= s.pre ? f : 0;
+}
+
+// One past the last page that the rows up to token i_last see (past page0 at least: rows
+// that see nothing are held by split 0 all the same).
+__device__ __forceinline__ int end_page(const SeqInfo& s, int i_last) {
+  return max(max(s.L - s.n + i_last, s.pre - 1) / kBlockSize, s.page0) + 1;
 }
 
 // largest b in [0, n) with arr[b] <= x (arr non-decreasing, arr[0] <= x)
@@ -138,12 +170,11 @@ __device__ int4 block_exscan4(int4 v, int4* sh, int4& total) {
 }
 
 // Token i (0-based within its sequence, at position L - n + i) lies on page (L - n + i) / 16;
-// split k of a sequence split ns ways starts at page (k * pages) / ns, so the first token
-// that split k covers is first_k = max(0, 16 * start_k - (L - n)). A token's rows are held
+// split k of a sequence split ns ways starts at page start_k (split_page), so the first
+// token that split k covers is first_k = first_token_at(start_k). A token's rows are held
 // by the splits with first_k <= i; with more than one, each holds H_q partial entries.
 __device__ __forceinline__ int split_first_token(const SeqInfo& s, int ns, int k) {
-  const int f = (k * s.pages) / ns * kBlockSize - (s.L - s.n);
-  return f > 0 ? f : 0;
+  return first_token_at(s, split_page(s, ns, k));
 }
 
 // For token i: the splits holding its rows (*held) and, summed over the tokens before it,
@@ -151,11 +182,11 @@ __device__ __forceinline__ int split_first_token(const SeqInfo& s, int ns, int k
 // split starts k * pages / ns are stepped with a running remainder, without dividing.
 __device__ __forceinline__ int split_entries_before(const SeqInfo& s, int ns, int i,
                                                     int* held = nullptr) {
-  const int q = s.pages / ns, r = s.pages - q * ns, p0 = s.L - s.n;
-  const int f1 = max(0, q * kBlockSize - p0);  // start_1 = q (r < ns)
-  int acc = 0, cnt = 0, start = 0, rem = 0;
+  const int span = s.pages - s.page0, q = span / ns, r = span - q * ns;
+  const int f1 = first_token_at(s, s.page0 + q);  // start_1 = page0 + q (r < ns)
+  int acc = 0, cnt = 0, start = s.page0, rem = 0;
   for (int k = 0; k < ns; ++k) {
-    const int fk = max(0, start * kBlockSize - p0);
+    const int fk = k == 0 ? 0 : first_token_at(s, start);
     cnt += fk <= i ? 1 : 0;
     const int from = fk > f1 ? fk : f1;
     acc += i > from ? i - from : 0;
@@ -218,7 +249,7 @@ __device__ __forceinline__ int pages_per_split(long long work, long long workers
 // items longer than the target (sequences at the split cap), then by quarters of the
 // target. Items are fetched in list order, so the short ones fill the workers' ends.
 __device__ __forceinline__ int split_class(const SeqInfo& s, int ns, int pps) {
-  const int len = (s.pages + ns - 1) / ns;
+  const int len = (s.pages - s.page0 + ns - 1) / ns;
   return len > pps ? 0 : 4 * len > 3 * pps ? 1 : 2 * len > pps ? 2 : 3;
 }
 __device__ __forceinline__ int int4_at(const int4& v, int k) {
@@ -234,6 +265,21 @@ __device__ __forceinline__ void store_item(WorkItem* dst_item, const WorkItem& i
   dst[3] = src[3];
 }
 
+// Masked attention: an item starts at the first page that its first row sees. An item that
+// rows are held by keeps one page at least (with every key of it masked), so that their
+// partial results are written. pad[1], pad[2]: the keys [lo, hi) that some row of the item
+// sees; pad[3]: the prefix.
+template <class Params>
+__device__ __forceinline__ void mask_item(const Params& p, const SeqInfo& s, WorkItem& it,
+                                          int i_first, int i_last) {
+  const int lo = p.row_lo(s.tok0 + i_first, s.L - s.n + i_first);
+  if (it.page_end > it.page_begin)
+    it.page_begin = min(max(it.page_begin, lo / kBlockSize), it.page_end - 1);
+  it.pad[1] = lo;
+  it.pad[2] = max(s.L - s.n + i_last + 1, s.pre);
+  it.pad[3] = s.pre;
+}
+
 // The planner turns the batch into two work lists: split-kernel items (sequences with at
 // most 64 packed rows: decodes, verify rows) and tile-kernel items (prefill chunks), plus
 // the per-token split table that the combine kernel reads and the slot of every new
@@ -247,7 +293,10 @@ constexpr int kPlanSmemArrays = 9;  // qsl, lens, five offset arrays, two tile l
 constexpr int kPlanRankSeqs = 512;  // tile sequences up to which every rank goes rank by rank
 constexpr int kPlanMaxCtas = 64;
 
-__global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p, int concurrency,
+// Masked attention plans with the same kernel: a sequence's pages then start at the first
+// one its rows see, an item's at the first one its own rows see.
+template <class Params>
+__global__ void __launch_bounds__(1024) plan_kernel(const Params p, int concurrency,
                                                     int tile_ctas, int plan_ctas,
                                                     const CopySegments pre, int copy_ctas) {
   __shared__ int4 sh4[32];
@@ -308,10 +357,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p, int conc
       continue;
     }
     if (s.tile) {
-      wt += static_cast<long long>(s.qtiles) * s.pages;
+      wt += static_cast<long long>(s.qtiles) * (s.pages - s.page0);
       pairs += (s.qtiles + 1) / 2;
     } else {
-      wd += static_cast<long long>(s.groups) * s.pages;
+      wd += static_cast<long long>(s.groups) * (s.pages - s.page0);
     }
   }
   const Sum3 W = block_sum3_ll(Sum3{wd, wt, pairs}, shl);
@@ -492,15 +541,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p, int conc
         it.row0 = 16 * j;
         it.nrows = min(16, rows - 16 * j);
         const int i_last = (it.row0 + it.nrows - 1) / p.G;
-        const int page_last = (s.L - s.n + i_last) / kBlockSize;
-        it.page_begin = (sp * s.pages) / ns;
-        it.page_end = min(((sp + 1) * s.pages) / ns, page_last + 1);
+        it.page_begin = split_page(s, ns, sp);
+        it.page_end = min(split_page(s, ns, sp + 1), end_page(s, i_last));
         it.split = sp;
         it.nsplit = ns;
         it.ctx_len = s.L;
         it.n_query = s.n;
         it.tok0 = s.tok0;
         it.pad[0] = it.pad[1] = it.pad[2] = it.pad[3] = it.pad[4] = 0;
+        if constexpr (Params::kMasked) mask_item(p, s, it, it.row0 / p.G, i_last);
         store_item(p.items + first + local, it);
       }
     } else {
@@ -539,9 +588,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p, int conc
         it.row0 = qa * p.G;
         it.nrows = na * p.G;
         const int i_last = nb > 0 ? qb + nb - 1 : qa + na - 1;
-        const int page_last = (s.L - s.n + i_last) / kBlockSize;
-        it.page_begin = (sp * s.pages) / ns;
-        it.page_end = min(((sp + 1) * s.pages) / ns, page_last + 1);
+        it.page_begin = split_page(s, ns, sp);
+        it.page_end = min(split_page(s, ns, sp + 1), end_page(s, i_last));
         it.split = sp;
         it.nsplit = ns;
         it.ctx_len = s.L;
@@ -549,6 +597,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnParams p, int conc
         it.tok0 = s.tok0;
         it.pad[0] = nb * p.G;
         it.pad[1] = it.pad[2] = it.pad[3] = it.pad[4] = 0;
+        if constexpr (Params::kMasked) mask_item(p, s, it, qa, i_last);
         store_item(p.tile_items + pos, it);
       }
     }
@@ -1143,14 +1192,15 @@ static int plan_threads(int B) {
   return t > 1024 ? 1024 : t;
 }
 
-cudaError_t launch_plan(const AttnParams& p, int concurrency, int tile_ctas, int num_sms,
-                        cudaStream_t stream, const CopySegments* pre) {
+template <class Params>
+static cudaError_t launch_plan_t(const Params& p, int concurrency, int tile_ctas, int num_sms,
+                                 cudaStream_t stream, const CopySegments* pre) {
   const int smem =
       p.B <= kPlanSmemSeqs ? kPlanSmemArrays * (p.B + 1) * static_cast<int>(sizeof(int)) : 0;
   if (smem > 48 * 1024) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e =
-        ensure_smem_limit(plan_kernel, kPlanSmemArrays * (kPlanSmemSeqs + 1) * 4, done);
+        ensure_smem_limit(plan_kernel<Params>, kPlanSmemArrays * (kPlanSmemSeqs + 1) * 4, done);
     if (e != cudaSuccess) return e;
   }
   // enough CTAs that the token and item passes are short (a CTA's warps share its SM's
@@ -1179,9 +1229,19 @@ cudaError_t launch_plan(const AttnParams& p, int concurrency, int tile_ctas, int
   }
   // programmatic dependent launch: the CTAs may start while the kernel before them on the
   // stream finishes (see plan_kernel for what they wait for, and when)
-  return launch_kernel(plan_kernel, dim3(static_cast<unsigned>(ctas + scatter + copies)),
+  return launch_kernel(plan_kernel<Params>, dim3(static_cast<unsigned>(ctas + scatter + copies)),
                        dim3(threads), static_cast<size_t>(smem), stream, true, p, concurrency,
                        tile_ctas, ctas, segs, static_cast<int>(copies));
+}
+
+cudaError_t launch_plan(const AttnParams& p, int concurrency, int tile_ctas, int num_sms,
+                        cudaStream_t stream, const CopySegments* pre) {
+  return launch_plan_t(p, concurrency, tile_ctas, num_sms, stream, pre);
+}
+
+cudaError_t launch_plan_masked(const MaskedAttnParams& p, int concurrency, int tile_ctas,
+                               int num_sms, cudaStream_t stream) {
+  return launch_plan_t(p, concurrency, tile_ctas, num_sms, stream, nullptr);
 }
 
 template <bool kBF16, int D, bool kDirect, int kS = 0>

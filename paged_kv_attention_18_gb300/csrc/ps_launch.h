@@ -13,6 +13,7 @@ struct WorkItem;
 
 // Everything the planner, the attention kernels and the combine kernel read.
 struct AttnParams {
+  static constexpr bool kMasked = false;  // the causal mask alone (see MaskedAttnParams)
   const void* q;                 // [T, H_q, D]
   void* out;                     // [T, H_q, D]
   const int32_t* block_tables;   // [B, max_blocks]
@@ -60,6 +61,34 @@ struct AttnParams {
   const void* new_v;
   void* k_pool;                  // [num_blocks, 16, H_kv, D]
   void* v_pool;
+};
+
+// Masked attention: row r of a sequence with context L, at position p, sees the keys
+// [lo, hi) with lo = max(0, p - window + 1 (window > 0), starts[r]) and hi = max(p + 1,
+// min(prefix, L)); none when lo >= hi. Scores are capped by a tanh and fall with the
+// distance as the fields below say.
+struct MaskedAttnParams : AttnParams {
+  static constexpr bool kMasked = true;
+  float cap_log2;         // cap * log2(e); 0: scores are not capped
+  float cap_arg;          // 2 * log2(e) * scale / cap (the tanh's exponent per raw score)
+  const float* slopes;    // [H_q] slope of the distance bias, or null
+  int window;             // keys a row sees, its own included; 0: all before it
+  const int32_t* prefix;  // [B] or null
+  const int32_t* starts;  // [T] or null
+
+  // the first key of the row at packed token `tok`, position `pos`
+  __device__ __forceinline__ int row_lo(int tok, int pos) const {
+    int lo = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
+    if (starts != nullptr) {
+      const int s = __ldg(starts + tok);
+      lo = s > lo ? s : lo;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ int prefix_len(int b, int L) const {
+    const int x = prefix != nullptr ? __ldg(prefix + b) : 0;
+    return x < 0 ? 0 : x > L ? L : x;
+  }
 };
 
 // Raise `kern`'s dynamic shared-memory limit to `bytes` once per device: the setting lasts
@@ -142,6 +171,56 @@ cudaError_t launch_rope_reshape_and_cache(void* q, const void* k, const void* v,
                                           int D, int num_blocks, float theta, bool bf16,
                                           int* err, int num_sms, cudaStream_t stream);
 
+// Rotary positions in their other layouts, fused with the KV scatter (16-bit values by
+// their bits; strides in elements).
+struct RotaryParams {
+  const uint16_t *q, *k, *v;      // [T, heads, D], token strides below
+  uint16_t* q_out;                // may be q
+  int64_t q_stride, k_stride, v_stride, qo_stride;
+  const int32_t* pos;             // [T]
+  const int32_t* slots;           // [T]
+  uint16_t *k_pool, *v_pool;      // [num_slots, H_kv, D]
+  const double* inv_freq;         // [rot / 2] radians per position
+  float magnitude;
+  int T, H_q, H_kv, rot;          // rot: elements of a head that are rotated
+  int64_t num_slots;
+  int* err;
+};
+cudaError_t launch_rotary(const RotaryParams& p, int D, bool interleaved, bool bf16, int num_sms,
+                          cudaStream_t stream);
+
+// Beam search's selection over beams and vocabulary.
+constexpr int kBeamChunk = 8192;    // logits per scanning CTA
+constexpr int kBeamMaxWidth = 32;   // beams, and candidates kept, at most
+struct BeamParams {
+  const void* logits;             // [B, W, V], rows `ld` elements apart
+  int64_t ld;
+  const float* scores;            // [B, W]
+  const uint8_t* finished;        // [B, W] or null
+  int B, W, V, n, pad, chunks;
+  float2* stat;                   // [B * W, chunks] workspace: maximum, sum of exp(x - max)
+  unsigned long long* cand;       // [B * W, chunks, n] workspace: best (logit, token), or 0
+  int32_t *parents, *tokens;      // [B, n]
+  float* out_scores;              // [B, n]
+};
+int beam_chunks(int V);
+// dtype: 0 fp16, 1 bf16, 2 fp32
+cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stream);
+
+// Forking sequences of the cache: tables by parent, tail rows copied in every layer.
+struct ForkParams {
+  const int32_t* tables;          // [groups * n_in, max_blocks]
+  const int32_t* seq_lens;        // [groups * n_in]
+  const int32_t* parents;         // [groups, n_out]
+  const int32_t* tails;           // [groups, n_out]
+  void *k_pool, *v_pool;          // [layers, num_blocks, 16, H_kv, D]
+  int32_t* out_tables;            // [groups * n_out, max_blocks]
+  int32_t* out_lens;              // [groups * n_out]
+  int max_blocks, groups, n_in, n_out, layers, num_blocks, H_kv, D;
+  int* err;
+};
+cudaError_t launch_fork(const ForkParams& p, int num_sms, cudaStream_t stream);
+
 // Speculative acceptance (rejection rule or greedy) of every sequence's k drafts.
 struct SpecParams {
   const float* p;          // [B, k + 1, V] target probabilities of the verify rows
@@ -176,6 +255,19 @@ int attention_warps(int D);
 // `pre`, further CTAs make those copies (inputs that only the later kernels read).
 cudaError_t launch_plan(const AttnParams& p, int concurrency, int tile_ctas, int num_sms,
                         cudaStream_t stream, const CopySegments* pre = nullptr);
+cudaError_t launch_plan_masked(const MaskedAttnParams& p, int concurrency, int tile_ctas,
+                               int num_sms, cudaStream_t stream);
+
+// The split and tile kernels with a mask, capped scores and a distance bias, launched as
+// their causal forms are.
+cudaError_t launch_masked_split(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, int ctas, cudaStream_t stream,
+                                bool pdl);
+cudaError_t launch_masked_tile(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
+                               cudaStream_t stream, bool direct);
+int run_masked_attention(const MaskedAttnParams& p, const void* k_pool, const void* v_pool,
+                         bool bf16, cudaStream_t s);
 
 // Query tokens per 128-row tile for G query heads per KV head (0 = use the split kernel).
 int tile_tokens(int G);

@@ -1,0 +1,448 @@
+// Masked paged attention, decode and verify rows: the split kernel with a mask that is an
+// interval of keys per row, scores capped by a tanh, and a bias that falls with the
+// distance.
+//
+//     x_j = c tanh(scale q.K_j / c) - slope_h |p - j|,  lo <= j < hi   (see MaskedAttnParams)
+//     out = sum_j softmax_j(x_j) V_j,  zeros for a row without keys
+//
+// in one pass over the keys with the running maximum and sum (log2 units). One warp streams
+// one work item (16 packed rows of one KV head over one split of the context) through its
+// own ring of TMA-filled pages, 8 warps an SM, like the causal split kernel; what the mask
+// adds:
+//   - the plan starts an item at the first page its rows see, so a sliding window costs
+//     the window's bytes whatever the context, and pages before it are never read;
+//   - a key that no row of the item sees has its V row zeroed in shared memory before the
+//     product (only the first and last page can hold one): 0 * V would keep a NaN of
+//     memory that was never written. Its score is replaced, whatever it is;
+//   - a row that has seen no key yet keeps its maximum at -inf and subtracts 0, so that
+//     its weights are exactly 0.
+// tanh(y) = 1 - 2 / (2^(2 y log2 e) + 1): one ex2 and one reciprocal. Its absolute error is
+// a few 2^-23 of 1, so a cap of 50 (72 in log2 units) puts under 2^-15 on x, against the
+// 2^-9 that P's rounding to bf16 costs. The kernel is bound by the bytes of K and V.
+#include "ps_common.cuh"
+#include "ps_launch.h"
+#include "ps_masked.cuh"
+
+namespace ps {
+
+namespace {
+
+constexpr int kWarps = 8;  // per CTA, one CTA per SM
+
+template <int D>
+struct MaskedSplit {
+  static constexpr int kStages = D == 128 ? 3 : 6;    // pages in flight per warp
+  static constexpr int kRing = kStages + 2;           // item records
+  static constexpr int kPage = kBlockSize * D * 2;    // one page of K (or V), one head
+  static constexpr int kStage = 2 * kPage;
+  static constexpr int kSmem =
+      1024 + kWarps * (kStages * kStage + kStages * 8 + kRing * 64);
+};
+
+template <bool kBF16, int D, bool kDirect>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    masked_split_kernel(const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap, const MaskedAttnParams p) {
+  using C = MaskedSplit<D>;
+  constexpr int S = C::kStages, kRing = C::kRing, kPage = C::kPage, kStage = C::kStage;
+  constexpr int kBoxes = D / 64, kKSteps = D / 16;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* tiles = smem + warp * S * kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kWarps * S * kStage) + warp * S;
+  WorkItem* ring =
+      reinterpret_cast<WorkItem*>(smem + kWarps * S * kStage + kWarps * S * 8) + warp * kRing;
+  const uint32_t tiles_addr = smem_u32(tiles);
+
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  __syncwarp();
+  pdl_wait();  // the plan (or, in direct mode, the work before this call) is complete
+  pdl_launch_dependents();
+
+  const int n_items = kDirect ? p.B * p.H_kv : *reinterpret_cast<volatile int*>(p.hdr);
+  int direct_next = blockIdx.x * kWarps + warp;
+  bool first_fetch = true;
+  const bool tile_planned = !kDirect && *reinterpret_cast<volatile int*>(p.hdr + 4) > 0;
+  const uint64_t policy = l2_policy_evict_first();
+
+  // ---------------- issue side (runs ahead of compute by up to S pages) -------------
+  int iss_page = 0, iss_end = 0, iss_seq = 0, iss_kv = 0;
+  int bt_base = 0, bt_reg = -1;
+  bool no_more = false;
+  uint32_t g_issue = 0, ring_tail = 0;
+
+  auto load_bt = [&](int first) {
+    bt_base = first;
+    const int pg = first + lane;
+    bt_reg = pg < iss_end
+                 ? __ldg(p.block_tables + static_cast<int64_t>(iss_seq) * p.max_blocks + pg)
+                 : -1;
+  };
+
+  // Direct mode: the record of item idx = (sequence idx / H_kv, KV head idx % H_kv), all
+  // of the sequence's rows (n * G <= 16) over every page they see; lane k returns field k.
+  auto direct_item = [&](int idx) -> int {
+    const int b = idx / p.H_kv, kv = idx - b * p.H_kv;
+    const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), L = __ldg(p.seq_lens + b);
+    const int pages = (L + kBlockSize - 1) / kBlockSize, n = q1 - q0;
+    if (idx == 0 && lane == 0 && (__ldg(p.qsl) != 0 || __ldg(p.qsl + p.B) != p.T))
+      record_error(p.err, kDevBadSequence);  // tokens outside every sequence
+    if (q0 < 0 || q1 > p.T || n < 0 || n > L || n * p.G > 16 || pages > p.max_blocks) {
+      if (lane == 0) record_error(p.err, kDevBadSequence);
+      return 0;
+    }
+    if (n == 0) return 0;
+    const int pre = p.prefix_len(b, L), lo = p.row_lo(q0, L - n);
+    int f = 0;
+    f = lane == 0 ? b : f;
+    f = lane == 1 ? kv : f;
+    f = lane == 3 ? n * p.G : f;                       // rows; row0 (lane 2) is 0
+    f = lane == 4 ? min(lo / kBlockSize, pages - 1) : f;  // one page at least
+    f = lane == 5 ? pages : f;
+    f = lane == 7 ? 1 : f;                             // one split (lane 6: split 0)
+    f = lane == 8 ? L : f;
+    f = lane == 9 ? n : f;
+    f = lane == 10 ? q0 : f;
+    f = lane == 12 ? lo : f;                           // pad[1..3]
+    f = lane == 13 ? L : f;                            // the last row is at L - 1
+    f = lane == 14 ? pre : f;
+    return f;
+  };
+
+  // Issue the next page of work into stage g_issue % S; false when nothing is left.
+  auto issue_one = [&]() -> bool {
+    while (iss_page >= iss_end) {
+      if (no_more) return false;
+      int idx = 0;
+      if constexpr (kDirect) {
+        idx = direct_next;
+        direct_next += gridDim.x * kWarps;
+      } else if (first_fetch) {
+        // each warp's first item is its own; with tile items planned a CTA's warps take
+        // consecutive items, so that the other SMs are free for the tile kernel
+        idx = tile_planned ? static_cast<int>(blockIdx.x) * kWarps + warp
+                           : warp * static_cast<int>(gridDim.x) + blockIdx.x;
+        first_fetch = false;
+      } else {
+        if (lane == 0) idx = atomicAdd(p.hdr + 1, 1) + static_cast<int>(gridDim.x) * kWarps;
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+      }
+      if (idx >= n_items) {
+        no_more = true;
+        return false;
+      }
+      int v;
+      if constexpr (kDirect) v = direct_item(idx);
+      else v = lane < 16 ? __ldg(reinterpret_cast<const int*>(p.items + idx) + lane) : 0;
+      const int pb = __shfl_sync(0xffffffffu, v, 4), pe = __shfl_sync(0xffffffffu, v, 5);
+      if (pe <= pb) continue;  // held by no row
+      WorkItem* slot = ring + (ring_tail % kRing);
+      if (lane < 16) reinterpret_cast<int*>(slot)[lane] = v;
+      ++ring_tail;
+      iss_seq = __shfl_sync(0xffffffffu, v, 0);
+      iss_kv = __shfl_sync(0xffffffffu, v, 1);
+      iss_page = pb;
+      iss_end = pe;
+      load_bt(pb);
+    }
+    if (iss_page - bt_base >= 32) load_bt(iss_page);
+    const int blk = __shfl_sync(0xffffffffu, bt_reg, iss_page - bt_base);
+    if (lane == 0) {
+      int row = blk * kBlockSize;
+      if (blk < 0 || blk >= p.num_blocks) {
+        record_error(p.err, kDevBadBlockId);
+        row = p.num_blocks * kBlockSize;  // past the tensor: the copy reads zeros
+      }
+      const uint32_t st = g_issue % S;
+      uint8_t* dst = tiles + st * kStage;
+      mbar_arrive_expect_tx(&full[st], kStage);
+#pragma unroll
+      for (int x = 0; x < kBoxes; ++x) {
+        tma_load_2d_hint(dst + x * (kBlockSize * 128), &kmap, &full[st], iss_kv * D + x * 64,
+                         row, policy);
+        tma_load_2d_hint(dst + kPage + x * (kBlockSize * 128), &vmap, &full[st],
+                         iss_kv * D + x * 64, row, policy);
+      }
+    }
+    ++iss_page;
+    ++g_issue;
+    return true;
+  };
+
+  // ---------------- compute side ---------------------------------------------------
+  const int g = lane >> 2, t4 = lane & 3;
+  uint32_t g_comp = 0, ring_head = 0;
+  int comp_left = 0, comp_page = 0;
+  bool have_item = false;
+  WorkItem cur;
+  // per-thread rows g and g + 8 of the item
+  int row_tok[2], row_h[2], row_pos[2], row_lo[2], row_hi[2];
+  float m_run[2], l_run[2], slope[2];
+  float o[D / 8][4];
+  uint32_t qa[kKSteps][4];
+  const uint16_t* qptr = static_cast<const uint16_t*>(p.q);
+
+  auto start_item = [&]() {
+    __syncwarp();  // the ring slot was written by lanes 0..15
+    cur = ring[ring_head % kRing];
+    ++ring_head;
+    comp_page = cur.page_begin;
+    comp_left = cur.page_end - cur.page_begin;
+    have_item = true;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int rr = g + 8 * r;
+      row_tok[r] = -1;
+      row_h[r] = row_pos[r] = row_lo[r] = row_hi[r] = 0;
+      slope[r] = 0.f;
+      if (rr < cur.nrows) {
+        const int R = cur.row0 + rr;
+        const int i = R / p.G;
+        row_tok[r] = cur.tok0 + i;
+        row_h[r] = cur.kv * p.G + (R - i * p.G);
+        row_pos[r] = cur.ctx_len - cur.n_query + i;
+        row_lo[r] = p.row_lo(row_tok[r], row_pos[r]);
+        row_hi[r] = max(row_pos[r] + 1, cur.pad[3]);
+        if (p.slopes != nullptr) slope[r] = -kLog2e * __ldg(p.slopes + row_h[r]);
+      }
+      m_run[r] = -INFINITY;
+      l_run[r] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    // query fragments straight from global memory (rows g, g + 8; columns 2*t4 ...)
+#pragma unroll
+    for (int kk = 0; kk < kKSteps; ++kk) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t lo = 0, hi = 0;
+        if (row_tok[r] >= 0) {
+          const uint16_t* src =
+              qptr + (static_cast<int64_t>(row_tok[r]) * p.H_q + row_h[r]) * D + kk * 16 + 2 * t4;
+          lo = __ldg(reinterpret_cast<const uint32_t*>(src));
+          hi = __ldg(reinterpret_cast<const uint32_t*>(src + 8));
+        }
+        qa[kk][r] = lo;       // columns 2t4, 2t4+1
+        qa[kk][2 + r] = hi;   // columns 2t4+8, 2t4+9
+      }
+    }
+  };
+
+  auto finish_item = [&]() {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {  // row sums across the quad of lanes sharing a row
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (row_tok[r] < 0) continue;
+      const int tok = row_tok[r];
+      const int ns_t = kDirect ? 1 : __ldg(p.tok_ns + tok);
+      if (cur.split >= ns_t) continue;  // this split does not hold the row
+      // a row without keys here gives zeros, whatever the products left in o
+      const bool any = !(l_run[r] == 0.f);
+      const float inv = any ? 1.f / l_run[r] : 0.f;
+      if (ns_t == 1) {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(
+            static_cast<uint16_t*>(p.out) + (static_cast<int64_t>(tok) * p.H_q + row_h[r]) * D +
+            2 * t4);
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          dst[j * 4] = any ? pack2<kBF16>(o[j][2 * r] * inv, o[j][2 * r + 1] * inv) : 0u;
+      } else {
+        const int64_t idx = static_cast<int64_t>(__ldg(p.tok_base + tok)) + cur.split * p.H_q +
+                            row_h[r];
+        float2* dst = reinterpret_cast<float2*>(p.part_o + idx * D + 2 * t4);
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          dst[j * 4] = any ? make_float2(o[j][2 * r] * inv, o[j][2 * r + 1] * inv)
+                           : make_float2(0.f, 0.f);
+        if (t4 == 0) p.part_lse[idx] = any ? m_run[r] + __log2f(l_run[r]) : -INFINITY;
+      }
+    }
+    have_item = false;
+  };
+
+  for (int s = 0; s < S; ++s)  // fill the ring
+    if (!issue_one()) break;
+
+  bool aborted = false;
+  while (true) {
+    if (comp_left == 0) {
+      if (have_item) finish_item();
+      if (ring_head == ring_tail) break;  // everything issued has been computed
+      start_item();
+    }
+    const uint32_t st = g_comp % S;
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (g_comp / S) & 1))) {
+      if (lane == 0) record_error(p.err, kDevWaitTimeout);
+      aborted = true;
+      break;
+    }
+    const uint32_t kbase = tiles_addr + st * kStage;
+    const uint32_t vbase = kbase + kPage;
+    const int key_base = comp_page * kBlockSize;
+
+    // V rows of keys that no row of the item sees (an edge page): zero
+    if (key_base < cur.pad[1] || key_base + kBlockSize > cur.pad[2]) {
+      uint8_t* v = tiles + st * kStage + kPage;
+#pragma unroll
+      for (int i = lane; i < kPage / 16; i += 32) {
+        const int key = key_base + (i % (kBlockSize * 8)) / 8;
+        if (key < cur.pad[1] || key >= cur.pad[2])
+          reinterpret_cast<uint4*>(v)[i] = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+    }
+
+    // S = Q K^T for the page's 16 keys: two n8 tiles, two accumulators per tile (even and
+    // odd k steps) to halve the dependent mma chain
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    {
+      float s2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const int mi = lane >> 3, rr = lane & 7;
+      const int key = (mi >> 1) * 8 + rr;
+#pragma unroll
+      for (int kk = 0; kk < kKSteps; ++kk) {
+        const int chunk = 2 * kk + (mi & 1);
+        const uint32_t addr = kbase + (chunk >> 3) * (kBlockSize * 128) + swz128(key, chunk & 7);
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(addr, b0, b1, b2, b3);
+        float (*acc)[4] = (kk & 1) ? s2 : s;
+        mma_16816<kBF16>(acc[0], qa[kk], b0, b1);
+        mma_16816<kBF16>(acc[1], qa[kk], b2, b3);
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] += s2[nt][e];
+    }
+    // the scores in log2 units: capped, biased, masked
+    if (p.cap_log2 > 0.f) {
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = capped(s[nt][e], p.cap_arg, p.cap_log2);
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] *= p.scale_log2;
+    }
+    const int key0 = key_base + 2 * t4;
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = e >> 1;
+        const int key = key0 + nt * 8 + (e & 1);
+        const float d = fabsf(static_cast<float>(row_pos[r] - key));
+        float x = fmaf(slope[r], d, s[nt][e]);
+        x = key >= row_lo[r] && key < row_hi[r] ? x : -INFINITY;
+        s[nt][e] = x;
+        mx[r] = fmaxf(mx[r], x);
+      }
+    float alpha[2], m_use[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      const float m_new = fmaxf(m_run[r], mx[r]);
+      m_use[r] = m_new == -INFINITY ? 0.f : m_new;
+      alpha[r] = fast_exp2(m_run[r] - m_use[r]);
+      m_run[r] = m_new;
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = fast_exp2(s[nt][e] - m_use[e >> 1]);
+    uint32_t pa[4];
+    pa[0] = pack2<kBF16>(s[0][0], s[0][1]);
+    pa[1] = pack2<kBF16>(s[0][2], s[0][3]);
+    pa[2] = pack2<kBF16>(s[1][0], s[1][1]);
+    pa[3] = pack2<kBF16>(s[1][2], s[1][3]);
+    // the row sums use the rounded P the tensor core multiplies with
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float2 acc = make_float2(l_run[r] * alpha[r], 0.f);
+      add_pair_exact<kBF16>(acc, pa[r]);
+      add_pair_exact<kBF16>(acc, pa[2 + r]);
+      l_run[r] = acc.x + acc.y;
+    }
+    const float2 a0 = make_float2(alpha[0], alpha[0]), a1 = make_float2(alpha[1], alpha[1]);
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+      const float2 u = fmul2(make_float2(o[j][0], o[j][1]), a0);
+      const float2 w = fmul2(make_float2(o[j][2], o[j][3]), a1);
+      o[j][0] = u.x;
+      o[j][1] = u.y;
+      o[j][2] = w.x;
+      o[j][3] = w.y;
+    }
+    {  // O += P V: the V page is [key][d], read transposed
+      const int mi = lane >> 3, rr = lane & 7;
+      const int key = (mi & 1) * 8 + rr;
+#pragma unroll
+      for (int np = 0; np < D / 16; ++np) {
+        const int chunk = 2 * np + (mi >> 1);
+        const uint32_t addr = vbase + (chunk >> 3) * (kBlockSize * 128) + swz128(key, chunk & 7);
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_t(addr, b0, b1, b2, b3);
+        mma_16816<kBF16>(o[2 * np], pa, b0, b1);
+        mma_16816<kBF16>(o[2 * np + 1], pa, b2, b3);
+      }
+    }
+    ++g_comp;
+    ++comp_page;
+    --comp_left;
+    __syncwarp();
+    fence_proxy_async_smem();
+    issue_one();
+  }
+  if (aborted) {
+    // let the copies already issued land before the CTA's shared memory goes away
+    for (uint32_t gg = g_comp; gg < g_issue; ++gg) mbar_wait(&full[gg % S], (gg / S) & 1, 1u << 20);
+  }
+}
+
+template <bool kBF16, int D, bool kDirect>
+cudaError_t launch_t(const MaskedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                     int ctas, cudaStream_t stream, bool pdl) {
+  constexpr int smem = MaskedSplit<D>::kSmem;
+  auto kern = masked_split_kernel<kBF16, D, kDirect>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = ensure_smem_limit(kern, smem, done);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(ctas), dim3(kWarps * 32), smem, stream, pdl, kmap, vmap, p);
+}
+
+template <bool kDirect>
+cudaError_t launch_d(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                     const CUtensorMap& vmap, int ctas, cudaStream_t stream, bool pdl) {
+  if (p.D == 128)
+    return bf16 ? launch_t<true, 128, kDirect>(p, kmap, vmap, ctas, stream, pdl)
+                : launch_t<false, 128, kDirect>(p, kmap, vmap, ctas, stream, pdl);
+  return bf16 ? launch_t<true, 64, kDirect>(p, kmap, vmap, ctas, stream, pdl)
+              : launch_t<false, 64, kDirect>(p, kmap, vmap, ctas, stream, pdl);
+}
+
+}  // namespace
+
+cudaError_t launch_masked_split(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, int ctas, cudaStream_t stream,
+                                bool pdl) {
+  return p.direct ? launch_d<true>(p, bf16, kmap, vmap, ctas, stream, pdl)
+                  : launch_d<false>(p, bf16, kmap, vmap, ctas, stream, pdl);
+}
+
+}  // namespace ps
