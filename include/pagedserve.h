@@ -205,8 +205,8 @@ int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, 
  * is. A logit of -inf or NaN is no continuation (and adds nothing to lse_w); nor has a beam
  * whose score is not finite, or one with a logit of +inf, any. Where fewer than n_select
  * remain, the rest are parent -1, token -1, score -inf.
- * lse is summed in fp32 within 8192 logits and in fp64 across them; scores are compared in
- * fp64 and rounded once to fp32.
+ * lse is summed in fp32 within a chunk of the row and in fp64 across chunks; scores are
+ * compared as pairs of floats (48 bits) and rounded once to fp32.
  *
  *   logits        [B, W, V] of logits_dtype (PS_F16, PS_BF16 or PS_F32), rows row_stride
  *                 ELEMENTS apart (at least V: a padded vocabulary is left out by it),
@@ -217,7 +217,7 @@ int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, 
  *   parents, tokens  int32 [B, n_select], out_scores float [B, n_select], written.
  *   workspace     device scratch of ps_beam_select_workspace_size() bytes, 256-byte aligned;
  *                 calls that share one must not overlap on the device.
- * W and n_select up to 32, W * V below 2^31 - 8192; PS_ERR_UNSUPPORTED beyond. B = 0 is a
+ * W and n_select up to 32, W * V below 2^31 - 2^17; PS_ERR_UNSUPPORTED beyond. B = 0 is a
  * no-op.
  */
 size_t ps_beam_select_workspace_size(int B, int W, int V, int n_select);

@@ -637,15 +637,17 @@ namespace {
 int check_beam(int B, int W, int V, int n) {
   if (B < 0 || W <= 0 || V <= 0 || n <= 0) return PS_ERR_ARG;
   if (W > ps::kBeamMaxWidth || n > ps::kBeamMaxWidth) return PS_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(W) * V > INT32_MAX - ps::kBeamChunk) return PS_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(B) * W * ps::beam_chunks(V) > INT32_MAX) return PS_ERR_UNSUPPORTED;
+  // flat indexes, and a chunk past the row's end, stay 32-bit; so do the CTAs
+  if (static_cast<int64_t>(W) * V > INT32_MAX - (1 << 17)) return PS_ERR_UNSUPPORTED;
+  const int64_t rows = static_cast<int64_t>(B) * W;
+  if (rows > INT32_MAX || rows * ps::beam_chunks(rows, V) > INT32_MAX) return PS_ERR_UNSUPPORTED;
   return PS_OK;
 }
 }  // namespace
 
 size_t ps_beam_select_workspace_size(int B, int W, int V, int n_select) {
   if (check_beam(B, W, V, n_select)) return 0;
-  const size_t lists = static_cast<size_t>(B) * W * ps::beam_chunks(V);
+  const size_t rows = static_cast<size_t>(B) * W, lists = rows * ps::beam_chunks(rows, V);
   return ps::up256(lists * sizeof(float2)) + ps::up256(lists * n_select * 8);
 }
 
@@ -677,7 +679,8 @@ int ps_beam_select(const void* logits, int64_t row_stride, const float* scores,
   a.V = V;
   a.n = n_select;
   a.pad = pad_token;
-  a.chunks = ps::beam_chunks(V);
+  a.chunk = ps::beam_chunk(static_cast<int64_t>(B) * W, V);
+  a.chunks = ps::beam_chunks(static_cast<int64_t>(B) * W, V);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.stat = reinterpret_cast<float2*>(ws);
   a.cand = reinterpret_cast<unsigned long long*>(
@@ -845,6 +848,7 @@ int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_p
   p.scale_log2 = static_cast<float>(scale * log2e);
   p.cap_log2 = static_cast<float>(softcap * log2e);
   p.cap_arg = softcap > 0.f ? static_cast<float>(2.0 * log2e * scale / softcap) : 0.f;
+  p.cap_y = softcap > 0.f ? scale / softcap : 0.f;
   // (a scale or cap at the ends of the range)
   if (!std::isfinite(p.scale_log2) || !std::isfinite(p.cap_log2) || !std::isfinite(p.cap_arg))
     return PS_ERR_ARG;

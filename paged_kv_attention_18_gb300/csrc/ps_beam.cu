@@ -5,16 +5,15 @@
 // One pass over the logits. Within a beam the order of the scores is the order of the
 // logits, so a chunk's n best candidates are chosen on the logits alone, before lse is
 // known; the few that are left are scored and compared across chunks and beams in 64 bits.
-//   scan    one CTA per (beam, chunk of kChunk logits). The chunk is held in registers:
-//           16-byte loads, all in flight at once. Its maximum M and sum of exp(x - M) are
-//           exact reductions of what is held; the candidates are the logits at or above a
-//           bound tau: the n-th largest of a warp's 32 thread maxima is at most the n-th
-//           largest logit of the chunk, and tau is the largest such bound of the CTA's
-//           warps. A few dozen logits pass it; they are ranked among themselves.
+//   scan    one CTA per (beam, chunk of logits), streamed in 16-byte loads: each thread keeps
+//           its maximum m and the sum of exp(x - m). The candidates are the logits at or
+//           above a bound tau: the n-th largest of a warp's 32 thread maxima is at most the
+//           n-th largest logit of the chunk, and tau is the largest such bound of the CTA's
+//           warps. The few threads whose maximum reaches tau read their words again (from
+//           the caches); a few dozen logits pass, and are ranked among themselves.
 //   merge   one CTA per prompt: lse of each beam from its chunks' (M, sum), then the same
 //           bound on the chunks' candidates, and the ranks of those that pass.
-// Bound by the bytes of the logits (read once). Sums: a chunk's 32 terms per thread are
-// added in fp32, then across threads in fp32 pairs and across chunks in 64 bits.
+// Bound by the bytes of the logits (read once).
 #include "ps_common.cuh"
 #include "ps_launch.h"
 
@@ -23,22 +22,10 @@ namespace ps {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kChunk = kBeamChunk;
-constexpr int kPerThread = kChunk / kThreads;  // logits per thread
-constexpr int kCap = 1024;                     // candidates ranked in shared memory
+constexpr int kRound = 8192;  // logits a CTA has in flight at a time
+constexpr int kCap = 1024;    // candidates ranked in shared memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994530942;
-
-template <typename T>
-__device__ __forceinline__ float widen(T x);
-template <>
-__device__ __forceinline__ float widen<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float widen<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 x) {
-  return __bfloat162float(x);
-}
 
 // NaN counts as -inf, -0 as +0 (so that it ties with it).
 __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
@@ -48,9 +35,8 @@ __device__ __forceinline__ uint32_t order32(float x) {
   const uint32_t u = __float_as_uint(x);
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
-__device__ __forceinline__ unsigned long long order64(double x) {
-  const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x));
-  return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+__device__ __forceinline__ float from_order32(uint32_t o) {
+  return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
 constexpr uint32_t kOrderNegInf = 0x007fffffu;  // order32(-inf)
 
@@ -102,10 +88,45 @@ __device__ __forceinline__ unsigned long long block_max(unsigned long long k,
   return k;
 }
 
+// The elements of one 16-byte word as floats, NaN as -inf.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& w, float* x);
+template <>
+__device__ __forceinline__ void unpack<float>(const uint4& w, float* x) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = fmaxf(__uint_as_float(u[i]), -INFINITY);
+}
+template <>
+__device__ __forceinline__ void unpack<__half>(const uint4& w, float* x) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&u[i]),
+                              __half2half2(__ushort_as_half(0xfc00)));
+    const float2 f = __half22float2(h);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& w, float* x) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&u[i]),
+                                     __bfloat162bfloat162(__ushort_as_bfloat16(0xff80)));
+    const float2 f = __bfloat1622float2(h);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-  constexpr int kLoads = kPerThread / kVec;
+  constexpr int kUnroll = kRound / kVec / kThreads;  // words of a thread per round
+  static_assert(kUnroll >= 1, "a round is at least one word per thread");
   __shared__ uint32_t sh_key[2 * kWarps];
   __shared__ float sh_sum[kWarps];
   __shared__ unsigned long long sh_max[kWarps];
@@ -119,61 +140,92 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
   }
   if (threadIdx.x == 0) count = 0;
   const T* base = static_cast<const T*>(p.logits) + row * p.ld;
-  // vectors start at the 16-byte boundary at or before the row's first logit
+  // words start at the 16-byte boundary at or before the row's first logit; `lo` is the
+  // token of the chunk's first place (below 0 by the row's offset from that boundary)
   const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / sizeof(T));
-  const int first = chunk * kChunk - skew;  // token of the chunk's first place
-  float x[kPerThread];
+  const int lo = chunk * p.chunk - skew;
+  const int end = min(lo + p.chunk, p.V);  // one past the chunk's last token
+  const int rounds = end > lo ? (end - lo + kRound - 1) / kRound : 0;
+  // the word at token t (a multiple of kVec past lo); outside the chunk -inf, not read
+  auto load = [&](int t) -> uint4 {
+    if (t >= 0 && t + kVec <= end) return __ldg(reinterpret_cast<const uint4*>(base + t));
+    union {
+      uint4 w;
+      T e[kVec];
+    } u;
 #pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int t0 = first + (j * kThreads + threadIdx.x) * kVec;
-    if (t0 >= 0 && t0 + kVec <= p.V) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(base + t0));
-      const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) x[j * kVec + i] = clean(widen<T>(e[i]));
-    } else {  // the row's ends: what lies outside the row is not read
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const int t = t0 + i;
-        x[j * kVec + i] = t >= 0 && t < p.V ? clean(widen<T>(base[t])) : -INFINITY;
-      }
-    }
-  }
-  auto token = [&](int i) {
-    return first + ((i / kVec) * kThreads + static_cast<int>(threadIdx.x)) * kVec + i % kVec;
+    for (int i = 0; i < kVec; ++i)
+      u.e[i] = t + i >= 0 && t + i < end ? base[t + i] : static_cast<T>(-INFINITY);
+    return u.w;
   };
-  float m = -INFINITY;
+  auto place = [&](int r, int j) {
+    return lo + r * kRound + (j * kThreads + static_cast<int>(threadIdx.x)) * kVec;
+  };
+  // one pass: the thread's maximum m and its sum of exp(x - sub), sub = m but for -inf
+  float m = -INFINITY, sub = 0.f;
+  float2 sum = make_float2(0.f, 0.f);
+  for (int r = 0; r < rounds; ++r) {
+    uint4 w[kUnroll];
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) m = fmaxf(m, x[i]);
-  uint32_t top, tau;
-  block_bound(order32(m), p.n, sh_key, top, tau);
-  const float M = __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xffffffffu));
-  // sum of exp(x - M), and the candidates
-  float s0 = 0.f, s1 = 0.f;
-  // (x - M first: rounding M log2(e) once for all terms would shift their sum)
-  const float sub = M == -INFINITY ? 0.f : M;
-  const uint32_t bound = tau > kOrderNegInf ? tau : kOrderNegInf + 1;
+    for (int j = 0; j < kUnroll; ++j) w[j] = load(place(r, j));
 #pragma unroll
-  for (int i = 0; i < kPerThread; i += 2) {
-    s0 += fast_exp2((x[i] - sub) * kLog2e);
-    s1 += fast_exp2((x[i + 1] - sub) * kLog2e);
-  }
-  if (order32(m) >= bound) {
+    for (int j = 0; j < kUnroll; ++j) {
+      float x[kVec];
+      unpack<T>(w[j], x);
+      float mx = m;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const uint32_t k = order32(x[i]);
-      if (k >= bound) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kCap)
-          list[at] = (static_cast<unsigned long long>(k) << 32) |
-                     (0xffffffffu - static_cast<uint32_t>(token(i)));
+      for (int i = 0; i < kVec; i += 2) mx = fmax3(mx, x[i], x[i + 1]);
+      if (mx > m) {
+        const float a = sum.x + sum.y > 0.f ? fast_exp2((sub - mx) * kLog2e) : 0.f;
+        sum = fmul2(sum, make_float2(a, a));
+        m = sub = mx;
+      }
+      // (x - sub first: rounding sub log2(e) once for all terms would shift their sum)
+      const float2 one = make_float2(1.f, 1.f), ns = make_float2(-sub, -sub);
+#pragma unroll
+      for (int i = 0; i < kVec; i += 2) {
+        const float2 y = fmul2(ffma2(make_float2(x[i], x[i + 1]), one, ns),
+                               make_float2(kLog2e, kLog2e));
+        sum = ffma2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), one, sum);
       }
     }
   }
-  float s = s0 + s1;
+  const uint32_t mine = order32(clean(m));
+  uint32_t top, tau;
+  block_bound(mine, p.n, sh_key, top, tau);
+  const float M = from_order32(top);
+  float s = m > -INFINITY ? (sum.x + sum.y) * fast_exp2((m - M) * kLog2e) : 0.f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((threadIdx.x & 31) == 0) sh_sum[threadIdx.x >> 5] = s;
+  // the candidates: the few threads whose maximum reaches the bound look again (their
+  // words are in the caches)
+  const uint32_t bound = tau > kOrderNegInf ? tau : kOrderNegInf + 1;
+  // f(key): of every logit of the thread at or above the bound
+  auto each = [&](auto f) {
+    for (int r = 0; r < rounds; ++r) {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) w[j] = load(place(r, j));
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        float x[kVec];
+        unpack<T>(w[j], x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const uint32_t k = order32(clean(x[i]));
+          if (k >= bound)
+            f((static_cast<unsigned long long>(k) << 32) |
+              (0xffffffffu - static_cast<uint32_t>(place(r, j) + i)));
+        }
+      }
+    }
+  };
+  if (mine >= bound)
+    each([&](unsigned long long k) {
+      const int at = atomicAdd(&count, 1);
+      if (at < kCap) list[at] = k;
+    });
   __syncthreads();
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -198,20 +250,27 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
     unsigned long long last = ~0ull;
     for (int r = 0; r < p.n; ++r) {
       unsigned long long best = 0;
-#pragma unroll
-      for (int i = 0; i < kPerThread; ++i) {
-        const uint32_t k32 = order32(x[i]);
-        const unsigned long long k = (static_cast<unsigned long long>(k32) << 32) |
-                                     (0xffffffffu - static_cast<uint32_t>(token(i)));
-        if (k32 >= bound && k < last && k > best) best = k;
-      }
+      if (mine >= bound)
+        each([&](unsigned long long k) {
+          if (k < last && k > best) best = k;
+        });
       last = block_max(best, sh_max);
       if (threadIdx.x == 0) out[r] = last;
     }
   }
 }
 
-// A candidate of the merge: its score's 64-bit order and its flat index (beam * V + token).
+// Scores are pairs of floats hi + lo (|lo| at most half a step of hi): cum + (x - lse) with
+// 2^-46 of the largest of the three lost at most, in fp32 adds alone (fp64 runs at a small
+// fraction of their rate here). Equal values give equal pairs, and pairs in the order of
+// (hi, lo) are in the order of their values.
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = __fadd_rn(a, b);
+  const float t = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+}
+
+// A candidate of the merge: its score's order and its flat index (beam * V + token).
 struct Best {
   unsigned long long score;
   int flat;
@@ -222,8 +281,8 @@ __device__ __forceinline__ bool better(const Best& a, const Best& b) {
 
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
   __shared__ uint32_t sh_key[2 * kWarps];
-  __shared__ double sh_lse[kBeamMaxWidth];
-  __shared__ double sh_cum[kBeamMaxWidth];
+  __shared__ float2 sh_lse[kBeamMaxWidth];  // hi, lo
+  __shared__ float sh_cum[kBeamMaxWidth];
   __shared__ int sh_kind[kBeamMaxWidth];  // 0 no candidate, 1 scored, 2 finished
   __shared__ Best list[kCap];
   __shared__ Best sh_best[kWarps];
@@ -262,7 +321,8 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     }
     if (lane == 0) {
       sh_kind[w] = kind;
-      sh_lse[w] = lse;
+      const float hi = static_cast<float>(lse);
+      sh_lse[w] = make_float2(hi, static_cast<float>(lse - hi));
       sh_cum[w] = cum;
     }
   }
@@ -272,32 +332,31 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   auto entry = [&](int i, Best& e) -> bool {
     const int w = i / per_beam, r = i - w * per_beam;
     const int kind = sh_kind[w];
-    double s;
+    float hi, lo = 0.f;
     if (kind == 2) {
       if (r != 0) return false;
-      s = sh_cum[w];
+      hi = sh_cum[w];
       e.flat = w * p.V + p.pad;
     } else {
       if (kind == 0) return false;
       const unsigned long long k = p.cand[(static_cast<int64_t>(b) * p.W + w) * per_beam + r];
       if (k == 0) return false;
-      const uint32_t o = static_cast<uint32_t>(k >> 32);
-      const float x = __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
-      s = sh_cum[w] + (static_cast<double>(x) - sh_lse[w]);
+      const float x = from_order32(static_cast<uint32_t>(k >> 32));
+      float d, e1, t, e2;
+      two_sum(x, -sh_lse[w].x, d, e1);
+      two_sum(sh_cum[w], d, t, e2);
+      const float rest = __fadd_rn(e2, __fsub_rn(e1, sh_lse[w].y));
+      two_sum(t, rest, hi, lo);
       e.flat = w * p.V + static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
     }
-    e.score = order64(s + 0.0);
+    e.score = (static_cast<unsigned long long>(order32(hi + 0.f)) << 32) | order32(lo + 0.f);
     return true;
   };
-  auto value = [](unsigned long long o) {
-    return __longlong_as_double(
-        static_cast<long long>(o ^ ((o >> 63) ? 0x8000000000000000ull : ~0ull)));
-  };
-  // the bound, on the scores rounded down to fp32 (which keeps their order)
+  // the bound, on the scores' high parts
   uint32_t mine = 0;
   for (int i = threadIdx.x; i < total; i += kThreads) {
     Best e;
-    if (entry(i, e)) mine = max(mine, order32(__double2float_rd(value(e.score))));
+    if (entry(i, e)) mine = max(mine, static_cast<uint32_t>(e.score >> 32));
   }
   uint32_t top, tau;
   block_bound(mine, p.n, sh_key, top, tau);
@@ -305,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   if (mine >= bound) {
     for (int i = threadIdx.x; i < total; i += kThreads) {
       Best e;
-      if (entry(i, e) && order32(__double2float_rd(value(e.score))) >= bound) {
+      if (entry(i, e) && static_cast<uint32_t>(e.score >> 32) >= bound) {
         const int at = atomicAdd(&count, 1);
         if (at < kCap) list[at] = e;
       }
@@ -316,7 +375,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   auto put = [&](int rank, const Best& e) {
     p.parents[o + rank] = e.flat / p.V;
     p.tokens[o + rank] = e.flat % p.V;
-    p.out_scores[o + rank] = static_cast<float>(value(e.score));
+    p.out_scores[o + rank] = from_order32(static_cast<uint32_t>(e.score >> 32));
   };
   auto none = [&](int rank) {
     p.parents[o + rank] = -1;
@@ -361,9 +420,20 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
 
 }  // namespace
 
-int beam_chunks(int V) {
-  // a row may start up to 15 bytes past a 16-byte boundary: 7 logits of 16 bits
-  return static_cast<int>((static_cast<int64_t>(V) + 7 + kChunk - 1) / kChunk);
+// Logits per CTA, a multiple of a round's share that fills the SMs a few times over: long
+// chunks spread a CTA's fixed costs (the bound, the ranks, its launch) over more bytes, short
+// ones keep a small batch's rows on many SMs.
+int beam_chunk(int64_t rows, int V) {
+  constexpr int64_t kStep = 2048, kTargetCtas = 1216;  // 8 a SM on 152 SMs
+  int64_t c = (rows * V / kTargetCtas + kStep - 1) / kStep * kStep;
+  c = c < kStep ? kStep : c > 65536 ? 65536 : c;
+  return static_cast<int>(c);
+}
+
+int beam_chunks(int64_t rows, int V) {
+  // a row may start up to 14 bytes past a 16-byte boundary: 7 logits of 16 bits
+  const int c = beam_chunk(rows, V);
+  return static_cast<int>((static_cast<int64_t>(V) + 7 + c - 1) / c);
 }
 
 cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stream) {

@@ -71,6 +71,7 @@ struct MaskedAttnParams : AttnParams {
   static constexpr bool kMasked = true;
   float cap_log2;         // cap * log2(e); 0: scores are not capped
   float cap_arg;          // 2 * log2(e) * scale / cap (the tanh's exponent per raw score)
+  float cap_y;            // scale / cap (its argument per raw score)
   const float* slopes;    // [H_q] slope of the distance bias, or null
   int window;             // keys a row sees, its own included; 0: all before it
   const int32_t* prefix;  // [B] or null
@@ -190,20 +191,21 @@ cudaError_t launch_rotary(const RotaryParams& p, int D, bool interleaved, bool b
                           cudaStream_t stream);
 
 // Beam search's selection over beams and vocabulary.
-constexpr int kBeamChunk = 8192;    // logits per scanning CTA
 constexpr int kBeamMaxWidth = 32;   // beams, and candidates kept, at most
 struct BeamParams {
   const void* logits;             // [B, W, V], rows `ld` elements apart
   int64_t ld;
   const float* scores;            // [B, W]
   const uint8_t* finished;        // [B, W] or null
-  int B, W, V, n, pad, chunks;
+  int B, W, V, n, pad;
+  int chunk, chunks;              // logits per scanning CTA, CTAs per row
   float2* stat;                   // [B * W, chunks] workspace: maximum, sum of exp(x - max)
   unsigned long long* cand;       // [B * W, chunks, n] workspace: best (logit, token), or 0
   int32_t *parents, *tokens;      // [B, n]
   float* out_scores;              // [B, n]
 };
-int beam_chunks(int V);
+int beam_chunk(int64_t rows, int V);
+int beam_chunks(int64_t rows, int V);
 // dtype: 0 fp16, 1 bf16, 2 fp32
 cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stream);
 

@@ -618,9 +618,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tS + 64 * h + 32, v + 32);
           tmem_ld_wait();
           if (has_cap) {
+            float top = 0.f;
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              v[e] = __float_as_uint(capped(__uint_as_float(v[e]), p.cap_arg, p.cap_log2));
+            for (int e = 0; e < 64; e += 2) {
+              const float2 x = capped_small2(
+                  make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), p.cap_y,
+                  p.cap_log2, top);
+              v[e] = __float_as_uint(x.x);
+              v[e + 1] = __float_as_uint(x.y);
+            }
+            if (__any_sync(0xffffffffu, top > 1.f)) {
+              // a score past the cap: the half again (S is still in TMEM)
+              tmem_ld32(tS + 64 * h, v);
+              tmem_ld32(tS + 64 * h + 32, v + 32);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                v[e] = __float_as_uint(capped(__uint_as_float(v[e]), p.cap_arg, p.cap_log2));
+            }
           }
           if (has_bias) {
             const float scale = has_cap ? 1.f : p.scale_log2;
