@@ -72,6 +72,7 @@ struct MaskedAttnParams : AttnParams {
   float cap_log2;         // cap * log2(e); 0: scores are not capped
   float cap_arg;          // 2 * log2(e) * scale / cap (the tanh's exponent per raw score)
   float cap_y;            // scale / cap (its argument per raw score)
+  float tanh4[4], tanh6[6];  // the cap's polynomials times cap_log2 (see capped_poly2)
   const float* slopes;    // [H_q] slope of the distance bias, or null
   int window;             // keys a row sees, its own included; 0: all before it
   const int32_t* prefix;  // [B] or null
@@ -265,9 +266,20 @@ cudaError_t launch_plan_masked(const MaskedAttnParams& p, int concurrency, int t
 cudaError_t launch_masked_split(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int ctas, cudaStream_t stream,
                                 bool pdl);
-cudaError_t launch_masked_tile(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
-                               const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
-                               cudaStream_t stream, bool direct);
+// (the tile kernel is one per kind of score, each in a file of its own)
+using MaskedTileLaunch = cudaError_t(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                                     const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
+                                     cudaStream_t stream, bool direct);
+MaskedTileLaunch launch_masked_tile_plain, launch_masked_tile_cap, launch_masked_tile_bias,
+    launch_masked_tile_cap_bias;
+inline cudaError_t launch_masked_tile(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                                      const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
+                                      cudaStream_t stream, bool direct) {
+  MaskedTileLaunch* const f =
+      p.cap_log2 > 0.f ? (p.slopes ? launch_masked_tile_cap_bias : launch_masked_tile_cap)
+                       : (p.slopes ? launch_masked_tile_bias : launch_masked_tile_plain);
+  return f(p, bf16, kmap, vmap, qmap, ctas, stream, direct);
+}
 int run_masked_attention(const MaskedAttnParams& p, const void* k_pool, const void* v_pool,
                          bool bf16, cudaStream_t s);
 

@@ -16,22 +16,23 @@ __device__ __forceinline__ float capped(float raw, float arg, float cap_log2) {
   return fmaf(r, -2.f * cap_log2, cap_log2);
 }
 
-// The same on two scores whose |y| = |raw| scale / cap is at most 1, without special
-// functions: tanh(y) = y P(y^2), P of degree 5 fitted to a largest relative error of
-// 2^-20.6 over |y| <= 1 (a cap of 50 is 72 in log2 units: 2^-14.4 on the score). `y_of` is
-// scale / cap. `top` is raised to the largest y^2: above 1 the result does not hold.
-__device__ __forceinline__ float2 capped_small2(float2 raw, float y_of, float cap_log2,
-                                                float& top) {
-  const float2 y = fmul2(raw, make_float2(y_of, y_of));
+// cap * log2(e) * tanh(y) + c on two scores y = raw * scale / cap of small size, without
+// special functions: y P(y^2) cap log2(e), P fitted to tanh(y) / y in the largest relative
+// error. kTerms = 4: |y| <= 1/2 within 2^-20.7; kTerms = 6: |y| <= 1 within 2^-20.6 (a cap
+// of 50 is 72 in log2 units: 2^-14.5 on the largest score). `k` holds P's coefficients
+// times cap * log2(e), highest first.
+template <int kTerms>
+__device__ __forceinline__ float2 capped_poly2(float2 y, const float* k, float2 c) {
   const float2 t = fmul2(y, y);
-  top = fmax3(top, t.x, t.y);
-  auto two = [](float c) { return make_float2(c, c); };
-  float2 q = ffma2(t, two(-0.003067068289965391f), two(0.016743160784244537f));
-  q = ffma2(q, t, two(-0.051605746150016785f));
-  q = ffma2(q, t, two(0.13281437754631042f));
-  q = ffma2(q, t, two(-0.3332904279232025f));
-  q = ffma2(q, t, two(0.9999994039535522f));
-  return fmul2(fmul2(y, two(cap_log2)), q);
+  float2 q = ffma2(t, make_float2(k[0], k[0]), make_float2(k[1], k[1]));
+#pragma unroll
+  for (int i = 2; i < kTerms; ++i) q = ffma2(q, t, make_float2(k[i], k[i]));
+  return ffma2(y, q, c);
 }
+constexpr float kTanh4[4] = {-0.04440223425626755f, 0.13190299272537231f,
+                                        -0.33326318860054016f, 0.999999463558197f};
+constexpr float kTanh6[6] = {-0.003067068289965391f, 0.016743160784244537f,
+                                        -0.051605746150016785f, 0.13281437754631042f,
+                                        -0.3332904279232025f,   0.9999994039535522f};
 
 }  // namespace ps

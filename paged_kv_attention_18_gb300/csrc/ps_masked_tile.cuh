@@ -18,6 +18,10 @@
 //   - a key tile inside every row's interval skips the mask; in others a row drops the
 //     columns outside [lo, hi);
 //   - rows without keys get zeros, and -inf as the log-sum of a split that holds them.
+#pragma once
+
+#include <type_traits>
+
 #include "ps_common.cuh"
 #include "ps_launch.h"
 #include "ps_masked.cuh"
@@ -78,6 +82,9 @@ struct TileBars {
 };
 static_assert(sizeof(TileBars) <= 512, "barrier block");
 
+// How a half's scores reach log2 units (see the softmax groups).
+enum ScoreKind : int { kFast, kWide, kReady };
+
 // An item fits this launch: a sequence and KV head of the batch, a page range inside the
 // block table, and query rows inside the packed batch. Every role checks each item the
 // same way and skips one that does not fit, so no role reads or writes outside its
@@ -94,7 +101,7 @@ __device__ __forceinline__ bool tile_item_ok(const WorkItem& w, const MaskedAttn
 
 // kDirect: no plan. Each CTA derives its items from seq_lens and qsl (every sequence
 // unsplit, its query-tile pairs longest first).
-template <bool kBF16, int D, bool kDirect>
+template <bool kBF16, int D, bool kDirect, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
     masked_tile_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap,
@@ -184,6 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();  // the inputs may still be being written by the kernel before
   }
 
+  // The key tile walked j-th of nt: with a bias the nearest first, so that the running
+  // reference is set by the scores the bias lowers least and later tiles seldom move it.
+  auto tile_at = [](int j, int nt) { return kBias ? nt - 1 - j : j; };
   // Bounded wait with a warp-uniform outcome: if any lane gives up (or another role has
   // given up), the whole warp leaves its loop together.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -352,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // K (or V) tiles of 8 pages; pages past the split read the zero fill. One lane per
       // page copy: lane = page * kHalves + half (64-element half of the head).
       const int32_t* bt = p.block_tables + static_cast<int64_t>(seq) * p.max_blocks;
-      int bt_base = -1000, bt_reg = -1;
+      int bt_base = 1 << 28, bt_reg = -1;
       bool ok = true;
       const int pp = lane / kHalves, h = lane % kHalves;
       for (int j = 0; j < nt; ++j) {
-        const int first = pb + j * kPagesPerTile;
-        if (first - bt_base + kPagesPerTile > 32) {
-          bt_base = first;
-          bt_reg = first + lane < pe ? __ldg(bt + first + lane) : -1;
+        const int first = pb + tile_at(j, nt) * kPagesPerTile;
+        if (first < bt_base || first - bt_base + kPagesPerTile > 32) {
+          bt_base = kBias ? max(first + kPagesPerTile - 32, 0) : first;
+          bt_reg = bt_base + lane < pe ? __ldg(bt + bt_base + lane) : -1;
         }
         const uint32_t st = g % n_stages;
         uint64_t* empty = is_k ? &bars->k_empty[st] : &bars->v_empty[st];
@@ -518,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
              (j + 1 >= nt || wait(&bars->k_full[gk % kKStages], (gk / kKStages) & 1));
         if (!ok) break;
         // keys of this tile's pages that no row of the item sees: their V rows are zeroed
-        const int kb = (pb + j * kPagesPerTile) * kBlockSize;
+        const int kb = (pb + tile_at(j, nt) * kPagesPerTile) * kBlockSize;
         const int ke = min(kb + kKeys, pe * kBlockSize);
         if (kb < w.pad[1] || ke > w.pad[2]) {
           uint8_t* v = smem + L::kOffV + (gv % kVStages) * L::kK;
@@ -544,9 +554,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = quarter * 32 + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t tS = trow + col_s(grp), tO = trow + col_o(grp);
-    // scores that are capped or biased come out of that in log2 units
-    const bool has_cap = p.cap_log2 > 0.f, has_bias = p.slopes != nullptr;
-    const float sl2 = has_cap || has_bias ? 1.f : p.scale_log2;
     uint32_t sc = 0, act = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
@@ -568,7 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the row's keys: [key_lo, key_hi] within the item
       const int key_hi = min(max(pos, w.pad[3] - 1), pe * kBlockSize - 1);
       const int key_lo = valid ? p.row_lo(tok, pos) : 0;
-      const float slope = has_bias && valid ? -kLog2e * __ldg(p.slopes + head) : 0.f;
+      const float slope = kBias && valid ? -kLog2e * __ldg(p.slopes + head) : 0.f;
+      float2 steps[4];  // the bias of columns 0..7 relative to column 0
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        steps[i] = make_float2(-slope * (2.f * i), -slope * (2.f * i + 1.f));
       // the row's split count and partial base, fetched now so that the epilogue's
       // stores do not wait on them
       // (both loads are issued at once; nothing waits for them before the epilogue)
@@ -580,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < nt; ++j) {
         // visible columns: c <= lim (a row past the tile's rows is computed unmasked and
         // not written)
-        const int tile0 = pb * kBlockSize + j * kKeys;  // the tile's first key
+        const int tile0 = pb * kBlockSize + tile_at(j, nt) * kKeys;  // the tile's first key
         const int lim = valid ? key_hi - tile0 : kKeys, low = valid ? key_lo - tile0 : 0;
         if (!wait(&bars->s_full[grp], sc & 1)) { ok = false; break; }
         ++sc;
@@ -608,6 +619,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P = 2^(s*scale*log2e - m_ref) as 16-bit pairs written over S; half h of P lands
         // on columns 32h..32h+31, which the loads of halves <= h have already read
         const bool full = __all_sync(0xffffffffu, lim >= kKeys - 1 && low <= 0);
+        // every column visible, and (with a bias) none past the row's own position
+        const bool one_sign =
+            full && (!kBias || __all_sync(0xffffffffu, !valid || pos >= tile0 + kKeys - 1));
         // l holds the earlier tiles' sum; this tile's halves are summed apart, so that a
         // reference moved in half 1 can re-sum the half-0 P it re-rounds
         float l_half0 = 0.f, l_h = 0.f;
@@ -617,44 +631,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tS + 64 * h, v);
           tmem_ld32(tS + 64 * h + 32, v + 32);
           tmem_ld_wait();
-          if (has_cap) {
-            float top = 0.f;
-#pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              const float2 x = capped_small2(
-                  make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), p.cap_y,
-                  p.cap_log2, top);
-              v[e] = __float_as_uint(x.x);
-              v[e + 1] = __float_as_uint(x.y);
-            }
-            if (__any_sync(0xffffffffu, top > 1.f)) {
-              // a score past the cap: the half again (S is still in TMEM)
-              tmem_ld32(tS + 64 * h, v);
-              tmem_ld32(tS + 64 * h + 32, v + 32);
-              tmem_ld_wait();
+          // How P is taken from the raw scores. kReady: they have been brought to log2 units in
+          // place (any cap, any bias, masked). The others do it on the way, with packed
+          // arithmetic alone, where every column is visible, the cap's argument is small and
+          // the distances have one sign. Without cap and bias the mask is all there is.
+          auto to_log2 = [&]() {
+            if constexpr (kCap) {
 #pragma unroll
               for (int e = 0; e < 64; ++e)
                 v[e] = __float_as_uint(capped(__uint_as_float(v[e]), p.cap_arg, p.cap_log2));
             }
-          }
-          if (has_bias) {
-            const float scale = has_cap ? 1.f : p.scale_log2;
-            const float d0 = static_cast<float>(pos - tile0 - 64 * h);  // distance of column 0
+            if constexpr (kBias) {
+              const float scale = kCap ? 1.f : p.scale_log2;
+              const float d0 = static_cast<float>(pos - tile0 - 64 * h);  // of the first column
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              v[e] = __float_as_uint(fmaf(slope, fabsf(d0 - static_cast<float>(e)),
-                                          __uint_as_float(v[e]) * scale));
-          }
-          if (!full) {
+              for (int e = 0; e < 64; ++e)
+                v[e] = __float_as_uint(fmaf(slope, fabsf(d0 - static_cast<float>(e)),
+                                            __uint_as_float(v[e]) * scale));
+            }
+            if (!full) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (64 * h + e > lim || 64 * h + e < low) v[e] = __float_as_uint(-INFINITY);
+              for (int e = 0; e < 64; ++e)
+                if (64 * h + e > lim || 64 * h + e < low) v[e] = __float_as_uint(-INFINITY);
+            }
+          };
+          int kind = kFast;
+          if constexpr (kCap) {
+            float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                a[k] = fmax3(a[k], fabsf(__uint_as_float(v[e + 2 * k])),
+                             fabsf(__uint_as_float(v[e + 2 * k + 1])));
+            const float y = fmax3(fmaxf(a[0], a[1]), a[2], a[3]) * p.cap_y;
+            kind = __all_sync(0xffffffffu, y <= 0.5f)              ? kFast
+                   : !kBias && __all_sync(0xffffffffu, y <= 1.f) ? kWide
+                                                                 : kReady;
+          }
+          // P is taken against the row's reference without the half's max; the max (and a move
+          // of the reference) is taken only when there is no reference yet, or when the half's
+          // sum shows that P outgrew its bound, and P is then taken again
+          bool with_max = __any_sync(0xffffffffu, m_ref == -INFINITY);
+          if constexpr (kCap || kBias) {
+            if (!one_sign || kind == kReady || (with_max && kBias)) {
+              to_log2();
+              kind = kReady;
+            }
+          } else if (!full) {
+            to_log2();
           }
           uint32_t pk[32];
-          // P is taken against the row's reference without the half's max; the max (and a
-          // move of the reference) is taken only when there is no reference yet, or when
-          // the half's sum shows that P outgrew its bound, and P is then taken again
-          bool with_max = __any_sync(0xffffffffu, m_ref == -INFINITY);
 #pragma unroll 1
           for (int pass = 0; pass < 2; ++pass) {
             if (with_max) {
@@ -666,7 +693,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 4; ++k)
                   mq[k] = fmax3(mq[k], __uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1]));
               const float mx = fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]);
-              const float m_half = mx == -INFINITY ? -INFINITY : mx * sl2;
+              // (the cap and the scale keep the order: the max of the raw scores will do)
+              const float m_half = mx == -INFINITY || kind == kReady ? mx
+                                   : kCap ? capped(mx, p.cap_arg, p.cap_log2)
+                                          : mx * p.scale_log2;
               // no reference yet, or a jump P could overflow on: move the reference now,
               // rescaling what is already taken against the old one
               const bool move = m_half > m_ref + kMoveLog2<kBF16> ||
@@ -697,15 +727,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
             float2 lq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // four sums
-            // scale and subtract two scores per packed fma; the row sum adds the 16-bit P
-            // values the MMA sees, widened exactly
-            const float2 sl2x2 = make_float2(sl2, sl2), nm2 = make_float2(neg_m, neg_m);
-#pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              const float2 x = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
-                                     sl2x2, nm2);
+            // the scores to log2 units below the reference, two per packed operation; the row
+            // sum adds the 16-bit P values the MMA sees, widened exactly
+            const float2 nm2 = make_float2(neg_m, neg_m);
+            auto raw = [&](int e) {
+              return make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            };
+            auto put = [&](int e, float2 x) {
               pk[e / 2] = pack2<kBF16>(fast_exp2(x.x), fast_exp2(x.y));
               add_pair_exact<kBF16>(lq[(e / 2) & 1], pk[e / 2]);
+            };
+            // bias - m of columns e, e + 1: slope * (distance of column e & ~7) - m, and the
+            // rest of the distance from steps[]
+            const float dist0 = static_cast<float>(pos - tile0 - 64 * h);
+            auto bias = [&](int e) {
+              const float x = fmaf(slope, dist0 - static_cast<float>(e & ~7), neg_m);
+              return ffma2(make_float2(x, x), make_float2(1.f, 1.f), steps[(e & 7) / 2]);
+            };
+            const float2 sl2x2 = make_float2(p.scale_log2, p.scale_log2);
+            const float2 cap_y2 = make_float2(p.cap_y, p.cap_y);
+            if ((kCap || kBias) && kind == kReady) {
+#pragma unroll
+              for (int e = 0; e < 64; e += 2) put(e, ffma2(raw(e), make_float2(1.f, 1.f), nm2));
+            } else if (kCap && !kBias && kind == kWide) {
+#pragma unroll
+              for (int e = 0; e < 64; e += 2)
+                put(e, capped_poly2<6>(fmul2(raw(e), cap_y2), p.tanh6, nm2));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 64; e += 2) {
+                const float2 c = kBias ? bias(e) : nm2;
+                put(e, kCap ? capped_poly2<4>(fmul2(raw(e), cap_y2), p.tanh4, c)
+                            : ffma2(raw(e), sl2x2, c));
+              }
             }
             // P goes out before its sum is checked; a second pass writes it again
             if (pass > 0) tmem_st_wait();
@@ -714,6 +768,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             l_h = (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
             if (with_max || __all_sync(0xffffffffu, l_h <= kHalfSumMax<kBF16>)) break;
             with_max = true;
+            if (kBias && kind != kReady) {  // the max is of the biased scores
+              to_log2();
+              kind = kReady;
+            }
           }
           if (h == 0) l_half0 = l_h;
           else l += l_half0 + l_h;
@@ -813,34 +871,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!kDirect && p.after_split && blockIdx.x == 0 && threadIdx.x == 0) pdl_wait();
 }
 
-template <bool kBF16, int D, bool kDirect>
-static cudaError_t launch_t(const MaskedAttnParams& p, const CUtensorMap& kmap,
-                                 const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
-                                 cudaStream_t stream) {
+template <bool kBF16, int D, bool kDirect, bool kCap, bool kBias>
+static cudaError_t launch_masked_tile_t(const MaskedAttnParams& p, const CUtensorMap& kmap,
+                                        const CUtensorMap& vmap, const CUtensorMap& qmap,
+                                        int ctas, cudaStream_t stream) {
   constexpr int smem = TileSmem<D>::kBytes;
-  auto kern = masked_tile_kernel<kBF16, D, kDirect>;
+  auto kern = masked_tile_kernel<kBF16, D, kDirect, kCap, kBias>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_limit(kern, smem, done);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(ctas), dim3(kThreads), smem, stream, true, kmap, vmap, qmap, p);
 }
 
-template <bool kDirect>
-static cudaError_t launch_d(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
-                                 const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
-                                 cudaStream_t stream) {
-  if (p.D == 128)
-    return bf16 ? launch_t<true, 128, kDirect>(p, kmap, vmap, qmap, ctas, stream)
-                : launch_t<false, 128, kDirect>(p, kmap, vmap, qmap, ctas, stream);
-  return bf16 ? launch_t<true, 64, kDirect>(p, kmap, vmap, qmap, ctas, stream)
-              : launch_t<false, 64, kDirect>(p, kmap, vmap, qmap, ctas, stream);
-}
-
-cudaError_t launch_masked_tile(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
-                               const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
-                               cudaStream_t stream, bool direct) {
-  return direct ? launch_d<true>(p, bf16, kmap, vmap, qmap, ctas, stream)
-                : launch_d<false>(p, bf16, kmap, vmap, qmap, ctas, stream);
+// The instantiations of one (cap, bias) pair: one per type, head size and mode.
+template <bool kCap, bool kBias>
+static cudaError_t launch_masked_tile_kind(const MaskedAttnParams& p, bool bf16,
+                                           const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                           const CUtensorMap& qmap, int ctas,
+                                           cudaStream_t stream, bool direct) {
+  auto go = [&](auto b, auto d, auto m) {
+    return launch_masked_tile_t<b.value, d.value, m.value, kCap, kBias>(p, kmap, vmap, qmap, ctas,
+                                                                        stream);
+  };
+  using std::bool_constant;
+  auto mode = [&](auto b, auto d) {
+    return direct ? go(b, d, bool_constant<true>{}) : go(b, d, bool_constant<false>{});
+  };
+  auto size = [&](auto b) {
+    return p.D == 128 ? mode(b, std::integral_constant<int, 128>{})
+                      : mode(b, std::integral_constant<int, 64>{});
+  };
+  return bf16 ? size(bool_constant<true>{}) : size(bool_constant<false>{});
 }
 
 }  // namespace ps
