@@ -198,25 +198,18 @@ def spec_accept(target_probs, draft_tokens, random_bits=None, draft_probs=None,
     return out, num
 
 
-def _device_of(t: torch.Tensor, name: str) -> int:
-    """Index of the device the tensors of a call live on: the current one."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise PagedServeError(f"{name} must be a CUDA tensor")
-    dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise PagedServeError(f"{name} is on device {dev}, not on the current CUDA device")
-    return dev
+_native_module = None
 
 
-def _on(t: torch.Tensor, name: str, dev: int, dtype, ndim: int) -> int:
-    """Address of a contiguous tensor of the given type and rank on device `dev`."""
-    try:
-        if t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _dev(t, name, dtype, ndim)  # says what is wrong with it
-    raise PagedServeError(f"{name} is on {t.device}, the other tensors on device {dev}")
+def _native():
+    """The compiled argument checks and calls (csrc/py_native.cpp); missing is an error."""
+    global _native_module
+    if _native_module is None:
+        lib()  # its own error when the build is missing
+        from . import _native as module
+        module.set_error(PagedServeError)
+        _native_module = module
+    return _native_module
 
 
 def _alloc(shape, dtype, device, stream) -> torch.Tensor:
@@ -227,22 +220,6 @@ def _alloc(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _tokens(t: torch.Tensor, name: str, dev: int, dtype) -> tuple[int, int]:
-    """Address and token stride of a tensor [T, heads, D] on device `dev` whose tokens are
-    dense rows, at any distance from one another."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        raise PagedServeError(f"{name} must be a tensor on CUDA device {dev}")
-    if t.dtype is not dtype:
-        raise PagedServeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 3:
-        raise PagedServeError(f"{name} must have 3 dimensions, has {t.dim()}")
-    T, H, D = t.shape
-    st = t.stride()
-    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
-        raise PagedServeError(f"{name}: a token's heads must lie together")
-    return t.data_ptr(), st[0] if T > 1 else H * D
-
-
 def rotary_reshape_and_cache(q, k, v, positions, slot_mapping_t, k_pool, v_pool, inv_freq,
                              interleaved: bool = False, magnitude: float = 1.0, q_out=None,
                              stream=None) -> torch.Tensor:
@@ -251,39 +228,8 @@ def rotary_reshape_and_cache(q, k, v, positions, slot_mapping_t, k_pool, v_pool,
     inv_freq is float64 [rotary_dim / 2] (see :func:`rotary.frequencies`); pairs are
     neighbours (interleaved) or halves of the first rotary_dim elements, the rest of a head
     passes through. q, k, v and q_out may be views whose tokens lie apart. Returns q_out."""
-    dev = _device_of(q, "q")
-    dt = q.dtype
-    if dt not in DTYPE_CODE:
-        raise PagedServeError("q must be a float16 or bfloat16 tensor")
-    if q_out is None:
-        q_out = q
-    qp, qs = _tokens(q, "q", dev, dt)
-    kp, ks = _tokens(k, "k", dev, dt)
-    vp, vs = _tokens(v, "v", dev, dt)
-    op, os_ = (qp, qs) if q_out is q else _tokens(q_out, "q_out", dev, dt)
-    pp = _on(positions, "positions", dev, torch.int32, 1)
-    sp = _on(slot_mapping_t, "slot_mapping", dev, torch.int32, 1)
-    kpp = _on(k_pool, "k_pool", dev, dt, 4)
-    vpp = _on(v_pool, "v_pool", dev, dt, 4)
-    fp = _on(inv_freq, "inv_freq", dev, torch.float64, 1)
-    T, H_q, D = q.shape
-    pool = k_pool.shape
-    H_kv = pool[2]
-    kv = (T, H_kv, D)
-    if k.shape != kv or v.shape != kv or q_out.shape != q.shape or pool[1] != BLOCK_SIZE or \
-            pool[3] != D or v_pool.shape != pool or len(positions) != T or \
-            len(slot_mapping_t) != T:
-        raise PagedServeError("rotary_reshape_and_cache: inconsistent shapes")
-    _check(lib().ps_rotary_reshape_and_cache(qp, qs, kp, ks, vp, vs, pp, sp, kpp, vpp, fp,
-                                             2 * inv_freq.shape[0], 1 if interleaved else 0,
-                                             float(magnitude), op, os_, T, H_q, H_kv, D, pool[0],
-                                             DTYPE_CODE[dt],
-                                             _stream(stream)),
-           "ps_rotary_reshape_and_cache")
-    return q_out
-
-
-LOGITS_CODE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+    return (_native_module or _native()).rotary(q, k, v, positions, slot_mapping_t, k_pool, v_pool,
+                                                inv_freq, interleaved, magnitude, q_out, stream)
 
 
 def alloc_beam_workspace(B: int, W: int, V: int, n_select: int, device=None) -> torch.Tensor:
@@ -298,37 +244,17 @@ def beam_select(logits, scores, n_select: int, finished=None, pad_token: int = 0
     float32; the last dimension of a padded vocabulary may be cut by a view), scores float32
     [B, W], finished uint8 or bool [B, W] or None. Returns (parents, tokens, scores), each
     [B, n_select]."""
-    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 3 or \
-            logits.dtype not in LOGITS_CODE:
-        raise PagedServeError("logits must be a float CUDA tensor with 3 dimensions")
-    B, W, V = logits.shape
-    st = logits.stride()
-    ld = st[1] if W > 1 else st[0] if B > 1 else V
-    if (V > 1 and st[2] != 1) or (B > 1 and W > 1 and st[0] != W * st[1]):
-        raise PagedServeError("logits: rows must be dense and equally far apart")
-    dev = _device_of(logits, "logits")
-    sp = _on(scores, "scores", dev, torch.float32, 2)
-    fp = None
-    if finished is not None:
-        kind = torch.bool if getattr(finished, "dtype", None) is torch.bool else torch.uint8
-        fp = _on(finished, "finished", dev, kind, 2)
-    if scores.shape != (B, W) or (finished is not None and finished.shape != (B, W)):
-        raise PagedServeError("beam_select: inconsistent shapes")
-    if n_select < 1:
-        raise PagedServeError("beam_select: n_select must be positive")
-    if workspace is None:
-        n = max(int(lib().ps_beam_select_workspace_size(B, W, V, n_select)), 256)
-        workspace = _alloc(n, torch.uint8, logits.device, stream)
-    wp = _on(workspace, "workspace", dev, torch.uint8, 1)
-    # the three results in one allocation (of int32, the last seen as float32)
-    res = _alloc((3, B, n_select), torch.int32, logits.device, stream)
-    rp, step = res.data_ptr(), 4 * B * n_select
-    _check(lib().ps_beam_select(logits.data_ptr(), ld, sp, fp, pad_token, B, W, V, n_select,
-                                LOGITS_CODE[logits.dtype], rp, rp + step, rp + 2 * step, wp,
-                                workspace.numel(), _stream(stream)),
-           "ps_beam_select")
-    parents, tokens, best = res.unbind(0)
-    return parents, tokens, best.view(torch.float32)
+    parents = tokens = best = None
+    if stream is not None and isinstance(logits, torch.Tensor) and logits.is_cuda and n_select > 0:
+        # memory for a stream that is not the current one comes from that stream
+        shape, dev = (logits.shape[0], n_select), logits.device
+        parents, tokens, best = (_alloc(shape, t, dev, stream)
+                                 for t in (torch.int32, torch.int32, torch.float32))
+        if workspace is None:
+            n = int(lib().ps_beam_select_workspace_size(*logits.shape, n_select))
+            workspace = _alloc(max(n, 256), torch.uint8, dev, stream)
+    return (_native_module or _native()).select(logits, scores, n_select, finished, pad_token,
+                                                workspace, parents, tokens, best, stream)
 
 
 def fork_sequences(block_tables, seq_lens, parents, tail_blocks, k_pool, v_pool,
@@ -339,32 +265,8 @@ def fork_sequences(block_tables, seq_lens, parents, tail_blocks, k_pool, v_pool,
     tail_blocks int32 [groups, n_out]; pools [layers, num_blocks, 16, H_kv, D] (or one
     layer's, without the first dimension); out_block_tables [groups * n_out, max_blocks] and
     out_seq_lens [groups * n_out] are written."""
-    dev = _device_of(k_pool, "k_pool")
-    dt, ndim = k_pool.dtype, k_pool.dim()
-    if dt not in DTYPE_CODE or ndim not in (4, 5):
-        raise PagedServeError("k_pool must be a float16 or bfloat16 tensor of 4 or 5 dimensions")
-    bt = _on(block_tables, "block_tables", dev, torch.int32, 2)
-    sl = _on(seq_lens, "seq_lens", dev, torch.int32, 1)
-    pp = _on(parents, "parents", dev, torch.int32, 2)
-    tp = _on(tail_blocks, "tail_blocks", dev, torch.int32, 2)
-    ot = _on(out_block_tables, "out_block_tables", dev, torch.int32, 2)
-    ol = _on(out_seq_lens, "out_seq_lens", dev, torch.int32, 1)
-    kp = _on(k_pool, "k_pool", dev, dt, ndim)
-    vp = _on(v_pool, "v_pool", dev, dt, ndim)
-    groups, n_out = parents.shape
-    n, width = block_tables.shape
-    pool = k_pool.shape
-    if v_pool.shape != pool or pool[-3] != BLOCK_SIZE or len(seq_lens) != n or \
-            tail_blocks.shape != parents.shape or \
-            out_block_tables.shape != (groups * n_out, width) or \
-            len(out_seq_lens) != groups * n_out or (groups > 0 and n % groups != 0):
-        raise PagedServeError("fork_sequences: inconsistent shapes")
-    if groups == 0:
-        return
-    _check(lib().ps_fork_sequences(bt, width, sl, pp, tp, groups, n // groups, n_out, kp, vp,
-                                   pool[0] if ndim == 5 else 1, pool[-4], pool[-2], pool[-1],
-                                   DTYPE_CODE[dt], ot, ol, _stream(stream)),
-           "ps_fork_sequences")
+    (_native_module or _native()).fork(block_tables, seq_lens, parents, tail_blocks, k_pool, v_pool,
+                                       out_block_tables, out_seq_lens, stream)
 
 
 def workspace_size(T: int, B: int, H_q: int, H_kv: int, D: int, max_seq_len: int) -> int:
@@ -413,52 +315,19 @@ def masked_paged_attention(q, k_pool, v_pool, block_tables, seq_lens, query_star
     (distance_slopes float32 [H_q]), a sliding window, a bidirectional prefix (prefix_lens
     int32 [B]) and documents packed into a sequence (key_starts int32 [T]); see
     ps_paged_attention_masked. Rows that see no key give zeros."""
-    dev = _device_of(q, "q")
-    dt = q.dtype
-    if dt not in DTYPE_CODE:
-        raise PagedServeError("q must be a float16 or bfloat16 tensor")
-    qp = _on(q, "q", dev, dt, 3)
-    kpp = _on(k_pool, "k_pool", dev, dt, 4)
-    vpp = _on(v_pool, "v_pool", dev, dt, 4)
-    bt = _on(block_tables, "block_tables", dev, torch.int32, 2)
-    sl = _on(seq_lens, "seq_lens", dev, torch.int32, 1)
-    qs = _on(query_start_loc, "query_start_loc", dev, torch.int32, 1)
-    T, H_q, D = q.shape
-    NB, bs, H_kv, Dk = k_pool.shape
-    B, maxblk = block_tables.shape
-    if len(seq_lens) != B or len(query_start_loc) != B + 1:
-        raise PagedServeError("block_tables / query_start_loc do not match seq_lens")
-    if bs != BLOCK_SIZE or Dk != D or v_pool.shape != k_pool.shape:
-        raise PagedServeError("masked_paged_attention: inconsistent pool shape")
-    dp = pp = sp = None
-    if distance_slopes is not None:
-        dp = _on(distance_slopes, "distance_slopes", dev, torch.float32, 1)
-        if len(distance_slopes) != H_q:
-            raise PagedServeError("distance_slopes: one per query head")
-    if prefix_lens is not None:
-        pp = _on(prefix_lens, "prefix_lens", dev, torch.int32, 1)
-        if len(prefix_lens) != B:
-            raise PagedServeError("prefix_lens: one per sequence")
-    if key_starts is not None:
-        sp = _on(key_starts, "key_starts", dev, torch.int32, 1)
-        if len(key_starts) != T:
-            raise PagedServeError("key_starts: one per packed token")
-    if out is None:
-        out = _alloc(q.shape, dt, q.device, stream)
-    op = _on(out, "out", dev, dt, 3)
-    if out.shape != q.shape:
-        raise PagedServeError("out must have q's shape")
-    if workspace is None:
-        msl = max_seq_len if max_seq_len is not None else maxblk * BLOCK_SIZE
-        workspace = _alloc(max(workspace_size(T, B, H_q, H_kv, D, msl), 256), torch.uint8,
-                           q.device, stream)
-    wp = _on(workspace, "workspace", dev, torch.uint8, 1)
-    _check(lib().ps_paged_attention_masked(qp, kpp, vpp, bt, maxblk, sl, qs, B, T, H_q, H_kv, D,
-                                           NB, float(scale), float(softcap), dp, window, pp, sp, op,
-                                           wp, workspace.numel(), DTYPE_CODE[dt],
-                                           _stream(stream)),
-           "ps_paged_attention_masked")
-    return out
+    if stream is not None and isinstance(q, torch.Tensor) and q.is_cuda:
+        # memory for a stream that is not the current one comes from that stream
+        if out is None:
+            out = _alloc(q.shape, q.dtype, q.device, stream)
+        if workspace is None and q.dim() == 3 and k_pool.dim() == 4:
+            B, width = block_tables.shape
+            msl = max_seq_len if max_seq_len is not None else width * BLOCK_SIZE
+            n = workspace_size(q.shape[0], B, q.shape[1], k_pool.shape[2], q.shape[2], msl)
+            workspace = _alloc(max(n, 256), torch.uint8, q.device, stream)
+    return (_native_module or _native()).attend(q, k_pool, v_pool, block_tables, seq_lens,
+                                                query_start_loc, scale, softcap, distance_slopes,
+                                                window, prefix_lens, key_starts, out, workspace,
+                                                max_seq_len, stream)
 
 
 def attention_step(q, k, v, k_pool, v_pool, block_tables, seq_lens, query_start_loc,

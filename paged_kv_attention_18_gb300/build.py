@@ -1,4 +1,5 @@
-"""Build the in-tree CUDA library ``libpagedserve.so`` for sm_103a with nvcc.
+"""Build the in-tree CUDA library ``libpagedserve.so`` for sm_103a with nvcc, and the Python
+module ``_native`` that calls it with the host compiler.
 
 Each ``csrc/*.cu`` file compiles in parallel to an object under ``_build/`` at the
 repository root; the objects link into ``paged_kv_attention_18_gb300/libpagedserve.so``
@@ -11,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpagedserve.so")
+NATIVE = os.path.join(PKG, "_native.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -30,6 +33,52 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build the library")
+
+
+def _run(cmd: list[str], what: str, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout + r.stderr, flush=True)
+
+
+def _native_object(verbose: bool) -> str:
+    """The Python module's object, by the torch it is compiled against."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    src = os.path.join(CSRC, "py_native.cpp")
+    obj = os.path.join(BUILD, f"py_native.{torch.__version__}.o")
+    if not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src),
+                                                              _newest_header()):
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+        abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC",
+              f"-D_GLIBCXX_USE_CXX11_ABI={abi}", f"-I{INCLUDE}",
+              f"-I{sysconfig.get_paths()['include']}", f"-I{inc}",
+              f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-I{cuda}", "-c", src,
+              "-o", obj], f"compiling {src}", verbose)
+    return obj
+
+
+def _link_native(obj: str, verbose: bool) -> None:
+    import torch
+    stamp = os.path.join(BUILD, "native.stamp")  # the object the module was linked from
+    linked = open(stamp).read() if os.path.exists(stamp) else ""
+    if os.path.exists(NATIVE) and linked == obj and \
+            os.path.getmtime(NATIVE) >= max(os.path.getmtime(obj), os.path.getmtime(LIB)):
+        return
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = NATIVE + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{PKG}",
+          "-l:libpagedserve.so", f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+          "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"],
+         "linking the Python module", verbose)
+    os.replace(tmp, NATIVE)
+    with open(stamp, "w") as f:
+        f.write(obj)
 
 
 def _newest_header() -> float:
@@ -59,17 +108,16 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
                 print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    # (the host compiler's one object beside nvcc's)
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        native = ex.submit(_native_object, verbose)
         objs = list(ex.map(compile_one, srcs))
+        native_obj = native.result()
     if (not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs)):
         tmp = LIB + ".tmp"
-        cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
+        _run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], "nvcc link", verbose)
         os.replace(tmp, LIB)
+    _link_native(native_obj, verbose)
     return LIB
 
 

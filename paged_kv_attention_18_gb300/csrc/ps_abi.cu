@@ -387,19 +387,28 @@ int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const v
   if ((rc = make_pool_map(&vmap, v_pool, p.num_blocks, p.H_kv, p.D, bf16))) return rc;
   if (tiles && (rc = make_q_map(&qmap, p.q, p.T, p.H_q, p.D, p.G, p.tpt, bf16))) return rc;
   cudaError_t e;
-  if (direct_fits(p, num_sms)) {
-    p.direct = 1;
-    const int64_t items = static_cast<int64_t>(p.B) * p.H_kv;
-    const int warps = attention_warps(p.D);
-    const int64_t want = (items + warps - 1) / warps;
+  // At most four 16-row groups in the whole batch and contexts that one CTA reads in the time
+  // a plan and a join would take: one launch, a CTA for each (sequence, KV head, group).
+  constexpr int kMaskedDirectGroups = 4, kMaskedDirectPages = 128;
+  const int64_t groups = (static_cast<int64_t>(p.T) * p.G + 15) / 16;
+  if (groups <= kMaskedDirectGroups && p.max_blocks <= kMaskedDirectPages &&
+      groups * p.B * p.H_kv <= num_sms) {
+    p.direct = static_cast<int>(groups);
     Timed tm(3, s);
-    if ((e = launch_masked_split(p, bf16, kmap, vmap,
-                                 static_cast<int>(want < num_sms ? want : num_sms), s, true)) !=
-        cudaSuccess)
+    if ((e = launch_masked_split(p, bf16, kmap, vmap, static_cast<int>(groups * p.B * p.H_kv), s,
+                                 true)) != cudaSuccess)
       return cuda_fail(e, "masked split attention kernel (direct)");
     return PS_OK;
   }
-  if (tiles && direct_tile_fits(p, num_sms)) {
+  // The tile kernel without a plan: short contexts, or longer ones with enough query tiles
+  // that the plan would not split a context either (it splits below half an item per CTA; a
+  // sequence's pairs of tiles are at least n / (2 tpt)). With contexts of 512 pages the
+  // plan's order, taken from a counter, is worth more than its launch: 725 us against 792
+  // for 4 x 2048 tokens over 8192 keys.
+  const bool few = tiles && p.B <= kDirectTileMaxSeqs && static_cast<int64_t>(p.B) * p.H_kv * 2 <= num_sms;
+  if (few && (p.max_blocks <= kDirectMaxPages ||
+              (p.max_blocks <= 2 * kDirectMaxPages &&
+               static_cast<int64_t>(p.T) / p.tpt * p.H_kv >= num_sms))) {
     Timed tm(5, s);
     if ((e = launch_masked_tile(p, bf16, kmap, vmap, qmap, direct_tile_ctas(p, num_sms), s,
                                 true)) != cudaSuccess)

@@ -9,8 +9,8 @@
 //           its maximum m and the sum of exp(x - m). The candidates are the logits at or
 //           above a bound tau: the n-th largest of a warp's 32 thread maxima is at most the
 //           n-th largest logit of the chunk, and tau is the largest such bound of the CTA's
-//           warps. The few threads whose maximum reaches tau read their words again (from
-//           the caches); a few dozen logits pass, and are ranked among themselves.
+//           warps. Where a thread's maximum of a round reaches tau, its warp reads those 32
+//           logits again (from the caches); a few dozen pass, and are ranked.
 //   merge   one CTA per prompt: lse of each beam from its chunks' (M, sum), then the same
 //           bound on the chunks' candidates, and the ranks of those that pass.
 // Bound by the bytes of the logits (read once).
@@ -22,10 +22,23 @@ namespace ps {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRound = 8192;  // logits a CTA has in flight at a time
-constexpr int kCap = 1024;    // candidates ranked in shared memory
+constexpr int kRound = 32 * kThreads;  // logits of a CTA per round of loads, two in flight
+constexpr int kRounds = 4;             // rounds, at most
+constexpr int kCap = 1024;             // candidates ranked in shared memory
+constexpr int kEarly = 2;              // entries a merging thread holds in registers
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994530942;
+
+template <typename T>
+__device__ __forceinline__ float widen(T x);
+template <>
+__device__ __forceinline__ float widen<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float widen<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 x) {
+  return __bfloat162float(x);
+}
 
 // NaN counts as -inf, -0 as +0 (so that it ties with it).
 __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
@@ -125,14 +138,15 @@ __device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& w, float* x) 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-  constexpr int kUnroll = kRound / kVec / kThreads;  // words of a thread per round
-  static_assert(kUnroll >= 1, "a round is at least one word per thread");
+  constexpr int kWords = kRound / kVec / kThreads;  // words of a thread per round
+  static_assert(kWords * kVec == 32, "a round is 32 logits per thread, one per lane");
   __shared__ uint32_t sh_key[2 * kWarps];
   __shared__ float sh_sum[kWarps];
   __shared__ unsigned long long sh_max[kWarps];
   __shared__ unsigned long long list[kCap];
   __shared__ int count;
   pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
   if (p.finished != nullptr && p.finished[row]) {
     pdl_launch_dependents();
@@ -145,7 +159,6 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
   const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / sizeof(T));
   const int lo = chunk * p.chunk - skew;
   const int end = min(lo + p.chunk, p.V);  // one past the chunk's last token
-  const int rounds = end > lo ? (end - lo + kRound - 1) / kRound : 0;
   // the word at token t (a multiple of kVec past lo); outside the chunk -inf, not read
   auto load = [&](int t) -> uint4 {
     if (t >= 0 && t + kVec <= end) return __ldg(reinterpret_cast<const uint4*>(base + t));
@@ -158,27 +171,35 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
       u.e[i] = t + i >= 0 && t + i < end ? base[t + i] : static_cast<T>(-INFINITY);
     return u.w;
   };
-  auto place = [&](int r, int j) {
-    return lo + r * kRound + (j * kThreads + static_cast<int>(threadIdx.x)) * kVec;
-  };
-  // one pass: the thread's maximum m and its sum of exp(x - sub), sub = m but for -inf
-  float m = -INFINITY, sub = 0.f;
+  // token of thread `thread`'s word j of round r
+  auto place = [&](int r, int j, int thread) { return lo + r * kRound + (j * kThreads + thread) * kVec; };
+  // one pass: the thread's maximum m, each round's own maximum, and the thread's sum of
+  // exp(x - sub), sub = m but for -inf; the next round's words are on their way meanwhile
+  float m = -INFINITY, sub = 0.f, mr[kRounds];
   float2 sum = make_float2(0.f, 0.f);
-  for (int r = 0; r < rounds; ++r) {
-    uint4 w[kUnroll];
+  uint4 w[kWords];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) w[j] = load(place(r, j));
+  for (int j = 0; j < kWords; ++j) w[j] = load(place(0, j, threadIdx.x));
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
+  for (int r = 0; r < kRounds; ++r) {
+    mr[r] = -INFINITY;
+    if (lo + r * kRound >= end) continue;
+    uint4 next[kWords];
+    const bool more = r + 1 < kRounds && lo + (r + 1) * kRound < end;
+    if (more) {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) next[j] = load(place(r + 1, j, threadIdx.x));
+    }
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
       float x[kVec];
       unpack<T>(w[j], x);
-      float mx = m;
 #pragma unroll
-      for (int i = 0; i < kVec; i += 2) mx = fmax3(mx, x[i], x[i + 1]);
-      if (mx > m) {
-        const float a = sum.x + sum.y > 0.f ? fast_exp2((sub - mx) * kLog2e) : 0.f;
+      for (int i = 0; i < kVec; i += 2) mr[r] = fmax3(mr[r], x[i], x[i + 1]);
+      if (mr[r] > m) {
+        const float a = sum.x + sum.y > 0.f ? fast_exp2((sub - mr[r]) * kLog2e) : 0.f;
         sum = fmul2(sum, make_float2(a, a));
-        m = sub = mx;
+        m = sub = mr[r];
       }
       // (x - sub first: rounding sub log2(e) once for all terms would shift their sum)
       const float2 one = make_float2(1.f, 1.f), ns = make_float2(-sub, -sub);
@@ -189,49 +210,45 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
         sum = ffma2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), one, sum);
       }
     }
+    if (more) {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) w[j] = next[j];
+    }
   }
-  const uint32_t mine = order32(clean(m));
   uint32_t top, tau;
-  block_bound(mine, p.n, sh_key, top, tau);
+  block_bound(order32(clean(m)), p.n, sh_key, top, tau);
   const float M = from_order32(top);
   float s = m > -INFINITY ? (sum.x + sum.y) * fast_exp2((m - M) * kLog2e) : 0.f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) sh_sum[threadIdx.x >> 5] = s;
-  // the candidates: the few threads whose maximum reaches the bound look again (their
-  // words are in the caches)
+  if (lane == 0) sh_sum[warp] = s;
+  // The candidates. A round of a thread is 32 logits: where its maximum reaches the bound,
+  // the warp reads them again (from the caches), one per lane. f(key) is called for every
+  // logit at or above the bound.
   const uint32_t bound = tau > kOrderNegInf ? tau : kOrderNegInf + 1;
-  // f(key): of every logit of the thread at or above the bound
   auto each = [&](auto f) {
-    for (int r = 0; r < rounds; ++r) {
-      uint4 w[kUnroll];
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) w[j] = load(place(r, j));
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        float x[kVec];
-        unpack<T>(w[j], x);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const uint32_t k = order32(clean(x[i]));
-          if (k >= bound)
-            f((static_cast<unsigned long long>(k) << 32) |
-              (0xffffffffu - static_cast<uint32_t>(place(r, j) + i)));
-        }
+    for (int r = 0; r < kRounds; ++r) {
+      uint32_t who = __ballot_sync(0xffffffffu, order32(clean(mr[r])) >= bound);
+      for (; who; who &= who - 1) {
+        const int t = place(r, lane / kVec, warp * 32 + __ffs(who) - 1) + lane % kVec;
+        if (t < 0 || t >= end) continue;
+        const uint32_t k = order32(clean(widen<T>(base[t])));
+        if (k >= bound)
+          f((static_cast<unsigned long long>(k) << 32) | (0xffffffffu - static_cast<uint32_t>(t)));
       }
     }
   };
-  if (mine >= bound)
-    each([&](unsigned long long k) {
-      const int at = atomicAdd(&count, 1);
-      if (at < kCap) list[at] = k;
-    });
+  each([&](unsigned long long k) {
+    const int at = atomicAdd(&count, 1);
+    if (at < kCap) list[at] = k;
+  });
   __syncthreads();
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += sh_sum[w];
+    for (int i = 0; i < kWarps; ++i) s += sh_sum[i];
     p.stat[blockIdx.x] = make_float2(M, s);
   }
   unsigned long long* out = p.cand + static_cast<int64_t>(blockIdx.x) * p.n;
@@ -248,14 +265,13 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
     // more equal logits than the list holds: n rounds of the block's largest key below
     // the one before
     unsigned long long last = ~0ull;
-    for (int r = 0; r < p.n; ++r) {
+    for (int i = 0; i < p.n; ++i) {
       unsigned long long best = 0;
-      if (mine >= bound)
-        each([&](unsigned long long k) {
-          if (k < last && k > best) best = k;
-        });
+      each([&](unsigned long long k) {
+        if (k < last && k > best) best = k;
+      });
       last = block_max(best, sh_max);
-      if (threadIdx.x == 0) out[r] = last;
+      if (threadIdx.x == 0) out[i] = last;
     }
   }
 }
@@ -287,9 +303,18 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   __shared__ Best list[kCap];
   __shared__ Best sh_best[kWarps];
   __shared__ int count;
-  pdl_wait();
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) count = 0;
+  const int per_beam = p.chunks * p.n, total = p.W * per_beam;
+  const unsigned long long* cand = p.cand + static_cast<int64_t>(b) * total;
+  pdl_wait();
+  // the thread's first entries, read beside the chunks' sums
+  unsigned long long early[kEarly];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    early[k] = i < total ? cand[i] : 0;
+  }
   for (int w = warp; w < p.W; w += kWarps) {
     const int row = b * p.W + w;
     const float cum = p.scores[row];
@@ -327,9 +352,8 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     }
   }
   __syncthreads();
-  const int per_beam = p.chunks * p.n, total = p.W * per_beam;
-  // entry i of the prompt's lists; false where there is none
-  auto entry = [&](int i, Best& e) -> bool {
+  // entry i (logit and token k) of the prompt's lists; false where there is none
+  auto entry = [&](int i, unsigned long long k, Best& e) -> bool {
     const int w = i / per_beam, r = i - w * per_beam;
     const int kind = sh_kind[w];
     float hi, lo = 0.f;
@@ -339,7 +363,6 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
       e.flat = w * p.V + p.pad;
     } else {
       if (kind == 0) return false;
-      const unsigned long long k = p.cand[(static_cast<int64_t>(b) * p.W + w) * per_beam + r];
       if (k == 0) return false;
       const float x = from_order32(static_cast<uint32_t>(k >> 32));
       float d, e1, t, e2;
@@ -353,22 +376,31 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     return true;
   };
   // the bound, on the scores' high parts
+  // f(entry) for each of the thread's entries
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      Best e;
+      if (i < total && entry(i, early[k], e)) f(e);
+    }
+    for (int i = threadIdx.x + kEarly * kThreads; i < total; i += kThreads) {
+      Best e;
+      if (entry(i, cand[i], e)) f(e);
+    }
+  };
   uint32_t mine = 0;
-  for (int i = threadIdx.x; i < total; i += kThreads) {
-    Best e;
-    if (entry(i, e)) mine = max(mine, static_cast<uint32_t>(e.score >> 32));
-  }
+  each([&](const Best& e) { mine = max(mine, static_cast<uint32_t>(e.score >> 32)); });
   uint32_t top, tau;
   block_bound(mine, p.n, sh_key, top, tau);
   const uint32_t bound = tau > 0 ? tau : 1;
   if (mine >= bound) {
-    for (int i = threadIdx.x; i < total; i += kThreads) {
-      Best e;
-      if (entry(i, e) && static_cast<uint32_t>(e.score >> 32) >= bound) {
+    each([&](const Best& e) {
+      if (static_cast<uint32_t>(e.score >> 32) >= bound) {
         const int at = atomicAdd(&count, 1);
         if (at < kCap) list[at] = e;
       }
-    }
+    });
   }
   __syncthreads();
   const int64_t o = static_cast<int64_t>(b) * p.n;
@@ -395,10 +427,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     Best last{~0ull, -1};
     for (int r = 0; r < p.n; ++r) {
       Best best{0, 0x7fffffff};
-      for (int i = threadIdx.x; i < total; i += kThreads) {
-        Best e;
-        if (entry(i, e) && better(last, e) && better(e, best)) best = e;
-      }
+      each([&](const Best& e) {
+        if (better(last, e) && better(e, best)) best = e;
+      });
 #pragma unroll
       for (int s = 16; s; s >>= 1) {
         Best y;
@@ -426,7 +457,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
 int beam_chunk(int64_t rows, int V) {
   constexpr int64_t kStep = 2048, kTargetCtas = 1216;  // 8 a SM on 152 SMs
   int64_t c = (rows * V / kTargetCtas + kStep - 1) / kStep * kStep;
-  c = c < kStep ? kStep : c > 65536 ? 65536 : c;
+  c = c < kStep ? kStep : c > kRounds * kRound ? kRounds * kRound : c;
   return static_cast<int>(c);
 }
 

@@ -263,6 +263,7 @@ cudaError_t launch_plan_masked(const MaskedAttnParams& p, int concurrency, int t
 
 // The split and tile kernels with a mask, capped scores and a distance bias, launched as
 // their causal forms are.
+// p.direct: 16-row groups per sequence in the split kernel's direct mode (0: planned).
 cudaError_t launch_masked_split(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int ctas, cudaStream_t stream,
                                 bool pdl);

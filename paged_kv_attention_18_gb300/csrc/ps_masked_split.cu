@@ -67,8 +67,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   pdl_wait();  // the plan (or, in direct mode, the work before this call) is complete
   pdl_launch_dependents();
 
-  const int n_items = kDirect ? p.B * p.H_kv : *reinterpret_cast<volatile int*>(p.hdr);
-  int direct_next = blockIdx.x * kWarps + warp;
+  const int n_items = kDirect ? 0 : *reinterpret_cast<volatile int*>(p.hdr);
   bool first_fetch = true;
   const bool tile_planned = !kDirect && *reinterpret_cast<volatile int*>(p.hdr + 4) > 0;
   const uint64_t policy = l2_policy_evict_first();
@@ -87,35 +86,44 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                  : -1;
   };
 
-  // Direct mode: the record of item idx = (sequence idx / H_kv, KV head idx % H_kv), all
-  // of the sequence's rows (n * G <= 16) over every page they see; lane k returns field k.
+  // Direct mode: the record of item idx = (sequence, KV head, 16-row group), over every page
+  // its rows see; the CTA's warps share the pages out. Lane k returns field k.
   auto direct_item = [&](int idx) -> int {
-    const int b = idx / p.H_kv, kv = idx - b * p.H_kv;
+    const int j = idx % p.direct, bk = idx / p.direct;
+    const int b = bk / p.H_kv, kv = bk - b * p.H_kv;
     const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), L = __ldg(p.seq_lens + b);
-    const int pages = (L + kBlockSize - 1) / kBlockSize, n = q1 - q0;
-    if (idx == 0 && lane == 0 && (__ldg(p.qsl) != 0 || __ldg(p.qsl + p.B) != p.T))
+    const int n = q1 - q0;
+    if (idx == 0 && warp == 0 && lane == 0 && (__ldg(p.qsl) != 0 || __ldg(p.qsl + p.B) != p.T))
       record_error(p.err, kDevBadSequence);  // tokens outside every sequence
-    if (q0 < 0 || q1 > p.T || n < 0 || n > L || n * p.G > 16 || pages > p.max_blocks) {
+    if (q0 < 0 || q1 > p.T || n < 0 || n > L || (L + kBlockSize - 1) / kBlockSize > p.max_blocks) {
       if (lane == 0) record_error(p.err, kDevBadSequence);
       return 0;
     }
-    if (n == 0) return 0;
-    const int pre = p.prefix_len(b, L), lo = p.row_lo(q0, L - n);
+    if (16 * j >= n * p.G) return 0;
+    const int nrows = min(16, n * p.G - 16 * j);
+    const int i0 = 16 * j / p.G, i1 = (16 * j + nrows - 1) / p.G;
+    const int pre = p.prefix_len(b, L), lo = p.row_lo(q0 + i0, L - n + i0);
+    const int hi = max(L - n + i1 + 1, pre);  // one past the last key (at most L)
+    const int pe = (hi + kBlockSize - 1) / kBlockSize;
+    const int pb = min(lo / kBlockSize, pe - 1);  // one page at least
+    const int share = (pe - pb + kWarps - 1) / kWarps, first = pb + warp * share;
     int f = 0;
     f = lane == 0 ? b : f;
     f = lane == 1 ? kv : f;
-    f = lane == 3 ? n * p.G : f;                       // rows; row0 (lane 2) is 0
-    f = lane == 4 ? min(lo / kBlockSize, pages - 1) : f;  // one page at least
-    f = lane == 5 ? pages : f;
-    f = lane == 7 ? 1 : f;                             // one split (lane 6: split 0)
+    f = lane == 2 ? 16 * j : f;
+    f = lane == 3 ? nrows : f;
+    f = lane == 4 ? first : f;                   // the warp's pages
+    f = lane == 5 ? min(first + share, pe) : f;
+    f = lane == 7 ? 1 : f;                       // one split (lane 6: split 0)
     f = lane == 8 ? L : f;
     f = lane == 9 ? n : f;
     f = lane == 10 ? q0 : f;
-    f = lane == 12 ? lo : f;                           // pad[1..3]
-    f = lane == 13 ? L : f;                            // the last row is at L - 1
+    f = lane == 12 ? lo : f;                     // pad[1..3], as the plan has them
+    f = lane == 13 ? hi : f;
     f = lane == 14 ? pre : f;
     return f;
   };
+  int dir_rows = 0, dir_row0 = 0, dir_tok0 = 0, dir_kv = 0;  // the CTA's item, for the join
 
   // Issue the next page of work into stage g_issue % S; false when nothing is left.
   auto issue_one = [&]() -> bool {
@@ -123,8 +131,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (no_more) return false;
       int idx = 0;
       if constexpr (kDirect) {
-        idx = direct_next;
-        direct_next += gridDim.x * kWarps;
+        no_more = !first_fetch;  // one item a CTA
+        first_fetch = false;
+        if (no_more) return false;
+        idx = blockIdx.x;
       } else if (first_fetch) {
         // each warp's first item is its own; with tile items planned a CTA's warps take
         // consecutive items, so that the other SMs are free for the tile kernel
@@ -135,13 +145,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (lane == 0) idx = atomicAdd(p.hdr + 1, 1) + static_cast<int>(gridDim.x) * kWarps;
         idx = __shfl_sync(0xffffffffu, idx, 0);
       }
-      if (idx >= n_items) {
+      if (!kDirect && idx >= n_items) {
         no_more = true;
         return false;
       }
       int v;
-      if constexpr (kDirect) v = direct_item(idx);
-      else v = lane < 16 ? __ldg(reinterpret_cast<const int*>(p.items + idx) + lane) : 0;
+      if constexpr (kDirect) {
+        v = direct_item(idx);
+        dir_kv = __shfl_sync(0xffffffffu, v, 1);
+        dir_row0 = __shfl_sync(0xffffffffu, v, 2);
+        dir_rows = __shfl_sync(0xffffffffu, v, 3);
+        dir_tok0 = __shfl_sync(0xffffffffu, v, 10);
+      } else v = lane < 16 ? __ldg(reinterpret_cast<const int*>(p.items + idx) + lane) : 0;
       const int pb = __shfl_sync(0xffffffffu, v, 4), pe = __shfl_sync(0xffffffffu, v, 5);
       if (pe <= pb) continue;  // held by no row
       WorkItem* slot = ring + (ring_tail % kRing);
@@ -246,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     for (int r = 0; r < 2; ++r) {
       if (row_tok[r] < 0) continue;
       const int tok = row_tok[r];
-      const int ns_t = kDirect ? 1 : __ldg(p.tok_ns + tok);
+      const int ns_t = __ldg(p.tok_ns + tok);
       if (cur.split >= ns_t) continue;  // this split does not hold the row
       // a row without keys here gives zeros, whatever the products left in o
       const bool any = !(l_run[r] == 0.f);
@@ -272,13 +287,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     have_item = false;
   };
 
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    m_run[r] = -INFINITY;
+    l_run[r] = 0.f;
+  }
   for (int s = 0; s < S; ++s)  // fill the ring
     if (!issue_one()) break;
 
   bool aborted = false;
   while (true) {
     if (comp_left == 0) {
-      if (have_item) finish_item();
+      if (!kDirect && have_item) finish_item();
       if (ring_head == ring_tail) break;  // everything issued has been computed
       start_item();
     }
@@ -412,6 +432,56 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (aborted) {
     // let the copies already issued land before the CTA's shared memory goes away
     for (uint32_t gg = g_comp; gg < g_issue; ++gg) mbar_wait(&full[gg % S], (gg / S) & 1, 1u << 20);
+  }
+  if constexpr (kDirect) {
+    // The warps' shares of the item's pages joined: each leaves its O (not normalised) in its
+    // own stages, which hold no page any more, and its rows' maxima and sums.
+    __shared__ float sh_m[kWarps][16], sh_l[kWarps][16];
+    const bool worked = g_comp > 0 && !aborted;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+      if (t4 == 0) {
+        sh_m[warp][g + 8 * r] = worked ? m_run[r] : -INFINITY;
+        sh_l[warp][g + 8 * r] = worked ? l_run[r] : 0.f;
+      }
+      if (worked) {
+        float* dst = reinterpret_cast<float*>(tiles) + (g + 8 * r) * D + 2 * t4;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<float2*>(dst + j * 8) = make_float2(o[j][2 * r], o[j][2 * r + 1]);
+      }
+    }
+    __syncthreads();
+    constexpr int kPer = D / 16;  // columns of a thread: 16 threads a row
+    const int row = threadIdx.x / 16, col = (threadIdx.x % 16) * kPer;
+    if (row < dir_rows) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) M = fmaxf(M, sh_m[k][row]);
+      float acc[kPer], sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float m = sh_m[k][row];
+        // (a warp whose share holds no key of the row is left out: its O may be anything)
+        if (sh_l[k][row] == 0.f) continue;
+        const float wgt = fast_exp2(m - M);
+        sum += wgt * sh_l[k][row];
+        const float* src = reinterpret_cast<const float*>(smem + k * S * kStage) + row * D + col;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] += wgt * src[e];
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int R = dir_row0 + row, i = R / p.G;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(
+          static_cast<uint16_t*>(p.out) +
+          (static_cast<int64_t>(dir_tok0 + i) * p.H_q + dir_kv * p.G + (R - i * p.G)) * D + col);
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack2<kBF16>(acc[e] * inv, acc[e + 1] * inv);
+    }
   }
 }
 

@@ -223,8 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Direct mode: lane b holds sequence b's query tokens n, context L, first token t0 and
     // query-tile pairs (0 for a sequence without rows or an invalid one). Items go rank by
     // rank (rank r: every sequence's r-th longest pair, in batch order, each KV head), so
-    // csum(r) = H_kv * sum_b min(pairs_b, r) items come before rank r; CTA c takes items
-    // c, c + gridDim.x, ...
+    // csum(r) = H_kv * sum_b min(pairs_b, r) items come before rank r.
     int d_n = 0, d_L = 0, d_t0 = 0, d_pre = 0, d_pairs = 0, d_max = 0, d_total = 0;
     auto csum = [&](int r) -> int {
       int v = min(d_pairs, r);
@@ -299,7 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (is_k && kDirect) {
         const int slot = it % kItemRing;
         if (!wait(&bars->item_empty[slot], ((it / kItemRing) & 1) ^ 1)) break;
-        idx = blockIdx.x + it * static_cast<int>(gridDim.x);
+        // (every other round in reverse, so that no CTA has the longest item of each)
+        idx = it * static_cast<int>(gridDim.x) +
+              static_cast<int>(it & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         if (idx >= d_total) idx = -1;
         if (idx >= 0) {
           const int f = direct_field(idx);
