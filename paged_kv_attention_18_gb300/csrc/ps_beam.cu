@@ -7,13 +7,19 @@
 // known; the few that are left are scored and compared across chunks and beams in 64 bits.
 //   scan    one CTA per (beam, chunk of logits), streamed in 16-byte loads: each thread keeps
 //           its maximum m and the sum of exp(x - m). The candidates are the logits at or
-//           above a bound tau: the n-th largest of a warp's 32 thread maxima is at most the
-//           n-th largest logit of the chunk, and tau is the largest such bound of the CTA's
-//           warps. Where a thread's maximum of a round reaches tau, its warp reads those 32
-//           logits again (from the caches); a few dozen pass, and are ranked.
+//           above a bound tau, the n-th largest of the threads' maxima: at most the n-th
+//           largest logit of the chunk. Where a thread's maximum of a round reaches tau, a
+//           warp reads those logits again (from the caches); little more than n pass, and
+//           are ranked.
 //   merge   one CTA per prompt: lse of each beam from its chunks' (M, sum), then the same
 //           bound on the chunks' candidates, and the ranks of those that pass.
-// Bound by the bytes of the logits (read once).
+// Bound by the bytes of the logits (read once): 192 rows of 151936 bf16 logits (58 MB) scan in
+// 17 us, of which 12.5 us are the stream (4.6 TB/s), 3 the bound and 1 the candidates; the
+// merge of 48 prompts adds 3 to 4 us behind it. Listing candidates from the registers in the
+// stream, against a bound from its first round, took 24 us: the few lanes that have one stop
+// their warps every round.
+#include <type_traits>
+
 #include "ps_common.cuh"
 #include "ps_launch.h"
 
@@ -22,9 +28,12 @@ namespace ps {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRound = 32 * kThreads;  // logits of a CTA per round of loads, two in flight
-constexpr int kRounds = 4;             // rounds, at most
-constexpr int kCap = 1024;             // candidates ranked in shared memory
+constexpr int kMaxChunk = 65536;       // logits of a CTA, at most
+constexpr int kWords = 4;              // 16-byte words of a thread per round
+constexpr int kDepth = 2;              // rounds in flight
+constexpr int kRingBytes = kDepth * kWords * kThreads * 16;
+constexpr int kCap = 512;              // candidates ranked in shared memory
+constexpr int kPairs = 256;            // rounds of threads looked at again, at most
 constexpr int kEarly = 2;              // entries a merging thread holds in registers
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994530942;
@@ -53,35 +62,56 @@ __device__ __forceinline__ float from_order32(uint32_t o) {
 }
 constexpr uint32_t kOrderNegInf = 0x007fffffu;  // order32(-inf)
 
-// The largest and the n-th largest of the warp's 32 keys (n in 1..32).
-__device__ __forceinline__ uint32_t warp_nth(uint32_t key, int n, uint32_t& top) {
-  const int lane = threadIdx.x & 31;
-  uint32_t m = __reduce_max_sync(0xffffffffu, key);
-  top = m;
-  for (int i = 1; i < n; ++i) {
-    const int who = __ffs(__ballot_sync(0xffffffffu, key == m)) - 1;
-    if (lane == who) key = 0;  // taken out (0 is below every key)
-    m = __reduce_max_sync(0xffffffffu, key);
-  }
-  return m;
-}
-
-// Block-wide: the largest key, and a bound that at least n of the keys' owners reach.
-__device__ __forceinline__ void block_bound(uint32_t key, int n, uint32_t* sh, uint32_t& top,
+// Block-wide: the largest of the threads' keys (each above 0) and the n-th largest, n in
+// 1 .. 32. Each warp takes its n largest out in turn; of the 8 n that leaves, those with
+// fewer than n above them are the block's n largest (equal ones included). (A looser bound
+// from two keys of each warp costs 2 us less, and 4 us more in candidates looked at.)
+struct BoundSmem {
+  alignas(16) uint32_t top[kWarps * kBeamMaxWidth];
+  uint32_t tau;
+};
+__device__ __forceinline__ void block_bound(uint32_t key, int n, BoundSmem& sh, uint32_t& top,
                                             uint32_t& tau) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t wt;
-  const uint32_t wn = warp_nth(key, n, wt);
-  if (lane == 0) {
-    sh[warp] = wt;
-    sh[kWarps + warp] = wn;
+  if (threadIdx.x == 0) sh.tau = 0xffffffffu;
+  uint32_t mine = 0;
+  for (int i = 0; i < n; ++i) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, key);
+    const int who = __ffs(__ballot_sync(0xffffffffu, key == m)) - 1;
+    if (lane == who) key = 0;  // taken out (0 is below every key)
+    if (lane == i) mine = m;
+  }
+  if (lane < n) sh.top[warp * n + lane] = mine;
+  __syncthreads();
+  top = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = max(top, sh.top[w * n]);
+  if (threadIdx.x < kWarps * n) {
+    const uint32_t k = sh.top[threadIdx.x];
+    int above = 0;
+#pragma unroll 4
+    for (int i = 0; i < kWarps / 4 * n; ++i) {
+      const uint4 t = reinterpret_cast<const uint4*>(sh.top)[i];
+      above += (t.x > k) + (t.y > k) + (t.z > k) + (t.w > k);
+    }
+    if (above < n) atomicMin(&sh.tau, k);
   }
   __syncthreads();
-  top = tau = 0;
+  tau = sh.tau;
+}
+
+// done(i, rank) for each i < n, rank the number of j < n with above(i, j): eight threads an i.
+template <class Above, class Done>
+__device__ __forceinline__ void rank_list(int n, Above above, Done done) {
+  const int part = threadIdx.x & 7;
+  for (int i0 = 0; i0 < n; i0 += kThreads / 8) {
+    const int i = i0 + (threadIdx.x >> 3);
+    int rank = 0;
+    if (i < n)
+      for (int j = part; j < n; j += 8) rank += above(i, j) ? 1 : 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    top = max(top, sh[w]);
-    tau = max(tau, sh[kWarps + w]);
+    for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (part == 0 && i < n) done(i, rank);
   }
 }
 
@@ -101,50 +131,59 @@ __device__ __forceinline__ unsigned long long block_max(unsigned long long k,
   return k;
 }
 
-// The elements of one 16-byte word as floats, NaN as -inf.
+// The elements of one 32-bit word as floats (one of fp32, two of a 16-bit type).
 template <typename T>
-__device__ __forceinline__ void unpack(const uint4& w, float* x);
+__device__ __forceinline__ void unpack(uint32_t u, float* x);
 template <>
-__device__ __forceinline__ void unpack<float>(const uint4& w, float* x) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = fmaxf(__uint_as_float(u[i]), -INFINITY);
+__device__ __forceinline__ void unpack<float>(uint32_t u, float* x) { x[0] = __uint_as_float(u); }
+template <>
+__device__ __forceinline__ void unpack<__half>(uint32_t u, float* x) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+  x[0] = f.x;
+  x[1] = f.y;
 }
 template <>
-__device__ __forceinline__ void unpack<__half>(const uint4& w, float* x) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&u[i]),
-                              __half2half2(__ushort_as_half(0xfc00)));
-    const float2 f = __half22float2(h);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+__device__ __forceinline__ void unpack<__nv_bfloat16>(uint32_t u, float* x) {
+  x[0] = __uint_as_float(u << 16);
+  x[1] = __uint_as_float(u & 0xffff0000u);
 }
-template <>
-__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& w, float* x) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+
+// The largest element of 16 such words; NaN only where all are.
+template <typename T>
+__device__ __forceinline__ float words_max(const uint32_t* w) {
+  if constexpr (sizeof(T) == 4) {
+    float m[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&u[i]),
-                                     __bfloat162bfloat162(__ushort_as_bfloat16(0xff80)));
-    const float2 f = __bfloat1622float2(h);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    for (int k = 0; k < 4; ++k)
+      m[k] = fmax3(__uint_as_float(w[k]), __uint_as_float(w[4 + k]), __uint_as_float(w[8 + k]));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], __uint_as_float(w[12 + k]));
+    return fmax3(fmaxf(m[0], m[1]), m[2], m[3]);
+  } else {
+    using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+    T2 m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = *reinterpret_cast<const T2*>(w + k);
+#pragma unroll
+    for (int i = 4; i < 16; i += 4)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = __hmax2(m[k], *reinterpret_cast<const T2*>(w + i + k));
+    const T2 x = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+    return fmaxf(widen<T>(x.x), widen<T>(x.y));
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-  constexpr int kWords = kRound / kVec / kThreads;  // words of a thread per round
-  static_assert(kWords * kVec == 32, "a round is 32 logits per thread, one per lane");
-  __shared__ uint32_t sh_key[2 * kWarps];
-  __shared__ float sh_sum[kWarps];
+  constexpr int kPer = kWords * kVec;  // logits of a thread per round
+  constexpr int kRound = kPer * kThreads, kRounds = kMaxChunk / kRound;
+  static_assert(kPer <= 32, "a warp looks at a thread's round again one logit per lane");
+  __shared__ BoundSmem sh_key;
+  __shared__ float sh_sum[kWarps], sh_round[kRounds][kThreads];
   __shared__ unsigned long long sh_max[kWarps];
   __shared__ unsigned long long list[kCap];
-  __shared__ int count;
+  __shared__ int count, pairs, pair[kPairs];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
@@ -152,97 +191,140 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
     pdl_launch_dependents();
     return;
   }
-  if (threadIdx.x == 0) count = 0;
+  if (threadIdx.x == 0) {
+    count = pairs = 0;
+  }
   const T* base = static_cast<const T*>(p.logits) + row * p.ld;
   // words start at the 16-byte boundary at or before the row's first logit; `lo` is the
   // token of the chunk's first place (below 0 by the row's offset from that boundary)
   const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / sizeof(T));
   const int lo = chunk * p.chunk - skew;
   const int end = min(lo + p.chunk, p.V);  // one past the chunk's last token
-  // the word at token t (a multiple of kVec past lo); outside the chunk -inf, not read
-  auto load = [&](int t) -> uint4 {
-    if (t >= 0 && t + kVec <= end) return __ldg(reinterpret_cast<const uint4*>(base + t));
-    union {
-      uint4 w;
-      T e[kVec];
-    } u;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      u.e[i] = t + i >= 0 && t + i < end ? base[t + i] : static_cast<T>(-INFINITY);
-    return u.w;
-  };
+  const int rounds = end > lo ? (end - lo + kRound - 1) / kRound : 0;
   // token of thread `thread`'s word j of round r
   auto place = [&](int r, int j, int thread) { return lo + r * kRound + (j * kThreads + thread) * kVec; };
-  // one pass: the thread's maximum m, each round's own maximum, and the thread's sum of
-  // exp(x - sub), sub = m but for -inf; the next round's words are on their way meanwhile
-  float m = -INFINITY, sub = 0.f, mr[kRounds];
+  // Each thread's words go through its own slots of a ring in shared memory, kDepth rounds
+  // deep, by asynchronous copies that it alone waits for and reads (no barrier). Outside the
+  // chunk nothing is read and a slot holds -inf.
+  extern __shared__ uint4 ring[];  // [kDepth][kWords][kThreads]
+  auto fetch = [&](int r) {
+    if (r < rounds) {
+      uint4* slot = ring + (r % kDepth) * kWords * kThreads + threadIdx.x;
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
+        const int t = place(r, j, threadIdx.x);
+        if (t >= 0 && t + kVec <= end) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           smem_u32(slot + j * kThreads)),
+                       "l"(base + t)
+                       : "memory");
+        } else {
+          T* e = reinterpret_cast<T*>(slot + j * kThreads);
+#pragma unroll 1
+          for (int i = 0; i < kVec; ++i)
+            e[i] = t + i >= 0 && t + i < end ? base[t + i] : static_cast<T>(-INFINITY);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int r = 0; r < kDepth; ++r) fetch(r);
+  // One pass. m: the thread's maximum; sum: of 2^(x L + c), L = log2(e) in fp32, c near -m L.
+  // Whatever c's rounding, 2^-(M L + c) brings the sum to the reference M in the end, M L + c
+  // in one rounding. (The rounds are not unrolled: straight-line code for all of them ran at
+  // the rate of its instruction fetches. A round's maximum is kept in shared memory.)
+  float m = -INFINITY, c = 0.f;
   float2 sum = make_float2(0.f, 0.f);
-  uint4 w[kWords];
+  const float2 l2 = make_float2(kLog2e, kLog2e);
+#pragma unroll 1
+  for (int r = 0; r < rounds; ++r) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    uint4 w[kWords];
+    const uint4* slot = ring + (r % kDepth) * kWords * kThreads + threadIdx.x;
 #pragma unroll
-  for (int j = 0; j < kWords; ++j) w[j] = load(place(0, j, threadIdx.x));
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    mr[r] = -INFINITY;
-    if (lo + r * kRound >= end) continue;
-    uint4 next[kWords];
-    const bool more = r + 1 < kRounds && lo + (r + 1) * kRound < end;
-    if (more) {
-#pragma unroll
-      for (int j = 0; j < kWords; ++j) next[j] = load(place(r + 1, j, threadIdx.x));
+    for (int j = 0; j < kWords; ++j) w[j] = slot[j * kThreads];
+    fetch(r + kDepth);
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(w);
+    const float mr = fmaxf(words_max<T>(words), -INFINITY);
+    sh_round[r][threadIdx.x] = mr;
+    if (mr > m) {
+      m = mr;
+      const float to = -m * kLog2e;
+      const float a = fast_exp2(to - c);  // (at most 1, but for the first round's empty sum)
+      sum = sum.x > 0.f || sum.y > 0.f ? fmul2(sum, make_float2(a, a)) : sum;
+      c = to;
     }
+    const float2 c2 = make_float2(c, c);
+    float2 add[2] = {sum, make_float2(0.f, 0.f)};
+    constexpr int kStep = sizeof(T) == 4 ? 2 : 1;  // words of a pair of logits
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) {
-      float x[kVec];
-      unpack<T>(w[j], x);
-#pragma unroll
-      for (int i = 0; i < kVec; i += 2) mr[r] = fmax3(mr[r], x[i], x[i + 1]);
-      if (mr[r] > m) {
-        const float a = sum.x + sum.y > 0.f ? fast_exp2((sub - mr[r]) * kLog2e) : 0.f;
-        sum = fmul2(sum, make_float2(a, a));
-        m = sub = mr[r];
+    for (int i = 0; i < 4 * kWords; i += kStep) {
+      float x[2];
+      if constexpr (sizeof(T) == 4) {
+        x[0] = __uint_as_float(words[i]);
+        x[1] = __uint_as_float(words[i + 1]);
+      } else {
+        unpack<T>(words[i], x);
       }
-      // (x - sub first: rounding sub log2(e) once for all terms would shift their sum)
-      const float2 one = make_float2(1.f, 1.f), ns = make_float2(-sub, -sub);
-#pragma unroll
-      for (int i = 0; i < kVec; i += 2) {
-        const float2 y = fmul2(ffma2(make_float2(x[i], x[i + 1]), one, ns),
-                               make_float2(kLog2e, kLog2e));
-        sum = ffma2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), one, sum);
-      }
+      const float2 y = ffma2(make_float2(x[0], x[1]), l2, c2);
+      add[i / kStep % 2].x += fast_exp2(y.x);
+      add[i / kStep % 2].y += fast_exp2(y.y);
     }
-    if (more) {
-#pragma unroll
-      for (int j = 0; j < kWords; ++j) w[j] = next[j];
-    }
+    sum = make_float2(add[0].x + add[1].x, add[0].y + add[1].y);
+  }
+  float total = sum.x + sum.y;
+  if (total != total && m < INFINITY) {
+    // a NaN among the thread's logits, which counts as -inf: the sum again without it
+    total = 0.f;
+    for (int r = 0; r < rounds; ++r)
+      for (int j = 0; j < kWords; ++j)
+        for (int i = 0; i < kVec; ++i) {
+          const int t = place(r, j, threadIdx.x) + i;
+          if (t >= 0 && t < end) total += fast_exp2(fmaf(clean(widen<T>(base[t])), kLog2e, c));
+        }
   }
   uint32_t top, tau;
   block_bound(order32(clean(m)), p.n, sh_key, top, tau);
   const float M = from_order32(top);
-  float s = m > -INFINITY ? (sum.x + sum.y) * fast_exp2((m - M) * kLog2e) : 0.f;
+  float s = m > -INFINITY ? total * fast_exp2(-fmaf(M, kLog2e, c)) : 0.f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) sh_sum[warp] = s;
-  // The candidates. A round of a thread is 32 logits: where its maximum reaches the bound,
-  // the warp reads them again (from the caches), one per lane. f(key) is called for every
-  // logit at or above the bound.
+  // The candidates. The rounds of threads whose maximum reaches the bound are listed; a warp
+  // reads a listed round's logits again (from the caches), one per lane, the rounds dealt to
+  // the warps so that their reads are on the way together.
   const uint32_t bound = tau > kOrderNegInf ? tau : kOrderNegInf + 1;
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      uint32_t who = __ballot_sync(0xffffffffu, order32(clean(mr[r])) >= bound);
-      for (; who; who &= who - 1) {
-        const int t = place(r, lane / kVec, warp * 32 + __ffs(who) - 1) + lane % kVec;
-        if (t < 0 || t >= end) continue;
-        const uint32_t k = order32(clean(widen<T>(base[t])));
-        if (k >= bound)
-          f((static_cast<unsigned long long>(k) << 32) | (0xffffffffu - static_cast<uint32_t>(t)));
-      }
+  for (int r = 0; r < rounds; ++r)
+    if (order32(clean(sh_round[r][threadIdx.x])) >= bound) {
+      const int at = atomicAdd(&pairs, 1);
+      if (at < kPairs) pair[at] = r * kThreads + threadIdx.x;
     }
+  __syncthreads();
+  const int n_pairs = pairs;
+  // key of the lane's logit of pair x, 0 where there is none at or above the bound
+  auto look = [&](int x) -> unsigned long long {
+    const int t = place(x / kThreads, lane / kVec, x % kThreads) + lane % kVec;
+    if (lane >= kPer || t < 0 || t >= end) return 0;
+    const uint32_t k = order32(clean(widen<T>(base[t])));
+    return k < bound ? 0
+                     : (static_cast<unsigned long long>(k) << 32) |
+                           (0xffffffffu - static_cast<uint32_t>(t));
   };
-  each([&](unsigned long long k) {
+  auto put = [&](unsigned long long k) {
+    if (k == 0) return;
     const int at = atomicAdd(&count, 1);
     if (at < kCap) list[at] = k;
-  });
+  };
+  constexpr int kLooks = 4;  // pairs of a warp on the way together
+  for (int i = warp; i < n_pairs && n_pairs <= kPairs; i += kLooks * kWarps) {
+    unsigned long long k[kLooks];
+#pragma unroll
+    for (int u = 0; u < kLooks; ++u)
+      k[u] = i + u * kWarps < n_pairs ? look(pair[i + u * kWarps]) : 0;
+#pragma unroll
+    for (int u = 0; u < kLooks; ++u) put(k[u]);
+  }
   __syncthreads();
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -252,24 +334,25 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
     p.stat[blockIdx.x] = make_float2(M, s);
   }
   unsigned long long* out = p.cand + static_cast<int64_t>(blockIdx.x) * p.n;
-  const int c = count;
-  if (c <= kCap) {
-    for (int i = threadIdx.x; i < c; i += kThreads) {
-      const unsigned long long k = list[i];
-      int rank = 0;
-      for (int j = 0; j < c; ++j) rank += list[j] > k ? 1 : 0;
-      if (rank < p.n) out[rank] = k;
-    }
-    for (int i = c + threadIdx.x; i < p.n; i += kThreads) out[i] = 0;  // none
+  const int found = count;
+  if (n_pairs <= kPairs && found <= kCap) {
+    rank_list(found, [&](int i, int j) { return list[j] > list[i]; },
+              [&](int i, int rank) {
+                if (rank < p.n) out[rank] = list[i];
+              });
+    for (int i = found + threadIdx.x; i < p.n; i += kThreads) out[i] = 0;  // none
   } else {
-    // more equal logits than the list holds: n rounds of the block's largest key below
-    // the one before
+    // more equal logits than the lists hold: n rounds of the block's largest key below the
+    // one before
     unsigned long long last = ~0ull;
     for (int i = 0; i < p.n; ++i) {
       unsigned long long best = 0;
-      each([&](unsigned long long k) {
-        if (k < last && k > best) best = k;
-      });
+      for (int r = 0; r < rounds; ++r)
+        for (int t = 0; t < 32; ++t) {
+          if (order32(clean(sh_round[r][warp * 32 + t])) < bound) continue;  // (warp-uniform)
+          const unsigned long long k = look(r * kThreads + warp * 32 + t);
+          if (k < last && k > best) best = k;
+        }
       last = block_max(best, sh_max);
       if (threadIdx.x == 0) out[i] = last;
     }
@@ -296,7 +379,7 @@ __device__ __forceinline__ bool better(const Best& a, const Best& b) {
 }
 
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
-  __shared__ uint32_t sh_key[2 * kWarps];
+  __shared__ BoundSmem sh_key;
   __shared__ float2 sh_lse[kBeamMaxWidth];  // hi, lo
   __shared__ float sh_cum[kBeamMaxWidth];
   __shared__ int sh_kind[kBeamMaxWidth];  // 0 no candidate, 1 scored, 2 finished
@@ -337,6 +420,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
         for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
         // log S = k ln 2 + log(f), f in [1, 2): fp32 serves for log(f), whose rounding
         // is then below 2^-24 whatever the size of S
+        if (!(S < 1e300)) kind = 0;  // a logit past 2^127, whose exponent left fp32
         const long long bits = __double_as_longlong(S);
         const int k = static_cast<int>(bits >> 52) - 1023;
         const double f =
@@ -375,7 +459,6 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     e.score = (static_cast<unsigned long long>(order32(hi + 0.f)) << 32) | order32(lo + 0.f);
     return true;
   };
-  // the bound, on the scores' high parts
   // f(entry) for each of the thread's entries
   auto each = [&](auto f) {
 #pragma unroll
@@ -389,12 +472,15 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
       if (entry(i, cand[i], e)) f(e);
     }
   };
-  uint32_t mine = 0;
-  each([&](const Best& e) { mine = max(mine, static_cast<uint32_t>(e.score >> 32)); });
-  uint32_t top, tau;
-  block_bound(mine, p.n, sh_key, top, tau);
-  const uint32_t bound = tau > 0 ? tau : 1;
-  if (mine >= bound) {
+  // few entries are ranked all of them; of many, those whose high part reaches a bound
+  uint32_t mine = 0, bound = 1;
+  if (total > kCap) {
+    each([&](const Best& e) { mine = max(mine, static_cast<uint32_t>(e.score >> 32)); });
+    uint32_t top, tau;
+    block_bound(mine, p.n, sh_key, top, tau);
+    bound = tau > 0 ? tau : 1;
+  }
+  if (mine >= bound || total <= kCap) {
     each([&](const Best& e) {
       if (static_cast<uint32_t>(e.score >> 32) >= bound) {
         const int at = atomicAdd(&count, 1);
@@ -416,12 +502,10 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
   };
   const int c = count;
   if (c <= kCap) {
-    for (int i = threadIdx.x; i < c; i += kThreads) {
-      const Best e = list[i];
-      int rank = 0;
-      for (int j = 0; j < c; ++j) rank += better(list[j], e) ? 1 : 0;
-      if (rank < p.n) put(rank, e);
-    }
+    rank_list(c, [&](int i, int j) { return better(list[j], list[i]); },
+              [&](int i, int rank) {
+                if (rank < p.n) put(rank, list[i]);
+              });
     for (int i = c + threadIdx.x; i < p.n; i += kThreads) none(i);
   } else {
     Best last{~0ull, -1};
@@ -451,14 +535,16 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
 
 }  // namespace
 
-// Logits per CTA, a multiple of a round's share that fills the SMs a few times over: long
-// chunks spread a CTA's fixed costs (the bound, the ranks, its launch) over more bytes, short
-// ones keep a small batch's rows on many SMs.
+// Logits per CTA: a row's equal shares (multiples of kStep) in as many chunks as keep the CTAs
+// to one wave (four an SM), but at least kStep and at most kMaxChunk logits. A CTA's fixed
+// costs (launch, bound, ranks: some 4 us) are then paid once.
 int beam_chunk(int64_t rows, int V) {
-  constexpr int64_t kStep = 2048, kTargetCtas = 1216;  // 8 a SM on 152 SMs
-  int64_t c = (rows * V / kTargetCtas + kStep - 1) / kStep * kStep;
-  c = c < kStep ? kStep : c > kRounds * kRound ? kRounds * kRound : c;
-  return static_cast<int>(c);
+  constexpr int64_t kStep = 2048, kWave = 608;
+  const int64_t places = static_cast<int64_t>(V) + 7;  // the row's offset from a boundary
+  int64_t n = rows > 0 && rows < kWave ? kWave / rows : 1;
+  const int64_t least = (places + kMaxChunk - 1) / kMaxChunk;
+  if (n < least) n = least;
+  return static_cast<int>(((places + n - 1) / n + kStep - 1) / kStep * kStep);
 }
 
 int beam_chunks(int64_t rows, int V) {
@@ -467,14 +553,19 @@ int beam_chunks(int64_t rows, int V) {
   return static_cast<int>((static_cast<int64_t>(V) + 7 + c - 1) / c);
 }
 
-cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stream) {
+template <typename T>
+static cudaError_t launch_scan(const BeamParams& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = ensure_smem_limit(beam_scan_kernel<T>, kRingBytes, done);
+  if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.W * p.chunks));
-  cudaError_t e;
-  if (dtype == 0) e = launch_kernel(beam_scan_kernel<__half>, grid, dim3(kThreads), 0, stream, true, p);
-  else if (dtype == 1)
-    e = launch_kernel(beam_scan_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, stream, true, p);
-  else
-    e = launch_kernel(beam_scan_kernel<float>, grid, dim3(kThreads), 0, stream, true, p);
+  return launch_kernel(beam_scan_kernel<T>, grid, dim3(kThreads), kRingBytes, stream, true, p);
+}
+
+cudaError_t launch_beam_select(const BeamParams& p, int dtype, cudaStream_t stream) {
+  const cudaError_t e = dtype == 0   ? launch_scan<__half>(p, stream)
+                        : dtype == 1 ? launch_scan<__nv_bfloat16>(p, stream)
+                                     : launch_scan<float>(p, stream);
   if (e != cudaSuccess) return e;
   return launch_kernel(beam_merge_kernel, dim3(static_cast<unsigned>(p.B)), dim3(kThreads), 0,
                        stream, true, p);
