@@ -38,18 +38,19 @@ constexpr int kSub = kRows * 128; // bytes of one [128 rows x 64 elements] swizz
 constexpr int kKStages = 3;       // K tile stages (freed once both products S have read them)
 constexpr int kVStages = 2;       // V tile stages (freed once both products PV have read them)
 constexpr int kItemRing = 4;     // item indices handed from the fetching warp to the others
-constexpr int kThreads = 384;
-constexpr float kRescaleLog2 = 8.f;  // rescale O only when the max grows by > 2^8
+constexpr int kSoftmaxWarps = 16;  // two a query row: a half of the columns each
+constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
+constexpr int kRescaleExp = 8;  // rescale O only when P sums to 2^8 or more
 // A larger jump inside a tile moves the reference at once; below it P can reach 2^kMove,
 // which must stay finite in the 16-bit type (fp16 tops out near 2^16, bf16 near 2^128).
 template <bool kBF16>
 constexpr float kMoveLog2 = kBF16 ? 64.f : 15.f;
-// Largest row sum of a 64-column half of P taken against the current reference without
-// looking at the half's max: every P is then at most this (bf16: 2^64, as above; fp16:
-// 64 finite values, so none overflowed). A larger (or infinite) sum sends the half
-// through the max and the reference move.
+// Exponent (biased, as in fp32) from which a half row's sum of P is too large: every P is
+// below 2 to the power of it less 127 otherwise (bf16: 2^64, as above; fp16: 2^22, so none of
+// 64 finite values overflowed). Such a sum (or an infinite one) sends the tile through the
+// max and the reference move.
 template <bool kBF16>
-constexpr float kHalfSumMax = kBF16 ? 18446744073709551616.f : 4194304.f;
+constexpr uint32_t kSumExp = kBF16 ? 127 + 64 : 127 + 22;
 constexpr uint32_t kTmemCols = 512;
 
 // TMEM columns of softmax group g: S (and P over it) at g*256, O at g*256 + 128
@@ -65,7 +66,8 @@ struct TileSmem {
   static constexpr int kOffV = kOffK + kKStages * kK;
   static constexpr int kOffBar = kOffV + kVStages * kK;
   static constexpr int kOffItems = kOffBar + 512;             // work items in flight
-  static constexpr int kBytes = kOffItems + 2 * kItemRing * 64 + 1024;  // + alignment slack
+  static constexpr int kOffPair = kOffItems + 2 * kItemRing * 64;  // two warps' exchanges
+  static constexpr int kBytes = kOffPair + 1024 + 1024;            // + alignment slack
 };
 static_assert(TileSmem<128>::kBytes <= 232448, "tile kernel shared memory");
 
@@ -74,6 +76,7 @@ struct TileBars {
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t pair[8];  // the two warps that share the rows of a (group, quarter)
   uint64_t mma_final;
   uint64_t item_full[kItemRing], item_empty[kItemRing];
   int item_idx[kItemRing];
@@ -81,9 +84,6 @@ struct TileBars {
   int abort;
 };
 static_assert(sizeof(TileBars) <= 512, "barrier block");
-
-// How a half's scores reach log2 units (see the softmax groups).
-enum ScoreKind : int { kFast, kWide, kReady };
 
 // An item fits this launch: a sequence and KV head of the batch, a page range inside the
 // block table, and query rows inside the packed batch. Every role checks each item the
@@ -140,13 +140,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&bars->s_full[g], 1);
-      mbar_init(&bars->p_full[g], g == 0 ? 5 : 4);  // tile A's: + the K/V watcher
+      mbar_init(&bars->p_full[g], g == 0 ? 9 : 8);  // tile A's: + the K/V watcher
       mbar_init(&bars->o_done[g], 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&bars->pair[i], 2);
     mbar_init(&bars->mma_final, 1);
     for (int s = 0; s < kItemRing; ++s) {
       mbar_init(&bars->item_full[s], 1);
-      mbar_init(&bars->item_empty[s], 11);  // V producer, MMA, K/V watcher, 8 softmax warps
+      mbar_init(&bars->item_empty[s], 3 + kSoftmaxWarps);  // V producer, MMA, K/V watcher, softmax
     }
     bars->abort = 0;
     fence_barrier_init();
@@ -476,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t acc0 = j > 0 ? 1u : 0u;
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            umma_f16_ts(tmem + col_o(grp), tmem + col_s(grp) + kk * 8, b0 + ((kk * 2048) >> 4),
-                        idPV, kk > 0 ? 1u : acc0);
+            umma_f16_ts(tmem + col_o(grp), tmem + col_s(grp) + (kk / 4) * 64 + (kk % 4) * 8,
+                        b0 + ((kk * 2048) >> 4), idPV, kk > 0 ? 1u : acc0);
           if (grp == ng - 1) umma_commit(&bars->v_empty[st]);  // last reader of the V stage
           return true;
         };
@@ -550,11 +551,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ============================ softmax groups + epilogue =========================
-    const int grp = (warp - 4) >> 2;   // 0: query tile A, 1: query tile B
-    const int quarter = warp & 3;      // TMEM lanes 32*quarter .. +31
+    const int grp = (warp - 4) >> 3;        // 0: query tile A, 1: query tile B
+    const int half = ((warp - 4) >> 2) & 1; // columns 64 * half .. + 63 of each key tile
+    const int quarter = warp & 3;           // TMEM lanes 32*quarter .. +31
     const int r = quarter * 32 + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t tS = trow + col_s(grp), tO = trow + col_o(grp);
+    const uint32_t tS = trow + col_s(grp) + 64 * half;            // P over its first 32 columns
+    const uint32_t tO = trow + col_o(grp) + (D / 2) * half;       // the half of O it keeps
+    // What the two warps of the same rows tell one another: 16 bits a row, through shared
+    // memory and a barrier of the two (bounded, like every wait).
+    uint64_t* pair_bar = &bars->pair[grp * 4 + quarter];
+    uint16_t* pair_mem =
+        reinterpret_cast<uint16_t*>(smem + L::kOffPair) + (grp * 4 + quarter) * 64;
+    uint32_t px = 0;  // barrier phases so far
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_bar);
+      return wait(pair_bar, px++ & 1);
+    };
+    // 8 bits each way, on alternate bytes: a slot is written again only after the next meeting
+    auto exchange8 = [&](uint32_t mine, uint32_t* theirs) -> bool {
+      uint8_t* mem = reinterpret_cast<uint8_t*>(pair_mem) + (px & 1) * 64;
+      mem[half * 32 + lane] = static_cast<uint8_t>(mine);
+      if (!meet()) return false;
+      *theirs = mem[(half ^ 1) * 32 + lane];
+      return true;
+    };
+    // a float each way, in two halves (rare: each half is read before the next is written)
+    auto exchange_float = [&](float mine, float* theirs) -> bool {
+      uint32_t got = 0;
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        if (!meet()) return false;
+        pair_mem[half * 32 + lane] = static_cast<uint16_t>(__float_as_uint(mine) >> (16 * k));
+        if (!meet()) return false;
+        got |= static_cast<uint32_t>(pair_mem[(half ^ 1) * 32 + lane]) << (16 * k);
+      }
+      *theirs = __uint_as_float(got);
+      return meet();
+    };
     uint32_t sc = 0, act = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
@@ -573,34 +608,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = w.tok0 + qtok;
       const int head = w.kv * p.G + R - qtok * p.G;
       const int pos = valid ? w.ctx_len - w.n_query + qtok : -1;
-      // the row's keys: [key_lo, key_hi] within the item
-      const int key_hi = min(max(pos, w.pad[3] - 1), pe * kBlockSize - 1);
-      const int key_lo = valid ? p.row_lo(tok, pos) : 0;
+      // the row's keys within the item, [key_lo, key_hi], relative to the warp's columns (a
+      // row past the tile's rows is computed unmasked and not written)
+      const int col0 = pb * kBlockSize + 64 * half;
+      const int key_hi =
+          valid ? min(max(pos, w.pad[3] - 1), pe * kBlockSize - 1) - col0 : (1 << 30);
+      const int key_lo = valid ? p.row_lo(tok, pos) - col0 : -(1 << 30);
       const float slope = kBias && valid ? -kLog2e * __ldg(p.slopes + head) : 0.f;
-      float2 steps[4];  // the bias of columns 0..7 relative to column 0
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        steps[i] = make_float2(-slope * (2.f * i), -slope * (2.f * i + 1.f));
-      // the row's split count and partial base, fetched now so that the epilogue's
-      // stores do not wait on them
-      // (both loads are issued at once; nothing waits for them before the epilogue)
-      const int ns_t = !valid ? 0 : kDirect ? 1 : __ldg(p.tok_ns + tok);
-      const int tok_part = kDirect || !valid ? 0 : __ldg(p.tok_base + tok);
+      const float first_dist = static_cast<float>(pos - col0);  // of the item's first column
       // m_ref: the reference max (log2 units) that P, O and l are currently taken against;
-      // m_next: a max more than 2^8 above it seen in the last tile, applied before the next
+      // m_next: the reference from the next tile on, when this one's P summed to over 2^8
       float m_ref = -INFINITY, m_next = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j) {
-        // visible columns: c <= lim (a row past the tile's rows is computed unmasked and
-        // not written)
-        const int tile0 = pb * kBlockSize + tile_at(j, nt) * kKeys;  // the tile's first key
-        const int lim = valid ? key_hi - tile0 : kKeys, low = valid ? key_lo - tile0 : 0;
+        const int t0 = tile_at(j, nt) * kKeys;  // the tile's first key, from the item's
+        const int lim = key_hi - t0, low = key_lo - t0;  // visible: low <= c <= lim
         if (!wait(&bars->s_full[grp], sc & 1)) { ok = false; break; }
         ++sc;
         tc_fence_after();
         // This group's previous PV has completed (this S was issued after it): O is stable.
+        // Each of the two warps keeps a half of its columns.
         auto rescale_o = [&](float alpha) {
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 64; ++c) {
             uint32_t v[32];
             tmem_ld32(tO + c * 32, v);
             tmem_ld_wait();
@@ -611,253 +640,206 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();
         };
         if (__any_sync(0xffffffffu, m_next > m_ref)) {
-          const bool need = m_next > m_ref;
-          const float alpha = need ? fast_exp2(m_ref - m_next) : 1.f;
+          const float alpha = m_next > m_ref ? fast_exp2(m_ref - m_next) : 1.f;
           if (j > 0) rescale_o(alpha);
           l *= alpha;
-          if (need) m_ref = m_next;
+          m_ref = fmaxf(m_ref, m_next);
         }
-        // P = 2^(s*scale*log2e - m_ref) as 16-bit pairs written over S; half h of P lands
-        // on columns 32h..32h+31, which the loads of halves <= h have already read
-        const bool full = __all_sync(0xffffffffu, lim >= kKeys - 1 && low <= 0);
+        const bool full = __all_sync(0xffffffffu, lim >= 63 && low <= 0);
         // every column visible, and (with a bias) none past the row's own position
         const bool one_sign =
-            full && (!kBias || __all_sync(0xffffffffu, !valid || pos >= tile0 + kKeys - 1));
-        // l holds the earlier tiles' sum; this tile's halves are summed apart, so that a
-        // reference moved in half 1 can re-sum the half-0 P it re-rounds
-        float l_half0 = 0.f, l_h = 0.f;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[64];
-          tmem_ld32(tS + 64 * h, v);
-          tmem_ld32(tS + 64 * h + 32, v + 32);
+            full && (!kBias || __all_sync(0xffffffffu, !valid || first_dist - t0 >= 63.f));
+        uint32_t pk[32];
+        float l_t = 0.f;
+        // 32 columns of scores, raw
+        auto load = [&](int h, uint32_t* v) {
+          tmem_ld32(tS + 32 * h, v);
           tmem_ld_wait();
-          // How P is taken from the raw scores. kReady: they have been brought to log2 units in
-          // place (any cap, any bias, masked). The others do it on the way, with packed
-          // arithmetic alone, where every column is visible, the cap's argument is small and
-          // the distances have one sign. Without cap and bias the mask is all there is.
-          auto to_log2 = [&]() {
-            if constexpr (kCap) {
+        };
+        // brought to log2 units in place: any cap, any bias, masked
+        auto to_log2 = [&](int h, uint32_t* v) {
+          if constexpr (kCap) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                v[e] = __float_as_uint(capped(__uint_as_float(v[e]), p.cap_arg, p.cap_log2));
-            }
-            if constexpr (kBias) {
-              const float scale = kCap ? 1.f : p.scale_log2;
-              const float d0 = static_cast<float>(pos - tile0 - 64 * h);  // of the first column
+            for (int e = 0; e < 32; ++e)
+              v[e] = __float_as_uint(capped(__uint_as_float(v[e]), p.cap_arg, p.cap_log2));
+          } else {
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                v[e] = __float_as_uint(fmaf(slope, fabsf(d0 - static_cast<float>(e)),
-                                            __uint_as_float(v[e]) * scale));
-            }
-            if (!full) {
+            for (int e = 0; e < 32; ++e)
+              v[e] = __float_as_uint(__uint_as_float(v[e]) * p.scale_log2);
+          }
+          if constexpr (kBias) {
+            const float d0 = first_dist - static_cast<float>(t0 + 32 * h);  // first column's
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (64 * h + e > lim || 64 * h + e < low) v[e] = __float_as_uint(-INFINITY);
-            }
+            for (int e = 0; e < 32; ++e)
+              v[e] = __float_as_uint(
+                  fmaf(slope, fabsf(d0 - static_cast<float>(e)), __uint_as_float(v[e])));
+          }
+          if (!full) {
+            const int hi = lim - 32 * h, lo = low - 32 * h;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e > hi || e < lo) v[e] = __float_as_uint(-INFINITY);
+          }
+        };
+        // P of 32 columns against the reference, 16-bit pairs; the row sum adds the values the
+        // MMA sees, widened exactly. Where every column is visible, the cap's argument small
+        // and the distances of one sign, packed arithmetic takes the scores straight to the
+        // exponent; otherwise to_log2 first.
+        auto take = [&](int h) {
+          uint32_t v[32];
+          load(h, v);
+          const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+          const float2 nm2 = make_float2(neg_m, neg_m);
+          float2 lq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // four sums
+          auto raw = [&](int e) {
+            return make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
           };
-          int kind = kFast;
+          auto put = [&](int e, float2 x) {
+            pk[16 * h + e / 2] = pack2<kBF16>(fast_exp2(x.x), fast_exp2(x.y));
+            add_pair_exact<kBF16>(lq[(e / 2) & 1], pk[16 * h + e / 2]);
+          };
+          bool fast = one_sign;
           if constexpr (kCap) {
             float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 64; e += 8)
+            for (int e = 0; e < 32; e += 8)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 a[k] = fmax3(a[k], fabsf(__uint_as_float(v[e + 2 * k])),
                              fabsf(__uint_as_float(v[e + 2 * k + 1])));
             const float y = fmax3(fmaxf(a[0], a[1]), a[2], a[3]) * p.cap_y;
-            kind = __all_sync(0xffffffffu, y <= 0.5f)              ? kFast
-                   : !kBias && __all_sync(0xffffffffu, y <= 1.f) ? kWide
-                                                                 : kReady;
+            fast = fast && __all_sync(0xffffffffu, y <= 0.5f);
           }
-          // P is taken against the row's reference without the half's max; the max (and a move
-          // of the reference) is taken only when there is no reference yet, or when the half's
-          // sum shows that P outgrew its bound, and P is then taken again
-          bool with_max = __any_sync(0xffffffffu, m_ref == -INFINITY);
-          if constexpr (kCap || kBias) {
-            if (!one_sign || kind == kReady || (with_max && kBias)) {
-              to_log2();
-              kind = kReady;
-            }
-          } else if (!full) {
-            to_log2();
-          }
-          uint32_t pk[32];
-#pragma unroll 1
-          for (int pass = 0; pass < 2; ++pass) {
-            if (with_max) {
-              // four independent max chains
-              float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-              for (int e = 0; e < 64; e += 8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mq[k] = fmax3(mq[k], __uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1]));
-              const float mx = fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]);
-              // (the cap and the scale keep the order: the max of the raw scores will do)
-              const float m_half = mx == -INFINITY || kind == kReady ? mx
-                                   : kCap ? capped(mx, p.cap_arg, p.cap_log2)
-                                          : mx * p.scale_log2;
-              // no reference yet, or a jump P could overflow on: move the reference now,
-              // rescaling what is already taken against the old one
-              const bool move = m_half > m_ref + kMoveLog2<kBF16> ||
-                                (m_ref == -INFINITY && m_half != -INFINITY);
-              if (__any_sync(0xffffffffu, move)) {
-                const float alpha = move && m_ref != -INFINITY ? fast_exp2(m_ref - m_half) : 1.f;
-                if (j > 0) rescale_o(alpha);
-                l *= alpha;
-                if (h == 1) {
-                  // the half of P already written (columns 0..31) is scaled and rounded
-                  // again; its sum is taken anew from the values the PV product will read
-                  uint32_t q[32];
-                  tmem_st_wait();
-                  tmem_ld32(tS, q);
-                  tmem_ld_wait();
-                  float2 lq0[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) {
-                    q[e] = scale_pair<kBF16>(q[e], alpha);
-                    add_pair_exact<kBF16>(lq0[e & 1], q[e]);
-                  }
-                  l_half0 = (lq0[0].x + lq0[0].y) + (lq0[1].x + lq0[1].y);
-                  tmem_st32(tS, q);
-                  tmem_st_wait();
-                }
-                if (move) m_ref = m_half;
-              }
-            }
-            const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-            float2 lq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // four sums
-            // the scores to log2 units below the reference, two per packed operation; the row
-            // sum adds the 16-bit P values the MMA sees, widened exactly
-            const float2 nm2 = make_float2(neg_m, neg_m);
-            auto raw = [&](int e) {
-              return make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-            };
-            auto put = [&](int e, float2 x) {
-              pk[e / 2] = pack2<kBF16>(fast_exp2(x.x), fast_exp2(x.y));
-              add_pair_exact<kBF16>(lq[(e / 2) & 1], pk[e / 2]);
-            };
-            // bias - m of columns e, e + 1: slope * (distance of column e & ~7) - m, and the
-            // rest of the distance from steps[]
-            const float dist0 = static_cast<float>(pos - tile0 - 64 * h);
-            auto bias = [&](int e) {
-              const float x = fmaf(slope, dist0 - static_cast<float>(e & ~7), neg_m);
-              return ffma2(make_float2(x, x), make_float2(1.f, 1.f), steps[(e & 7) / 2]);
-            };
+          if (fast) {
             const float2 sl2x2 = make_float2(p.scale_log2, p.scale_log2);
             const float2 cap_y2 = make_float2(p.cap_y, p.cap_y);
-            if ((kCap || kBias) && kind == kReady) {
+            const float d0 = first_dist - static_cast<float>(t0 + 32 * h);
 #pragma unroll
-              for (int e = 0; e < 64; e += 2) put(e, ffma2(raw(e), make_float2(1.f, 1.f), nm2));
-            } else if (kCap && !kBias && kind == kWide) {
-#pragma unroll
-              for (int e = 0; e < 64; e += 2)
-                put(e, capped_poly2<6>(fmul2(raw(e), cap_y2), p.tanh6, nm2));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 64; e += 2) {
-                const float2 c = kBias ? bias(e) : nm2;
-                put(e, kCap ? capped_poly2<4>(fmul2(raw(e), cap_y2), p.tanh4, c)
-                            : ffma2(raw(e), sl2x2, c));
+            for (int e = 0; e < 32; e += 2) {
+              float2 c = nm2;
+              if constexpr (kBias) {
+                const float x = fmaf(slope, d0 - static_cast<float>(e), neg_m);
+                c = make_float2(x, x - slope);
               }
+              put(e, kCap ? capped_poly2<4>(fmul2(raw(e), cap_y2), p.tanh4, c)
+                          : ffma2(raw(e), sl2x2, c));
             }
-            // P goes out before its sum is checked; a second pass writes it again
-            if (pass > 0) tmem_st_wait();
-            tmem_st16(tS + 32 * h, pk);
-            tmem_st16(tS + 32 * h + 16, pk + 16);
-            l_h = (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
-            if (with_max || __all_sync(0xffffffffu, l_h <= kHalfSumMax<kBF16>)) break;
-            with_max = true;
-            if (kBias && kind != kReady) {  // the max is of the biased scores
-              to_log2();
-              kind = kReady;
-            }
+          } else {
+            to_log2(h, v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) put(e, ffma2(raw(e), make_float2(1.f, 1.f), nm2));
           }
-          if (h == 0) l_half0 = l_h;
-          else l += l_half0 + l_h;
+          l_t += (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
+        };
+        // P is taken against the row's reference without the tile's max; the max (and a move
+        // of the reference) is taken only when there is no reference yet, or when a half's
+        // sum shows that P outgrew its bound (S is whole until then), and P is taken again.
+        // Both warps see both sums and maxima, so they decide alike.
+        uint32_t top = 0;  // exponent of the larger of the row's half sums
+        bool redo = __any_sync(0xffffffffu, m_ref == -INFINITY);
+        if (!redo) {
+          take(0);
+          take(1);
+          const uint32_t mine = __float_as_uint(l_t) >> 23;
+          if (!exchange8(mine, &top)) { ok = false; break; }
+          top = max(top, mine);
+          redo = __any_sync(0xffffffffu, top >= kSumExp<kBF16>);
         }
-        // O is rescaled lazily: when this tile's P summed to more than 2^8, the reference
-        // moves up by log2 of that sum before the next tile (the new reference is at least
-        // the row's max, so P stays at most 1 there)
-        const float l_tile = l_half0 + l_h;
-        m_next = l_tile > (1 << static_cast<int>(kRescaleLog2)) ? m_ref + __log2f(l_tile) : m_ref;
+        if (redo) {
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+            load(h, v);
+            to_log2(h, v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          }
+          float other;
+          if (!exchange_float(mx, &other)) { ok = false; break; }
+          mx = fmaxf(mx, other);
+          // no reference yet, or a jump P could overflow on: move it now
+          const bool move = mx > m_ref + kMoveLog2<kBF16> || (m_ref == -INFINITY && mx != -INFINITY);
+          if (__any_sync(0xffffffffu, move)) {
+            const float alpha = move && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
+            if (j > 0) rescale_o(alpha);
+            l *= alpha;
+            if (move) m_ref = mx;
+          }
+          l_t = 0.f;
+          take(0);
+          take(1);
+          const uint32_t mine = __float_as_uint(l_t) >> 23;
+          if (!exchange8(mine, &top)) { ok = false; break; }
+          top = max(top, mine);
+        }
+        l += l_t;
+        // O is rescaled lazily: when a half's P summed to 2^8 or more, the reference moves up
+        // past log2 of that sum before the next tile (so that P stays at most 1 there)
+        m_next = top >= 127 + kRescaleExp ? m_ref + static_cast<float>(static_cast<int>(top) - 126)
+                                          : m_ref;
+        tmem_st16(tS, pk);
+        tmem_st16(tS + 16, pk + 16);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_full[grp]);
       }
       if (!ok) break;
-      // epilogue: O / l of this group's rows to the output, or to the split partials
+      // the row's sum, from both halves (in one order, so that both warps have the same)
+      float other;
+      if (!exchange_float(l, &other)) break;
+      l = half ? other + l : l + other;
+      const int ns_t = !valid ? 0 : kDirect ? 1 : __ldg(p.tok_ns + tok);
+      // epilogue: O / l of the warp's half of the columns to the output, or to the split
+      // partials
       if (!wait(&bars->o_done[grp], act & 1)) break;
       tc_fence_after();
       const bool write = valid && w.split < ns_t;
       const bool any = !(l == 0.f);  // a row without keys gives zeros, whatever O holds
       const float inv = any ? 1.f / l : 0.f;
-      if (__all_sync(0xffffffffu, !write || ns_t == 1)) {
-        // Direct output: each lane writes its own row, 64 columns (128 bytes) per TMEM
-        // wait, as 32-byte stores when the output is 32-byte aligned (16-byte stores
-        // otherwise), so every store instruction fills whole 32-byte sectors of 32 rows.
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + (static_cast<int64_t>(tok) * p.H_q + head) * D;
-        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-        const float2 inv2 = make_float2(inv, inv);
+      const float2 inv2 = make_float2(inv, inv);
+      uint16_t* dst = static_cast<uint16_t*>(p.out) +
+                      (static_cast<int64_t>(tok) * p.H_q + head) * D + (D / 2) * half;
+      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+      const int64_t pidx = kDirect || ns_t <= 1
+                               ? 0
+                               : static_cast<int64_t>(__ldg(p.tok_base + tok)) + w.split * p.H_q + head;
+      if (write && ns_t > 1 && half == 0)
+        p.part_lse[pidx] = any ? m_ref + __log2f(l) : -INFINITY;
 #pragma unroll 1
-        for (int c4 = 0; c4 < D / 64; ++c4) {
-          uint32_t v[64];
-          tmem_ld32(tO + c4 * 64, v);
-          tmem_ld32(tO + c4 * 64 + 32, v + 32);
-          tmem_ld_wait();
-          uint32_t w[32];
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tO + c * 32, v);
+        tmem_ld_wait();
+        if (!write) continue;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 x =
-                fmul2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), inv2);
-            w[e] = any ? pack2<kBF16>(x.x, x.y) : 0u;
-          }
-          if (write) {
-            if (wide) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) st_global_v8(dst + c4 * 64 + 16 * q, w + 8 * q);
-            } else {
-              uint4* d4 = reinterpret_cast<uint4*>(dst + c4 * 64);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) d4[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-            }
-          }
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x =
+              fmul2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), inv2);
+          v[e] = any ? __float_as_uint(x.x) : 0u;
+          v[e + 1] = any ? __float_as_uint(x.y) : 0u;
         }
-      } else {
-        // split partials (fp32), one row per lane
-#pragma unroll 1
-        for (int c2 = 0; c2 < D / 64; ++c2) {
-          uint32_t v[64];
-          tmem_ld32(tO + c2 * 64, v);
-          tmem_ld32(tO + c2 * 64 + 32, v + 32);
-          tmem_ld_wait();
-          if (!write) continue;
-          if (!any) {
+        if (ns_t == 1) {
+          uint32_t o[16];
 #pragma unroll
-            for (int e = 0; e < 64; ++e) v[e] = 0u;
-          }
-          if (ns_t == 1) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                                  (static_cast<int64_t>(tok) * p.H_q + head) * D +
-                                                  c2 * 64);
+          for (int e = 0; e < 16; ++e)
+            o[e] = pack2<kBF16>(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+          if (wide) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[q] = make_uint4(
-                  pack2<kBF16>(__uint_as_float(v[8 * q + 0]) * inv, __uint_as_float(v[8 * q + 1]) * inv),
-                  pack2<kBF16>(__uint_as_float(v[8 * q + 2]) * inv, __uint_as_float(v[8 * q + 3]) * inv),
-                  pack2<kBF16>(__uint_as_float(v[8 * q + 4]) * inv, __uint_as_float(v[8 * q + 5]) * inv),
-                  pack2<kBF16>(__uint_as_float(v[8 * q + 6]) * inv, __uint_as_float(v[8 * q + 7]) * inv));
+            for (int q = 0; q < 2; ++q) st_global_v8(dst + c * 32 + 16 * q, o + 8 * q);
           } else {
-            const int64_t pidx = static_cast<int64_t>(tok_part) + w.split * p.H_q + head;
-            float4* dst = reinterpret_cast<float4*>(p.part_o + pidx * D + c2 * 64);
+            uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-              dst[q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
-                                   __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
-            if (c2 == 0) p.part_lse[pidx] = any ? m_ref + __log2f(l) : -INFINITY;
+            for (int q = 0; q < 4; ++q)
+              d4[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
+        } else {
+          uint4* d4 = reinterpret_cast<uint4*>(p.part_o + pidx * D + (D / 2) * half + c * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            d4[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         }
       }
       ++act;
