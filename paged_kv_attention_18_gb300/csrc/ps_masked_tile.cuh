@@ -51,6 +51,7 @@ constexpr float kMoveLog2 = kBF16 ? 64.f : 15.f;
 // max and the reference move.
 template <bool kBF16>
 constexpr uint32_t kSumExp = kBF16 ? 127 + 64 : 127 + 22;
+constexpr float kFixedCapLog2 = 90.f;  // caps up to 62 keep a fixed reference (bf16)
 constexpr uint32_t kTmemCols = 512;
 
 // TMEM columns of softmax group g: S (and P over it) at g*256, O at g*256 + 128
@@ -590,6 +591,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       *theirs = __uint_as_float(got);
       return meet();
     };
+    // Capped scores lie within cap_log2 of 0. Against a fixed reference of cap_log2 - 60 (0 at
+    // least) every P is below 2^60 and, up to kFixedCapLog2, at least 2^-120: within bf16's
+    // normal range and, summed, within fp32's. Then no maximum is taken, nothing moves, and
+    // the two warps of a row have nothing to tell one another before the end.
+    const bool fixed = kCap && !kBias && kBF16 && p.cap_log2 <= kFixedCapLog2;
+    const float m_fixed = fixed ? fmaxf(p.cap_log2 - 60.f, 0.f) : -INFINITY;
     uint32_t sc = 0, act = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
@@ -618,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float first_dist = static_cast<float>(pos - col0);  // of the item's first column
       // m_ref: the reference max (log2 units) that P, O and l are currently taken against;
       // m_next: the reference from the next tile on, when this one's P summed to over 2^8
-      float m_ref = -INFINITY, m_next = -INFINITY, l = 0.f;
+      float m_ref = m_fixed, m_next = m_fixed, l = 0.f;
       for (int j = 0; j < nt; ++j) {
         const int t0 = tile_at(j, nt) * kKeys;  // the tile's first key, from the item's
         const int lim = key_hi - t0, low = key_lo - t0;  // visible: low <= c <= lim
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_st_wait();
         };
-        if (__any_sync(0xffffffffu, m_next > m_ref)) {
+        if (!fixed && __any_sync(0xffffffffu, m_next > m_ref)) {
           const float alpha = m_next > m_ref ? fast_exp2(m_ref - m_next) : 1.f;
           if (j > 0) rescale_o(alpha);
           l *= alpha;
@@ -736,8 +743,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // sum shows that P outgrew its bound (S is whole until then), and P is taken again.
         // Both warps see both sums and maxima, so they decide alike.
         uint32_t top = 0;  // exponent of the larger of the row's half sums
-        bool redo = __any_sync(0xffffffffu, m_ref == -INFINITY);
-        if (!redo) {
+        bool redo = !fixed && __any_sync(0xffffffffu, m_ref == -INFINITY);
+        if (fixed) {
+          take(0);
+          take(1);
+        } else if (!redo) {
           take(0);
           take(1);
           const uint32_t mine = __float_as_uint(l_t) >> 23;
