@@ -416,6 +416,9 @@ int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const v
     return PS_OK;
   }
   if (tiles && static_cast<int64_t>(p.B) * p.H_kv * 2 <= num_sms) p.all_tiles = 1;
+  // One token a sequence or less, on average, of at most 8 heads per KV head: items of 8 rows
+  // on the narrow kernel (a sequence with more tokens gets more items, and is right as well).
+  p.group_rows = !tiles && p.T <= p.B && p.G <= 8 ? 8 : 16;
   const int split_grid = split_ctas(p, num_sms);
   {
     Timed tm(2, s);

@@ -32,6 +32,13 @@ struct SeqInfo {
   int page0, pre;
 };
 
+// Packed rows of a split-kernel item.
+template <class Params>
+__device__ __forceinline__ int group_rows(const Params& p) {
+  if constexpr (Params::kMasked) return p.group_rows;
+  else return 16;
+}
+
 // groups: 16-row groups of the split kernel; tile / qtiles: the sequence goes to the tile
 // kernel (more than 16 packed rows and a tile size exists) in qtiles 128-row tiles.
 template <class Params>
@@ -53,7 +60,8 @@ __device__ __forceinline__ SeqInfo seq_info(const Params& p, const int* qsl, con
     }
   }
   const int rows = s.valid ? s.n * p.G : 0;
-  s.groups = (rows + 15) / 16;
+  const int gr = group_rows(p);
+  s.groups = (rows + gr - 1) / gr;
   s.tile = p.tpt > 0 && (s.groups > kTileMinGroups || (p.all_tiles && s.groups > 0));
   s.qtiles = s.tile ? (s.n + p.tpt - 1) / p.tpt : 0;
   return s;
@@ -538,8 +546,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int concurre
         WorkItem it;
         it.seq = b;
         it.kv = kv;
-        it.row0 = 16 * j;
-        it.nrows = min(16, rows - 16 * j);
+        const int gr = group_rows(p);
+        it.row0 = gr * j;
+        it.nrows = min(gr, rows - gr * j);
         const int i_last = (it.row0 + it.nrows - 1) / p.G;
         it.page_begin = split_page(s, ns, sp);
         it.page_end = min(split_page(s, ns, sp + 1), end_page(s, i_last));

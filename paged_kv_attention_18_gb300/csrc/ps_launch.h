@@ -77,6 +77,7 @@ struct MaskedAttnParams : AttnParams {
   int window;             // keys a row sees, its own included; 0: all before it
   const int32_t* prefix;  // [B] or null
   const int32_t* starts;  // [T] or null
+  int group_rows;         // packed rows of a split-kernel item: 16, or 8 (the narrow kernel)
 
   // the first key of the row at packed token `tok`, position `pos`
   __device__ __forceinline__ int row_lo(int tok, int pos) const {

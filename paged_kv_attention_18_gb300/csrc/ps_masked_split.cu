@@ -39,7 +39,18 @@ struct MaskedSplit {
       1024 + kWarps * (kStages * kStage + kStages * 8 + kRing * 64);
 };
 
-template <bool kBF16, int D, bool kDirect>
+// 8 x 8 16-bit values transposed across the warp: lane 4 a + b holds (a, 2b), (a, 2b + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// kNarrow: items of at most 8 rows (one token of up to 8 query heads per KV head). The
+// products are taken transposed, S^T = K Q^T and O^T = V^T P^T, with the 16 keys or 16 of
+// the head's elements as the MMA's 16 rows and the item's 8 rows as its 8 columns: half the
+// MMAs, scores and accumulators of a 16-row item whose upper half would be empty.
+template <bool kBF16, int D, bool kDirect, bool kNarrow>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     masked_split_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const MaskedAttnParams p) {
@@ -198,11 +209,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   int comp_left = 0, comp_page = 0;
   bool have_item = false;
   WorkItem cur;
-  // per-thread rows g and g + 8 of the item
+  // per-thread rows of the item: g and g + 8 (narrow: 2 t4 and 2 t4 + 1)
   int row_tok[2], row_h[2], row_pos[2], row_lo[2], row_hi[2];
   float m_run[2], l_run[2], slope[2];
-  float o[D / 8][4];
-  uint32_t qa[kKSteps][4];
+  // wide: O of rows g, g + 8, columns 8 j + 2 t4 ..; narrow: O^T of elements 16 j + g, + 8
+  // and rows 2 t4, 2 t4 + 1
+  constexpr int kO = kNarrow ? D / 16 : D / 8;
+  float o[kO][4];
+  uint32_t qa[kKSteps][kNarrow ? 2 : 4];
   const uint16_t* qptr = static_cast<const uint16_t*>(p.q);
 
   auto start_item = [&]() {
@@ -214,7 +228,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     have_item = true;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int rr = g + 8 * r;
+      const int rr = kNarrow ? 2 * t4 + r : g + 8 * r;
       row_tok[r] = -1;
       row_h[r] = row_pos[r] = row_lo[r] = row_hi[r] = 0;
       slope[r] = 0.f;
@@ -232,56 +246,103 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       l_run[r] = 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    // query fragments straight from global memory (rows g, g + 8; columns 2*t4 ...)
+    for (int j = 0; j < kO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    // query fragments straight from global memory: rows g (and, wide, g + 8); columns 2 t4,
+    // 2 t4 + 1 and 8 further on
 #pragma unroll
-    for (int kk = 0; kk < kKSteps; ++kk) {
+    for (int r = 0; r < (kNarrow ? 1 : 2); ++r) {
+      const int R = cur.row0 + g + 8 * r, i = R / p.G;
+      const bool in = g + 8 * r < cur.nrows;
+      const uint16_t* src = qptr + (static_cast<int64_t>(cur.tok0 + i) * p.H_q + cur.kv * p.G +
+                                    (R - i * p.G)) * D + 2 * t4;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t lo = 0, hi = 0;
-        if (row_tok[r] >= 0) {
-          const uint16_t* src =
-              qptr + (static_cast<int64_t>(row_tok[r]) * p.H_q + row_h[r]) * D + kk * 16 + 2 * t4;
-          lo = __ldg(reinterpret_cast<const uint32_t*>(src));
-          hi = __ldg(reinterpret_cast<const uint32_t*>(src + 8));
+      for (int kk = 0; kk < kKSteps; ++kk) {
+        const uint32_t lo = in ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16)) : 0;
+        const uint32_t hi = in ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8)) : 0;
+        if constexpr (kNarrow) {
+          qa[kk][0] = lo;
+          qa[kk][1] = hi;
+        } else {
+          qa[kk][r] = lo;
+          qa[kk][2 + r] = hi;
         }
-        qa[kk][r] = lo;       // columns 2t4, 2t4+1
-        qa[kk][2 + r] = hi;   // columns 2t4+8, 2t4+9
       }
     }
   };
 
   auto finish_item = [&]() {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {  // row sums across the quad of lanes sharing a row
-      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
-      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+    for (int r = 0; r < 2; ++r) {  // row sums across the lanes sharing a row
+#pragma unroll
+      for (int x = kNarrow ? 4 : 1; x < (kNarrow ? 32 : 4); x <<= 1)
+        l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], x);
     }
+    bool any[2], held[2];
+    float inv[2];
+    int64_t part[2];  // the row's partial entry, or -1: straight to the output
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      if (row_tok[r] < 0) continue;
-      const int tok = row_tok[r];
-      const int ns_t = __ldg(p.tok_ns + tok);
-      if (cur.split >= ns_t) continue;  // this split does not hold the row
       // a row without keys here gives zeros, whatever the products left in o
-      const bool any = !(l_run[r] == 0.f);
-      const float inv = any ? 1.f / l_run[r] : 0.f;
-      if (ns_t == 1) {
-        uint32_t* dst = reinterpret_cast<uint32_t*>(
-            static_cast<uint16_t*>(p.out) + (static_cast<int64_t>(tok) * p.H_q + row_h[r]) * D +
-            2 * t4);
+      any[r] = !(l_run[r] == 0.f);
+      inv[r] = any[r] ? 1.f / l_run[r] : 0.f;
+      part[r] = -1;
+      const int ns_t = row_tok[r] < 0 ? 0 : __ldg(p.tok_ns + row_tok[r]);
+      held[r] = cur.split < ns_t;  // else this split does not hold the row
+      if (held[r] && ns_t > 1) {
+        part[r] = static_cast<int64_t>(__ldg(p.tok_base + row_tok[r])) + cur.split * p.H_q + row_h[r];
+        if (kNarrow ? g == 0 : t4 == 0)
+          p.part_lse[part[r]] = any[r] ? m_run[r] + __log2f(l_run[r]) : -INFINITY;
+      }
+    }
+    auto norm = [&](float x, int r) { return any[r] ? x * inv[r] : 0.f; };
+    if constexpr (kNarrow) {
+      // partials: eight lanes write a row's 8 consecutive elements
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          dst[j * 4] = any ? pack2<kBF16>(o[j][2 * r] * inv, o[j][2 * r + 1] * inv) : 0u;
-      } else {
-        const int64_t idx = static_cast<int64_t>(__ldg(p.tok_base + tok)) + cur.split * p.H_q +
-                            row_h[r];
-        float2* dst = reinterpret_cast<float2*>(p.part_o + idx * D + 2 * t4);
+      for (int r = 0; r < 2; ++r) {
+        if (!held[r] || part[r] < 0) continue;
+        float* dst = p.part_o + part[r] * D + g;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          dst[j * 4] = any ? make_float2(o[j][2 * r] * inv, o[j][2 * r + 1] * inv)
-                           : make_float2(0.f, 0.f);
-        if (t4 == 0) p.part_lse[idx] = any ? m_run[r] + __log2f(l_run[r]) : -INFINITY;
+        for (int j = 0; j < kO; ++j) {
+          dst[16 * j] = norm(o[j][r], r);
+          dst[16 * j + 8] = norm(o[j][2 + r], r);
+        }
+      }
+      // outputs: transposed back, lane 4 a + b then has row a's elements 2 b, 2 b + 1. The
+      // rows of an item are of one token or of tokens split alike or not: row g's fate is
+      // that of the lane that holds its sums.
+      const bool direct0 = __shfl_sync(0xffffffffu, held[0] && part[0] < 0, g >> 1);
+      const bool direct1 = __shfl_sync(0xffffffffu, held[1] && part[1] < 0, g >> 1);
+      const int R = cur.row0 + g, i = R / p.G;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(
+          static_cast<uint16_t*>(p.out) +
+          (static_cast<int64_t>(cur.tok0 + i) * p.H_q + cur.kv * p.G + (R - i * p.G)) * D + 2 * t4);
+      const bool mine = (g & 1) ? direct1 : direct0;
+#pragma unroll
+      for (int j = 0; j < kO; ++j) {
+        const uint32_t lo = transpose8(pack2<kBF16>(norm(o[j][0], 0), norm(o[j][1], 1)));
+        const uint32_t hi = transpose8(pack2<kBF16>(norm(o[j][2], 0), norm(o[j][3], 1)));
+        if (mine) {
+          dst[8 * j] = lo;
+          dst[8 * j + 4] = hi;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (!held[r]) continue;
+        if (part[r] < 0) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(
+              static_cast<uint16_t*>(p.out) +
+              (static_cast<int64_t>(row_tok[r]) * p.H_q + row_h[r]) * D + 2 * t4);
+#pragma unroll
+          for (int j = 0; j < kO; ++j)
+            dst[j * 4] = pack2<kBF16>(norm(o[j][2 * r], r), norm(o[j][2 * r + 1], r));
+        } else {
+          float2* dst = reinterpret_cast<float2*>(p.part_o + part[r] * D + 2 * t4);
+#pragma unroll
+          for (int j = 0; j < kO; ++j)
+            dst[j * 4] = make_float2(norm(o[j][2 * r], r), norm(o[j][2 * r + 1], r));
+        }
       }
     }
     have_item = false;
@@ -324,102 +385,184 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       __syncwarp();
     }
 
-    // S = Q K^T for the page's 16 keys: two n8 tiles, two accumulators per tile (even and
-    // odd k steps) to halve the dependent mma chain
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    {
-      float s2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      const int mi = lane >> 3, rr = lane & 7;
-      const int key = (mi >> 1) * 8 + rr;
+    if constexpr (kNarrow) {
+      // S^T = K Q^T for the page's 16 keys: lane holds keys g, g + 8 of rows 2 t4, 2 t4 + 1
+      // (two accumulators, even and odd k steps, to halve the dependent mma chain)
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        float s2[4] = {0.f, 0.f, 0.f, 0.f};
+        const int mi = lane >> 3, key = (mi & 1) * 8 + (lane & 7);
 #pragma unroll
-      for (int kk = 0; kk < kKSteps; ++kk) {
-        const int chunk = 2 * kk + (mi & 1);
-        const uint32_t addr = kbase + (chunk >> 3) * (kBlockSize * 128) + swz128(key, chunk & 7);
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4(addr, b0, b1, b2, b3);
-        float (*acc)[4] = (kk & 1) ? s2 : s;
-        mma_16816<kBF16>(acc[0], qa[kk], b0, b1);
-        mma_16816<kBF16>(acc[1], qa[kk], b2, b3);
+        for (int kk = 0; kk < kKSteps; ++kk) {
+          const int chunk = 2 * kk + (mi >> 1);
+          const uint32_t addr = kbase + (chunk >> 3) * (kBlockSize * 128) + swz128(key, chunk & 7);
+          uint32_t a[4];
+          ldsm_x4(addr, a[0], a[1], a[2], a[3]);
+          mma_16816<kBF16>((kk & 1) ? s2 : s, a, qa[kk][0], qa[kk][1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += s2[e];
       }
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] += s2[nt][e];
-    }
-    // the scores in log2 units: capped, biased, masked
-    if (p.cap_log2 > 0.f) {
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = capped(s[nt][e], p.cap_arg, p.cap_log2);
-    } else {
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] *= p.scale_log2;
-    }
-    const int key0 = key_base + 2 * t4;
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+      // the scores in log2 units: capped, biased, masked (element e: key g + 8 (e / 2), row e % 2)
+      bool up = false;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = e >> 1;
-        const int key = key0 + nt * 8 + (e & 1);
-        const float d = fabsf(static_cast<float>(row_pos[r] - key));
-        float x = fmaf(slope[r], d, s[nt][e]);
-        x = key >= row_lo[r] && key < row_hi[r] ? x : -INFINITY;
-        s[nt][e] = x;
-        mx[r] = fmaxf(mx[r], x);
+        const int r = e & 1, key = key_base + g + 8 * (e >> 1);
+        const float c = p.cap_log2 > 0.f ? capped(s[e], p.cap_arg, p.cap_log2) : s[e] * p.scale_log2;
+        const float x = fmaf(slope[r], fabsf(static_cast<float>(row_pos[r] - key)), c);
+        s[e] = key >= row_lo[r] && key < row_hi[r] ? x : -INFINITY;
+        up |= s[e] > m_run[r] + 8.f;
       }
-    float alpha[2], m_use[2];
+      // The reference moves only when some score is more than 2^8 above it (P then stays
+      // within 2^8, a sum of any length in fp32): the maxima across lanes and the rescaling
+      // of O are paid a few times an item, not every page.
+      if (__any_sync(0xffffffffu, up)) {
+        float alpha[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-      const float m_new = fmaxf(m_run[r], mx[r]);
-      m_use[r] = m_new == -INFINITY ? 0.f : m_new;
-      alpha[r] = fast_exp2(m_run[r] - m_use[r]);
-      m_run[r] = m_new;
-    }
+        for (int r = 0; r < 2; ++r) {
+          float mx = fmaxf(s[r], s[2 + r]);
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+          for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+          const float m_new = fmaxf(m_run[r], mx);
+          alpha[r] = m_run[r] == -INFINITY ? 1.f : fast_exp2(m_run[r] - m_new);
+          m_run[r] = m_new;
+          l_run[r] *= alpha[r];
+        }
+        const float2 a2 = make_float2(alpha[0], alpha[1]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = fast_exp2(s[nt][e] - m_use[e >> 1]);
-    uint32_t pa[4];
-    pa[0] = pack2<kBF16>(s[0][0], s[0][1]);
-    pa[1] = pack2<kBF16>(s[0][2], s[0][3]);
-    pa[2] = pack2<kBF16>(s[1][0], s[1][1]);
-    pa[3] = pack2<kBF16>(s[1][2], s[1][3]);
-    // the row sums use the rounded P the tensor core multiplies with
+        for (int j = 0; j < kO; ++j) {
+          const float2 u = fmul2(make_float2(o[j][0], o[j][1]), a2);
+          const float2 v = fmul2(make_float2(o[j][2], o[j][3]), a2);
+          o[j][0] = u.x;
+          o[j][1] = u.y;
+          o[j][2] = v.x;
+          o[j][3] = v.y;
+        }
+      }
+      uint32_t pt[2];  // P^T: keys g (g + 8), rows 2 t4, 2 t4 + 1
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float2 acc = make_float2(l_run[r] * alpha[r], 0.f);
-      add_pair_exact<kBF16>(acc, pa[r]);
-      add_pair_exact<kBF16>(acc, pa[2 + r]);
-      l_run[r] = acc.x + acc.y;
-    }
-    const float2 a0 = make_float2(alpha[0], alpha[0]), a1 = make_float2(alpha[1], alpha[1]);
+      for (int h = 0; h < 2; ++h) {
+        float x[2];
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-      const float2 u = fmul2(make_float2(o[j][0], o[j][1]), a0);
-      const float2 w = fmul2(make_float2(o[j][2], o[j][3]), a1);
-      o[j][0] = u.x;
-      o[j][1] = u.y;
-      o[j][2] = w.x;
-      o[j][3] = w.y;
-    }
-    {  // O += P V: the V page is [key][d], read transposed
-      const int mi = lane >> 3, rr = lane & 7;
-      const int key = (mi & 1) * 8 + rr;
+        for (int r = 0; r < 2; ++r)
+          x[r] = fast_exp2(s[2 * h + r] - (m_run[r] == -INFINITY ? 0.f : m_run[r]));
+        pt[h] = pack2<kBF16>(x[0], x[1]);
+        // the row sums use the rounded P the tensor core multiplies with
+        float2 acc = make_float2(l_run[0], l_run[1]);
+        add_pair_exact<kBF16>(acc, pt[h]);
+        l_run[0] = acc.x;
+        l_run[1] = acc.y;
+      }
+      const uint32_t b0 = transpose8(pt[0]), b1 = transpose8(pt[1]);
+      {  // O^T += V^T P^T: the V page is [key][d], read transposed
+        const int mi = lane >> 3, key = (mi >> 1) * 8 + (lane & 7);
 #pragma unroll
-      for (int np = 0; np < D / 16; ++np) {
-        const int chunk = 2 * np + (mi >> 1);
-        const uint32_t addr = vbase + (chunk >> 3) * (kBlockSize * 128) + swz128(key, chunk & 7);
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4_t(addr, b0, b1, b2, b3);
-        mma_16816<kBF16>(o[2 * np], pa, b0, b1);
-        mma_16816<kBF16>(o[2 * np + 1], pa, b2, b3);
+        for (int j = 0; j < kO; ++j) {
+          const int chunk = 2 * j + (mi & 1);
+          const uint32_t addr = vbase + (chunk >> 3) * (kBlockSize * 128) + swz128(key, chunk & 7);
+          uint32_t a[4];
+          ldsm_x4_t(addr, a[0], a[1], a[2], a[3]);
+          mma_16816<kBF16>(o[j], a, b0, b1);
+        }
+      }
+    } else {
+      // S = Q K^T for the page's 16 keys: two n8 tiles, two accumulators per tile (even and
+      // odd k steps) to halve the dependent mma chain
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      {
+        float s2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const int mi = lane >> 3, rr = lane & 7;
+        const int key = (mi >> 1) * 8 + rr;
+#pragma unroll
+        for (int kk = 0; kk < kKSteps; ++kk) {
+          const int chunk = 2 * kk + (mi & 1);
+          const uint32_t addr = kbase + (chunk >> 3) * (kBlockSize * 128) + swz128(key, chunk & 7);
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(addr, b0, b1, b2, b3);
+          float (*acc)[4] = (kk & 1) ? s2 : s;
+          mma_16816<kBF16>(acc[0], qa[kk], b0, b1);
+          mma_16816<kBF16>(acc[1], qa[kk], b2, b3);
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] += s2[nt][e];
+      }
+      // the scores in log2 units: capped, biased, masked
+      if (p.cap_log2 > 0.f) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] = capped(s[nt][e], p.cap_arg, p.cap_log2);
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] *= p.scale_log2;
+      }
+      const int key0 = key_base + 2 * t4;
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = e >> 1;
+          const int key = key0 + nt * 8 + (e & 1);
+          const float d = fabsf(static_cast<float>(row_pos[r] - key));
+          float x = fmaf(slope[r], d, s[nt][e]);
+          x = key >= row_lo[r] && key < row_hi[r] ? x : -INFINITY;
+          s[nt][e] = x;
+          mx[r] = fmaxf(mx[r], x);
+        }
+      float alpha[2], m_use[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        const float m_new = fmaxf(m_run[r], mx[r]);
+        m_use[r] = m_new == -INFINITY ? 0.f : m_new;
+        alpha[r] = fast_exp2(m_run[r] - m_use[r]);
+        m_run[r] = m_new;
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = fast_exp2(s[nt][e] - m_use[e >> 1]);
+      uint32_t pa[4];
+      pa[0] = pack2<kBF16>(s[0][0], s[0][1]);
+      pa[1] = pack2<kBF16>(s[0][2], s[0][3]);
+      pa[2] = pack2<kBF16>(s[1][0], s[1][1]);
+      pa[3] = pack2<kBF16>(s[1][2], s[1][3]);
+      // the row sums use the rounded P the tensor core multiplies with
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float2 acc = make_float2(l_run[r] * alpha[r], 0.f);
+        add_pair_exact<kBF16>(acc, pa[r]);
+        add_pair_exact<kBF16>(acc, pa[2 + r]);
+        l_run[r] = acc.x + acc.y;
+      }
+      const float2 a0 = make_float2(alpha[0], alpha[0]), a1 = make_float2(alpha[1], alpha[1]);
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        const float2 u = fmul2(make_float2(o[j][0], o[j][1]), a0);
+        const float2 w = fmul2(make_float2(o[j][2], o[j][3]), a1);
+        o[j][0] = u.x;
+        o[j][1] = u.y;
+        o[j][2] = w.x;
+        o[j][3] = w.y;
+      }
+      {  // O += P V: the V page is [key][d], read transposed
+        const int mi = lane >> 3, rr = lane & 7;
+        const int key = (mi & 1) * 8 + rr;
+#pragma unroll
+        for (int np = 0; np < D / 16; ++np) {
+          const int chunk = 2 * np + (mi >> 1);
+          const uint32_t addr = vbase + (chunk >> 3) * (kBlockSize * 128) + swz128(key, chunk & 7);
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4_t(addr, b0, b1, b2, b3);
+          mma_16816<kBF16>(o[2 * np], pa, b0, b1);
+          mma_16816<kBF16>(o[2 * np + 1], pa, b2, b3);
+        }
       }
     }
     ++g_comp;
@@ -485,25 +628,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
 }
 
-template <bool kBF16, int D, bool kDirect>
+template <bool kBF16, int D, bool kDirect, bool kNarrow>
 cudaError_t launch_t(const MaskedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                      int ctas, cudaStream_t stream, bool pdl) {
   constexpr int smem = MaskedSplit<D>::kSmem;
-  auto kern = masked_split_kernel<kBF16, D, kDirect>;
+  auto kern = masked_split_kernel<kBF16, D, kDirect, kNarrow>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_limit(kern, smem, done);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(ctas), dim3(kWarps * 32), smem, stream, pdl, kmap, vmap, p);
 }
 
-template <bool kDirect>
+template <bool kDirect, bool kNarrow>
 cudaError_t launch_d(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                      const CUtensorMap& vmap, int ctas, cudaStream_t stream, bool pdl) {
   if (p.D == 128)
-    return bf16 ? launch_t<true, 128, kDirect>(p, kmap, vmap, ctas, stream, pdl)
-                : launch_t<false, 128, kDirect>(p, kmap, vmap, ctas, stream, pdl);
-  return bf16 ? launch_t<true, 64, kDirect>(p, kmap, vmap, ctas, stream, pdl)
-              : launch_t<false, 64, kDirect>(p, kmap, vmap, ctas, stream, pdl);
+    return bf16 ? launch_t<true, 128, kDirect, kNarrow>(p, kmap, vmap, ctas, stream, pdl)
+                : launch_t<false, 128, kDirect, kNarrow>(p, kmap, vmap, ctas, stream, pdl);
+  return bf16 ? launch_t<true, 64, kDirect, kNarrow>(p, kmap, vmap, ctas, stream, pdl)
+              : launch_t<false, 64, kDirect, kNarrow>(p, kmap, vmap, ctas, stream, pdl);
 }
 
 }  // namespace
@@ -511,8 +654,9 @@ cudaError_t launch_d(const MaskedAttnParams& p, bool bf16, const CUtensorMap& km
 cudaError_t launch_masked_split(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int ctas, cudaStream_t stream,
                                 bool pdl) {
-  return p.direct ? launch_d<true>(p, bf16, kmap, vmap, ctas, stream, pdl)
-                  : launch_d<false>(p, bf16, kmap, vmap, ctas, stream, pdl);
+  if (p.direct) return launch_d<true, false>(p, bf16, kmap, vmap, ctas, stream, pdl);
+  return p.group_rows == 8 ? launch_d<false, true>(p, bf16, kmap, vmap, ctas, stream, pdl)
+                           : launch_d<false, false>(p, bf16, kmap, vmap, ctas, stream, pdl);
 }
 
 }  // namespace ps

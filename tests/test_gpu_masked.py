@@ -286,6 +286,20 @@ def test_captured_with_lengths_that_grow():
     assert binding.device_error() == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (6, 2, 64), (5, 5, 128), (14, 2, 128)])
+@pytest.mark.parametrize("kw", [{}, dict(window=700, softcap=12.0, std=5.0), dict(bias=1)])
+def test_decode_items_of_eight_rows(hq, hkv, d, kw):
+    # no more tokens than sequences: 8-row items, some of a sequence with several tokens
+    kw = dict(kw)
+    if kw.pop("bias", None):
+        kw["slopes"] = slopes_of(hq)
+    seqs = [(5000, 1), (2300, 5), (9, 0), (7000, 0), (2049, 1), (15, 2), (3000, 0), (77, 1),
+            (1, 1), (0, 0), (4000, 1), (600, 0)]
+    for dt in DTS:
+        b = Batch(seqs, hq, hkv, d, dt, 18, **kw)
+        b.check(b.run())
+
+
 def test_many_sequences():
     # more sequences than the planner stages in shared memory
     seqs = [(1 + (7 * i) % 90, 1) for i in range(4200)]
