@@ -38,8 +38,15 @@ constexpr int kSub = kRows * 128; // bytes of one [128 rows x 64 elements] swizz
 constexpr int kKStages = 3;       // K tile stages (freed once both products S have read them)
 constexpr int kVStages = 2;       // V tile stages (freed once both products PV have read them)
 constexpr int kItemRing = 4;     // item indices handed from the fetching warp to the others
-constexpr int kSoftmaxWarps = 16;  // two a query row: a half of the columns each
-constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
+// Softmax warps: one for every 32 query rows, or two (kDuo) with half of a key tile's columns
+// each where a cap or a bias makes the softmax the longest part. (4 x 2048 tokens over 8192
+// keys, 32/8 heads, D 128: capped 729 us with one, 580 with two; masks alone 486 and 495, and
+// short documents, 1000 tokens of up to 300 each, 28 and 33: the two must agree on a row's
+// reference.)
+template <bool kDuo>
+constexpr int kSoftmaxWarps = kDuo ? 16 : 8;
+template <bool kDuo>
+constexpr int kThreads = 128 + 32 * kSoftmaxWarps<kDuo>;
 constexpr int kRescaleExp = 8;  // rescale O only when P sums to 2^8 or more
 // A larger jump inside a tile moves the reference at once; below it P can reach 2^kMove,
 // which must stay finite in the 16-bit type (fp16 tops out near 2^16, bf16 near 2^128).
@@ -51,6 +58,9 @@ constexpr float kMoveLog2 = kBF16 ? 64.f : 15.f;
 // max and the reference move.
 template <bool kBF16>
 constexpr uint32_t kSumExp = kBF16 ? 127 + 64 : 127 + 22;
+// The same bound for a 64-column half taken by one warp.
+template <bool kBF16>
+constexpr float kHalfSumMax = kBF16 ? 18446744073709551616.f : 4194304.f;
 constexpr float kFixedCapLog2 = 90.f;  // caps up to 62 keep a fixed reference (bf16)
 constexpr uint32_t kTmemCols = 512;
 
@@ -103,12 +113,13 @@ __device__ __forceinline__ bool tile_item_ok(const WorkItem& w, const MaskedAttn
 // kDirect: no plan. Each CTA derives its items from seq_lens and qsl (every sequence
 // unsplit, its query-tile pairs longest first).
 template <bool kBF16, int D, bool kDirect, bool kCap, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
     masked_tile_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap,
                        const __grid_constant__ CUtensorMap qmap, const MaskedAttnParams p) {
   using L = TileSmem<D>;
   constexpr int kHalves = D / 64;
+  constexpr bool kDuo = kCap || kBias;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
 
@@ -141,14 +152,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&bars->s_full[g], 1);
-      mbar_init(&bars->p_full[g], g == 0 ? 9 : 8);  // tile A's: + the K/V watcher
+      mbar_init(&bars->p_full[g], kSoftmaxWarps<kDuo> / 2 + (g == 0 ? 1 : 0));  // A's: + watcher
       mbar_init(&bars->o_done[g], 1);
     }
     for (int i = 0; i < 8; ++i) mbar_init(&bars->pair[i], 2);
     mbar_init(&bars->mma_final, 1);
     for (int s = 0; s < kItemRing; ++s) {
       mbar_init(&bars->item_full[s], 1);
-      mbar_init(&bars->item_empty[s], 3 + kSoftmaxWarps);  // V producer, MMA, K/V watcher, softmax
+      mbar_init(&bars->item_empty[s], 3 + kSoftmaxWarps<kDuo>);  // V producer, MMA, K/V watcher, softmax
     }
     bars->abort = 0;
     fence_barrier_init();
@@ -165,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // once, so that their S is 0 and they go through the softmax like any unmasked row.
     const int rows = p.G * p.tpt;
     const int words = (kRows - rows) * 128 / 16;  // 16-byte words per sub-tile
-    for (int i = threadIdx.x; i < 2 * kHalves * words; i += kThreads) {
+    for (int i = threadIdx.x; i < 2 * kHalves * words; i += kThreads<kDuo>) {
       const int sub = i / words, wd = i - sub * words;
       reinterpret_cast<uint4*>(smem + L::kOffQ + sub * kSub + rows * 128)[wd] = make_uint4(0, 0, 0, 0);
     }
@@ -478,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t acc0 = j > 0 ? 1u : 0u;
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            umma_f16_ts(tmem + col_o(grp), tmem + col_s(grp) + (kk / 4) * 64 + (kk % 4) * 8,
+            umma_f16_ts(tmem + col_o(grp),
+                        tmem + col_s(grp) + (kDuo ? (kk / 4) * 64 + (kk % 4) * 8 : kk * 8),
                         b0 + ((kk * 2048) >> 4), idPV, kk > 0 ? 1u : acc0);
           if (grp == ng - 1) umma_commit(&bars->v_empty[st]);  // last reader of the V stage
           return true;
@@ -552,307 +564,570 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ============================ softmax groups + epilogue =========================
-    const int grp = (warp - 4) >> 3;        // 0: query tile A, 1: query tile B
-    const int half = ((warp - 4) >> 2) & 1; // columns 64 * half .. + 63 of each key tile
-    const int quarter = warp & 3;           // TMEM lanes 32*quarter .. +31
-    const int r = quarter * 32 + lane;
-    const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t tS = trow + col_s(grp) + 64 * half;            // P over its first 32 columns
-    const uint32_t tO = trow + col_o(grp) + (D / 2) * half;       // the half of O it keeps
-    // What the two warps of the same rows tell one another: 16 bits a row, through shared
-    // memory and a barrier of the two (bounded, like every wait).
-    uint64_t* pair_bar = &bars->pair[grp * 4 + quarter];
-    uint16_t* pair_mem =
-        reinterpret_cast<uint16_t*>(smem + L::kOffPair) + (grp * 4 + quarter) * 64;
-    uint32_t px = 0;  // barrier phases so far
-    auto meet = [&]() -> bool {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pair_bar);
-      return wait(pair_bar, px++ & 1);
-    };
-    // 8 bits each way, on alternate bytes: a slot is written again only after the next meeting
-    auto exchange8 = [&](uint32_t mine, uint32_t* theirs) -> bool {
-      uint8_t* mem = reinterpret_cast<uint8_t*>(pair_mem) + (px & 1) * 64;
-      mem[half * 32 + lane] = static_cast<uint8_t>(mine);
-      if (!meet()) return false;
-      *theirs = mem[(half ^ 1) * 32 + lane];
-      return true;
-    };
-    // a float each way, in two halves (rare: each half is read before the next is written)
-    auto exchange_float = [&](float mine, float* theirs) -> bool {
-      uint32_t got = 0;
+    if constexpr (!kDuo) {
+      // ---- masks alone: one warp for 32 rows, a half of a tile's columns after the other
+      const int grp = (warp - 4) >> 2;   // 0: query tile A, 1: query tile B
+      const int quarter = warp & 3;      // TMEM lanes 32*quarter .. +31
+      const int r = quarter * 32 + lane;
+      const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t tS = trow + col_s(grp), tO = trow + col_o(grp);
+      uint32_t sc = 0, act = 0;
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        const int idx = next_item(it);
+        if (idx < 0) break;
+        const WorkItem& w = items[it % (2 * kItemRing)];
+        const int pb = w.page_begin, pe = w.page_end;
+        if (pe <= pb || !tile_item_ok(w, p)) continue;
+        const int nt = (pe - pb + kPagesPerTile - 1) / kPagesPerTile;
+        const int nrows = grp == 0 ? w.nrows : w.pad[0];
+        if (nrows == 0) continue;  // no query tile B in this item
+        // this thread's query row
+        const bool valid = r < nrows;
+        const int R = w.row0 + grp * p.tpt * p.G + r;  // packed row within the sequence
+        const int qtok = R / p.G;                        // query index within the sequence
+        const int tok = w.tok0 + qtok;
+        const int head = w.kv * p.G + R - qtok * p.G;
+        const int pos = valid ? w.ctx_len - w.n_query + qtok : -1;
+        // the row's keys: [key_lo, key_hi] within the item
+        const int key_hi = min(max(pos, w.pad[3] - 1), pe * kBlockSize - 1);
+        const int key_lo = valid ? p.row_lo(tok, pos) : 0;
+        // the row's split count and partial base, fetched now so that the epilogue's
+        // stores do not wait on them
+        // (both loads are issued at once; nothing waits for them before the epilogue)
+        const int ns_t = !valid ? 0 : kDirect ? 1 : __ldg(p.tok_ns + tok);
+        const int tok_part = kDirect || !valid ? 0 : __ldg(p.tok_base + tok);
+        // m_ref: the reference max (log2 units) that P, O and l are currently taken against;
+        // m_next: a max more than 2^8 above it seen in the last tile, applied before the next
+        float m_ref = -INFINITY, m_next = -INFINITY, l = 0.f;
+        for (int j = 0; j < nt; ++j) {
+          // visible columns: c <= lim (a row past the tile's rows is computed unmasked and
+          // not written)
+          const int tile0 = pb * kBlockSize + j * kKeys;  // the tile's first key
+          const int lim = valid ? key_hi - tile0 : kKeys, low = valid ? key_lo - tile0 : 0;
+          if (!wait(&bars->s_full[grp], sc & 1)) { ok = false; break; }
+          ++sc;
+          tc_fence_after();
+          // This group's previous PV has completed (this S was issued after it): O is stable.
+          auto rescale_o = [&](float alpha) {
 #pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        if (!meet()) return false;
-        pair_mem[half * 32 + lane] = static_cast<uint16_t>(__float_as_uint(mine) >> (16 * k));
-        if (!meet()) return false;
-        got |= static_cast<uint32_t>(pair_mem[(half ^ 1) * 32 + lane]) << (16 * k);
-      }
-      *theirs = __uint_as_float(got);
-      return meet();
-    };
-    // Capped scores lie within cap_log2 of 0. Against a fixed reference of cap_log2 - 60 (0 at
-    // least) every P is below 2^60 and, up to kFixedCapLog2, at least 2^-120: within bf16's
-    // normal range and, summed, within fp32's. Then no maximum is taken, nothing moves, and
-    // the two warps of a row have nothing to tell one another before the end.
-    const bool fixed = kCap && !kBias && kBF16 && p.cap_log2 <= kFixedCapLog2;
-    const float m_fixed = fixed ? fmaxf(p.cap_log2 - 60.f, 0.f) : -INFINITY;
-    uint32_t sc = 0, act = 0;
-    bool ok = true;
-    for (int it = 0; ok; ++it) {
-      const int idx = next_item(it);
-      if (idx < 0) break;
-      const WorkItem& w = items[it % (2 * kItemRing)];
-      const int pb = w.page_begin, pe = w.page_end;
-      if (pe <= pb || !tile_item_ok(w, p)) continue;
-      const int nt = (pe - pb + kPagesPerTile - 1) / kPagesPerTile;
-      const int nrows = grp == 0 ? w.nrows : w.pad[0];
-      if (nrows == 0) continue;  // no query tile B in this item
-      // this thread's query row
-      const bool valid = r < nrows;
-      const int R = w.row0 + grp * p.tpt * p.G + r;  // packed row within the sequence
-      const int qtok = R / p.G;                        // query index within the sequence
-      const int tok = w.tok0 + qtok;
-      const int head = w.kv * p.G + R - qtok * p.G;
-      const int pos = valid ? w.ctx_len - w.n_query + qtok : -1;
-      // the row's keys within the item, [key_lo, key_hi], relative to the warp's columns (a
-      // row past the tile's rows is computed unmasked and not written)
-      const int col0 = pb * kBlockSize + 64 * half;
-      const int key_hi =
-          valid ? min(max(pos, w.pad[3] - 1), pe * kBlockSize - 1) - col0 : (1 << 30);
-      const int key_lo = valid ? p.row_lo(tok, pos) - col0 : -(1 << 30);
-      const float slope = kBias && valid ? -kLog2e * __ldg(p.slopes + head) : 0.f;
-      const float first_dist = static_cast<float>(pos - col0);  // of the item's first column
-      // m_ref: the reference max (log2 units) that P, O and l are currently taken against;
-      // m_next: the reference from the next tile on, when this one's P summed to over 2^8
-      float m_ref = m_fixed, m_next = m_fixed, l = 0.f;
-      for (int j = 0; j < nt; ++j) {
-        const int t0 = tile_at(j, nt) * kKeys;  // the tile's first key, from the item's
-        const int lim = key_hi - t0, low = key_lo - t0;  // visible: low <= c <= lim
-        if (!wait(&bars->s_full[grp], sc & 1)) { ok = false; break; }
-        ++sc;
-        tc_fence_after();
-        // This group's previous PV has completed (this S was issued after it): O is stable.
-        // Each of the two warps keeps a half of its columns.
-        auto rescale_o = [&](float alpha) {
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t v[32];
-            tmem_ld32(tO + c * 32, v);
-            tmem_ld_wait();
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(tO + c * 32, v);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-            tmem_st32(tO + c * 32, v);
-          }
-          tmem_st_wait();
-        };
-        if (!fixed && __any_sync(0xffffffffu, m_next > m_ref)) {
-          const float alpha = m_next > m_ref ? fast_exp2(m_ref - m_next) : 1.f;
-          if (j > 0) rescale_o(alpha);
-          l *= alpha;
-          m_ref = fmaxf(m_ref, m_next);
-        }
-        const bool full = __all_sync(0xffffffffu, lim >= 63 && low <= 0);
-        // every column visible, and (with a bias) none past the row's own position
-        const bool one_sign =
-            full && (!kBias || __all_sync(0xffffffffu, !valid || first_dist - t0 >= 63.f));
-        uint32_t pk[32];
-        float l_t = 0.f;
-        // 32 columns of scores, raw
-        auto load = [&](int h, uint32_t* v) {
-          tmem_ld32(tS + 32 * h, v);
-          tmem_ld_wait();
-        };
-        // brought to log2 units in place: any cap, any bias, masked
-        auto to_log2 = [&](int h, uint32_t* v) {
-          if constexpr (kCap) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              v[e] = __float_as_uint(capped(__uint_as_float(v[e]), p.cap_arg, p.cap_log2));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              v[e] = __float_as_uint(__uint_as_float(v[e]) * p.scale_log2);
-          }
-          if constexpr (kBias) {
-            const float d0 = first_dist - static_cast<float>(t0 + 32 * h);  // first column's
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              v[e] = __float_as_uint(
-                  fmaf(slope, fabsf(d0 - static_cast<float>(e)), __uint_as_float(v[e])));
-          }
-          if (!full) {
-            const int hi = lim - 32 * h, lo = low - 32 * h;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e > hi || e < lo) v[e] = __float_as_uint(-INFINITY);
-          }
-        };
-        // P of 32 columns against the reference, 16-bit pairs; the row sum adds the values the
-        // MMA sees, widened exactly. Where every column is visible, the cap's argument small
-        // and the distances of one sign, packed arithmetic takes the scores straight to the
-        // exponent; otherwise to_log2 first.
-        auto take = [&](int h) {
-          uint32_t v[32];
-          load(h, v);
-          const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-          const float2 nm2 = make_float2(neg_m, neg_m);
-          float2 lq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // four sums
-          auto raw = [&](int e) {
-            return make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-          };
-          auto put = [&](int e, float2 x) {
-            pk[16 * h + e / 2] = pack2<kBF16>(fast_exp2(x.x), fast_exp2(x.y));
-            add_pair_exact<kBF16>(lq[(e / 2) & 1], pk[16 * h + e / 2]);
-          };
-          bool fast = one_sign;
-          if constexpr (kCap) {
-            float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                a[k] = fmax3(a[k], fabsf(__uint_as_float(v[e + 2 * k])),
-                             fabsf(__uint_as_float(v[e + 2 * k + 1])));
-            const float y = fmax3(fmaxf(a[0], a[1]), a[2], a[3]) * p.cap_y;
-            fast = fast && __all_sync(0xffffffffu, y <= 0.5f);
-          }
-          if (fast) {
-            const float2 sl2x2 = make_float2(p.scale_log2, p.scale_log2);
-            const float2 cap_y2 = make_float2(p.cap_y, p.cap_y);
-            const float d0 = first_dist - static_cast<float>(t0 + 32 * h);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 c = nm2;
-              if constexpr (kBias) {
-                const float x = fmaf(slope, d0 - static_cast<float>(e), neg_m);
-                c = make_float2(x, x - slope);
-              }
-              put(e, kCap ? capped_poly2<4>(fmul2(raw(e), cap_y2), p.tanh4, c)
-                          : ffma2(raw(e), sl2x2, c));
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tmem_st32(tO + c * 32, v);
             }
-          } else {
-            to_log2(h, v);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) put(e, ffma2(raw(e), make_float2(1.f, 1.f), nm2));
-          }
-          l_t += (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
-        };
-        // P is taken against the row's reference without the tile's max; the max (and a move
-        // of the reference) is taken only when there is no reference yet, or when a half's
-        // sum shows that P outgrew its bound (S is whole until then), and P is taken again.
-        // Both warps see both sums and maxima, so they decide alike.
-        uint32_t top = 0;  // exponent of the larger of the row's half sums
-        bool redo = !fixed && __any_sync(0xffffffffu, m_ref == -INFINITY);
-        if (fixed) {
-          take(0);
-          take(1);
-        } else if (!redo) {
-          take(0);
-          take(1);
-          const uint32_t mine = __float_as_uint(l_t) >> 23;
-          if (!exchange8(mine, &top)) { ok = false; break; }
-          top = max(top, mine);
-          redo = __any_sync(0xffffffffu, top >= kSumExp<kBF16>);
-        }
-        if (redo) {
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[32];
-            load(h, v);
-            to_log2(h, v);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-          }
-          float other;
-          if (!exchange_float(mx, &other)) { ok = false; break; }
-          mx = fmaxf(mx, other);
-          // no reference yet, or a jump P could overflow on: move it now
-          const bool move = mx > m_ref + kMoveLog2<kBF16> || (m_ref == -INFINITY && mx != -INFINITY);
-          if (__any_sync(0xffffffffu, move)) {
-            const float alpha = move && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
+            tmem_st_wait();
+          };
+          if (__any_sync(0xffffffffu, m_next > m_ref)) {
+            const bool need = m_next > m_ref;
+            const float alpha = need ? fast_exp2(m_ref - m_next) : 1.f;
             if (j > 0) rescale_o(alpha);
             l *= alpha;
-            if (move) m_ref = mx;
+            if (need) m_ref = m_next;
           }
-          l_t = 0.f;
-          take(0);
-          take(1);
-          const uint32_t mine = __float_as_uint(l_t) >> 23;
-          if (!exchange8(mine, &top)) { ok = false; break; }
-          top = max(top, mine);
-        }
-        l += l_t;
-        // O is rescaled lazily: when a half's P summed to 2^8 or more, the reference moves up
-        // past log2 of that sum before the next tile (so that P stays at most 1 there)
-        m_next = top >= 127 + kRescaleExp ? m_ref + static_cast<float>(static_cast<int>(top) - 126)
-                                          : m_ref;
-        tmem_st16(tS, pk);
-        tmem_st16(tS + 16, pk + 16);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[grp]);
-      }
-      if (!ok) break;
-      // the row's sum, from both halves (in one order, so that both warps have the same)
-      float other;
-      if (!exchange_float(l, &other)) break;
-      l = half ? other + l : l + other;
-      const int ns_t = !valid ? 0 : kDirect ? 1 : __ldg(p.tok_ns + tok);
-      // epilogue: O / l of the warp's half of the columns to the output, or to the split
-      // partials
-      if (!wait(&bars->o_done[grp], act & 1)) break;
-      tc_fence_after();
-      const bool write = valid && w.split < ns_t;
-      const bool any = !(l == 0.f);  // a row without keys gives zeros, whatever O holds
-      const float inv = any ? 1.f / l : 0.f;
-      const float2 inv2 = make_float2(inv, inv);
-      uint16_t* dst = static_cast<uint16_t*>(p.out) +
-                      (static_cast<int64_t>(tok) * p.H_q + head) * D + (D / 2) * half;
-      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-      const int64_t pidx = kDirect || ns_t <= 1
-                               ? 0
-                               : static_cast<int64_t>(__ldg(p.tok_base + tok)) + w.split * p.H_q + head;
-      if (write && ns_t > 1 && half == 0)
-        p.part_lse[pidx] = any ? m_ref + __log2f(l) : -INFINITY;
+          // P = 2^(s*scale*log2e - m_ref) as 16-bit pairs written over S; half h of P lands
+          // on columns 32h..32h+31, which the loads of halves <= h have already read
+          const bool full = __all_sync(0xffffffffu, lim >= kKeys - 1 && low <= 0);
+          // l holds the earlier tiles' sum; this tile's halves are summed apart, so that a
+          // reference moved in half 1 can re-sum the half-0 P it re-rounds
+          float l_half0 = 0.f, l_h = 0.f;
 #pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t v[32];
-        tmem_ld32(tO + c * 32, v);
-        tmem_ld_wait();
-        if (!write) continue;
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[64];
+            tmem_ld32(tS + 64 * h, v);
+            tmem_ld32(tS + 64 * h + 32, v + 32);
+            tmem_ld_wait();
+            if (!full) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 x =
-              fmul2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), inv2);
-          v[e] = any ? __float_as_uint(x.x) : 0u;
-          v[e + 1] = any ? __float_as_uint(x.y) : 0u;
+              for (int e = 0; e < 64; ++e)
+                if (64 * h + e > lim || 64 * h + e < low) v[e] = __float_as_uint(-INFINITY);
+            }
+            // P is taken against the row's reference without the half's max; the max (and a move
+            // of the reference) is taken only when there is no reference yet, or when the half's
+            // sum shows that P outgrew its bound, and P is then taken again
+            bool with_max = __any_sync(0xffffffffu, m_ref == -INFINITY);
+            uint32_t pk[32];
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+              if (with_max) {
+                // four independent max chains
+                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    mq[k] = fmax3(mq[k], __uint_as_float(v[e + 2 * k]), __uint_as_float(v[e + 2 * k + 1]));
+                const float mx = fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]);
+                const float m_half = mx == -INFINITY ? mx : mx * p.scale_log2;
+                // no reference yet, or a jump P could overflow on: move the reference now,
+                // rescaling what is already taken against the old one
+                const bool move = m_half > m_ref + kMoveLog2<kBF16> ||
+                                  (m_ref == -INFINITY && m_half != -INFINITY);
+                if (__any_sync(0xffffffffu, move)) {
+                  const float alpha = move && m_ref != -INFINITY ? fast_exp2(m_ref - m_half) : 1.f;
+                  if (j > 0) rescale_o(alpha);
+                  l *= alpha;
+                  if (h == 1) {
+                    // the half of P already written (columns 0..31) is scaled and rounded
+                    // again; its sum is taken anew from the values the PV product will read
+                    uint32_t q[32];
+                    tmem_st_wait();
+                    tmem_ld32(tS, q);
+                    tmem_ld_wait();
+                    float2 lq0[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                      q[e] = scale_pair<kBF16>(q[e], alpha);
+                      add_pair_exact<kBF16>(lq0[e & 1], q[e]);
+                    }
+                    l_half0 = (lq0[0].x + lq0[0].y) + (lq0[1].x + lq0[1].y);
+                    tmem_st32(tS, q);
+                    tmem_st_wait();
+                  }
+                  if (move) m_ref = m_half;
+                }
+              }
+              const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+              float2 lq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // four sums
+              // scale and subtract two scores per packed fma; the row sum adds the 16-bit P
+              // values the MMA sees, widened exactly
+              const float2 sl2x2 = make_float2(p.scale_log2, p.scale_log2);
+              const float2 nm2 = make_float2(neg_m, neg_m);
+#pragma unroll
+              for (int e = 0; e < 64; e += 2) {
+                const float2 x = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                                       sl2x2, nm2);
+                pk[e / 2] = pack2<kBF16>(fast_exp2(x.x), fast_exp2(x.y));
+                add_pair_exact<kBF16>(lq[(e / 2) & 1], pk[e / 2]);
+              }
+              // P goes out before its sum is checked; a second pass writes it again
+              if (pass > 0) tmem_st_wait();
+              tmem_st16(tS + 32 * h, pk);
+              tmem_st16(tS + 32 * h + 16, pk + 16);
+              l_h = (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
+              if (with_max || __all_sync(0xffffffffu, l_h <= kHalfSumMax<kBF16>)) break;
+              with_max = true;
+            }
+            if (h == 0) l_half0 = l_h;
+            else l += l_half0 + l_h;
+          }
+          // O is rescaled lazily: when this tile's P summed to more than 2^8, the reference
+          // moves up by log2 of that sum before the next tile (the new reference is at least
+          // the row's max, so P stays at most 1 there)
+          const float l_tile = l_half0 + l_h;
+          m_next = l_tile > (1 << kRescaleExp) ? m_ref + __log2f(l_tile) : m_ref;
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[grp]);
         }
-        if (ns_t == 1) {
-          uint32_t o[16];
+        if (!ok) break;
+        // epilogue: O / l of this group's rows to the output, or to the split partials
+        if (!wait(&bars->o_done[grp], act & 1)) break;
+        tc_fence_after();
+        const bool write = valid && w.split < ns_t;
+        const bool any = !(l == 0.f);  // a row without keys gives zeros, whatever O holds
+        const float inv = any ? 1.f / l : 0.f;
+        if (__all_sync(0xffffffffu, !write || ns_t == 1)) {
+          // Direct output: each lane writes its own row, 64 columns (128 bytes) per TMEM
+          // wait, as 32-byte stores when the output is 32-byte aligned (16-byte stores
+          // otherwise), so every store instruction fills whole 32-byte sectors of 32 rows.
+          uint16_t* dst = static_cast<uint16_t*>(p.out) + (static_cast<int64_t>(tok) * p.H_q + head) * D;
+          const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+          const float2 inv2 = make_float2(inv, inv);
+#pragma unroll 1
+          for (int c4 = 0; c4 < D / 64; ++c4) {
+            uint32_t v[64];
+            tmem_ld32(tO + c4 * 64, v);
+            tmem_ld32(tO + c4 * 64 + 32, v + 32);
+            tmem_ld_wait();
+            uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            o[e] = pack2<kBF16>(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-          if (wide) {
+            for (int e = 0; e < 32; ++e) {
+              const float2 x =
+                  fmul2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), inv2);
+              w[e] = any ? pack2<kBF16>(x.x, x.y) : 0u;
+            }
+            if (write) {
+              if (wide) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) st_global_v8(dst + c * 32 + 16 * q, o + 8 * q);
-          } else {
-            uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
+                for (int q = 0; q < 4; ++q) st_global_v8(dst + c4 * 64 + 16 * q, w + 8 * q);
+              } else {
+                uint4* d4 = reinterpret_cast<uint4*>(dst + c4 * 64);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              d4[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                for (int q = 0; q < 8; ++q) d4[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+              }
+            }
           }
         } else {
-          uint4* d4 = reinterpret_cast<uint4*>(p.part_o + pidx * D + (D / 2) * half + c * 32);
+          // split partials (fp32), one row per lane
+#pragma unroll 1
+          for (int c2 = 0; c2 < D / 64; ++c2) {
+            uint32_t v[64];
+            tmem_ld32(tO + c2 * 64, v);
+            tmem_ld32(tO + c2 * 64 + 32, v + 32);
+            tmem_ld_wait();
+            if (!write) continue;
+            if (!any) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            d4[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+              for (int e = 0; e < 64; ++e) v[e] = 0u;
+            }
+            if (ns_t == 1) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                                    (static_cast<int64_t>(tok) * p.H_q + head) * D +
+                                                    c2 * 64);
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                dst[q] = make_uint4(
+                    pack2<kBF16>(__uint_as_float(v[8 * q + 0]) * inv, __uint_as_float(v[8 * q + 1]) * inv),
+                    pack2<kBF16>(__uint_as_float(v[8 * q + 2]) * inv, __uint_as_float(v[8 * q + 3]) * inv),
+                    pack2<kBF16>(__uint_as_float(v[8 * q + 4]) * inv, __uint_as_float(v[8 * q + 5]) * inv),
+                    pack2<kBF16>(__uint_as_float(v[8 * q + 6]) * inv, __uint_as_float(v[8 * q + 7]) * inv));
+            } else {
+              const int64_t pidx = static_cast<int64_t>(tok_part) + w.split * p.H_q + head;
+              float4* dst = reinterpret_cast<float4*>(p.part_o + pidx * D + c2 * 64);
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                dst[q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
+                                     __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+              if (c2 == 0) p.part_lse[pidx] = any ? m_ref + __log2f(l) : -INFINITY;
+            }
+          }
         }
+        ++act;
       }
-      ++act;
+    } else {
+      // ---- a cap or a bias: two warps for 32 rows, a half of the columns each
+      const int grp = (warp - 4) >> 3;        // 0: query tile A, 1: query tile B
+      const int half = ((warp - 4) >> 2) & 1; // columns 64 * half .. + 63 of each key tile
+      const int quarter = warp & 3;           // TMEM lanes 32*quarter .. +31
+      const int r = quarter * 32 + lane;
+      const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t tS = trow + col_s(grp) + 64 * half;            // P over its first 32 columns
+      const uint32_t tO = trow + col_o(grp) + (D / 2) * half;       // the half of O it keeps
+      // What the two warps of the same rows tell one another goes through 128 bytes of shared
+      // memory and a barrier of the two (bounded, like every wait). A slot may be written once
+      // the other warp has read what it held: before a tile's first exchange both warps' P of
+      // the tile before has arrived, and with it their reads; otherwise a meeting lies between.
+      uint64_t* pair_bar = &bars->pair[grp * 4 + quarter];
+      uint8_t* slots = smem + L::kOffPair + (grp * 4 + quarter) * 128;
+      const int own_slot = half * 32 + lane, other_slot = own_slot ^ 32;
+      uint32_t px = 0;  // barrier phases so far
+      auto meet = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pair_bar);
+        return wait(pair_bar, px++ & 1);
+      };
+      auto exchange8 = [&](uint32_t mine, uint32_t* theirs) -> bool {
+        slots[own_slot] = static_cast<uint8_t>(mine);
+        if (!meet()) return false;
+        *theirs = slots[other_slot];
+        return true;
+      };
+      auto exchange16 = [&](uint32_t mine, uint32_t* theirs) -> bool {
+        slots[own_slot] = static_cast<uint8_t>(mine);
+        slots[64 + own_slot] = static_cast<uint8_t>(mine >> 8);
+        if (!meet()) return false;
+        *theirs = slots[other_slot] | static_cast<uint32_t>(slots[64 + other_slot]) << 8;
+        return meet();
+      };
+      // a float, in two halves
+      auto exchange_float = [&](float mine, float* theirs) -> bool {
+        uint32_t hi, lo;
+        if (!exchange16(__float_as_uint(mine) >> 16, &hi) ||
+            !exchange16(__float_as_uint(mine) & 0xffffu, &lo))
+          return false;
+        *theirs = __uint_as_float(hi << 16 | lo);
+        return true;
+      };
+      // The larger of the row's two maxima, rounded up to a whole number of log2 units (as a
+      // reference it need not be exact): 16 bits, or a float's exchange if some row's is out of
+      // their range.
+      auto row_max = [&](float* mx) -> bool {
+        constexpr int kNone = -32768, kFar = 32767;
+        const float up = ceilf(*mx);
+        const int q = *mx == -INFINITY ? kNone : fabsf(up) < 32767.f ? static_cast<int>(up) : kFar;
+        uint32_t got;
+        if (!exchange16(static_cast<uint32_t>(q), &got)) return false;
+        const int o = static_cast<int16_t>(got);
+        if (__any_sync(0xffffffffu, q == kFar || o == kFar)) {
+          float other;
+          if (!exchange_float(*mx, &other)) return false;
+          *mx = fmaxf(*mx, other);
+          return true;
+        }
+        const int m = max(q, o);
+        *mx = m == kNone ? -INFINITY : static_cast<float>(m);
+        return true;
+      };
+      // Capped scores lie within cap_log2 of 0. Against a fixed reference of cap_log2 - 60 (0 at
+      // least) every P is below 2^60 and, up to kFixedCapLog2, at least 2^-120: within bf16's
+      // normal range and, summed, within fp32's. Then no maximum is taken, nothing moves, and
+      // the two warps of a row have nothing to tell one another before the end.
+      const bool fixed = kCap && !kBias && kBF16 && p.cap_log2 <= kFixedCapLog2;
+      const float m_fixed = fixed ? fmaxf(p.cap_log2 - 60.f, 0.f) : -INFINITY;
+      uint32_t sc = 0, act = 0;
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        const int idx = next_item(it);
+        if (idx < 0) break;
+        const WorkItem& w = items[it % (2 * kItemRing)];
+        const int pb = w.page_begin, pe = w.page_end;
+        if (pe <= pb || !tile_item_ok(w, p)) continue;
+        const int nt = (pe - pb + kPagesPerTile - 1) / kPagesPerTile;
+        const int nrows = grp == 0 ? w.nrows : w.pad[0];
+        if (nrows == 0) continue;  // no query tile B in this item
+        // this thread's query row
+        const bool valid = r < nrows;
+        const int R = w.row0 + grp * p.tpt * p.G + r;  // packed row within the sequence
+        const int qtok = R / p.G;                        // query index within the sequence
+        const int tok = w.tok0 + qtok;
+        const int head = w.kv * p.G + R - qtok * p.G;
+        const int pos = valid ? w.ctx_len - w.n_query + qtok : -1;
+        // the row's keys within the item, [key_lo, key_hi], relative to the warp's columns (a
+        // row past the tile's rows is computed unmasked and not written)
+        const int col0 = pb * kBlockSize + 64 * half;
+        const int key_hi =
+            valid ? min(max(pos, w.pad[3] - 1), pe * kBlockSize - 1) - col0 : (1 << 30);
+        const int key_lo = valid ? p.row_lo(tok, pos) - col0 : -(1 << 30);
+        const float slope = kBias && valid ? -kLog2e * __ldg(p.slopes + head) : 0.f;
+        const float first_dist = static_cast<float>(pos - col0);  // of the item's first column
+        // m_ref: the reference max (log2 units) that P, O and l are currently taken against;
+        // m_next: the reference from the next tile on, when this one's P summed to over 2^8
+        float m_ref = m_fixed, m_next = m_fixed, l = 0.f;
+        for (int j = 0; j < nt; ++j) {
+          const int t0 = tile_at(j, nt) * kKeys;  // the tile's first key, from the item's
+          const int lim = key_hi - t0, low = key_lo - t0;  // visible: low <= c <= lim
+          if (!wait(&bars->s_full[grp], sc & 1)) { ok = false; break; }
+          ++sc;
+          tc_fence_after();
+          // This group's previous PV has completed (this S was issued after it): O is stable.
+          // Each of the two warps keeps a half of its columns.
+          auto rescale_o = [&](float alpha) {
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t v[32];
+              tmem_ld32(tO + c * 32, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tmem_st32(tO + c * 32, v);
+            }
+            tmem_st_wait();
+          };
+          if (!fixed && __any_sync(0xffffffffu, m_next > m_ref)) {
+            const float alpha = m_next > m_ref ? fast_exp2(m_ref - m_next) : 1.f;
+            if (j > 0) rescale_o(alpha);
+            l *= alpha;
+            m_ref = fmaxf(m_ref, m_next);
+          }
+          const bool full = __all_sync(0xffffffffu, lim >= 63 && low <= 0);
+          // every column visible, and (with a bias) none past the row's own position
+          const bool one_sign =
+              full && (!kBias || __all_sync(0xffffffffu, !valid || first_dist - t0 >= 63.f));
+          uint32_t pk[32];
+          float l_t = 0.f;
+          // 32 columns of scores, raw
+          auto load = [&](int h, uint32_t* v) {
+            tmem_ld32(tS + 32 * h, v);
+            tmem_ld_wait();
+          };
+          // brought to log2 units in place: any cap, any bias, masked
+          auto to_log2 = [&](int h, uint32_t* v) {
+            if constexpr (kCap) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                v[e] = __float_as_uint(capped(__uint_as_float(v[e]), p.cap_arg, p.cap_log2));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                v[e] = __float_as_uint(__uint_as_float(v[e]) * p.scale_log2);
+            }
+            if constexpr (kBias) {
+              const float d0 = first_dist - static_cast<float>(t0 + 32 * h);  // first column's
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                v[e] = __float_as_uint(
+                    fmaf(slope, fabsf(d0 - static_cast<float>(e)), __uint_as_float(v[e])));
+            }
+            if (!full) {
+              const int hi = lim - 32 * h, lo = low - 32 * h;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e > hi || e < lo) v[e] = __float_as_uint(-INFINITY);
+            }
+          };
+          // P of 32 columns against the reference, 16-bit pairs; the row sum adds the values the
+          // MMA sees, widened exactly. Where every column is visible, the cap's argument small
+          // and the distances of one sign, packed arithmetic takes the scores straight to the
+          // exponent; otherwise to_log2 first.
+          auto take = [&](int h) {
+            uint32_t v[32];
+            load(h, v);
+            const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+            const float2 nm2 = make_float2(neg_m, neg_m);
+            float2 lq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // four sums
+            auto raw = [&](int e) {
+              return make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            };
+            auto put = [&](int e, float2 x) {
+              pk[16 * h + e / 2] = pack2<kBF16>(fast_exp2(x.x), fast_exp2(x.y));
+              add_pair_exact<kBF16>(lq[(e / 2) & 1], pk[16 * h + e / 2]);
+            };
+            bool fast = one_sign;
+            if constexpr (kCap) {
+              float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  a[k] = fmax3(a[k], fabsf(__uint_as_float(v[e + 2 * k])),
+                               fabsf(__uint_as_float(v[e + 2 * k + 1])));
+              const float y = fmax3(fmaxf(a[0], a[1]), a[2], a[3]) * p.cap_y;
+              fast = fast && __all_sync(0xffffffffu, y <= 0.5f);
+            }
+            if (fast) {
+              const float2 sl2x2 = make_float2(p.scale_log2, p.scale_log2);
+              const float2 cap_y2 = make_float2(p.cap_y, p.cap_y);
+              const float d0 = first_dist - static_cast<float>(t0 + 32 * h);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float2 c = nm2;
+                if constexpr (kBias) {
+                  const float x = fmaf(slope, d0 - static_cast<float>(e), neg_m);
+                  c = make_float2(x, x - slope);
+                }
+                put(e, kCap ? capped_poly2<4>(fmul2(raw(e), cap_y2), p.tanh4, c)
+                            : ffma2(raw(e), sl2x2, c));
+              }
+            } else {
+              to_log2(h, v);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) put(e, ffma2(raw(e), make_float2(1.f, 1.f), nm2));
+            }
+            l_t += (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
+          };
+          // P is taken against the row's reference without the tile's max; the max (and a move
+          // of the reference) is taken only when there is no reference yet, or when a half's
+          // sum shows that P outgrew its bound (S is whole until then), and P is taken again.
+          // Both warps see both sums and maxima, so they decide alike.
+          uint32_t top = 0;  // exponent of the larger of the row's half sums
+          // (a row without a reference asks for one only once it sees a key: lim and low are
+          // those of the warp's half of the tile)
+          const bool sees = lim + 64 * half >= 0 && low + 64 * half <= kKeys - 1;
+          bool redo = !fixed && __any_sync(0xffffffffu, m_ref == -INFINITY && sees);
+          if (fixed) {
+            take(0);
+            take(1);
+          } else if (!redo) {
+            take(0);
+            take(1);
+            const uint32_t mine = __float_as_uint(l_t) >> 23;
+            if (!exchange8(mine, &top)) { ok = false; break; }
+            top = max(top, mine);
+            redo = __any_sync(0xffffffffu, top >= kSumExp<kBF16>);
+            if (redo && !meet()) { ok = false; break; }  // the slots have been read
+          }
+          if (redo) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[32];
+              load(h, v);
+              to_log2(h, v);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            }
+            if (!row_max(&mx)) { ok = false; break; }
+            // no reference yet, or a jump P could overflow on: move it now
+            const bool move = mx > m_ref + kMoveLog2<kBF16> || (m_ref == -INFINITY && mx != -INFINITY);
+            if (__any_sync(0xffffffffu, move)) {
+              const float alpha = move && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
+              if (j > 0) rescale_o(alpha);
+              l *= alpha;
+              if (move) m_ref = mx;
+            }
+            l_t = 0.f;
+            take(0);
+            take(1);
+            const uint32_t mine = __float_as_uint(l_t) >> 23;
+            if (!exchange8(mine, &top)) { ok = false; break; }
+            top = max(top, mine);
+          }
+          l += l_t;
+          // O is rescaled lazily: when a half's P summed to 2^8 or more, the reference moves up
+          // past log2 of that sum before the next tile (so that P stays at most 1 there)
+          m_next = top >= 127 + kRescaleExp ? m_ref + static_cast<float>(static_cast<int>(top) - 126)
+                                            : m_ref;
+          tmem_st16(tS, pk);
+          tmem_st16(tS + 16, pk + 16);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[grp]);
+        }
+        if (!ok) break;
+        const int ns_t = !valid ? 0 : kDirect ? 1 : __ldg(p.tok_ns + tok);
+        // epilogue: O / l of the warp's half of the columns to the output, or to the split
+        // partials
+        if (!wait(&bars->o_done[grp], act & 1)) break;
+        tc_fence_after();
+        // the row's sum, from both halves (in one order, so that both warps have the same)
+        float other;
+        if (!exchange_float(l, &other)) break;
+        l = half ? other + l : l + other;
+        const bool write = valid && w.split < ns_t;
+        const bool any = !(l == 0.f);  // a row without keys gives zeros, whatever O holds
+        const float inv = any ? 1.f / l : 0.f;
+        const float2 inv2 = make_float2(inv, inv);
+        uint16_t* dst = static_cast<uint16_t*>(p.out) +
+                        (static_cast<int64_t>(tok) * p.H_q + head) * D + (D / 2) * half;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+        const int64_t pidx = kDirect || ns_t <= 1
+                                 ? 0
+                                 : static_cast<int64_t>(__ldg(p.tok_base + tok)) + w.split * p.H_q + head;
+        if (write && ns_t > 1 && half == 0)
+          p.part_lse[pidx] = any ? m_ref + __log2f(l) : -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tO + c * 32, v);
+          tmem_ld_wait();
+          if (!write) continue;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x =
+                fmul2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), inv2);
+            v[e] = any ? __float_as_uint(x.x) : 0u;
+            v[e + 1] = any ? __float_as_uint(x.y) : 0u;
+          }
+          if (ns_t == 1) {
+            uint32_t o[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              o[e] = pack2<kBF16>(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+            if (wide) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) st_global_v8(dst + c * 32 + 16 * q, o + 8 * q);
+            } else {
+              uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                d4[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
+          } else {
+            uint4* d4 = reinterpret_cast<uint4*>(p.part_o + pidx * D + (D / 2) * half + c * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              d4[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          }
+        }
+        ++act;
+      }
     }
   }
   tc_fence_before();
@@ -873,7 +1148,7 @@ static cudaError_t launch_masked_tile_t(const MaskedAttnParams& p, const CUtenso
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_limit(kern, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(ctas), dim3(kThreads), smem, stream, true, kmap, vmap, qmap, p);
+  return launch_kernel(kern, dim3(ctas), dim3(kThreads<(kCap || kBias)>), smem, stream, true, kmap, vmap, qmap, p);
 }
 
 // The instantiations of one (cap, bias) pair: one per type, head size and mode.
