@@ -863,7 +863,6 @@ int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_p
   p.cap_arg = softcap > 0.f ? static_cast<float>(2.0 * log2e * scale / softcap) : 0.f;
   p.cap_y = softcap > 0.f ? scale / softcap : 0.f;
   for (int i = 0; i < 4; ++i) p.tanh4[i] = ps::kTanh4[i] * p.cap_log2;
-  for (int i = 0; i < 6; ++i) p.tanh6[i] = ps::kTanh6[i] * p.cap_log2;
   // (a scale or cap at the ends of the range)
   if (!std::isfinite(p.scale_log2) || !std::isfinite(p.cap_log2) || !std::isfinite(p.cap_arg))
     return PS_ERR_ARG;

@@ -72,7 +72,7 @@ struct MaskedAttnParams : AttnParams {
   float cap_log2;         // cap * log2(e); 0: scores are not capped
   float cap_arg;          // 2 * log2(e) * scale / cap (the tanh's exponent per raw score)
   float cap_y;            // scale / cap (its argument per raw score)
-  float tanh4[4], tanh6[6];  // the cap's polynomials times cap_log2 (see capped_poly2)
+  float tanh4[4];         // the cap's polynomial times cap_log2 (see capped_poly2)
   const float* slopes;    // [H_q] slope of the distance bias, or null
   int window;             // keys a row sees, its own included; 0: all before it
   const int32_t* prefix;  // [B] or null

@@ -1,4 +1,5 @@
-// What the masked attention kernels share: the capped score.
+// What the masked attention kernels share: the capped score, with and without special
+// functions.
 #pragma once
 
 #include "ps_common.cuh"
@@ -17,22 +18,17 @@ __device__ __forceinline__ float capped(float raw, float arg, float cap_log2) {
 }
 
 // cap * log2(e) * tanh(y) + c on two scores y = raw * scale / cap of small size, without
-// special functions: y P(y^2) cap log2(e), P fitted to tanh(y) / y in the largest relative
-// error. kTerms = 4: |y| <= 1/2 within 2^-20.7; kTerms = 6: |y| <= 1 within 2^-20.6 (a cap
-// of 50 is 72 in log2 units: 2^-14.5 on the largest score). `k` holds P's coefficients
-// times cap * log2(e), highest first.
-template <int kTerms>
+// special functions: y P(y^2) cap log2(e), P fitted to tanh(y) / y over |y| <= 1/2 within
+// 2^-20.7 relative (a cap of 50 is 72 in log2 units: 2^-15.6 on the largest such score). `k`
+// holds P's coefficients times cap * log2(e), highest first.
 __device__ __forceinline__ float2 capped_poly2(float2 y, const float* k, float2 c) {
   const float2 t = fmul2(y, y);
   float2 q = ffma2(t, make_float2(k[0], k[0]), make_float2(k[1], k[1]));
-#pragma unroll
-  for (int i = 2; i < kTerms; ++i) q = ffma2(q, t, make_float2(k[i], k[i]));
+  q = ffma2(q, t, make_float2(k[2], k[2]));
+  q = ffma2(q, t, make_float2(k[3], k[3]));
   return ffma2(y, q, c);
 }
 constexpr float kTanh4[4] = {-0.04440223425626755f, 0.13190299272537231f,
                                         -0.33326318860054016f, 0.999999463558197f};
-constexpr float kTanh6[6] = {-0.003067068289965391f, 0.016743160784244537f,
-                                        -0.051605746150016785f, 0.13281437754631042f,
-                                        -0.3332904279232025f,   0.9999994039535522f};
 
 }  // namespace ps

@@ -64,11 +64,14 @@ __device__ __forceinline__ void turn_unit(uint4& a, uint4& b, const float* c, co
   }
 }
 
-// A CTA takes a contiguous range of passes of `ppt` tokens; a pass's rows are its tokens'
-// H_q query, H_kv key and H_kv value rows, D/16 units each.
+// A CTA takes an equal share of the tokens (one wave, to a token), in equal passes of at most
+// kMaxPassTokens; a pass's rows are its tokens' H_q query, H_kv key and H_kv value rows, D/16
+// units each. (Whole passes of 8 tokens dealt to the CTAs left some with half as many again:
+// 8192 tokens of 32 + 8 + 8 heads took 36.6 us, equal
+// shares take 34.2: 5.9 TB/s.)
 template <bool kBF16, int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    rotary_kernel(const RotaryParams p, int ppt) {
+    rotary_kernel(const RotaryParams p) {
   constexpr int kRowUnits = D / 16, kRowsPerRound = kThreads / kRowUnits;
   __shared__ unsigned long long turns[D / 2];
   __shared__ float cs[2][kMaxPassTokens][D / 2], sn[2][kMaxPassTokens][D / 2];
@@ -78,19 +81,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const double t = p.inv_freq[i] * kInvTwoPi;
     turns[i] = __double2ull_rn((t - floor(t)) * kTwoTo64);
   }
-  const int heads = p.H_q + 2 * p.H_kv, rows = ppt * heads;
+  const int heads = p.H_q + 2 * p.H_kv;
   const int un = threadIdx.x % kRowUnits, row0 = threadIdx.x / kRowUnits;
   const bool rotates = un < rot_units;
   const int ca = rotates && !kInter ? un : 2 * un;
   const int cb = rotates && !kInter ? un + rot_units : 2 * un + 1;
-  const int passes = (p.T + ppt - 1) / ppt;
-  const int p_lo = static_cast<int>(static_cast<int64_t>(passes) * blockIdx.x / gridDim.x);
-  const int p_hi = static_cast<int>(static_cast<int64_t>(passes) * (blockIdx.x + 1) / gridDim.x);
+  const int t_lo = static_cast<int>(static_cast<int64_t>(p.T) * blockIdx.x / gridDim.x);
+  const int t_hi = static_cast<int>(static_cast<int64_t>(p.T) * (blockIdx.x + 1) / gridDim.x);
+  const int passes = (t_hi - t_lo + kMaxPassTokens - 1) / kMaxPassTokens;
+  const int ppt = passes > 0 ? (t_hi - t_lo + passes - 1) / passes : 0;  // tokens of a pass
+  const int rows = ppt * heads;
   const bool in_place = p.q_out == p.q;
   __syncthreads();
   int buf = 0;
-  for (int pass = p_lo; pass < p_hi; ++pass, buf ^= 1) {
-    const int t0 = pass * ppt;
+  for (int t0 = t_lo; t0 < t_hi; t0 += ppt, buf ^= 1) {
     for (int r0 = 0; r0 < rows; r0 += kUnits * kRowsPerRound) {
       uint4 a[kUnits], b[kUnits];
       uint4* dst[kUnits];
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int row = r0 + row0 + j * kRowsPerRound;
         const int u = row / heads, head = row - u * heads, t = t0 + u;
         kind[j] = -1;
-        if (row >= rows || t >= p.T) continue;
+        if (row >= rows || t >= t_hi) continue;
         const uint4* src;
         if (head < p.H_q) {
           if (in_place && !rotates) continue;
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (r0 == 0) {
         for (int x = threadIdx.x; x < ppt * half; x += kThreads) {
           const int u = x / half, i = x - u * half, t = t0 + u;
-          if (t >= p.T) continue;
+          if (t >= t_hi) continue;
           const unsigned long long ph =
               static_cast<unsigned long long>(static_cast<long long>(p.pos[t])) * turns[i];
           float s, c;
@@ -158,16 +162,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 template <bool kBF16, int D>
 cudaError_t launch_t(const RotaryParams& p, bool inter, int num_sms, cudaStream_t stream) {
-  // few tokens: fewer per pass, so that they spread over the SMs
   const int ctas = num_sms * kCtasPerSm;
-  int ppt = (p.T + ctas - 1) / ctas;
-  ppt = ppt > kMaxPassTokens ? kMaxPassTokens : ppt;
-  const int passes = (p.T + ppt - 1) / ppt;
-  const dim3 grid(static_cast<unsigned>(passes < ctas ? passes : ctas));
+  const dim3 grid(static_cast<unsigned>(p.T < ctas ? p.T : ctas));
   return inter ? launch_kernel(rotary_kernel<kBF16, D, true>, grid, dim3(kThreads), 0, stream,
-                               true, p, ppt)
+                               true, p)
                : launch_kernel(rotary_kernel<kBF16, D, false>, grid, dim3(kThreads), 0, stream,
-                               true, p, ppt);
+                               true, p);
 }
 
 }  // namespace
