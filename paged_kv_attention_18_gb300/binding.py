@@ -1,5 +1,9 @@
 """Python binding of the C ABI: argument marshalling from torch tensors, nothing else.
 
+The calls that a decode loop makes for every layer and token (rotary_reshape_and_cache,
+masked_paged_attention, beam_select, fork_sequences) do their checks and the C call in a
+compiled module (csrc/py_native.cpp); the others go through ctypes. Either way:
+
 Every function checks that its tensors live on the current CUDA device, are
 contiguous and have the expected dtypes and shapes, passes their addresses and the
 current stream to the matching ``ps_*`` entry point of include/pagedserve.h, and
@@ -245,7 +249,8 @@ def beam_select(logits, scores, n_select: int, finished=None, pad_token: int = 0
     [B, W], finished uint8 or bool [B, W] or None. Returns (parents, tokens, scores), each
     [B, n_select]."""
     parents = tokens = best = None
-    if stream is not None and isinstance(logits, torch.Tensor) and logits.is_cuda and n_select > 0:
+    if stream is not None and isinstance(logits, torch.Tensor) and logits.is_cuda and \
+            logits.dim() == 3 and n_select > 0:
         # memory for a stream that is not the current one comes from that stream
         shape, dev = (logits.shape[0], n_select), logits.device
         parents, tokens, best = (_alloc(shape, t, dev, stream)
@@ -319,7 +324,9 @@ def masked_paged_attention(q, k_pool, v_pool, block_tables, seq_lens, query_star
         # memory for a stream that is not the current one comes from that stream
         if out is None:
             out = _alloc(q.shape, q.dtype, q.device, stream)
-        if workspace is None and q.dim() == 3 and k_pool.dim() == 4:
+        if workspace is None and q.dim() == 3 and isinstance(k_pool, torch.Tensor) and \
+                k_pool.dim() == 4 and isinstance(block_tables, torch.Tensor) and \
+                block_tables.dim() == 2:
             B, width = block_tables.shape
             msl = max_seq_len if max_seq_len is not None else width * BLOCK_SIZE
             n = workspace_size(q.shape[0], B, q.shape[1], k_pool.shape[2], q.shape[2], msl)

@@ -422,8 +422,8 @@ int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const v
   const int split_grid = split_ctas(p, num_sms);
   {
     Timed tm(2, s);
-    if ((e = launch_plan_masked(p, split_grid * attention_warps(p.D), num_sms, num_sms, s)) !=
-        cudaSuccess)
+    const int workers = split_grid * masked_split_warps(p.D, p.group_rows == 8);
+    if ((e = launch_plan_masked(p, workers, num_sms, num_sms, s)) != cudaSuccess)
       return cuda_fail(e, "masked plan kernel");
   }
   if (!p.all_tiles) {

@@ -27,11 +27,14 @@ namespace ps {
 
 namespace {
 
-constexpr int kWarps = 8;  // per CTA, one CTA per SM
-
-template <int D>
+// One CTA per SM. Items of 8 rows of 64 elements are light on registers: 16 warps with three
+// pages each in flight hide their dependent steps better than 8 with six (contexts to 8191,
+// 16 heads of 64 elements, each its own: 285 us with 8 warps, 272 with 16). Items of 128
+// elements take 166 registers, and 12 warps with two pages each gained nothing.
+template <int D, bool kNarrow>
 struct MaskedSplit {
-  static constexpr int kStages = D == 128 ? 3 : 6;    // pages in flight per warp
+  static constexpr int kWarps = masked_split_warps(D, kNarrow);
+  static constexpr int kStages = (D == 128 ? 24 : 48) / kWarps;  // pages in flight per warp
   static constexpr int kRing = kStages + 2;           // item records
   static constexpr int kPage = kBlockSize * D * 2;    // one page of K (or V), one head
   static constexpr int kStage = 2 * kPage;
@@ -51,10 +54,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // the head's elements as the MMA's 16 rows and the item's 8 rows as its 8 columns: half the
 // MMAs, scores and accumulators of a 16-row item whose upper half would be empty.
 template <bool kBF16, int D, bool kDirect, bool kNarrow>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
     masked_split_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const MaskedAttnParams p) {
-  using C = MaskedSplit<D>;
+  using C = MaskedSplit<D, kNarrow>;
+  constexpr int kWarps = C::kWarps;
   constexpr int S = C::kStages, kRing = C::kRing, kPage = C::kPage, kStage = C::kStage;
   constexpr int kBoxes = D / 64, kKSteps = D / 16;
 
@@ -631,12 +635,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 template <bool kBF16, int D, bool kDirect, bool kNarrow>
 cudaError_t launch_t(const MaskedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                      int ctas, cudaStream_t stream, bool pdl) {
-  constexpr int smem = MaskedSplit<D>::kSmem;
+  using C = MaskedSplit<D, kNarrow>;
+  constexpr int smem = C::kSmem;
   auto kern = masked_split_kernel<kBF16, D, kDirect, kNarrow>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_limit(kern, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(ctas), dim3(kWarps * 32), smem, stream, pdl, kmap, vmap, p);
+  return launch_kernel(kern, dim3(ctas), dim3(C::kWarps * 32), smem, stream, pdl, kmap, vmap, p);
 }
 
 template <bool kDirect, bool kNarrow>

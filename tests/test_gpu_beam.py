@@ -9,9 +9,10 @@ from tests import operator_ref as R
 
 pytestmark = pytest.mark.gpu
 
-# lse: ex2 is off by 2^-22, each of a thread's at most 24 adds in turn (chunks of up to 12288
-# logits at these sizes), of the 13 joins across the threads and of the log by 2^-24, so lse
-# by less than 2^-18
+# lse: ex2 is off by 2^-22 and the exponent's argument, a fused multiply-add, by half a step of
+# at most 2^6 for terms that weigh; each of a thread's at most 40 adds in turn (chunks of up
+# to 40960 logits at these sizes, four sums), of the 13 joins across the threads and of the log
+# by 2^-24: (4 + 4 + 40 + 13 + 1) 2^-24 < 2^-18
 LSE_TOL = 2.0 ** -18
 
 
@@ -35,7 +36,8 @@ def check(logits, scores, n, got, finished=None, pad=0):
 @pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("B,W,V,n", [
     (1, 1, 1, 1), (1, 1, 5, 8), (2, 4, 1003, 4), (3, 3, 8191, 6), (2, 2, 8192, 2),
-    (1, 5, 8193, 32), (4, 4, 50001, 8), (2, 32, 700, 32), (1, 2, 151936, 4), (70, 1, 333, 1), (64, 4, 50001, 8)])
+    (1, 5, 8193, 32), (4, 4, 50001, 8), (2, 32, 700, 32), (1, 2, 151936, 4), (70, 1, 333, 1), (64, 4, 50001, 8),
+    (700, 1, 333, 2), (160, 4, 70001, 8)])
 def test_selection(B, W, V, n, dt):
     g = torch.Generator("cuda").manual_seed(B * 7 + V)
     logits = (torch.randn(B, W, V, generator=g, device="cuda") * 3).to(dt)
@@ -96,6 +98,16 @@ def test_ties_go_to_the_lowest_index(V):
     par, tok, _ = binding.beam_select(logits, scores, n)
     want = [(w, t) for w in range(W) for t in range(5, V, 7)][:n]
     assert [(int(a), int(b)) for a, b in zip(par[1], tok[1])] == want
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.float32])
+def test_logits_in_order(dt):
+    # rising and falling along the vocabulary, in steps that the type can tell apart or not
+    V, n = 40000, 8
+    for x in (torch.arange(V) / 500.0, -torch.arange(V) / 500.0, torch.arange(V) // 1000 * 1.0):
+        logits = x.to(dt).cuda().expand(2, 2, V).contiguous()
+        scores = torch.tensor([[-1.0, -0.5], [0.0, 0.0]], device="cuda")
+        check(logits, scores, n, binding.beam_select(logits, scores, n))
 
 
 def test_identical_beams_and_one_workspace_twice():

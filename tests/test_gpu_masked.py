@@ -259,6 +259,24 @@ def test_one_workspace_two_calls_and_other_stream():
     b.check(out)
 
 
+def test_two_streams_at_once_with_a_workspace_each():
+    batches = [Batch(LONG, 12, 2, 128, torch.bfloat16, 22, window=3000, softcap=20.0, std=3.0),
+               Batch(CHUNKS, 12, 2, 128, torch.bfloat16, 23, slopes=slopes_of(12))]
+    want = [b.run() for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    outs = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for i, b in enumerate(batches):
+            outs[i].append(binding.masked_paged_attention(
+                b.q, b.k, b.v, b.bt, b.sl, b.qs, b.scale, stream=streams[i], **b.kwargs()))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert torch.equal(o, want[i])
+
+
 def test_a_small_workspace_splits_less():
     b = Batch([(20000, 1), (7000, 1)], 12, 2, 128, torch.bfloat16, 14, softcap=20.0, std=3.0)
     ws = binding.alloc_workspace(2, 2, 12, 2, 128, 0)
