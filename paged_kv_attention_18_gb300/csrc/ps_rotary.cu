@@ -92,19 +92,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const int ppt = passes > 0 ? (t_hi - t_lo + passes - 1) / passes : 0;  // tokens of a pass
   const int rows = ppt * heads;
   const bool in_place = p.q_out == p.q;
+  // (token of the pass, head) of the thread's first row, and what the next one adds to it
+  const int u_first = row0 / heads, head_first = row0 - u_first * heads;
+  const int u_step = kRowsPerRound / heads, head_step = kRowsPerRound - u_step * heads;
   __syncthreads();
   int buf = 0;
   for (int t0 = t_lo; t0 < t_hi; t0 += ppt, buf ^= 1) {
+    int u = u_first, head = head_first;
     for (int r0 = 0; r0 < rows; r0 += kUnits * kRowsPerRound) {
       uint4 a[kUnits], b[kUnits];
       uint4* dst[kUnits];
       int kind[kUnits];  // -1: nothing to do; 0: copied as it is; 1 + token of the pass: turned
 #pragma unroll
-      for (int j = 0; j < kUnits; ++j) {
-        const int row = r0 + row0 + j * kRowsPerRound;
-        const int u = row / heads, head = row - u * heads, t = t0 + u;
+      for (int j = 0; j < kUnits; ++j, u += u_step, head += head_step) {
+        if (head >= heads) {
+          head -= heads;
+          ++u;
+        }
+        const int t = t0 + u;
         kind[j] = -1;
-        if (row >= rows || t >= t_hi) continue;
+        if (u >= ppt || t >= t_hi) continue;
         const uint4* src;
         if (head < p.H_q) {
           if (in_place && !rotates) continue;
@@ -132,14 +139,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       if (r0 == 0) {
         for (int x = threadIdx.x; x < ppt * half; x += kThreads) {
-          const int u = x / half, i = x - u * half, t = t0 + u;
+          const int ux = x / half, i = x - ux * half, t = t0 + ux;
           if (t >= t_hi) continue;
           const unsigned long long ph =
               static_cast<unsigned long long>(static_cast<long long>(p.pos[t])) * turns[i];
           float s, c;
           sincosf(static_cast<float>(static_cast<int32_t>(ph >> 32)) * kTurnToRad, &s, &c);
-          cs[buf][u][i] = c * p.magnitude;
-          sn[buf][u][i] = s * p.magnitude;
+          cs[buf][ux][i] = c * p.magnitude;
+          sn[buf][ux][i] = s * p.magnitude;
         }
         __syncthreads();
       }
