@@ -12,8 +12,8 @@
 // thread for a query row or two (kSoftmaxWarps).
 // Bound: a group's chain S -> softmax -> PV -> next S (S overwrites P, so they cannot
 // overlap), the two groups filling each other's gaps. 4 x 2048 tokens over 8192 keys, 32/8
-// heads, D 128, 566 GFLOP: masks alone 485 us (1.17 PFLOP/s,
-// 0.60 of the measured burst peak), capped 583 (bf16) and 638 (fp16), biased 570, both 716.
+// heads, D 128, 629 GFLOP: masks alone 485 us (1.30 PFLOP/s,
+// 0.67 of the measured burst peak), capped 583 (bf16) and 638 (fp16), biased 570, both 716.
 // What the mask adds:
 //   - an item's keys start at the first page its rows see and end with the last, so a
 //     window or a packed document costs its own keys only;
