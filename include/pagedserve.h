@@ -360,8 +360,10 @@ int ps_paged_attention(const void* q, const void* k_pool, const void* v_pool,
  *   key_starts    int32 [T] or NULL: first key of the row's document in a sequence packed of
  *                 several; must not fall from one row of a sequence to the next (else keys
  *                 that a row should see may be left out). Negative counts as 0.
- * Other arguments, workspace and errors as for ps_paged_attention. A sequence whose tokens
- * lie outside [0, T) records PS_DEV_BAD_SEQUENCE and its rows are left unwritten.
+ * Other arguments, workspace and errors as for ps_paged_attention, but that
+ * query_start_loc[B] may be below T (a batch padded to a fixed size): rows from there on
+ * belong to no sequence and are left as they were. A sequence whose tokens lie outside
+ * [0, T) records PS_DEV_BAD_SEQUENCE and its rows are left unwritten.
  * K and V at keys that no row of the sequence sees (rows of a block never written, blocks
  * given back) may hold anything, NaN included. V at a key that one row of the step sees must
  * be finite for the others' sake: a NaN or infinity there may reach rows of the same

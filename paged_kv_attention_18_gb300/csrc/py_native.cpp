@@ -263,7 +263,7 @@ PyObject* select(PyObject* const* a) {
     refuse("logits: rows must be dense and equally far apart");
   const at::Tensor& scores = c.on(a[1], "scores", at::kFloat, 2);
   const int n = arg_int(a[2], "n_select");
-  if (n < 1) refuse("beam_select: n_select must be positive");
+  if (n < 1 || n > 32) refuse("beam_select: n_select must be 1 to 32");
   const uint8_t* fin = nullptr;
   if (a[3] != Py_None) {
     const at::Tensor& t = arg_tensor(a[3], "finished");

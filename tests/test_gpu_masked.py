@@ -212,17 +212,18 @@ def test_saturated_caps():
     b.check(b.run())
 
 
-def test_rows_behind_the_last_sequence_and_other_sequences_stay():
-    b = Batch([(100, 3), (50, 40)], 12, 2, 128, torch.bfloat16, 10, window=30)
-    q = torch.cat([b.q, b.q[:5]])
+@pytest.mark.parametrize("name", ["one", "small_chunks", "chunks", "one_chunk", "long", "decodes"])
+def test_rows_behind_the_last_sequence_stay(name):
+    # a batch padded to a fixed number of tokens, in every mode: direct, tiles alone, planned
+    b = Batch(BATCHES[name], 12, 2, 128, torch.bfloat16, 10, window=300)
+    T = b.q.shape[0]
+    q = torch.cat([b.q, b.q[:1].expand(9, -1, -1)]).contiguous()
     out = torch.full_like(q, 7.0)
-    # a packed batch shorter than the tensor is a malformed one for T of the tensor: the rows
-    # of no sequence are left as they were
-    binding.masked_paged_attention(q[:43], b.k, b.v, b.bt, b.sl, b.qs, b.scale, window=30,
-                                   out=out[:43])
+    binding.masked_paged_attention(q, b.k, b.v, b.bt, b.sl, b.qs, b.scale, window=300, out=out)
     torch.cuda.synchronize()
-    b.check(out[:43])
-    assert (out[43:] == 7.0).all() and binding.device_error() == 0
+    assert binding.device_error() == 0
+    b.check(out[:T])
+    assert (out[T:] == 7.0).all()
 
 
 def test_bad_blocks_and_sequences_are_recorded():
