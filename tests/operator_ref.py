@@ -34,8 +34,9 @@ def gather(pool, table, L):
 
 def attend_dense(q, K, V, pos, scale, softcap=0.0, slopes=None, window=0, prefix=0, starts=None):
     """q [n, H_q, D] at positions pos over K, V [L, H_kv, D]. Returns (out, tol_terms): the
-    output in 64 bits, sum_j w_j |V_j|, and the largest magnitude met in a row's scores
-    (sum |q k| scale, in log2 units, with the bias), all [n, H_q, (D)]."""
+    output in 64 bits, sum_j w_j |V_j|, the largest magnitude met in a row's scores (sum |q k|
+    scale, in log2 units, with the bias), and sum_j e_j (|V_j| + |out|), e_j what the rounding
+    of a weight too small for a normal fp16 can add (attention_tolerance), all [n, H_q, (D)]."""
     n, H_q, D = q.shape
     L, H_kv, _ = K.shape
     j = torch.arange(L, device=q.device)
@@ -46,7 +47,8 @@ def attend_dense(q, K, V, pos, scale, softcap=0.0, slopes=None, window=0, prefix
     if starts is not None:
         see &= j >= starts.long()[:, None]
     out = torch.zeros(n, H_q, D, dtype=torch.float64, device=q.device)
-    absv, size = torch.zeros_like(out), torch.zeros(n, H_q, dtype=torch.float64, device=q.device)
+    absv, tail = torch.zeros_like(out), torch.zeros_like(out)
+    size = torch.zeros(n, H_q, dtype=torch.float64, device=q.device)
     used = see.any(0)
     Kz = torch.where(used[:, None, None], K.double(), 0.0)
     Vz = torch.where(used[:, None, None], V.double(), 0.0)
@@ -65,15 +67,22 @@ def attend_dense(q, K, V, pos, scale, softcap=0.0, slopes=None, window=0, prefix
         w = torch.where(see, torch.exp(x - torch.where(top.isinf(), 0.0, top)), 0.0)
         w = w / w.sum(-1, keepdim=True).clamp(min=1e-300)
         out[:, h], absv[:, h] = w @ Vz[:, g], w @ Vz[:, g].abs()
+        e = (w.clamp(max=2.0 ** -24) - 2.0 ** -11 * w).clamp(min=0.0)
+        tail[:, h] = e @ Vz[:, g].abs() + e.sum(-1, keepdim=True) * out[:, h].abs()
         # (keys far below the row's maximum carry no weight, so neither do their errors)
         size[:, h] = torch.where(w > 1e-12, m, 0.0).max(-1).values * math.log2(math.e)
-    return out, absv, size
+    return out, absv, size, tail
 
 
-def attention_tolerance(out, absv, size, D, dtype):
+def attention_tolerance(out, absv, size, tail, D, dtype):
     """Largest error of an element of the output. u is half a step of the 16-bit type.
       - every weight is rounded to it, in the products and in the sum alike: weights are off
         by at most 2 u relative, the normalised sum by u (sum w |V| + |out|);
+      - fp16 weights below the type's least normal, 2^-14, are off by half its least step,
+        2^-25, whatever they are. They are taken relative to a sum of at least 1/2 (the
+        reference is at most the sum so far, rounded to a power of two), so a weight is off by
+        2^-24, or by all of itself if that is less: e = min(w, 2^-24) - u w more than the
+        line above counts (bf16 has fp32's exponents: none);
       - the fp32 score is a sum of D products (each add off by at most 2^-23, the tensor
         core truncating) and a few roundings of values of its size: (D + 16) 2^-23 size in
         log2 units; a weight is off by ln 2 of that, and by 2^-22 from ex2; in numerator and
@@ -84,7 +93,8 @@ def attention_tolerance(out, absv, size, D, dtype):
     u = torch.finfo(dtype).eps / 2
     rel = u + math.log(2) * (D + 16) * 2.0 ** -23 * size[..., None] + 2.0 ** -22
     tiny = torch.finfo(dtype).smallest_normal * u * 4
-    return rel * (absv + out.abs()) + 2.0 ** -16 * absv + u * out.abs() + tiny
+    tail = tail if dtype == torch.float16 else 0.0
+    return rel * (absv + out.abs()) + 2.0 ** -16 * absv + u * out.abs() + tail + tiny
 
 
 def beam(logits, scores, n, finished=None, pad=0):

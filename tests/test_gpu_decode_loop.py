@@ -62,9 +62,9 @@ def test_beam_search_steps(dt, hq, hkv, d, window):
             hk = flat_k[at:at + n] if history[b] is None else torch.cat([history[b][0], flat_k[at:at + n]])
             hv = flat_v[at:at + n] if history[b] is None else torch.cat([history[b][1], flat_v[at:at + n]])
             history[b] = (hk, hv)
-            ref, absv, size = R.attend_dense(qr[at:at + n], hk, hv, pos[at:at + n], d ** -0.5, 20.0,
-                                             slopes, window)
-            tol = R.attention_tolerance(ref, absv, size, d, dt)
+            ref, absv, size, tail = R.attend_dense(qr[at:at + n], hk, hv, pos[at:at + n],
+                                                   d ** -0.5, 20.0, slopes, window)
+            tol = R.attention_tolerance(ref, absv, size, tail, d, dt)
             assert ((out[at:at + n].double() - ref).abs() <= tol).all(), b
             at += n
         return out
