@@ -369,6 +369,9 @@ int encode_pool_map(CUtensorMap* map, const void* pool, int num_blocks, int H_kv
   return make_pool_map(map, pool, num_blocks, H_kv, D, bf16);
 }
 
+// Direct launch: (sequence, KV head) pairs per SM, and pages x head size, at most.
+constexpr int kMaskedDirectHeads = 2, kMaskedDirectKeys = 128 * 128;
+
 // The masked attention's chain: as run_attention's without a scatter. A small batch runs on
 // the split or the tile kernel's direct mode alone; otherwise planner, split kernel, tile
 // kernel and combine, chained with programmatic dependent launch.
@@ -387,16 +390,28 @@ int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const v
   if ((rc = make_pool_map(&vmap, v_pool, p.num_blocks, p.H_kv, p.D, bf16))) return rc;
   if (tiles && (rc = make_q_map(&qmap, p.q, p.T, p.H_q, p.D, p.G, p.tpt, bf16))) return rc;
   cudaError_t e;
-  // At most four 16-row groups in the whole batch and contexts that one CTA reads in the time
-  // a plan and a join would take: one launch, a CTA for each (sequence, KV head, group).
-  constexpr int kMaskedDirectGroups = 4, kMaskedDirectPages = 128;
-  const int64_t groups = (static_cast<int64_t>(p.T) * p.G + 15) / 16;
-  if (groups <= kMaskedDirectGroups && p.max_blocks <= kMaskedDirectPages &&
-      groups * p.B * p.H_kv <= num_sms) {
-    p.direct = static_cast<int>(groups);
+  // One token a sequence or less, on average, of at most 8 heads per KV head: items of 8 rows
+  // on the narrow kernel (a sequence with more tokens gets more items, and is right as well).
+  p.group_rows = !tiles && p.T <= p.B && p.G <= 8 ? 8 : 16;
+  // One launch without a plan, a CTA for each (sequence, KV head) or, where SMs are left, for
+  // each of its row groups: for few of those, with contexts that a CTA reads in the time a plan
+  // and a join would take, and a token a sequence or few rows in all (of a sequence with more
+  // groups than CTAs, the groups follow one another). Both ways, us (planned / direct), one
+  // token a sequence:
+  //   12 heads on 2, D 128:  1 sequence of 2048 19.2 / 15.6, of 4096 21.1 / 26.3, of 8192 27 / 48;
+  //                          36 of 512 20.2 / 7.5, of 2048 22.9 / 15.8; 152 of 2048 53.9 / 37.8
+  //   14 heads on 2, D 64:   1 sequence of 2048 17.3 / 10.7, of 4096 19.8 / 16.0, of 8192 24 / 27
+  //   32 heads on 8, D 128:  76 of 64 13.7 / 14.9, of 2048 84.8 / 70.5 (4 CTAs an SM:
+  //                          left to the plan, which evens out lengths that differ)
+  const int64_t heads = static_cast<int64_t>(p.B) * p.H_kv;
+  const bool few_rows = p.T == p.B || static_cast<int64_t>(p.T) * p.G <= 64;
+  if (few_rows && heads <= kMaskedDirectHeads * num_sms &&
+      static_cast<int64_t>(p.max_blocks) * p.D <= kMaskedDirectKeys) {
+    const int64_t groups = (static_cast<int64_t>(p.T) * p.G + p.group_rows - 1) / p.group_rows;
+    p.direct = static_cast<int>(std::max<int64_t>(1, std::min(groups, num_sms / heads)));
     Timed tm(3, s);
-    if ((e = launch_masked_split(p, bf16, kmap, vmap, static_cast<int>(groups * p.B * p.H_kv), s,
-                                 true)) != cudaSuccess)
+    const int ctas = static_cast<int>(heads * p.direct);
+    if ((e = launch_masked_split(p, bf16, kmap, vmap, ctas, s, true)) != cudaSuccess)
       return cuda_fail(e, "masked split attention kernel (direct)");
     return PS_OK;
   }
@@ -416,9 +431,6 @@ int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const v
     return PS_OK;
   }
   if (tiles && static_cast<int64_t>(p.B) * p.H_kv * 2 <= num_sms) p.all_tiles = 1;
-  // One token a sequence or less, on average, of at most 8 heads per KV head: items of 8 rows
-  // on the narrow kernel (a sequence with more tokens gets more items, and is right as well).
-  p.group_rows = !tiles && p.T <= p.B && p.G <= 8 ? 8 : 16;
   const int split_grid = split_ctas(p, num_sms);
   {
     Timed tm(2, s);

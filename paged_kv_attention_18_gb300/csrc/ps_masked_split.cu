@@ -101,20 +101,23 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
                  : -1;
   };
 
-  // Direct mode: the record of item idx = (sequence, KV head, 16-row group), over every page
-  // its rows see; the CTA's warps share the pages out. Lane k returns field k.
-  auto direct_item = [&](int idx) -> int {
-    const int j = idx % p.direct, bk = idx / p.direct;
-    const int b = bk / p.H_kv, kv = bk - b * p.H_kv;
+  // Direct mode: each (sequence, KV head) has p.direct CTAs, which take its groups of rows in
+  // turn. The record of group j, over every page its rows see; the CTA's warps share the pages
+  // out. Lane k returns field k.
+  constexpr int kGroup = kNarrow ? 8 : 16;
+  int dir_all = 0;  // packed rows of the sequence
+  auto direct_item = [&](int j) -> int {
+    const int bk = blockIdx.x / p.direct, b = bk / p.H_kv, kv = bk - b * p.H_kv;
     const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), L = __ldg(p.seq_lens + b);
     const int n = q1 - q0;
     if (q0 < 0 || q1 > p.T || n < 0 || n > L || (L + kBlockSize - 1) / kBlockSize > p.max_blocks) {
       if (lane == 0) record_error(p.err, kDevBadSequence);
       return 0;
     }
-    if (16 * j >= n * p.G) return 0;
-    const int nrows = min(16, n * p.G - 16 * j);
-    const int i0 = 16 * j / p.G, i1 = (16 * j + nrows - 1) / p.G;
+    dir_all = n * p.G;
+    if (kGroup * j >= dir_all) return 0;
+    const int nrows = min(kGroup, dir_all - kGroup * j);
+    const int i0 = kGroup * j / p.G, i1 = (kGroup * j + nrows - 1) / p.G;
     const int pre = p.prefix_len(b, L), lo = p.row_lo(q0 + i0, L - n + i0);
     const int hi = max(L - n + i1 + 1, pre);  // one past the last key (at most L)
     const int pe = (hi + kBlockSize - 1) / kBlockSize;
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
     int f = 0;
     f = lane == 0 ? b : f;
     f = lane == 1 ? kv : f;
-    f = lane == 2 ? 16 * j : f;
+    f = lane == 2 ? kGroup * j : f;
     f = lane == 3 ? nrows : f;
     f = lane == 4 ? first : f;                   // the warp's pages
     f = lane == 5 ? min(first + share, pe) : f;
@@ -136,6 +139,7 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
     f = lane == 14 ? pre : f;
     return f;
   };
+  int dir_group = kDirect ? blockIdx.x % p.direct : 0;
   int dir_rows = 0, dir_row0 = 0, dir_tok0 = 0, dir_kv = 0;  // the CTA's item, for the join
 
   // Issue the next page of work into stage g_issue % S; false when nothing is left.
@@ -144,10 +148,10 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
       if (no_more) return false;
       int idx = 0;
       if constexpr (kDirect) {
-        no_more = !first_fetch;  // one item a CTA
+        no_more = !first_fetch;  // one item at a time
         first_fetch = false;
         if (no_more) return false;
-        idx = blockIdx.x;
+        idx = dir_group;
       } else if (first_fetch) {
         // each warp's first item is its own; with tile items planned a CTA's warps take
         // consecutive items, so that the other SMs are free for the tile kernel
@@ -350,15 +354,17 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
     have_item = false;
   };
 
+  bool aborted = false;
+[[maybe_unused]] next_group:  // (direct mode only)
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     m_run[r] = -INFINITY;
     l_run[r] = 0.f;
   }
+  const uint32_t g_first = g_comp;
   for (int s = 0; s < S; ++s)  // fill the ring
     if (!issue_one()) break;
 
-  bool aborted = false;
   while (true) {
     if (comp_left == 0) {
       if (!kDirect && have_item) finish_item();
@@ -581,26 +587,38 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
   if constexpr (kDirect) {
     // The warps' shares of the item's pages joined: each leaves its O (not normalised) in its
     // own stages, which hold no page any more, and its rows' maxima and sums.
-    __shared__ float sh_m[kWarps][16], sh_l[kWarps][16];
-    const bool worked = g_comp > 0 && !aborted;
+    __shared__ float sh_m[kWarps][kGroup], sh_l[kWarps][kGroup];
+    const bool worked = g_comp != g_first && !aborted;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
-      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
-      if (t4 == 0) {
-        sh_m[warp][g + 8 * r] = worked ? m_run[r] : -INFINITY;
-        sh_l[warp][g + 8 * r] = worked ? l_run[r] : 0.f;
+#pragma unroll
+      for (int x = kNarrow ? 4 : 1; x < (kNarrow ? 32 : 4); x <<= 1)
+        l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], x);
+      const int row = kNarrow ? 2 * t4 + r : g + 8 * r;
+      if (kNarrow ? g == 0 : t4 == 0) {
+        sh_m[warp][row] = worked ? m_run[r] : -INFINITY;
+        sh_l[warp][row] = worked ? l_run[r] : 0.f;
       }
       if (worked) {
-        float* dst = reinterpret_cast<float*>(tiles) + (g + 8 * r) * D + 2 * t4;
+        float* dst = reinterpret_cast<float*>(tiles) + row * D;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          *reinterpret_cast<float2*>(dst + j * 8) = make_float2(o[j][2 * r], o[j][2 * r + 1]);
+        for (int j = 0; j < kO; ++j) {
+          if constexpr (kNarrow) {
+            dst[16 * j + g] = o[j][r];
+            dst[16 * j + 8 + g] = o[j][2 + r];
+          } else {
+            *reinterpret_cast<float2*>(dst + j * 8 + 2 * t4) =
+                make_float2(o[j][2 * r], o[j][2 * r + 1]);
+          }
+        }
       }
     }
     __syncthreads();
-    constexpr int kPer = D / 16;  // columns of a thread: 16 threads a row
-    const int row = threadIdx.x / 16, col = (threadIdx.x % 16) * kPer;
+    // threads of a row (of two columns at least: they are stored in pairs), columns of each
+    constexpr int kShare = kWarps * 32 / kGroup, kLanes = kShare < D / 2 ? kShare : D / 2;
+    constexpr int kPer = D / kLanes;
+    static_assert(kPer * kLanes == D && kPer % 2 == 0 && kLanes * kGroup <= kWarps * 32, "join");
+    const int row = threadIdx.x / kLanes, col = (threadIdx.x % kLanes) * kPer;
     if (row < dir_rows) {
       float M = -INFINITY;
 #pragma unroll
@@ -626,6 +644,14 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
           (static_cast<int64_t>(dir_tok0 + i) * p.H_q + dir_kv * p.G + (R - i * p.G)) * D + col);
 #pragma unroll
       for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack2<kBF16>(acc[e] * inv, acc[e + 1] * inv);
+    }
+    // the CTA's next group, once the stages that held O have been read
+    dir_group += p.direct;
+    fence_proxy_async_smem();
+    if (__syncthreads_or(aborted) == 0 && kGroup * dir_group < dir_all) {
+      no_more = have_item = false;
+      first_fetch = true;
+      goto next_group;
     }
   }
 }
@@ -657,7 +683,9 @@ cudaError_t launch_d(const MaskedAttnParams& p, bool bf16, const CUtensorMap& km
 cudaError_t launch_masked_split(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int ctas, cudaStream_t stream,
                                 bool pdl) {
-  if (p.direct) return launch_d<true, false>(p, bf16, kmap, vmap, ctas, stream, pdl);
+  if (p.direct)
+    return p.group_rows == 8 ? launch_d<true, true>(p, bf16, kmap, vmap, ctas, stream, pdl)
+                             : launch_d<true, false>(p, bf16, kmap, vmap, ctas, stream, pdl);
   return p.group_rows == 8 ? launch_d<false, true>(p, bf16, kmap, vmap, ctas, stream, pdl)
                            : launch_d<false, false>(p, bf16, kmap, vmap, ctas, stream, pdl);
 }

@@ -88,12 +88,12 @@ class Batch:
                 continue
             a, e = self.off[b], self.off[b + 1]
             pos = torch.arange(L - n, L, device="cuda")
-            ref, absv, size = R.attend_dense(
+            ref, absv, size, tail = R.attend_dense(
                 self.q[a:e], R.gather(self.k, self.bt[b], L), R.gather(self.v, self.bt[b], L), pos,
                 self.scale, self.softcap, self.slopes, self.window,
                 0 if self.prefix is None else int(self.prefix[b]),
                 None if self.starts is None else self.starts[a:e])
-            tol = R.attention_tolerance(ref, absv, size, self.d, self.dt)
+            tol = R.attention_tolerance(ref, absv, size, tail, self.d, self.dt)
             err = (out[a:e].double() - ref).abs()
             assert not (err > tol).any() and torch.isfinite(out[a:e]).all(), \
                 (b, L, n, float((err - tol).max()), int((~(err <= tol)).sum()))
@@ -316,6 +316,29 @@ def test_decode_items_of_eight_rows(hq, hkv, d, kw):
             (1, 1), (0, 0), (4000, 1), (600, 0)]
     for dt in DTS:
         b = Batch(seqs, hq, hkv, d, dt, 18, **kw)
+        b.check(b.run())
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(12, 4, 128), (14, 2, 64), (40, 4, 64), (36, 3, 128)])
+@pytest.mark.parametrize("count", [1, 12, 60, 90])
+@pytest.mark.parametrize("kw", [{}, dict(window=40, softcap=12.0, std=5.0), dict(prefix=30)])
+def test_small_batches_in_one_launch(hq, hkv, d, count, kw):
+    # as many tokens as sequences, contexts of at most 2048: a sequence's row groups are taken
+    # by several CTAs, by one CTA after the other, and with 90 sequences planned
+    kw = dict(kw)
+    some = [(2048, 1), (900, 9), (5, 0), (0, 0), (31, 4), (17, 1), (600, 0), (1, 1), (1300, 1),
+            (16, 0), (33, 1), (700, 0)]
+    seqs = [(700, 1)] if count == 1 else \
+        [(max(L - 3 * (i // 12), n), n) for i in range(0, count, 12) for L, n in some][:count]
+    while sum(n for _, n in seqs) < len(seqs):
+        i = [n for _, n in seqs].index(0)
+        seqs[i] = (max(seqs[i][0], 1), 1)
+    while sum(n for _, n in seqs) > len(seqs):
+        seqs.append((40, 0))
+    if kw.get("prefix"):
+        kw["prefix"] = [kw["prefix"]] * len(seqs)
+    for dt in DTS:
+        b = Batch(seqs, hq, hkv, d, dt, 24, **kw)
         b.check(b.run())
 
 
