@@ -363,7 +363,8 @@ int ps_paged_attention(const void* q, const void* k_pool, const void* v_pool,
  * Other arguments, workspace and errors as for ps_paged_attention, but that
  * query_start_loc[B] may be below T (a batch padded to a fixed size): rows from there on
  * belong to no sequence and are left as they were. A sequence whose tokens lie outside
- * [0, T) records PS_DEV_BAD_SEQUENCE and its rows are left unwritten.
+ * [0, T) records PS_DEV_BAD_SEQUENCE and its rows are left unwritten; with offsets that fall
+ * all rows may be.
  * K and V at keys that no row of the sequence sees (rows of a block never written, blocks
  * given back) may hold anything, NaN included. V at a key that one row of the step sees must
  * be finite for the others' sake: a NaN or infinity there may reach rows of the same

@@ -52,7 +52,7 @@ __device__ __forceinline__ SeqInfo seq_info(const Params& p, const int* qsl, con
   s.valid = s.n >= 0 && s.n <= s.L && s.pages <= p.max_blocks;
   s.page0 = s.pre = 0;
   if constexpr (Params::kMasked) {
-    s.valid = s.valid && s.tok0 >= 0 && s.tok0 + s.n <= p.T;
+    s.valid = p.sequence_ok(s.tok0, qsl[b + 1], s.L);
     if (s.valid && s.n > 0) {
       // the rows' lower bounds do not fall from one row to the next: the first row's holds
       s.pre = p.prefix_len(b, s.L);
@@ -358,7 +358,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int concurre
 
   // cost of the batch in pages read, per kernel
   long long wd = 0, wt = 0, pairs = 0;
+  bool ordered = true;
   for (int b = tid; b < p.B; b += nth) {
+    if constexpr (Params::kMasked) ordered = ordered && qsl[b] <= qsl[b + 1];
     const SeqInfo s = seq_info(p, qsl, lens, b);
     if (!s.valid) {
       record_error(p.err, kDevBadSequence);
@@ -439,6 +441,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int concurre
     pps_d = pps_d >= (1 << 23) ? (1 << 24) : 2 * pps_d;
     pps_t = pps_t >= (1 << 23) ? (1 << 24) : 2 * pps_t;
   }
+  if constexpr (Params::kMasked) {
+    // offsets that fall (recorded above): sequences may overlap, and the search for a token's
+    // own fails, so nothing is planned
+    if (!__syncthreads_and(ordered)) tot = make_int4(0, 0, 0, 0);
+  }
   if (tid == 0) {
     off_d[p.B] = tot.x;
     off_t[p.B] = tot.y;
@@ -511,7 +518,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int concurre
       const SeqInfo s = seq_info(p, qsl, lens, b);
       const int i = t - s.tok0;
       int ns_t = 0, tb = 0;
-      if (planned && s.valid && s.groups > 0) {
+      bool own = planned && s.valid && s.groups > 0;
+      if constexpr (Params::kMasked) own = own && i >= 0 && i < s.n;  // a padded batch's rows
+      if (own) {
         const int ns = seq_splits(s, pps_d, pps_t);
         ns_t = 1;
         if (ns > 1) {

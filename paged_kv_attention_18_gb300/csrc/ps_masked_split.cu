@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
     const int bk = blockIdx.x / p.direct, b = bk / p.H_kv, kv = bk - b * p.H_kv;
     const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), L = __ldg(p.seq_lens + b);
     const int n = q1 - q0;
-    if (q0 < 0 || q1 > p.T || n < 0 || n > L || (L + kBlockSize - 1) / kBlockSize > p.max_blocks) {
+    if (!p.sequence_ok(q0, q1, L)) {
       if (lane == 0) record_error(p.err, kDevBadSequence);
       return 0;
     }

@@ -243,6 +243,28 @@ def test_bad_blocks_and_sequences_are_recorded():
     b.check(out)
 
 
+@pytest.mark.parametrize("name", ["one", "small_chunks", "chunks", "long"])
+@pytest.mark.parametrize("what", ["length", "offsets"])
+def test_lengths_and_offsets_at_the_end_of_32_bits(name, what):
+    # recorded and left unwritten in every mode, the other sequences served
+    b = Batch(BATCHES[name] + [(30, 3)], 12, 2, 128, torch.float16, 25, window=50, holes=False)
+    b.bt[b.bt < 0] = 0
+    T, last = b.q.shape[0], len(b.seqs) - 1
+    if what == "length":
+        b.sl[last] = 2 ** 31 - 1  # a few more, and the count of its pages would be negative
+        bad, b.seqs = slice(T - 3, T), b.seqs[:last]
+    else:
+        b.qs[last] = 2 ** 31 - 1  # the last two sequences' tokens; the others may be left too
+        b.qs[last + 1] = -2 ** 31
+        bad, b.seqs = slice(b.off[last - 1], T), []
+    out = torch.full_like(b.q, 7.0)
+    binding.masked_paged_attention(b.q, b.k, b.v, b.bt, b.sl, b.qs, b.scale, window=50, out=out)
+    torch.cuda.synchronize()
+    assert binding.device_error() == 3
+    assert (out[bad] == 7.0).all()
+    b.check(out)
+
+
 def test_one_workspace_two_calls_and_other_stream():
     b = Batch(LONG, 12, 2, 128, torch.bfloat16, 12, window=300, softcap=20.0, std=3.0)
     c = Batch(CHUNKS, 12, 2, 128, torch.bfloat16, 13, prefix=[40] * len(CHUNKS))
