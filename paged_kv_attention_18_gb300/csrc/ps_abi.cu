@@ -369,8 +369,8 @@ int encode_pool_map(CUtensorMap* map, const void* pool, int num_blocks, int H_kv
   return make_pool_map(map, pool, num_blocks, H_kv, D, bf16);
 }
 
-// Direct launch: (sequence, KV head) pairs per SM, and pages x head size, at most.
-constexpr int kMaskedDirectHeads = 2, kMaskedDirectKeys = 128 * 128;
+// Direct launch: items per SM, and pages x head size, at most.
+constexpr int kMaskedDirectItems = 2, kMaskedDirectKeys = 128 * 128;
 
 // The masked attention's chain: as run_attention's without a scatter. A small batch runs on
 // the split or the tile kernel's direct mode alone; otherwise planner, split kernel, tile
@@ -393,25 +393,26 @@ int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const v
   // One token a sequence or less, on average, of at most 8 heads per KV head: items of 8 rows
   // on the narrow kernel (a sequence with more tokens gets more items, and is right as well).
   p.group_rows = !tiles && p.T <= p.B && p.G <= 8 ? 8 : 16;
-  // One launch without a plan, a CTA for each (sequence, KV head) or, where SMs are left, for
-  // each of its row groups: for few of those, with contexts that a CTA reads in the time a plan
-  // and a join would take, and a token a sequence or few rows in all (of a sequence with more
-  // groups than CTAs, the groups follow one another). Both ways, us (planned / direct), one
-  // token a sequence:
+  // One launch without a plan, a CTA for each group of rows of a (sequence, KV head): for few of
+  // those, with contexts that a CTA reads in the time a plan and a join would take, and no more
+  // than 64 rows a sequence on average (the kernel finds its items from the offsets, so a
+  // sequence with more is served by more CTAs). Both ways, us (planned / direct), one token a
+  // sequence unless said:
   //   12 heads on 2, D 128:  1 sequence of 2048 19.2 / 15.6, of 4096 21.1 / 26.3, of 8192 27 / 48;
-  //                          36 of 512 20.2 / 7.5, of 2048 22.9 / 15.8; 152 of 2048 53.9 / 37.8
+  //                          36 of 512 20.2 / 7.9, of 2048 22.9 / 16.3; 152 of 2048 53.9 / 39.7;
+  //                          16 of 2048 with 4 tokens 35.2 / 21.8 (without a plan on the tile
+  //                          kernel); 16 of 512 and one with 48 tokens 18.4 / 10.2
   //   14 heads on 2, D 64:   1 sequence of 2048 17.3 / 10.7, of 4096 19.8 / 16.0, of 8192 24 / 27
-  //   32 heads on 8, D 128:  76 of 64 13.7 / 14.9, of 2048 84.8 / 70.5 (4 CTAs an SM:
+  //   32 heads on 8, D 128:  76 of 64 13.7 / 14.9, of 2048 84.8 / 70.5 (4 items an SM:
   //                          left to the plan, which evens out lengths that differ)
-  const int64_t heads = static_cast<int64_t>(p.B) * p.H_kv;
-  const bool few_rows = p.T == p.B || static_cast<int64_t>(p.T) * p.G <= 64;
-  if (few_rows && heads <= kMaskedDirectHeads * num_sms &&
+  const int64_t rows = static_cast<int64_t>(p.T) * p.G, gr = p.group_rows;
+  const int64_t items = p.H_kv * (p.T <= p.B ? p.T * ((p.G + gr - 1) / gr) : rows / gr + p.B);
+  if (rows <= 64 * static_cast<int64_t>(p.B) && items <= kMaskedDirectItems * num_sms &&
       static_cast<int64_t>(p.max_blocks) * p.D <= kMaskedDirectKeys) {
-    const int64_t groups = (static_cast<int64_t>(p.T) * p.G + p.group_rows - 1) / p.group_rows;
-    p.direct = static_cast<int>(std::max<int64_t>(1, std::min(groups, num_sms / heads)));
+    p.direct = 1;
     Timed tm(3, s);
-    const int ctas = static_cast<int>(heads * p.direct);
-    if ((e = launch_masked_split(p, bf16, kmap, vmap, ctas, s, true)) != cudaSuccess)
+    if ((e = launch_masked_split(p, bf16, kmap, vmap, static_cast<int>(items), s, true)) !=
+        cudaSuccess)
       return cuda_fail(e, "masked split attention kernel (direct)");
     return PS_OK;
   }

@@ -274,7 +274,8 @@ cudaError_t launch_plan_masked(const MaskedAttnParams& p, int concurrency, int t
 // their causal forms are.
 // Warps of the masked split kernel's CTA (narrow: its 8-row items).
 constexpr int masked_split_warps(int D, bool narrow) { return narrow && D == 64 ? 16 : 8; }
-// p.direct: CTAs of each (sequence, KV head) in the split kernel's direct mode (0: planned).
+// p.direct: the split kernel's direct mode, about a CTA for each group of rows of a
+// (sequence, KV head).
 cudaError_t launch_masked_split(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int ctas, cudaStream_t stream,
                                 bool pdl);

@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
 
   const int n_items = kDirect ? 0 : *reinterpret_cast<volatile int*>(p.hdr);
   bool first_fetch = true;
+  [[maybe_unused]] bool first_scan = true;
   const bool tile_planned = !kDirect && *reinterpret_cast<volatile int*>(p.hdr + 4) > 0;
   const uint64_t policy = l2_policy_evict_first();
 
@@ -101,22 +102,54 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
                  : -1;
   };
 
-  // Direct mode: each (sequence, KV head) has p.direct CTAs, which take its groups of rows in
-  // turn. The record of group j, over every page its rows see; the CTA's warps share the pages
-  // out. Lane k returns field k.
+  // Direct mode: the items are the groups of rows of each (sequence, KV head), in order; a CTA
+  // takes its own and those a grid's width on. Each warp counts the groups of every sequence
+  // (few: the launch has about an item a CTA) to find item idx. The item's record covers every
+  // page its rows see; the CTA's warps share the pages out. Lane k returns field k.
   constexpr int kGroup = kNarrow ? 8 : 16;
-  int dir_all = 0;  // packed rows of the sequence
-  auto direct_item = [&](int j) -> int {
-    const int bk = blockIdx.x / p.direct, b = bk / p.H_kv, kv = bk - b * p.H_kv;
-    const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), L = __ldg(p.seq_lens + b);
-    const int n = q1 - q0;
-    if (!p.sequence_ok(q0, q1, L)) {
-      if (lane == 0) record_error(p.err, kDevBadSequence);
-      return 0;
+  int dir_item = blockIdx.x, dir_items = 0;  // the CTA's item, items in all
+  auto direct_item = [&](int idx) -> int {
+    int b = -1, q0 = 0, n = 0, L = 0, nth = 0, groups = 0;  // the item's sequence, from its lane
+    dir_items = 0;
+    int q0a = 0, q1a = 0, La = 0;  // the next 32 sequences, one a lane, loaded ahead
+    auto load = [&](int bl) {
+      if (bl < p.B) {
+        q0a = __ldg(p.qsl + bl);
+        q1a = __ldg(p.qsl + bl + 1);
+        La = __ldg(p.seq_lens + bl);
+      }
+    };
+    load(lane);
+    for (int base = 0; base < p.B; base += 32) {
+      const int q0l = q0a, nl = q1a - q0a, Ll = La;
+      const bool in = base + lane < p.B, ok = in && p.sequence_ok(q0a, q1a, La);
+      load(base + 32 + lane);
+      if (in && !ok && blockIdx.x == 0 && warp == 0 && first_scan)
+        record_error(p.err, kDevBadSequence);
+      const int gl = ok ? (nl * p.G + kGroup - 1) / kGroup : 0;
+      int end = gl * p.H_kv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += y;
+      }
+      const int at = idx - dir_items;  // within these 32 sequences
+      const unsigned past = __ballot_sync(0xffffffffu, end > at);
+      if (b < 0 && past != 0) {
+        const int src = __ffs(past) - 1;
+        b = base + src;
+        q0 = __shfl_sync(0xffffffffu, q0l, src);
+        n = __shfl_sync(0xffffffffu, nl, src);
+        L = __shfl_sync(0xffffffffu, Ll, src);
+        groups = __shfl_sync(0xffffffffu, gl, src);
+        nth = at - (__shfl_sync(0xffffffffu, end, src) - groups * p.H_kv);
+      }
+      dir_items += __shfl_sync(0xffffffffu, end, 31);
     }
-    dir_all = n * p.G;
-    if (kGroup * j >= dir_all) return 0;
-    const int nrows = min(kGroup, dir_all - kGroup * j);
+    first_scan = false;
+    if (b < 0) return 0;
+    const int kv = nth / groups, j = nth - kv * groups;
+    const int nrows = min(kGroup, n * p.G - kGroup * j);
     const int i0 = kGroup * j / p.G, i1 = (kGroup * j + nrows - 1) / p.G;
     const int pre = p.prefix_len(b, L), lo = p.row_lo(q0 + i0, L - n + i0);
     const int hi = max(L - n + i1 + 1, pre);  // one past the last key (at most L)
@@ -139,7 +172,6 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
     f = lane == 14 ? pre : f;
     return f;
   };
-  int dir_group = kDirect ? blockIdx.x % p.direct : 0;
   int dir_rows = 0, dir_row0 = 0, dir_tok0 = 0, dir_kv = 0;  // the CTA's item, for the join
 
   // Issue the next page of work into stage g_issue % S; false when nothing is left.
@@ -151,7 +183,7 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
         no_more = !first_fetch;  // one item at a time
         first_fetch = false;
         if (no_more) return false;
-        idx = dir_group;
+        idx = dir_item;
       } else if (first_fetch) {
         // each warp's first item is its own; with tile items planned a CTA's warps take
         // consecutive items, so that the other SMs are free for the tile kernel
@@ -355,7 +387,7 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
   };
 
   bool aborted = false;
-[[maybe_unused]] next_group:  // (direct mode only)
+[[maybe_unused]] next_item:  // (direct mode only)
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     m_run[r] = -INFINITY;
@@ -645,13 +677,13 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
 #pragma unroll
       for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack2<kBF16>(acc[e] * inv, acc[e + 1] * inv);
     }
-    // the CTA's next group, once the stages that held O have been read
-    dir_group += p.direct;
+    // the CTA's next item, once the stages that held O have been read
+    dir_item += gridDim.x;
     fence_proxy_async_smem();
-    if (__syncthreads_or(aborted) == 0 && kGroup * dir_group < dir_all) {
+    if (__syncthreads_or(aborted) == 0 && dir_item < dir_items) {
       no_more = have_item = false;
       first_fetch = true;
-      goto next_group;
+      goto next_item;
     }
   }
 }

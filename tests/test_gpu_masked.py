@@ -364,6 +364,21 @@ def test_small_batches_in_one_launch(hq, hkv, d, count, kw):
         b.check(b.run())
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(12, 2, 128), (14, 2, 64), (8, 8, 64), (32, 2, 128)])
+@pytest.mark.parametrize("seqs", [
+    [(700 + i, 4) for i in range(16)],                           # tokens to verify
+    [(50 * i + 1, 1) for i in range(40)] + [(1900, 48)],         # decodes and a short chunk
+    [(300, 7), (0, 0), (2000, 2), (1, 1), (64, 64), (5, 0)] * 6 + [(9, 0)] * 29,  # over 64
+    [(200, 12)],
+    [(i % 50 + 1, (1, 1, 2, 0, 1)[i % 5]) for i in range(150)],  # found by several counts
+])
+def test_several_tokens_in_one_launch(hq, hkv, d, seqs):
+    for dt, kw in ((torch.float16, dict(slopes=slopes_of(hq), window=333)),
+                   (torch.bfloat16, dict(softcap=20.0, std=4.0))):
+        b = Batch(seqs, hq, hkv, d, dt, 26, **kw)
+        b.check(b.run())
+
+
 def test_many_sequences():
     # more sequences than the planner stages in shared memory
     seqs = [(1 + (7 * i) % 90, 1) for i in range(4200)]
