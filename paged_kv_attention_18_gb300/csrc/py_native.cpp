@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -138,6 +139,13 @@ PyObject* give(PyObject* o) {
   return o;
 }
 
+// New tensors on device `dev`, past the dispatcher (a selection of one prompt with its three
+// results: 7.8 -> 6.9 us with a workspace given, 8.9 -> 7.8 without).
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, int dev) {
+  return at::Tensor(
+      at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, dev), std::nullopt));
+}
+
 // q, k, v, positions, slots, k_pool, v_pool, inv_freq, interleaved, magnitude, q_out | None,
 // stream | None
 PyObject* rotary(PyObject* const* a) {
@@ -221,14 +229,14 @@ PyObject* attend(PyObject* const* a) {
   const float scale = arg_float(a[6]), cap = arg_float(a[7]);
   const int window = arg_int(a[9], "window");
   void* s = arg_stream(a[15], c.dev);
-  at::Tensor out = a[12] == Py_None ? at::empty_like(q) : c.on(a[12], "out", st, 3);
+  at::Tensor out = a[12] == Py_None ? fresh(q.sizes(), st, c.dev) : c.on(a[12], "out", st, 3);
   if (!out.sizes().equals(q.sizes())) refuse("out must have q's shape");
   at::Tensor ws;
   if (a[13] == Py_None) {
     const int64_t len = a[14] == Py_None ? static_cast<int64_t>(width) * PS_BLOCK_SIZE
                                          : arg_int(a[14], "max_seq_len");
     const size_t n = ps_paged_attention_workspace_size(T, B, H_q, H_kv, D, to_int(len, "max_seq_len"));
-    ws = at::empty({static_cast<int64_t>(n > 256 ? n : 256)}, q.options().dtype(at::kByte));
+    ws = fresh({static_cast<int64_t>(n > 256 ? n : 256)}, at::kByte, c.dev);
   } else {
     ws = c.on(a[13], "workspace", at::kByte, 1);
   }
@@ -278,17 +286,16 @@ PyObject* select(PyObject* const* a) {
   at::Tensor ws;
   if (a[5] == Py_None) {
     const size_t need = ps_beam_select_workspace_size(b, w, v, n);
-    ws = at::empty({static_cast<int64_t>(need > 256 ? need : 256)}, x.options().dtype(at::kByte));
+    ws = fresh({static_cast<int64_t>(need > 256 ? need : 256)}, at::kByte, c.dev);
   } else {
     ws = c.on(a[5], "workspace", at::kByte, 1);
   }
   const bool own = a[6] == Py_None;
   at::Tensor par, tok, best;
   if (own) {
-    const auto int_opts = x.options().dtype(at::kInt);
-    par = at::empty({B, n}, int_opts);
-    tok = at::empty({B, n}, int_opts);
-    best = at::empty({B, n}, x.options().dtype(at::kFloat));
+    par = fresh({B, n}, at::kInt, c.dev);
+    tok = fresh({B, n}, at::kInt, c.dev);
+    best = fresh({B, n}, at::kFloat, c.dev);
   } else {
     par = c.on(a[6], "parents", at::kInt, 2);
     tok = c.on(a[7], "tokens", at::kInt, 2);
