@@ -77,6 +77,7 @@ struct MaskedAttnParams : AttnParams {
   int window;             // keys a row sees, its own included; 0: all before it
   const int32_t* prefix;  // [B] or null
   const int32_t* starts;  // [T] or null
+  int tile_step;          // query tiles of a tile item in direct mode: 2, or 1
   int group_rows;         // packed rows of a split-kernel item: 16, or 8 (the narrow kernel)
 
   // Whether a sequence of packed tokens q0 .. q1 - 1 and context L may be served: its tokens

@@ -239,9 +239,10 @@ __global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
     const int n_stages = is_k ? kKStages : kVStages;
     uint32_t g = 0, qa = 0, qb = 0;
     // Direct mode: lane b holds sequence b's query tokens n, context L, first token t0 and
-    // query-tile pairs (0 for a sequence without rows or an invalid one). Items go rank by
-    // rank (rank r: every sequence's r-th longest pair, in batch order, each KV head), so
-    // csum(r) = H_kv * sum_b min(pairs_b, r) items come before rank r.
+    // items, each a pair of query tiles or one tile (p.tile_step; 0 for a sequence without
+    // rows or an invalid one). Items go rank by rank (rank r: every sequence's r-th longest,
+    // in batch order, each KV head), so csum(r) = H_kv * sum_b min(items_b, r) come before
+    // rank r.
     int d_n = 0, d_L = 0, d_t0 = 0, d_pre = 0, d_pairs = 0, d_max = 0, d_total = 0;
     auto csum = [&](int r) -> int {
       int v = min(d_pairs, r);
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
           d_L = L;
           d_t0 = q0;
           d_pre = p.prefix_len(lane, L);
-          d_pairs = ((n + p.tpt - 1) / p.tpt + 1) / 2;
+          d_pairs = ((n + p.tpt - 1) / p.tpt + p.tile_step - 1) / p.tile_step;
         }
       }
       d_max = d_pairs;
@@ -285,8 +286,9 @@ __global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
       const int n = __shfl_sync(0xffffffffu, d_n, b), L = __shfl_sync(0xffffffffu, d_L, b);
       const int t0 = __shfl_sync(0xffffffffu, d_t0, b);
       const int j = __shfl_sync(0xffffffffu, d_pairs, b) - 1 - r;  // rank 0: the last pair
-      const int qa_ = 2 * j * p.tpt, qb_ = qa_ + p.tpt;
-      const int na = min(p.tpt, n - qa_), nb = qb_ < n ? min(p.tpt, n - qb_) : 0;
+      const int qa_ = p.tile_step * j * p.tpt, qb_ = qa_ + p.tpt;
+      const int na = min(p.tpt, n - qa_);
+      const int nb = p.tile_step == 2 && qb_ < n ? min(p.tpt, n - qb_) : 0;
       const int i_last = nb > 0 ? qb_ + nb - 1 : qa_ + na - 1;
       const int pre = __shfl_sync(0xffffffffu, d_pre, b);
       const int key_end = max(L - n + i_last + 1, pre);  // one past the last key (at most L)
