@@ -203,7 +203,9 @@ int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, 
  * and the n_select best of the W * V are returned in falling order, ties to the lowest beam,
  * then the lowest token. A finished beam has one continuation: pad_token, at its score as it
  * is. A logit of -inf or NaN is no continuation (and adds nothing to lse_w); nor has a beam
- * whose score is not finite, or one with a logit of 2^127 or more, any. Where fewer than n_select
+ * whose score is not finite, or one with a logit of +inf, any. Finite logits are served whatever
+ * their size: tokens masked by a large negative number, the type's least value included, are
+ * continuations with the scores that follow from it. Where fewer than n_select
  * remain, the rest are parent -1, token -1, score -inf.
  * lse is summed in fp32 within a chunk of the row and in fp64 across chunks; scores are
  * compared as pairs of floats (48 bits) and rounded once to fp32.

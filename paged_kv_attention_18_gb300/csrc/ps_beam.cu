@@ -231,13 +231,16 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
   };
 #pragma unroll 1
   for (int r = 0; r < kDepth; ++r) fetch(r);
-  // One pass. m: the thread's maximum; sum: of 2^(x L + c), L = log2(e) in fp32, c near -m L.
-  // Whatever c's rounding, 2^-(M L + c) brings the sum to the reference M in the end, M L + c
-  // in one rounding. (The rounds are not unrolled: straight-line code for all of them ran at
-  // the rate of its instruction fetches. A round's maximum is kept in shared memory.)
+  // One pass. m: the thread's maximum; sum: of 2^((x + c) L), L = log2(e) in fp32, c = -m (0
+  // before the first logit above -inf). The difference comes first: it is 0 at the maximum and
+  // rounded by 2^-24 of itself elsewhere, whatever the logits' size, where x L - m L in one
+  // fused operation is off by m L's rounding, 2^8 and more from |m| = 2^31 on, and overflows at
+  // masks of the type's least value. (The rounds are not unrolled: straight-line code for all
+  // of them ran at the rate of its instruction fetches. A round's maximum is kept in shared
+  // memory.)
   float m = -INFINITY, c = 0.f;
   float2 sum = make_float2(0.f, 0.f);
-  const float2 l2 = make_float2(kLog2e, kLog2e);
+  const float2 l2 = make_float2(kLog2e, kLog2e), one2 = make_float2(1.f, 1.f);
 #pragma unroll 1
   for (int r = 0; r < rounds; ++r) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
@@ -250,11 +253,10 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
     const float mr = fmaxf(words_max<T>(words), -INFINITY);
     sh_round[r][threadIdx.x] = mr;
     if (mr > m) {
+      const float a = fast_exp2((m - mr) * kLog2e);  // (0 from -inf, whose sum is 0)
+      sum = fmul2(sum, make_float2(a, a));
       m = mr;
-      const float to = -m * kLog2e;
-      const float a = fast_exp2(to - c);  // (at most 1, but for the first round's empty sum)
-      sum = sum.x > 0.f || sum.y > 0.f ? fmul2(sum, make_float2(a, a)) : sum;
-      c = to;
+      c = -m;
     }
     const float2 c2 = make_float2(c, c);
     float2 add[2] = {sum, make_float2(0.f, 0.f)};
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
       } else {
         unpack<T>(words[i], x);
       }
-      const float2 y = ffma2(make_float2(x[0], x[1]), l2, c2);
+      const float2 y = fmul2(ffma2(make_float2(x[0], x[1]), one2, c2), l2);
       add[i / kStep % 2].x += fast_exp2(y.x);
       add[i / kStep % 2].y += fast_exp2(y.y);
     }
@@ -282,13 +284,13 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
       for (int j = 0; j < kWords; ++j)
         for (int i = 0; i < kVec; ++i) {
           const int t = place(r, j, threadIdx.x) + i;
-          if (t >= 0 && t < end) total += fast_exp2(fmaf(clean(widen<T>(base[t])), kLog2e, c));
+          if (t >= 0 && t < end) total += fast_exp2((clean(widen<T>(base[t])) + c) * kLog2e);
         }
   }
   uint32_t top, tau;
   block_bound(order32(clean(m)), p.n, sh_key, top, tau);
   const float M = from_order32(top);
-  float s = m > -INFINITY ? total * fast_exp2(-fmaf(M, kLog2e, c)) : 0.f;
+  float s = m > -INFINITY ? total * fast_exp2((m - M) * kLog2e) : 0.f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) sh_sum[warp] = s;
@@ -360,10 +362,10 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
   }
 }
 
-// Scores are pairs of floats hi + lo (|lo| at most half a step of hi): cum + (x - lse) with
-// 2^-46 of the largest of the three lost at most, in fp32 adds alone (fp64 runs at a small
-// fraction of their rate here). Equal values give equal pairs, and pairs in the order of
-// (hi, lo) are in the order of their values.
+// Scores are pairs of floats hi + lo (|lo| at most half a step of hi): cum + (x - M - log S),
+// lse = M + log S, with 2^-46 of the largest of x - M, cum and log S lost at most, in fp32 adds
+// alone (fp64 runs at a small fraction of their rate here). Equal values give equal pairs, and
+// pairs in the order of (hi, lo) are in the order of their values.
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   s = __fadd_rn(a, b);
   const float t = __fsub_rn(s, a);
@@ -381,8 +383,8 @@ __device__ __forceinline__ bool better(const Best& a, const Best& b) {
 
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
   __shared__ BoundSmem sh_key;
-  __shared__ float2 sh_lse[kBeamMaxWidth];  // hi, lo
-  __shared__ float sh_cum[kBeamMaxWidth];
+  __shared__ float sh_M[kBeamMaxWidth];     // the beam's largest logit
+  __shared__ float2 sh_cum[kBeamMaxWidth];  // cum - log S (a finished beam: cum): hi, lo
   __shared__ int sh_kind[kBeamMaxWidth];  // 0 no candidate, 1 scored, 2 finished
   __shared__ Best list[kCap];
   __shared__ Best sh_best[kWarps];
@@ -404,10 +406,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     const float cum = p.scores[row];
     const bool fin = p.finished != nullptr && p.finished[row];
     int kind = cum > -INFINITY && cum < INFINITY ? (fin ? 2 : 1) : 0;
-    double lse = 0.0;
+    float M = 0.f;
+    float2 from = make_float2(cum, 0.f);
     if (kind == 1) {
       const float2* st = p.stat + static_cast<int64_t>(row) * p.chunks;
-      float M = -INFINITY;
+      M = -INFINITY;
       for (int c = lane; c < p.chunks; c += 32) M = fmaxf(M, st[c].x);
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -420,20 +423,21 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
 #pragma unroll
         for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
         // log S = k ln 2 + log(f), f in [1, 2): fp32 serves for log(f), whose rounding
-        // is then below 2^-24 whatever the size of S
-        if (!(S < 1e300)) kind = 0;  // a logit past 2^127, whose exponent left fp32
+        // is then below 2^-24 whatever the size of S (1 at least: the largest logit's term)
         const long long bits = __double_as_longlong(S);
         const int k = static_cast<int>(bits >> 52) - 1023;
         const double f =
             __longlong_as_double((bits & 0xfffffffffffffll) | 0x3ff0000000000000ll);
-        lse = static_cast<double>(M) + k * kLn2 + static_cast<double>(logf(static_cast<float>(f)));
+        const double log_s = k * kLn2 + static_cast<double>(logf(static_cast<float>(f)));
+        const float hi = static_cast<float>(log_s);
+        two_sum(cum, -hi, from.x, from.y);
+        from.y = __fsub_rn(from.y, static_cast<float>(log_s - hi));
       }
     }
     if (lane == 0) {
       sh_kind[w] = kind;
-      const float hi = static_cast<float>(lse);
-      sh_lse[w] = make_float2(hi, static_cast<float>(lse - hi));
-      sh_cum[w] = cum;
+      sh_M[w] = M;
+      sh_cum[w] = from;
     }
   }
   __syncthreads();
@@ -444,16 +448,16 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     float hi, lo = 0.f;
     if (kind == 2) {
       if (r != 0) return false;
-      hi = sh_cum[w];
+      hi = sh_cum[w].x;
       e.flat = w * p.V + p.pad;
     } else {
       if (kind == 0) return false;
       if (k == 0) return false;
       const float x = from_order32(static_cast<uint32_t>(k >> 32));
       float d, e1, t, e2;
-      two_sum(x, -sh_lse[w].x, d, e1);
-      two_sum(sh_cum[w], d, t, e2);
-      const float rest = __fadd_rn(e2, __fsub_rn(e1, sh_lse[w].y));
+      two_sum(x, -sh_M[w], d, e1);
+      two_sum(sh_cum[w].x, d, t, e2);
+      const float rest = __fadd_rn(e2, __fadd_rn(e1, sh_cum[w].y));
       two_sum(t, rest, hi, lo);
       e.flat = w * p.V + static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
     }

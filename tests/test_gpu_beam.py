@@ -244,3 +244,77 @@ def test_fork_of_one_layer_without_its_dimension():
     binding.fork_sequences(bt.cuda(), lens.cuda(), parents.cuda(), tails.cuda(), dp[0], dp[1], ob,
                            ol)
     assert torch.equal(ob.cpu(), want[0]) and torch.equal(dp.cpu(), want[2][:, 0])
+
+
+# ------------------------------------------------------------------------------------
+# masks that are finite numbers
+# ------------------------------------------------------------------------------------
+MIN32, MIN16 = torch.finfo(torch.float32).min, torch.finfo(torch.bfloat16).min
+
+
+def best_of(logits, scores, n):
+    """(score, flat index), best first, in 64 bits with the largest logit taken off first (a log
+    of the sum added to a logit of 1e30 is lost in 64 bits too); below fp32's range -inf."""
+    B, W, V = logits.shape
+    res = []
+    for b in range(B):
+        cand = []
+        for w in range(W):
+            x = logits[b, w].double().cpu()
+            d = x - x.max()
+            s = float(scores[b, w]) + (d - math.log(float(torch.exp(d).sum())))
+            s = torch.where(s < MIN32 * (1 + 2.0 ** -25), -math.inf, s)
+            for t in torch.sort(-x, stable=True).indices[:n].tolist():
+                cand.append((float(s[t]), w * V + t))
+        res.append(sorted(cand, key=lambda c: (-c[0], c[1]))[:n])
+    return res
+
+
+def check_best(logits, scores, n, got, live=None):
+    """Parents, tokens and scores; with `live` only the first `live` of each prompt by index. A
+    score is the sum of numbers up to its size, 48 bits of them (2^-46), and the fp32 rounding."""
+    par, tok, val = (x.cpu() for x in got)
+    V = logits.shape[2]
+    for b, want in enumerate(best_of(logits, scores, n)):
+        for i, (s, flat) in enumerate(want):
+            got_s = float(val[b, i])
+            assert got_s == s or abs(got_s - s) <= LSE_TOL + 2.0 ** -23 * abs(s), (b, i, got_s, s)
+            if live is None or i < live:
+                assert (int(par[b, i]), int(tok[b, i])) == (flat // V, flat % V), (b, i)
+
+
+@pytest.mark.parametrize("dt,mask", [
+    (torch.float32, MIN32), (torch.float32, -1e30), (torch.float32, -1e12), (torch.float32, -1e10),
+    (torch.float32, -1e9), (torch.float32, -1e4), (torch.bfloat16, MIN16), (torch.bfloat16, -1e10),
+    (torch.float16, -65504.0)])
+@pytest.mark.parametrize("V", [700, 50001, 151936])
+def test_finite_masks(dt, mask, V):
+    # constrained to a few tokens (whole threads and chunks masked); a vocabulary's tail masked;
+    # every other run of 8 masked, ahead of live ones in a thread's rounds; the first half masked
+    g = torch.Generator("cuda").manual_seed(V)
+    scores = torch.tensor([[-1.0, -4.0, -9.0, -13.0]] * 4, device="cuda")
+    logits = (torch.randn(4, 4, V, generator=g, device="cuda") * 3).to(dt)
+    keep = logits.clone()
+    logits[0] = mask
+    for w, t in enumerate((1, V // 2, V - 1, 17)):
+        logits[0, w, t] = keep[0, w, t]
+        logits[0, w, (t + 300) % V] = keep[0, w, 0]
+    logits[1, :, V - 200:] = mask
+    logits[2] = torch.where(torch.arange(V, device="cuda") // 8 % 2 == 0, mask, keep[2])
+    logits[3, :, :V // 2] = mask
+    got = binding.beam_select(logits, scores, 8)
+    check_best(logits, scores, 8, got)
+    # more than the live tokens: the masked ones, whose order is decided where fp32 pairs tell
+    # the beams' scores apart; their scores are those of the masks
+    check_best(logits, scores, 12, binding.beam_select(logits, scores, 12), live=8)
+
+
+@pytest.mark.parametrize("dt,fill", [
+    (torch.float32, MIN32), (torch.float32, -1e30), (torch.float32, -1e10), (torch.float32, 1e10),
+    (torch.float32, 3.4e38), (torch.bfloat16, MIN16), (torch.bfloat16, -1e10),
+    (torch.bfloat16, 3.3e38), (torch.float16, 65504.0)])
+@pytest.mark.parametrize("V", [9, 8200, 151936])
+def test_every_logit_the_same_far_from_zero(dt, fill, V):
+    logits = torch.full((2, 3, V), fill, device="cuda", dtype=dt)
+    scores = torch.tensor([[-1.0, -2.0, -4.0], [-7.0, -1.0, -2.0]], device="cuda")
+    check_best(logits, scores, 6, binding.beam_select(logits, scores, 6))
