@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p)
 // Scores are pairs of floats hi + lo (|lo| at most half a step of hi): cum + (x - M - log S),
 // lse = M + log S, with 2^-46 of the largest of x - M, cum and log S lost at most, in fp32 adds
 // alone (fp64 runs at a small fraction of their rate here). Equal values give equal pairs, and
-// pairs in the order of (hi, lo) are in the order of their values.
+// pairs in the order of (hi, lo) are in the order of their values. A sum below fp32's range (a
+// masked logit of a beam that is masked itself) is -inf, behind every other.
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   s = __fadd_rn(a, b);
   const float t = __fsub_rn(s, a);
@@ -459,6 +460,10 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
       two_sum(sh_cum[w].x, d, t, e2);
       const float rest = __fadd_rn(e2, __fadd_rn(e1, sh_cum[w].y));
       two_sum(t, rest, hi, lo);
+      if (!(hi > -INFINITY)) {
+        hi = -INFINITY;
+        lo = 0.f;
+      }
       e.flat = w * p.V + static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
     }
     e.score = (static_cast<unsigned long long>(order32(hi + 0.f)) << 32) | order32(lo + 0.f);

@@ -318,3 +318,39 @@ def test_every_logit_the_same_far_from_zero(dt, fill, V):
     logits = torch.full((2, 3, V), fill, device="cuda", dtype=dt)
     scores = torch.tensor([[-1.0, -2.0, -4.0], [-7.0, -1.0, -2.0]], device="cuda")
     check_best(logits, scores, 6, binding.beam_select(logits, scores, 6))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_large_logits_among_small_ones(dt):
+    # one logit far above (alone it has all the weight), one thread's share, a whole chunk
+    V = 151936
+    g = torch.Generator("cuda").manual_seed(5)
+    logits = torch.randn(3, 2, V, generator=g, device="cuda").to(dt)
+    logits[0, :, 77] = 1e10
+    logits[1, :, 800:808] = 1e10
+    logits[2, 0, 4096:8192] = 3e38
+    logits[2, 1] = -3e38
+    logits[2, 1, 5] = 3e38
+    scores = torch.tensor([[-1.0, -3.0]] * 3, device="cuda")
+    check_best(logits, scores, 8, binding.beam_select(logits, scores, 8), live=1)
+
+
+def test_scores_and_logits_both_masked():
+    # the first step with the other beams at finfo.min, and logits at finfo.min: their sums leave
+    # fp32 and come last, at -inf
+    V, n = 20011, 8
+    scores = torch.tensor([[-1.0, MIN32, MIN32]], device="cuda")
+    logits = torch.full((1, 3, V), MIN32, device="cuda")
+    logits[0, 0, 4:7] = torch.tensor([1.0, 3.0, 2.0])
+    logits[0, 1, 9] = logits[0, 2, 3] = 0.0
+    got = binding.beam_select(logits, scores, n)
+    check_best(logits, scores, n, got, live=3)
+    fin = torch.tensor([[0, 1, 0]], dtype=torch.uint8, device="cuda")
+    par, tok, val = binding.beam_select(logits, scores, n, finished=fin, pad_token=2)
+    assert par[0, :3].tolist() == [0, 0, 0] and tok[0, :3].tolist() == [5, 6, 4]
+    assert (val[0, 3:] == MIN32).all()
+    logits[0, 0] = torch.where(logits[0, 0] == MIN32, -math.inf, logits[0, 0])
+    par, tok, val = binding.beam_select(logits, scores, n)
+    assert par[0].tolist() == [0, 0, 0, 1, 2, 1, 1, 1]
+    assert tok[0].tolist() == [5, 6, 4, 9, 3, 0, 1, 2]
+    assert (val[0, 3:5] == MIN32).all() and (val[0, 5:] == -math.inf).all()
