@@ -49,10 +49,9 @@ __device__ __forceinline__ SeqInfo seq_info(const Params& p, const int* qsl, con
   s.n = qsl[b + 1] - s.tok0;
   s.L = lens[b];
   s.pages = (s.L + kBlockSize - 1) / kBlockSize;
-  s.valid = s.n >= 0 && s.n <= s.L && s.pages <= p.max_blocks;
+  s.valid = p.sequence_ok(s.tok0, qsl[b + 1], s.L);
   s.page0 = s.pre = 0;
   if constexpr (Params::kMasked) {
-    s.valid = p.sequence_ok(s.tok0, qsl[b + 1], s.L);
     if (s.valid && s.n > 0) {
       // the rows' lower bounds do not fall from one row to the next: the first row's holds
       s.pre = p.prefix_len(b, s.L);
@@ -779,7 +778,7 @@ __global__ void __launch_bounds__(SplitCfg<D>::kWarps * 32, PS_SPLIT_CTAS_PER_SM
       if (lane == 0) record_error(p.err, kDevBadSequence);
       return 0;
     }
-    const bool bad = n > L || n * p.G > 16 || pe > p.max_blocks;
+    const bool bad = !p.sequence_ok(q0, q1, L) || n * p.G > 16;
     if (bad && lane == 0) record_error(p.err, kDevBadSequence);
     bt_lane = !bad && lane < pe ? bt_raw : -1;
     dir_seq = b;

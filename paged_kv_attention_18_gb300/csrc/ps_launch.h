@@ -61,6 +61,14 @@ struct AttnParams {
   const void* new_v;
   void* k_pool;                  // [num_blocks, 16, H_kv, D]
   void* v_pool;
+
+  // Whether a sequence of packed tokens q0 .. q1 - 1 and context L may be served: its tokens
+  // lie in the batch, its context in the table. Compared without sums that could pass 32
+  // bits; contexts end a tile short of them.
+  __device__ __forceinline__ bool sequence_ok(int q0, int q1, int L) const {
+    return q0 >= 0 && q0 <= q1 && q1 <= T && q1 - q0 <= L && L <= 0x7fffffff - 1024 &&
+           (L + kBlockSize - 1) / kBlockSize <= max_blocks;
+  }
 };
 
 // Masked attention: row r of a sequence with context L, at position p, sees the keys
@@ -79,14 +87,6 @@ struct MaskedAttnParams : AttnParams {
   const int32_t* starts;  // [T] or null
   int tile_step;          // query tiles of a tile item in direct mode: 2, or 1
   int group_rows;         // packed rows of a split-kernel item: 16, or 8 (the narrow kernel)
-
-  // Whether a sequence of packed tokens q0 .. q1 - 1 and context L may be served: its tokens
-  // lie in the batch, its context in the table. Compared without sums that could pass 32
-  // bits; contexts end a tile short of them.
-  __device__ __forceinline__ bool sequence_ok(int q0, int q1, int L) const {
-    return q0 >= 0 && q0 <= q1 && q1 <= T && q1 - q0 <= L && L <= 0x7fffffff - 1024 &&
-           (L + kBlockSize - 1) / kBlockSize <= max_blocks;
-  }
 
   // the first key of the row at packed token `tok`, position `pos`
   __device__ __forceinline__ int row_lo(int tok, int pos) const {

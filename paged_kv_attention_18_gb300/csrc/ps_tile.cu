@@ -236,9 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (is_k && lane < p.B) {
         const int q0 = __ldg(p.qsl + lane), q1 = __ldg(p.qsl + lane + 1);
         const int L = __ldg(p.seq_lens + lane), n = q1 - q0;
-        const bool valid = n >= 0 && n <= L && (L + kBlockSize - 1) / kBlockSize <= p.max_blocks &&
-                           q0 >= 0 && q1 <= p.T;
-        if (!valid) {
+        if (!p.sequence_ok(q0, q1, L)) {
           if (blockIdx.x == 0) record_error(p.err, kDevBadSequence);
         } else if (n > 0) {
           d_n = n;
