@@ -97,6 +97,13 @@ struct MaskedAttnParams : AttnParams {
     }
     return lo;
   }
+  // Whether key `key` below `end` (one past the last key that some of the rows sees) is seen by
+  // none of the rows from position `own` on, `own` not inside the prefix. Bounds do not fall
+  // along the rows, so the first row at or behind the key has the lowest: the key's own row. It
+  // sees nothing at all (its document starts behind it) if not itself.
+  __device__ __forceinline__ bool key_unseen(int key, int own, int end, int tok_minus_pos) const {
+    return starts != nullptr && key >= own && key < end && __ldg(starts + tok_minus_pos + key) > key;
+  }
   __device__ __forceinline__ int prefix_len(int b, int L) const {
     const int x = prefix != nullptr ? __ldg(prefix + b) : 0;
     return x < 0 ? 0 : x > L ? L : x;

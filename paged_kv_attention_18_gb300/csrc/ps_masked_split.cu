@@ -12,8 +12,10 @@
 //   - the plan starts an item at the first page its rows see, so a sliding window costs
 //     the window's bytes whatever the context, and pages before it are never read;
 //   - a key that no row of the item sees has its V row zeroed in shared memory before the
-//     product (only the first and last page can hold one): 0 * V would keep a NaN of
-//     memory that was never written. Its score is replaced, whatever it is;
+//     product: 0 * V would keep a NaN of memory that was never written. Only the first and
+//     last page can hold one, and with documents the pages of the item's own tokens (a row
+//     that starts behind its own position sees nothing, nor does another see its key). Its
+//     score is replaced, whatever it is;
 //   - a row that has seen no key yet keeps its maximum at -inf and subtracts 0, so that
 //     its weights are exactly 0.
 // tanh(y) = 1 - 2 / (2^(2 y log2 e) + 1): one ex2 and one reciprocal. Its absolute error is
@@ -245,6 +247,9 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
   const int g = lane >> 2, t4 = lane & 3;
   uint32_t g_comp = 0, ring_head = 0;
   int comp_left = 0, comp_page = 0;
+  // position from which a key may be seen by no row though others around it are: the item's
+  // first token's, or the prefix's end behind it, where some row of the item sees nothing
+  int own_key = 0;
   bool have_item = false;
   WorkItem cur;
   // per-thread rows of the item: g and g + 8 (narrow: 2 t4 and 2 t4 + 1)
@@ -283,6 +288,10 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
       m_run[r] = -INFINITY;
       l_run[r] = 0.f;
     }
+    const bool empty = row_lo[0] > row_pos[0] || row_lo[1] > row_pos[1];
+    own_key = __any_sync(0xffffffffu, empty)
+                  ? max(cur.ctx_len - cur.n_query + cur.row0 / p.G, cur.pad[3])
+                  : 0x7fffffff - kBlockSize;
 #pragma unroll
     for (int j = 0; j < kO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     // query fragments straight from global memory: rows g (and, wide, g + 8); columns 2 t4,
@@ -413,15 +422,19 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
     const uint32_t vbase = kbase + kPage;
     const int key_base = comp_page * kBlockSize;
 
-    // V rows of keys that no row of the item sees (an edge page): zero
-    if (key_base < cur.pad[1] || key_base + kBlockSize > cur.pad[2]) {
+    // V rows of keys that no row of the item sees: zero
+    if (key_base < cur.pad[1] || key_base + kBlockSize > cur.pad[2] ||
+        key_base + kBlockSize > own_key) {
+      const int mine = key_base + (lane & 15);
+      const unsigned dead = __ballot_sync(
+          0xffffffffu, mine < cur.pad[1] || mine >= cur.pad[2] ||
+                           p.key_unseen(mine, own_key, cur.pad[2],
+                                        cur.tok0 - (cur.ctx_len - cur.n_query)));
       uint8_t* v = tiles + st * kStage + kPage;
 #pragma unroll
-      for (int i = lane; i < kPage / 16; i += 32) {
-        const int key = key_base + (i % (kBlockSize * 8)) / 8;
-        if (key < cur.pad[1] || key >= cur.pad[2])
+      for (int i = lane; i < kPage / 16; i += 32)
+        if (dead >> (i % (kBlockSize * 8)) / 8 & 1u)
           reinterpret_cast<uint4*>(v)[i] = make_uint4(0, 0, 0, 0);
-      }
       __syncwarp();
     }
 

@@ -18,8 +18,8 @@
 //   - an item's keys start at the first page its rows see and end with the last, so a
 //     window or a packed document costs its own keys only;
 //   - the watcher zeroes, before a V tile is handed to the tensor core, the V rows of keys
-//     that no row of the item sees (on its first and last page): 0 * V would keep a NaN
-//     of memory that was never written;
+//     that no row of the item sees (on its first and last page, and with documents among the
+//     item's own tokens): 0 * V would keep a NaN of memory that was never written;
 //   - a key tile inside every row's interval skips the mask; in others a row drops the
 //     columns outside [lo, hi);
 //   - rows without keys get zeros, and -inf as the log-sum of a split that holds them.
@@ -542,21 +542,43 @@ __global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
       const int pb = w.page_begin, pe = w.page_end;
       if (pe <= pb || !tile_item_ok(w, p)) continue;
       const int nt = (pe - pb + kPagesPerTile - 1) / kPagesPerTile;
+      // Where some row of the item sees nothing, a key from the item's first token on (`own`,
+      // behind the prefix) may be seen by none.
+      const int pos0 = w.ctx_len - w.n_query, i0 = w.row0 / p.G;
+      const int i1 = i0 + (w.pad[0] > 0 ? p.tpt + w.pad[0] / p.G : w.nrows / p.G);
+      int own = 0x7fffffff;
+      if (p.starts != nullptr) {
+        bool empty = false;
+        for (int i = i0 + lane; i < i1; i += 32) empty |= __ldg(p.starts + w.tok0 + i) > pos0 + i;
+        if (__any_sync(0xffffffffu, empty)) own = max(pos0 + i0, w.pad[3]);
+      }
       for (int j = 0; j < nt && ok; ++j) {
         const uint32_t gv = gt + j, gk = gv + 1;
         ok = wait(&bars->v_full[gv % kVStages], (gv / kVStages) & 1) &&
              (j + 1 >= nt || wait(&bars->k_full[gk % kKStages], (gk / kKStages) & 1));
         if (!ok) break;
-        // keys of this tile's pages that no row of the item sees: their V rows are zeroed
+        // keys of this tile's pages that no row of the item sees (bits of `dead`): their V
+        // rows are zeroed, four at a time (this code runs once or twice an item, so its size
+        // counts: unrolled it cost the documents' 29 us another 0.6)
         const int kb = (pb + tile_at(j, nt) * kPagesPerTile) * kBlockSize;
         const int ke = min(kb + kKeys, pe * kBlockSize);
-        if (kb < w.pad[1] || ke > w.pad[2]) {
-          uint8_t* v = smem + L::kOffV + (gv % kVStages) * L::kK;
-          for (int i = lane; i < (ke - kb) * 8 * kHalves; i += 32) {
-            const int row = i / (8 * kHalves), c = i % (8 * kHalves), key = kb + row;
-            if (key < w.pad[1] || key >= w.pad[2])
-              *reinterpret_cast<uint4*>(v + (c / 8) * kSub + row * 128 + (c % 8) * 16) =
-                  make_uint4(0, 0, 0, 0);
+        if (kb < w.pad[1] || ke > w.pad[2] || ke > own) {
+          uint8_t* v = smem + L::kOffV + (gv % kVStages) * L::kK + (lane & 7) * 16;
+#pragma unroll 1
+          for (int k = 0; k < kKeys; k += 32) {
+            const int key = kb + k + lane;
+            uint32_t dead = __ballot_sync(
+                0xffffffffu, key < ke && (key < w.pad[1] || key >= w.pad[2] ||
+                                          p.key_unseen(key, own, w.pad[2], w.tok0 - pos0)));
+            while (dead != 0) {
+              const int four = (__ffs(dead) - 1) & ~3, r = four + (lane >> 3);
+              if (dead >> r & 1u) {
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+                  *reinterpret_cast<uint4*>(v + h * kSub + (k + r) * 128) = make_uint4(0, 0, 0, 0);
+              }
+              dead &= ~(15u << four);
+            }
           }
           fence_proxy_async_smem();  // before the tensor core reads them
           __syncwarp();

@@ -394,3 +394,30 @@ def test_math_of_the_cap_at_zero_length_scores():
     out = b.run()
     b.check(out)
     assert math.isfinite(float(out.float().sum()))
+
+
+@pytest.mark.parametrize("seqs", [
+    [(300, 200)], [(700 + i, 4) for i in range(16)], [(200, 100), (90, 33)], [(33, 1), (47, 20)],
+    [(1500, 1400)], [(513, 200), (1, 1), (64, 64), (900, 129), (40, 1), (5000, 2)],
+    [(9000, 4), (700, 1), (12000, 2)]])
+@pytest.mark.parametrize("step,live", [(40, 30), (4, 3), (7, 2), (160, 16)])
+def test_rows_without_keys_between_documents(seqs, step, live):
+    # documents padded to a multiple of `step`: a padding row starts at the next document, so it
+    # sees nothing, and nothing sees its key, which was never written
+    starts = [[p // step * step + (step if p % step >= live else 0) for p in range(L - n, L)]
+              for L, n in seqs]
+    for dt, heads, kw in ((torch.bfloat16, (12, 2, 128), {}),
+                          (torch.float16, (14, 2, 64), dict(window=50, softcap=20.0)),
+                          (torch.bfloat16, (4, 4, 64), dict(slopes=slopes_of(4)))):
+        b = Batch(seqs, *heads, dt, 27, starts=starts, holes=False, **kw)
+        for i, (L, _) in enumerate(seqs):
+            p = torch.arange(L, device="cuda")
+            p = p[p % step >= live]
+            blk = b.bt[i].long()[p // 16]
+            b.k[blk, p % 16] = float("nan")
+            b.v[blk, p % 16] = float("nan")
+        out = b.run()
+        b.check(out)
+        empty = torch.tensor([s > p for (L, n), row in zip(seqs, starts)
+                              for p, s in zip(range(L - n, L), row)], device="cuda")
+        assert (out[empty] == 0).all()
