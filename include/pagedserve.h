@@ -351,7 +351,9 @@ int ps_paged_attention(const void* q, const void* k_pool, const void* v_pool,
  * A row that sees no key (lo >= hi) gives zeros. With all of it absent the result is
  * ps_paged_attention's up to rounding.
  *
- *   scale         > 0 and finite.     softcap  >= 0, 0: none.
+ *   scale         > 0 and finite.     softcap  >= 0, 0: none. A capped score is off by 2^-20 of
+ *                 itself at most (or 2^-15 in log2 units, up to caps of 88, if that is more),
+ *                 so that a large cap tends to none; from 2^100 times the scale it is none.
  *   distance_slopes float [H_q] (finite) or NULL: the linear distance bias.
  *   window        keys a row sees, its own included (a sliding window); 0: none. Block-table
  *                 entries of pages that lie before the first page any row of the sequence

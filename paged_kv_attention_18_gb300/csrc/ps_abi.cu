@@ -884,6 +884,9 @@ int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_p
   // (a scale or cap at the ends of the range)
   if (!std::isfinite(p.scale_log2) || !std::isfinite(p.cap_log2) || !std::isfinite(p.cap_arg))
     return PS_ERR_ARG;
+  // A cap of 2^100 times the scale is none: up to raw scores of 2^88 tanh(y) is y to the last
+  // bit of fp32, and scale / cap soon has no bits left.
+  if (softcap > 0.f && p.cap_y < 0x1p-100f) p.cap_log2 = 0.f;
   p.slopes = distance_slopes;
   p.window = window;
   p.prefix = prefix_lens;

@@ -292,13 +292,18 @@ using MaskedTileLaunch = cudaError_t(const MaskedAttnParams& p, bool bf16, const
                                      const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
                                      cudaStream_t stream, bool direct);
 MaskedTileLaunch launch_masked_tile_plain, launch_masked_tile_cap, launch_masked_tile_bias,
-    launch_masked_tile_cap_bias;
+    launch_masked_tile_cap_bias, launch_masked_tile_large_cap, launch_masked_tile_large_cap_bias;
+// Caps, in log2 units, up to which the tile kernel takes the score's form whose error is 2^-22 of
+// the cap (2^-15 then), where its polynomial does not serve a whole tile (see capped_far).
+constexpr float kLargeCapLog2 = 128.f;
 inline cudaError_t launch_masked_tile(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                       const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
                                       cudaStream_t stream, bool direct) {
   MaskedTileLaunch* const f =
-      p.cap_log2 > 0.f ? (p.slopes ? launch_masked_tile_cap_bias : launch_masked_tile_cap)
-                       : (p.slopes ? launch_masked_tile_bias : launch_masked_tile_plain);
+      p.cap_log2 > kLargeCapLog2
+          ? (p.slopes ? launch_masked_tile_large_cap_bias : launch_masked_tile_large_cap)
+      : p.cap_log2 > 0.f ? (p.slopes ? launch_masked_tile_cap_bias : launch_masked_tile_cap)
+                         : (p.slopes ? launch_masked_tile_bias : launch_masked_tile_plain);
   return f(p, bf16, kmap, vmap, qmap, ctas, stream, direct);
 }
 int run_masked_attention(const MaskedAttnParams& p, const void* k_pool, const void* v_pool,

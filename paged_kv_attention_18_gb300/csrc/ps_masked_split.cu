@@ -18,8 +18,9 @@
 //     score is replaced, whatever it is;
 //   - a row that has seen no key yet keeps its maximum at -inf and subtracts 0, so that
 //     its weights are exactly 0.
-// tanh(y) = 1 - 2 / (2^(2 y log2 e) + 1): one ex2 and one reciprocal. Its absolute error is
-// a few 2^-23 of 1, so a cap of 50 (72 in log2 units) puts under 2^-15 on x, against the
+// The cap is a polynomial in packed arithmetic where a warp's scores of a page lie within half
+// of it, else a polynomial or one ex2 and one reciprocal by the score's size (ps_masked.cuh):
+// within 2^-20 of the score, under 2^-14 on one at a cap of 50 (72 in log2 units), against the
 // 2^-9 that P's rounding to bf16 costs. The kernel is bound by the bytes of K and V.
 #include "ps_common.cuh"
 #include "ps_launch.h"
@@ -289,9 +290,8 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
       l_run[r] = 0.f;
     }
     const bool empty = row_lo[0] > row_pos[0] || row_lo[1] > row_pos[1];
-    own_key = __any_sync(0xffffffffu, empty)
-                  ? max(cur.ctx_len - cur.n_query + cur.row0 / p.G, cur.pad[3])
-                  : 0x7fffffff - kBlockSize;
+    const int pos0 = __shfl_sync(0xffffffffu, row_pos[0], 0);  // the item's first row's
+    own_key = __any_sync(0xffffffffu, empty) ? max(pos0, cur.pad[3]) : 0x7fffffff - kBlockSize;
 #pragma unroll
     for (int j = 0; j < kO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     // query fragments straight from global memory: rows g (and, wide, g + 8); columns 2 t4,
@@ -457,12 +457,17 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
         for (int e = 0; e < 4; ++e) s[e] += s2[e];
       }
       // the scores in log2 units: capped, biased, masked (element e: key g + 8 (e / 2), row e % 2)
+      if (p.cap_log2 > 0.f) {
+        cap_scores<4>(s, p);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] *= p.scale_log2;
+      }
       bool up = false;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = e & 1, key = key_base + g + 8 * (e >> 1);
-        const float c = p.cap_log2 > 0.f ? capped(s[e], p.cap_arg, p.cap_log2) : s[e] * p.scale_log2;
-        const float x = fmaf(slope[r], fabsf(static_cast<float>(row_pos[r] - key)), c);
+        const float x = fmaf(slope[r], fabsf(static_cast<float>(row_pos[r] - key)), s[e]);
         s[e] = key >= row_lo[r] && key < row_hi[r] ? x : -INFINITY;
         up |= s[e] > m_run[r] + 8.f;
       }
@@ -543,10 +548,8 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
       }
       // the scores in log2 units: capped, biased, masked
       if (p.cap_log2 > 0.f) {
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] = capped(s[nt][e], p.cap_arg, p.cap_log2);
+        cap_scores<4>(s[0], p);
+        cap_scores<4>(s[1], p);
       } else {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)

@@ -117,14 +117,16 @@ __device__ __forceinline__ bool tile_item_ok(const WorkItem& w, const MaskedAttn
 
 // kDirect: no plan. Each CTA derives its items from seq_lens and qsl (every sequence
 // unsplit, its query-tile pairs longest first).
-template <bool kBF16, int D, bool kDirect, bool kCap, bool kBias>
-__global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
+// kCap: 0 none, 1 up to kLargeCapLog2, 2 beyond (the exact form of small scores in every tile; as
+// a branch inside it made the kernel larger and its other caps 1.5 % slower).
+template <bool kBF16, int D, bool kDirect, int kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
     masked_tile_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap,
                        const __grid_constant__ CUtensorMap qmap, const MaskedAttnParams p) {
   using L = TileSmem<D>;
   constexpr int kHalves = D / 64;
-  constexpr bool kDuo = kCap || kBias;
+  constexpr bool kDuo = kCap > 0 || kBias;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
 
@@ -894,7 +896,7 @@ __global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
       // least) every P is below 2^60 and, up to kFixedCapLog2, at least 2^-120: within bf16's
       // normal range and, summed, within fp32's. Then no maximum is taken, nothing moves, and
       // the two warps of a row have nothing to tell one another before the end.
-      const bool fixed = kCap && !kBias && kBF16 && p.cap_log2 <= kFixedCapLog2;
+      const bool fixed = kCap == 1 && !kBias && kBF16 && p.cap_log2 <= kFixedCapLog2;
       const float m_fixed = fixed ? fmaxf(p.cap_log2 - 60.f, 0.f) : -INFINITY;
       uint32_t sc = 0, act = 0;
       bool ok = true;
@@ -964,10 +966,12 @@ __global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
           };
           // brought to log2 units in place: any cap, any bias, masked
           auto to_log2 = [&](int h, uint32_t* v) {
-            if constexpr (kCap) {
+            if constexpr (kCap > 0) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                v[e] = __float_as_uint(capped(__uint_as_float(v[e]), p.cap_arg, p.cap_log2));
+              for (int e = 0; e < 32; ++e) {
+                const float raw = __uint_as_float(v[e]);
+                v[e] = __float_as_uint(kCap == 1 ? capped_far(raw, p) : capped(raw, p));
+              }
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
@@ -1005,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
               add_pair_exact<kBF16>(lq[(e / 2) & 1], pk[16 * h + e / 2]);
             };
             bool fast = one_sign;
-            if constexpr (kCap) {
+            if constexpr (kCap > 0) {
               float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int e = 0; e < 32; e += 8)
@@ -1027,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
                   const float x = fmaf(slope, d0 - static_cast<float>(e), neg_m);
                   c = make_float2(x, x - slope);
                 }
-                put(e, kCap ? capped_poly2(fmul2(raw(e), cap_y2), p.tanh4, c)
+                put(e, kCap > 0 ? capped_poly2(fmul2(raw(e), cap_y2), p.tanh4, c)
                             : ffma2(raw(e), sl2x2, c));
               }
             } else {
@@ -1166,7 +1170,7 @@ __global__ void __launch_bounds__(kThreads<(kCap || kBias)>, 1)
   if (!kDirect && p.after_split && blockIdx.x == 0 && threadIdx.x == 0) pdl_wait();
 }
 
-template <bool kBF16, int D, bool kDirect, bool kCap, bool kBias>
+template <bool kBF16, int D, bool kDirect, int kCap, bool kBias>
 static cudaError_t launch_masked_tile_t(const MaskedAttnParams& p, const CUtensorMap& kmap,
                                         const CUtensorMap& vmap, const CUtensorMap& qmap,
                                         int ctas, cudaStream_t stream) {
@@ -1175,11 +1179,11 @@ static cudaError_t launch_masked_tile_t(const MaskedAttnParams& p, const CUtenso
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_limit(kern, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(ctas), dim3(kThreads<(kCap || kBias)>), smem, stream, true, kmap, vmap, qmap, p);
+  return launch_kernel(kern, dim3(ctas), dim3(kThreads<(kCap > 0 || kBias)>), smem, stream, true, kmap, vmap, qmap, p);
 }
 
 // The instantiations of one (cap, bias) pair: one per type, head size and mode.
-template <bool kCap, bool kBias>
+template <int kCap, bool kBias>
 static cudaError_t launch_masked_tile_kind(const MaskedAttnParams& p, bool bf16,
                                            const CUtensorMap& kmap, const CUtensorMap& vmap,
                                            const CUtensorMap& qmap, int ctas,

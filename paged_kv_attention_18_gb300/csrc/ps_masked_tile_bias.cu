@@ -6,7 +6,7 @@ namespace ps {
 cudaError_t launch_masked_tile_bias(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                     const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
                                     cudaStream_t stream, bool direct) {
-  return launch_masked_tile_kind<false, true>(p, bf16, kmap, vmap, qmap, ctas, stream, direct);
+  return launch_masked_tile_kind<0, true>(p, bf16, kmap, vmap, qmap, ctas, stream, direct);
 }
 
 }  // namespace ps

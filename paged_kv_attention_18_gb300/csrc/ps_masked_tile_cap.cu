@@ -6,7 +6,7 @@ namespace ps {
 cudaError_t launch_masked_tile_cap(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                     const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
                                     cudaStream_t stream, bool direct) {
-  return launch_masked_tile_kind<true, false>(p, bf16, kmap, vmap, qmap, ctas, stream, direct);
+  return launch_masked_tile_kind<1, false>(p, bf16, kmap, vmap, qmap, ctas, stream, direct);
 }
 
 }  // namespace ps

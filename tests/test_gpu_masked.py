@@ -421,3 +421,29 @@ def test_rows_without_keys_between_documents(seqs, step, live):
         empty = torch.tensor([s > p for (L, n), row in zip(seqs, starts)
                               for p, s in zip(range(L - n, L), row)], device="cuda")
         assert (out[empty] == 0).all()
+
+
+@pytest.mark.parametrize("name", list(BATCHES))
+@pytest.mark.parametrize("cap", [1e3, 1e4, 1e5, 1e6, 1e8, 1e30, 2e38])
+def test_caps_far_above_the_scores(name, cap):
+    # cap * tanh(x / cap) tends to x: the error has the size of the score, not of the cap. The
+    # cap takes a score's value off by 2^-20 of it at most (the polynomial 2^-20.7, or one
+    # reciprocal's 2^-22 of the cap where the score is half of it at least), in numerator and
+    # denominator; without the cap's own share `size` is the scores' (tanh only shrinks them).
+    for dt, heads, kw in ((torch.bfloat16, (12, 2, 128), {}), (torch.float16, (7, 1, 64), {}),
+                          (torch.bfloat16, (14, 2, 64), dict(slopes=slopes_of(14)))):
+        b = Batch(BATCHES[name], *heads, dt, 28, softcap=cap, **kw)
+        out = b.run()
+        for i, (L, n) in enumerate(b.seqs):
+            if n == 0:
+                continue
+            a, e = b.off[i], b.off[i + 1]
+            args = (b.q[a:e], R.gather(b.k, b.bt[i], L), R.gather(b.v, b.bt[i], L),
+                    torch.arange(L - n, L, device="cuda"), b.scale)
+            _, _, size, _ = R.attend_dense(*args, 0.0, b.slopes)
+            ref, absv, _, tail = R.attend_dense(*args, cap, b.slopes)
+            tol = R.attention_tolerance(ref, absv, size, tail, b.d, dt) + \
+                math.log(2) * 2.0 ** -20 * size[..., None] * (absv + ref.abs())
+            err = (out[a:e].double() - ref).abs()
+            assert not (err > tol).any() and torch.isfinite(out[a:e]).all(), \
+                (i, L, n, float((err - tol).max()))
