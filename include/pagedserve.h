@@ -372,7 +372,8 @@ int ps_paged_attention(const void* q, const void* k_pool, const void* v_pool,
  * K and V at keys that no row of the sequence sees (rows of a block never written, blocks
  * given back) may hold anything, NaN included. V at a key that one row of the step sees must
  * be finite for the others' sake: a NaN or infinity there may reach rows of the same
- * sequence and step that do not see it.
+ * sequence and step that do not see it. In bf16 the fp32 sums hold values of V up to 2^40 in
+ * magnitude whatever the scores; beyond, they may overflow.
  */
 int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_pool,
                               const int32_t* block_tables, int max_blocks_per_seq,

@@ -66,7 +66,8 @@ constexpr uint32_t kSumExp = kBF16 ? 127 + 64 : 127 + 22;
 // The same bound for a 64-column half taken by one warp.
 template <bool kBF16>
 constexpr float kHalfSumMax = kBF16 ? 18446744073709551616.f : 4194304.f;
-constexpr float kFixedCapLog2 = 90.f;  // caps up to 62 keep a fixed reference (bf16)
+constexpr float kFixedCapLog2 = 73.f;  // caps up to 50.6 keep a fixed reference (bf16)
+constexpr float kFixedLeastLog2 = -86.f;  // the least P against it (see `fixed`)
 constexpr uint32_t kTmemCols = 512;
 
 // TMEM columns of softmax group g: S (and P over it) at g*256, O at g*256 + 128
@@ -892,12 +893,13 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         *mx = m == kNone ? -INFINITY : static_cast<float>(m);
         return true;
       };
-      // Capped scores lie within cap_log2 of 0. Against a fixed reference of cap_log2 - 60 (0 at
-      // least) every P is below 2^60 and, up to kFixedCapLog2, at least 2^-120: within bf16's
-      // normal range and, summed, within fp32's. Then no maximum is taken, nothing moves, and
-      // the two warps of a row have nothing to tell one another before the end.
+      // Capped scores lie within c = cap_log2 of 0. Against a fixed reference of 86 - c (c at
+      // most) every P is between 2^-86, so that products with |V| down to 2^-40 are normal in
+      // fp32, and 2^(2 c - 86), 2^60 at kFixedCapLog2 (1 for caps up to 29), so that sums with
+      // |V| up to 2^40 hold 2^28 keys. Then no maximum is taken, nothing moves, and the two warps
+      // of a row have nothing to tell one another before the end.
       const bool fixed = kCap == 1 && !kBias && kBF16 && p.cap_log2 <= kFixedCapLog2;
-      const float m_fixed = fixed ? fmaxf(p.cap_log2 - 60.f, 0.f) : -INFINITY;
+      const float m_fixed = fixed ? fminf(p.cap_log2, -kFixedLeastLog2 - p.cap_log2) : -INFINITY;
       uint32_t sc = 0, act = 0;
       bool ok = true;
       for (int it = 0; ok; ++it) {

@@ -447,3 +447,20 @@ def test_caps_far_above_the_scores(name, cap):
             err = (out[a:e].double() - ref).abs()
             assert not (err > tol).any() and torch.isfinite(out[a:e]).all(), \
                 (i, L, n, float((err - tol).max()))
+
+
+@pytest.mark.parametrize("name", ["small_chunks", "chunks", "one_chunk", "decodes"])
+@pytest.mark.parametrize("cap", [15.0, 29.0, 31.0, 45.0, 50.0, 51.0, 62.0, 63.0, 200.0])
+def test_rows_near_either_end_of_the_cap(name, cap):
+    # every score of a row within a few hundredths of -cap, or of +cap: whatever the softmax is
+    # taken against, products with small and with large values keep their bits
+    for dt, std in ((torch.bfloat16, 2.0 ** -36), (torch.bfloat16, 1.0), (torch.bfloat16, 2.0 ** 36),
+                    (torch.float16, 1.0)):
+        b = Batch(BATCHES[name], 12, 2, 128, dt, 29, softcap=cap, holes=False)
+        g = torch.Generator("cuda").manual_seed(30)
+        u = 0.7 + 0.6 * torch.rand(b.k.shape[:3], generator=g, device="cuda")
+        b.k = u[..., None].expand(b.k.shape).to(dt).contiguous()
+        sign = torch.randint(0, 2, b.q.shape[:2], generator=g, device="cuda") * 2.0 - 1.0
+        b.q = (sign * (2.0 * cap / b.scale / b.d))[..., None].expand(b.q.shape).to(dt).contiguous()
+        b.v = (b.v.float() * std).to(dt)
+        b.check(b.run())
