@@ -4,11 +4,14 @@ module ``_native`` that calls it with the host compiler.
 Each ``csrc/*.cu`` file compiles in parallel to an object under ``_build/`` at the
 repository root; the objects link into ``paged_kv_attention_18_gb300/libpagedserve.so``
 with the CUDA runtime linked statically. Objects are rebuilt when a source or header
-is newer.
+is newer. The library needs nvcc alone: where torch is not installed the Python module is left
+out, and where it does not compile (no host C++ compiler, no Python headers) the error comes
+once the library is in place.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -110,14 +113,14 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
 
     # (the host compiler's one object beside nvcc's)
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        native = ex.submit(_native_object, verbose)
+        native = ex.submit(_native_object, verbose) if importlib.util.find_spec("torch") else None
         objs = list(ex.map(compile_one, srcs))
-        native_obj = native.result()
     if (not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs)):
         tmp = LIB + ".tmp"
         _run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], "nvcc link", verbose)
         os.replace(tmp, LIB)
-    _link_native(native_obj, verbose)
+    if native is not None:
+        _link_native(native.result(), verbose)
     return LIB
 
 
