@@ -396,7 +396,9 @@ int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const v
   // One launch without a plan, a CTA for each group of rows of a (sequence, KV head): for few of
   // those, with contexts that a CTA reads in the time a plan and a join would take, and no more
   // than 64 rows a sequence on average (the kernel finds its items from the offsets, so a
-  // sequence with more is served by more CTAs). Both ways, us (planned / direct), one token a
+  // sequence with more is served by more CTAs). The lengths are on the device: the width of the
+  // tables stands for them, so tables wider than the contexts need are planned (36 of 512 with 2048
+  // entries each: 18.3 against 7.5). Both ways, us (planned / direct), one token a
   // sequence unless said:
   //   12 heads on 2, D 128:  1 sequence of 2048 19.2 / 15.6, of 4096 21.1 / 26.3, of 8192 27 / 48;
   //                          36 of 512 20.2 / 7.9, of 2048 22.9 / 16.3; 152 of 2048 53.9 / 39.7;

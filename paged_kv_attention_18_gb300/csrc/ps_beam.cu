@@ -14,7 +14,7 @@
 //   merge   one CTA per prompt: lse of each beam from its chunks' (M, sum), then the same
 //           bound on the chunks' candidates, and the ranks of those that pass.
 // Bound by the bytes of the logits (read once): 192 rows of 151936 bf16 logits (58 MB) scan in
-// 17 us, of which 12.5 us are the stream (4.6 TB/s), 3 the bound and 1 the candidates; the
+// 17.5 us, of which 13 us are the stream (4.5 TB/s), 3 the bound and 1 the candidates; the
 // merge of 48 prompts adds 3 to 4 us behind it. Listing candidates from the registers in the
 // stream, against a bound from its first round, took 24 us: the few lanes that have one stop
 // their warps every round.

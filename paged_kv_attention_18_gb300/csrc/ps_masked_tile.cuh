@@ -11,9 +11,9 @@
 // and every MMA; warp 3 the K/V watcher; from warp 4 the softmax groups of A and B, with one
 // thread for a query row or two (kSoftmaxWarps).
 // Bound: a group's chain S -> softmax -> PV -> next S (S overwrites P, so they cannot
-// overlap), the two groups filling each other's gaps. 4 x 2048 tokens over 8192 keys, 32/8
-// heads, D 128, 629 GFLOP: masks alone 485 us (1.30 PFLOP/s,
-// 0.67 of the measured burst peak), capped 583 (bf16) and 638 (fp16), biased 570, both 716.
+// overlap), the two groups filling each other's gaps. 4 x 2048 tokens, each over 8192 keys, 32/8
+// heads, D 128, 962 GFLOP: masks alone 670 us (1.44 PFLOP/s, 0.74 of the measured burst peak),
+// capped 800 (bf16) and 877 (fp16), biased 777, both 997 (bf16) and 1020 (fp16).
 // What the mask adds:
 //   - an item's keys start at the first page its rows see and end with the last, so a
 //     window or a packed document costs its own keys only;
@@ -44,8 +44,8 @@ constexpr int kKStages = 3;       // K tile stages (freed once both products S h
 constexpr int kVStages = 2;       // V tile stages (freed once both products PV have read them)
 constexpr int kItemRing = 4;     // item indices handed from the fetching warp to the others
 // Softmax warps: one for every 32 query rows, or two (kDuo) with half of a key tile's columns
-// each where a cap or a bias makes the softmax the longest part. (4 x 2048 tokens over 8192
-// keys, 32/8 heads, D 128: capped 729 us with one, 580 with two; masks alone 486 and 495, and
+// each where a cap or a bias makes the softmax the longest part. (4 x 2048 tokens, contexts to
+// 8192, 32/8 heads, D 128: capped 729 us with one, 580 with two; masks alone 486 and 495, and
 // short documents, 1000 tokens of up to 300 each, 28 and 33: the two must agree on a row's
 // reference.)
 template <bool kDuo>
@@ -563,8 +563,8 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         if (!ok) break;
         // keys of this tile's pages that no row of the item sees (bits of `dead`): their V
         // rows are zeroed, four at a time (this code runs once or twice an item, so its size
-        // counts: with loops unrolled the documents' 30.5 us were 31.1, and a chunk's 777 with a
-        // bias 788)
+        // counts: with loops unrolled, 6 chunks of documents took 31.1 us in place of 30.5, and
+        // the 777 us with a bias above 788)
         const int kb = (pb + tile_at(j, nt) * kPagesPerTile) * kBlockSize;
         const int ke = min(kb + kKeys, pe * kBlockSize);
         if (kb < w.pad[1] || ke > w.pad[2] || ke > own) {
