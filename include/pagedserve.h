@@ -210,10 +210,10 @@ int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, 
  * lse is summed in fp32 within a chunk of the row and in fp64 across chunks, and is off by
  * 2^-16 at most for vocabularies to 2^17 (the exponentials, 64 adds and 16 rescalings of a
  * thread, 15 joins, the logarithm; usually by 2^-20): continuations of two beams whose scores
- * lie closer than twice that may change places. Given lse, scores are compared as pairs of floats (48 bits of
- * the largest of x - max x, scores[b, w] and lse_w - max x; what is below that counts as
- * equal) and rounded once to fp32, below its range to -inf. So the order within a beam is its
- * logits' as long as scores[b, w] leaves room for their differences.
+ * lie closer than twice that may change places. Given lse, scores are compared as pairs of
+ * floats (48 bits of the largest of x - max x, scores[b, w] and lse_w - max x; what is below
+ * that counts as equal) and rounded once to fp32, below its range to -inf. So the order within
+ * a beam is its logits' as long as scores[b, w] leaves room for their differences.
  *
  *   logits        [B, W, V] of logits_dtype (PS_F16, PS_BF16 or PS_F32), rows row_stride
  *                 ELEMENTS apart (at least V: a padded vocabulary is left out by it),

@@ -3,8 +3,9 @@
 
 namespace ps {
 
-cudaError_t launch_masked_tile_large_cap_bias(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
-                                              const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
+cudaError_t launch_masked_tile_large_cap_bias(const MaskedAttnParams& p, bool bf16,
+                                              const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                              const CUtensorMap& qmap, int ctas,
                                               cudaStream_t stream, bool direct) {
   return launch_masked_tile_kind<2, true>(p, bf16, kmap, vmap, qmap, ctas, stream, direct);
 }
