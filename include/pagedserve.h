@@ -50,7 +50,7 @@ extern "C" {
 
 #define PS_BLOCK_SIZE 16
 
-typedef enum { PS_F16 = 0, PS_BF16 = 1, PS_F32 = 2 } ps_dtype; /* F32: ps_beam_select's logits */
+typedef enum { PS_F16 = 0, PS_BF16 = 1, PS_F32 = 2 } ps_dtype; /* F32: logits alone */
 
 typedef enum {
   PS_OK = 0,
@@ -67,10 +67,13 @@ typedef enum {
   PS_DEV_BAD_BLOCK_ID = 1,   /* a block-table entry outside [0, num_blocks)            */
   PS_DEV_BAD_SLOT = 2,       /* a slot_mapping entry >= num_blocks * 16                */
   PS_DEV_BAD_SEQUENCE = 3,   /* query count > context, context beyond the table, or a
-                                parent outside its group (ps_fork_sequences)           */
+                                parent outside its group (ps_fork_sequences), or
+                                tokens beyond the packed batch (ps_extend_sequences)   */
   PS_DEV_WAIT_TIMEOUT = 4,   /* a kernel's bounded wait ran out (the kernel returned)  */
   PS_DEV_PLAN_OVERFLOW = 5,  /* the work plan did not fit the workspace                */
-  PS_DEV_BAD_TOKEN = 6       /* a draft token id outside [0, V)                          */
+  PS_DEV_BAD_TOKEN = 6,      /* a draft token id outside [0, V)                          */
+  PS_DEV_NO_BLOCKS = 7,      /* a step needs more blocks than are free                   */
+  PS_DEV_BAD_AXIS = 8        /* a frequency's axis outside [0, num_axes)                 */
 } ps_device_error;
 
 /*
@@ -193,6 +196,106 @@ int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, 
                                 float magnitude, void* q_out, int64_t q_out_stride, int T,
                                 int H_q, int H_kv, int D, int num_blocks, int dtype,
                                 void* stream);
+
+/*
+ * ps_rotary_axes_reshape_and_cache -- ps_rotary_reshape_and_cache with positions of several
+ * axes (time, height and width of images and video): frequency i turns by the position on its
+ * own axis, a = positions[axes[i]][t] * inv_freq[i].
+ *
+ *   positions     int32 [num_axes, T]: every token's position on each axis (text has the same
+ *                 on all of them).
+ *   axes          int32 [R / 2]: the axis of every frequency, in [0, num_axes), in any order
+ *                 (sections one after another, or the axes in turns). Another value records
+ *                 PS_DEV_BAD_AXIS, and its frequency does not turn.
+ * Other arguments, precision and errors as for ps_rotary_reshape_and_cache.
+ */
+int ps_rotary_axes_reshape_and_cache(const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     const int32_t* positions, const int32_t* axes, int num_axes,
+                                     const int32_t* slot_mapping, void* k_pool, void* v_pool,
+                                     const double* inv_freq, int rotary_dim, int interleaved,
+                                     float magnitude, void* q_out, int64_t q_out_stride, int T,
+                                     int H_q, int H_kv, int D, int num_blocks, int dtype,
+                                     void* stream);
+
+/*
+ * ps_extend_sequences -- the blocks, slots, positions and packed offsets of a step, from every
+ * sequence's length and number of new tokens, on the device.
+ *
+ * Sequence b of L_b = seq_lens[b] tokens adds n_b = new_lens[b] (0: none; negative: it ends).
+ * Its pages L_b / 16 (rounded up) .. (L_b + n_b - 1) / 16 get blocks from the top of a stack of
+ * free ones: the i-th new block of the step, in order of sequences and pages, is
+ * free_blocks[count - 1 - i]. Before that go onto the stack, in order of sequences:
+ *   - the blocks of a sequence that ends, from its last page to its first; its length becomes 0;
+ *   - with window > 0, the blocks that no token from L_b on sees through a sliding window of
+ *     `window` keys and the sequence's first `sinks` (see ps_paged_attention_streaming): pages
+ *     that end at or before L_b - window + 1 and begin at or behind `sinks`, from the last one
+ *     down to the first whose entry is negative already.
+ * Their entries become -1. Such a block must not be in another sequence's table (nor twice in
+ * one): what sequences share (prefixes, forks) is for the caller to count and to give back.
+ *
+ *   block_tables  int32 [B, max_blocks_per_seq], updated in place.
+ *   seq_lens, new_lens  int32 [B]. (An empty place of a batch: length 0, 0 new tokens.)
+ *   free_blocks   int32 [free_capacity]: the stack, updated in place (room for every block that
+ *                 comes back: num_blocks entries are enough); free_count int32 [1]: its entries.
+ *   T             room for packed tokens: at least the sum of the new ones.
+ *   query_start_loc int32 [B + 1], written: packed offsets (the last one the tokens in all, at
+ *                 most T).
+ *   slot_mapping, positions  int32 [T], written: each packed token's pool slot and position; -1
+ *                 and 0 from query_start_loc[B] on.
+ *   out_seq_lens  int32 [B], written: the lengths after the step; may be seq_lens.
+ *   out_free_count int32 [1], written; may be free_count.
+ * Entries of pages that a sequence holds already, and those past its new ones, are left as they
+ * were. A sequence is left out of the step (no tokens, its length as it was) where
+ *   - its length is negative or it would outgrow its table, or its tokens and those asked for
+ *     before it do not fit T (PS_DEV_BAD_SEQUENCE);
+ *   - it needs new blocks, and those with the ones needed before it are more than are free
+ *     (PS_DEV_NO_BLOCKS).
+ * The host sees who was left out by query_start_loc. A stack entry or table entry outside the
+ * pool that is to be used records PS_DEV_BAD_BLOCK_ID (its slots are -1, the new table entry
+ * -1), and so does a free_count outside [0, free_capacity] (which counts as 0) and a stack that
+ * overflows. B up to 8192 and B * max_blocks_per_seq below 2^31 (PS_ERR_UNSUPPORTED).
+ */
+int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                        const int32_t* new_lens, int32_t* free_blocks, int free_capacity,
+                        const int32_t* free_count, int B, int T, int num_blocks, int window,
+                        int sinks, int32_t* query_start_loc, int32_t* slot_mapping,
+                        int32_t* positions, int32_t* out_seq_lens, int32_t* out_free_count,
+                        void* stream);
+
+/*
+ * ps_sample -- one token of every row of logits, by temperature, top-k, top-p and min-p, from a
+ * given random word.
+ *
+ * With T = temperature[b] and w_v = exp((x_v - max x) / T) for the row's logits x, tokens in
+ * order of falling x (ties: the lowest first), the kept tokens are those in all of
+ *   - the first top_k[b] (0, negative, or V and more: all);
+ *   - of these, the ones whose predecessors' weights sum to less than top_p[b] times the sum
+ *     over the first top_k[b] (the fewest that reach that share; 1 and more: all; 0 and less:
+ *     the first alone);
+ *   - those with w_v >= min_p[b] (0 and less: all; 1 and more: the largest).
+ * The token is the first kept one, in order of the vocabulary, whose running sum of kept weights
+ * exceeds floor(R Z / 2^32), with Z their sum and R = random_bits[b]; its log probability is
+ * ln(w / Z). A temperature of 0 (below 2^-100, or NaN) takes the first of the largest logits,
+ * log probability 0. A logit of -inf or NaN is no token; a row without any, or with one of +inf,
+ * gives token -1 and log probability -inf. Finite logits are served whatever their size. A NaN
+ * in top_p or min_p is no filter.
+ * Weights are off by 2^-29 of themselves at most, and those below 2^(log2(V) - 62) of the
+ * largest (2^-58 if that is more) are rounded to multiples of that; their sums are exact. So a
+ * draw or a border of top_p is decided as in exact arithmetic but for R or top_p within about
+ * 2^-30 of a border between two tokens. min_p's border is exact but for fp64's rounding.
+ *
+ *   logits        [B, V] of logits_dtype (PS_F16, PS_BF16 or PS_F32), rows row_stride ELEMENTS
+ *                 apart (at least V), aligned to an element. Read once.
+ *   temperature   float [B] or NULL (1).     top_k  int32 [B] or NULL.
+ *   top_p, min_p  float [B] or NULL.         random_bits  uint32 [B].
+ *   tokens        int32 [B], logprobs float [B], written.
+ * V up to 393216 (PS_ERR_UNSUPPORTED beyond). B = 0 is a no-op.
+ */
+int ps_sample(const void* logits, int64_t row_stride, const float* temperature,
+              const int32_t* top_k, const float* top_p, const float* min_p,
+              const uint32_t* random_bits, int B, int V, int logits_dtype, int32_t* tokens,
+              float* logprobs, void* stream);
 
 /*
  * ps_beam_select -- beam search's selection over beams and vocabulary.
@@ -389,6 +492,31 @@ int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_p
                               void* workspace, size_t workspace_bytes, int dtype, void* stream);
 
 /*
+ * ps_paged_attention_streaming -- ps_paged_attention for streams longer than the cache: a row
+ * sees the last keys before it and the first ones of its sequence.
+ *
+ * For packed row r at position p of sequence b and query head h:
+ *     x_j = softcap * tanh(scale * q . K_j / softcap)    (softcap > 0; else scale * q . K_j)
+ *     out[r, h, :] = sum_j softmax_j(x_j) V_j over the keys j <= p with j > p - window or
+ *     j < sinks
+ *
+ *   window        keys a row sees up to its own, its own included; 0: all.
+ *   sinks         first keys of every sequence that stay visible; 0: none.
+ *                 Block-table entries of pages that lie behind the sinks' and before the first
+ *                 page of the first row's window are not read: those blocks may have been given
+ *                 back (ps_extend_sequences does).
+ * scale, softcap, other arguments, workspace, errors, batches padded behind the last sequence
+ * and NaN at keys that no row sees as for ps_paged_attention_masked.
+ */
+int ps_paged_attention_streaming(const void* q, const void* k_pool, const void* v_pool,
+                                 const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* seq_lens, const int32_t* query_start_loc, int B,
+                                 int T, int H_q, int H_kv, int D, int num_blocks, float scale,
+                                 float softcap, int window, int sinks, void* out,
+                                 void* workspace, size_t workspace_bytes, int dtype,
+                                 void* stream);
+
+/*
  * ps_paged_attention_noalloc -- ps_paged_attention for callers that cannot allocate.
  *
  * The pages describe no such call; it exists for users of this library. Some callers
@@ -519,12 +647,13 @@ const char* ps_status_string(int status);
  * around the next n launches of each kernel kind (host memory only; events are created
  * here, not in the timed calls). ps_profile_end() waits for the recorded events and
  * stops recording. ps_profile_read(kind, &ms, &launches) then gives the summed device
- * time and the launch count of one kind: 0 slot mapping, 1 KV scatter as its own launch
+ * time and the launch count of one kind: 0 slot mapping (and sequence extension), 1 KV scatter as its own launch
  * (ps_reshape_and_cache, or the step's scatter ahead of the tile kernel's direct mode),
  * 2 planner (carrying the step's KV scatter when there is one), 3 split attention (decode
  * and verify rows), 4 split combine, 5 tile attention (prefill rows, tcgen05), 6 block
- * copy (and sequence forks), 7 speculative acceptance (and beam selection), 8 rotary KV
- * scatter (either form). The masked attention's kernels count under 2 to 5.
+ * copy (and sequence forks), 7 speculative acceptance (and beam selection and
+ * sampling), 8 rotary KV scatter (any form). The masked and streaming attention's kernels count under
+ * 2 to 5.
  */
 int ps_profile_begin(int max_launches_per_kind);
 int ps_profile_end(void);

@@ -29,6 +29,13 @@ SIGNATURES = {
     "ps_rotary_reshape_and_cache": (c_int, [_p, c_i64, _p, c_i64, _p, c_i64, _p, _p, _p, _p, _p,
                                             c_int, c_int, c_float, _p, c_i64, c_int, c_int,
                                             c_int, c_int, c_int, c_int, _p]),
+    "ps_rotary_axes_reshape_and_cache": (c_int, [_p, c_i64, _p, c_i64, _p, c_i64, _p, _p, c_int,
+                                                 _p, _p, _p, _p, c_int, c_int, c_float, _p,
+                                                 c_i64, c_int, c_int, c_int, c_int, c_int, c_int,
+                                                 _p]),
+    "ps_extend_sequences": (c_int, [_p, c_int, _p, _p, _p, c_int, _p, c_int, c_int, c_int, c_int,
+                                    c_int, _p, _p, _p, _p, _p, _p]),
+    "ps_sample": (c_int, [_p, c_i64, _p, _p, _p, _p, _p, c_int, c_int, c_int, _p, _p, _p]),
     "ps_beam_select_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
     "ps_beam_select": (c_int, [_p, c_i64, _p, _p, c_int, c_int, c_int, c_int, c_int, c_int, _p,
                                _p, _p, _p, c_size_t, _p]),
@@ -43,6 +50,9 @@ SIGNATURES = {
     "ps_paged_attention_masked": (c_int, [_p, _p, _p, _p, c_int, _p, _p, c_int, c_int, c_int,
                                           c_int, c_int, c_int, c_float, c_float, _p, c_int, _p,
                                           _p, _p, _p, c_size_t, c_int, _p]),
+    "ps_paged_attention_streaming": (c_int, [_p, _p, _p, _p, c_int, _p, _p, c_int, c_int, c_int,
+                                             c_int, c_int, c_int, c_float, c_float, c_int, c_int,
+                                             _p, _p, c_size_t, c_int, _p]),
     "ps_paged_attention_noalloc": (c_int, [_p, _p, _p, _p, c_int, _p, _p, c_int, c_int, c_int,
                                            c_int, c_int, c_int, c_float, _p, c_int, _p]),
     "ps_attention_step": (c_int, [_p, _p, _p, _p, _p, _p, c_int, _p, _p, c_int, c_int, c_int,

@@ -1,7 +1,8 @@
 """Python binding of the C ABI: argument marshalling from torch tensors, nothing else.
 
 The calls that a decode loop makes for every layer and token (rotary_reshape_and_cache,
-masked_paged_attention, beam_select, fork_sequences) do their checks and the C call in a
+rotary_axes_reshape_and_cache, masked_paged_attention, streaming_paged_attention, sample,
+extend_sequences, beam_select, fork_sequences) do their checks and the C call in a
 compiled module (csrc/py_native.cpp); the others go through ctypes. Either way:
 
 Every function checks that its tensors live on the current CUDA device, are
@@ -236,6 +237,51 @@ def rotary_reshape_and_cache(q, k, v, positions, slot_mapping_t, k_pool, v_pool,
                                                 inv_freq, interleaved, magnitude, q_out, stream)
 
 
+def rotary_axes_reshape_and_cache(q, k, v, positions, slot_mapping_t, k_pool, v_pool, inv_freq,
+                                  axes, interleaved: bool = False, magnitude: float = 1.0,
+                                  q_out=None, stream=None) -> torch.Tensor:
+    """rotary_reshape_and_cache with positions of several axes, time, height and width of images
+    and video (ps_rotary_axes_reshape_and_cache): positions int32 [num_axes, T], axes int32
+    [rotary_dim / 2] the axis of every frequency (see :func:`rotary.axes`)."""
+    return (_native_module or _native()).rotary_axes(q, k, v, positions, slot_mapping_t, k_pool,
+                                                     v_pool, inv_freq, axes, interleaved,
+                                                     magnitude, q_out, stream)
+
+
+def extend_sequences(block_tables, seq_lens, new_lens, free_blocks, free_count, num_blocks: int,
+                     query_start_loc, slot_mapping_t, positions, window: int = 0, sinks: int = 0,
+                     out_seq_lens=None, out_free_count=None, stream=None) -> None:
+    """The blocks, slots, positions and packed offsets of a step, on the device
+    (ps_extend_sequences). Sequence b of seq_lens[b] tokens adds new_lens[b] (negative: it ends):
+    new pages get blocks from the top of the stack free_blocks [capacity] of free_count [1]
+    entries, and with a window the blocks behind it go back first, as do those of sequences that
+    end. All int32 CUDA tensors; block_tables [B, max_blocks], free_blocks, seq_lens and
+    free_count (the last two unless out_seq_lens, out_free_count are given) are updated in place;
+    query_start_loc [B + 1], slot_mapping_t [T] and positions [T] are written, with -1 and 0
+    behind the last token."""
+    (_native_module or _native()).extend(block_tables, seq_lens, new_lens, free_blocks,
+                                         free_count, num_blocks, query_start_loc, slot_mapping_t,
+                                         positions, window, sinks, out_seq_lens, out_free_count,
+                                         stream)
+
+
+def sample(logits, random_bits, temperature=None, top_k=None, top_p=None, min_p=None,
+           stream=None):
+    """One token of every row (ps_sample) by temperature (float32, 0: the largest logit), top_k
+    (int32, 0: all), top_p and min_p (float32), each [B] or None. logits [B, V] (float16,
+    bfloat16 or float32; the last dimension of a padded vocabulary may be cut by a view);
+    random_bits int32 [B] holding uint32 words. Returns (tokens int32 [B], the logarithm float32
+    [B] of the probability that each was drawn with)."""
+    tokens = logprobs = None
+    if stream is not None and isinstance(logits, torch.Tensor) and logits.is_cuda and \
+            logits.dim() == 2:
+        # memory for a stream that is not the current one comes from that stream
+        tokens, logprobs = (_alloc(logits.shape[:1], t, logits.device, stream)
+                            for t in (torch.int32, torch.float32))
+    return (_native_module or _native()).sample(logits, random_bits, temperature, top_k, top_p,
+                                                min_p, tokens, logprobs, stream)
+
+
 def alloc_beam_workspace(B: int, W: int, V: int, n_select: int, device=None) -> torch.Tensor:
     n = max(int(lib().ps_beam_select_workspace_size(B, W, V, n_select)), 256)
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
@@ -311,17 +357,10 @@ def paged_attention(q, k_pool, v_pool, block_tables, seq_lens, query_start_loc, 
     return out
 
 
-def masked_paged_attention(q, k_pool, v_pool, block_tables, seq_lens, query_start_loc,
-                           scale: float, softcap: float = 0.0, distance_slopes=None,
-                           window: int = 0, prefix_lens=None, key_starts=None, out=None,
-                           workspace=None, max_seq_len: int | None = None,
-                           stream=None) -> torch.Tensor:
-    """Paged attention with scores capped by a tanh (softcap), lowered by the distance
-    (distance_slopes float32 [H_q]), a sliding window, a bidirectional prefix (prefix_lens
-    int32 [B]) and documents packed into a sequence (key_starts int32 [T]); see
-    ps_paged_attention_masked. Rows that see no key give zeros."""
+def _attention_memory(q, k_pool, block_tables, out, workspace, max_seq_len, stream):
+    """Memory for a stream that is not the current one comes from that stream (without one, the
+    compiled call allocates what is None)."""
     if stream is not None and isinstance(q, torch.Tensor) and q.is_cuda:
-        # memory for a stream that is not the current one comes from that stream
         if out is None:
             out = _alloc(q.shape, q.dtype, q.device, stream)
         if workspace is None and q.dim() == 3 and isinstance(k_pool, torch.Tensor) and \
@@ -331,10 +370,39 @@ def masked_paged_attention(q, k_pool, v_pool, block_tables, seq_lens, query_star
             msl = max_seq_len if max_seq_len is not None else width * BLOCK_SIZE
             n = workspace_size(q.shape[0], B, q.shape[1], k_pool.shape[2], q.shape[2], msl)
             workspace = _alloc(max(n, 256), torch.uint8, q.device, stream)
+    return out, workspace
+
+
+def masked_paged_attention(q, k_pool, v_pool, block_tables, seq_lens, query_start_loc,
+                           scale: float, softcap: float = 0.0, distance_slopes=None,
+                           window: int = 0, prefix_lens=None, key_starts=None, out=None,
+                           workspace=None, max_seq_len: int | None = None,
+                           stream=None) -> torch.Tensor:
+    """Paged attention with scores capped by a tanh (softcap), lowered by the distance
+    (distance_slopes float32 [H_q]), a sliding window, a bidirectional prefix (prefix_lens
+    int32 [B]) and documents packed into a sequence (key_starts int32 [T]); see
+    ps_paged_attention_masked. Rows that see no key give zeros."""
+    out, workspace = _attention_memory(q, k_pool, block_tables, out, workspace, max_seq_len,
+                                       stream)
     return (_native_module or _native()).attend(q, k_pool, v_pool, block_tables, seq_lens,
                                                 query_start_loc, scale, softcap, distance_slopes,
                                                 window, prefix_lens, key_starts, out, workspace,
                                                 max_seq_len, stream)
+
+
+def streaming_paged_attention(q, k_pool, v_pool, block_tables, seq_lens, query_start_loc,
+                              scale: float, window: int, sinks: int, softcap: float = 0.0,
+                              out=None, workspace=None, max_seq_len: int | None = None,
+                              stream=None) -> torch.Tensor:
+    """Paged attention of streams (ps_paged_attention_streaming): a row sees the last `window`
+    keys up to its own (0: all) and the first `sinks` of its sequence; scores may be capped by a
+    tanh (softcap)."""
+    out, workspace = _attention_memory(q, k_pool, block_tables, out, workspace, max_seq_len,
+                                       stream)
+    return (_native_module or _native()).stream_attend(q, k_pool, v_pool, block_tables, seq_lens,
+                                                       query_start_loc, scale, window, sinks,
+                                                       softcap, out, workspace, max_seq_len,
+                                                       stream)
 
 
 def attention_step(q, k, v, k_pool, v_pool, block_tables, seq_lens, query_start_loc,

@@ -375,9 +375,10 @@ constexpr int kMaskedDirectItems = 2, kMaskedDirectKeys = 128 * 128;
 // The masked attention's chain: as run_attention's without a scatter. A small batch runs on
 // the split or the tile kernel's direct mode alone; otherwise planner, split kernel, tile
 // kernel and combine, chained with programmatic dependent launch.
-int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const void* v_pool,
-                         bool bf16, cudaStream_t s) {
-  MaskedAttnParams p = p0;
+template <class Params>
+int run_masked_attention(const Params& p0, const void* k_pool, const void* v_pool, bool bf16,
+                         cudaStream_t s) {
+  Params p = p0;
   int num_sms = 0;
   int* err = nullptr;
   int rc = current_device(&num_sms, &err);
@@ -409,8 +410,16 @@ int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const v
   //                          left to the plan, which evens out lengths that differ)
   const int64_t rows = static_cast<int64_t>(p.T) * p.G, gr = p.group_rows;
   const int64_t items = p.H_kv * (p.T <= p.B ? p.T * ((p.G + gr - 1) / gr) : rows / gr + p.B);
+  // Pages that an item may read: a table's width, or what a stream's mask leaves of it whatever
+  // that is (the window before a group's tokens, at most 16, and the sinks).
+  int64_t item_pages = p.max_blocks;
+  if constexpr (Params::kSinks) {
+    const int64_t seen = (static_cast<int64_t>(p.window) + 15 + 15) / kBlockSize + 1 +
+                         (p.sinks + kBlockSize - 1) / kBlockSize;
+    if (p.window > 0 && seen < item_pages) item_pages = seen;
+  }
   if (rows <= 64 * static_cast<int64_t>(p.B) && items <= kMaskedDirectItems * num_sms &&
-      static_cast<int64_t>(p.max_blocks) * p.D <= kMaskedDirectKeys) {
+      item_pages * p.D <= kMaskedDirectKeys) {
     p.direct = 1;
     Timed tm(3, s);
     if ((e = launch_masked_split(p, bf16, kmap, vmap, static_cast<int>(items), s, true)) !=
@@ -452,13 +461,14 @@ int run_masked_attention(const MaskedAttnParams& p0, const void* k_pool, const v
       return cuda_fail(e, "masked split attention kernel");
   }
   if (tiles) {
-    MaskedAttnParams pt = p;
+    Params pt = p;
     pt.after_split = !p.all_tiles;
     Timed tm(5, s);
     if ((e = launch_masked_tile(pt, bf16, kmap, vmap, qmap, num_sms, s, false)) != cudaSuccess)
       return cuda_fail(e, "masked tile attention kernel");
   }
-  if (p.max_blocks > kMinSplitPages) {
+  // (a stream's page that holds sinks and window both counts twice)
+  if (p.max_blocks + (Params::kSinks ? 1 : 0) > kMinSplitPages) {
     Timed tm(4, s);
     if ((e = launch_combine(p, bf16, num_sms, s, true)) != cudaSuccess)
       return cuda_fail(e, "combine kernel");
@@ -564,13 +574,14 @@ int ps_rope_reshape_and_cache(void* q, const void* k, const void* v, const int32
                      "rotary KV scatter kernel");
 }
 
-int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                                const void* v, int64_t v_stride, const int32_t* positions,
-                                const int32_t* slot_mapping, void* k_pool, void* v_pool,
-                                const double* inv_freq, int rotary_dim, int interleaved,
-                                float magnitude, void* q_out, int64_t q_out_stride, int T,
-                                int H_q, int H_kv, int D, int num_blocks, int dtype,
-                                void* stream) {
+namespace {
+// Rotary positions of one axis (axes null) or of num_axes.
+int rotary_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                 int64_t v_stride, const int32_t* positions, const int32_t* axes, int num_axes,
+                 const int32_t* slot_mapping, void* k_pool, void* v_pool, const double* inv_freq,
+                 int rotary_dim, int interleaved, float magnitude, void* q_out,
+                 int64_t q_out_stride, int T, int H_q, int H_kv, int D, int num_blocks,
+                 int dtype, void* stream) {
   int rc = check_shapes(H_q, H_kv, D, dtype);
   if (rc) return rc;
   if (T < 0 || num_blocks <= 0 || rotary_dim <= 0 || rotary_dim > D || !std::isfinite(magnitude))
@@ -602,6 +613,8 @@ int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, 
   a.v_stride = v_stride;
   a.qo_stride = q_out_stride;
   a.pos = positions;
+  a.axes = axes;
+  a.num_axes = num_axes;
   a.slots = slot_mapping;
   a.k_pool = static_cast<uint16_t*>(k_pool);
   a.v_pool = static_cast<uint16_t*>(v_pool);
@@ -617,6 +630,33 @@ int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, 
   Timed tm(8, s);
   return cuda_status(ps::launch_rotary(a, D, interleaved != 0, dtype == PS_BF16, ds->num_sms, s),
                      "rotary KV scatter kernel (table of frequencies)");
+}
+}  // namespace
+
+int ps_rotary_reshape_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const int32_t* positions,
+                                const int32_t* slot_mapping, void* k_pool, void* v_pool,
+                                const double* inv_freq, int rotary_dim, int interleaved,
+                                float magnitude, void* q_out, int64_t q_out_stride, int T,
+                                int H_q, int H_kv, int D, int num_blocks, int dtype,
+                                void* stream) {
+  return rotary_cache(q, q_stride, k, k_stride, v, v_stride, positions, nullptr, 1, slot_mapping,
+                      k_pool, v_pool, inv_freq, rotary_dim, interleaved, magnitude, q_out,
+                      q_out_stride, T, H_q, H_kv, D, num_blocks, dtype, stream);
+}
+
+int ps_rotary_axes_reshape_and_cache(const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     const int32_t* positions, const int32_t* axes, int num_axes,
+                                     const int32_t* slot_mapping, void* k_pool, void* v_pool,
+                                     const double* inv_freq, int rotary_dim, int interleaved,
+                                     float magnitude, void* q_out, int64_t q_out_stride, int T,
+                                     int H_q, int H_kv, int D, int num_blocks, int dtype,
+                                     void* stream) {
+  if (num_axes <= 0 || (T > 0 && !axes)) return PS_ERR_ARG;
+  return rotary_cache(q, q_stride, k, k_stride, v, v_stride, positions, axes, num_axes,
+                      slot_mapping, k_pool, v_pool, inv_freq, rotary_dim, interleaved, magnitude,
+                      q_out, q_out_stride, T, H_q, H_kv, D, num_blocks, dtype, stream);
 }
 
 int ps_fork_sequences(const int32_t* block_tables, int max_blocks_per_seq,
@@ -724,6 +764,81 @@ int ps_beam_select(const void* logits, int64_t row_stride, const float* scores,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Timed tm(7, s);
   return cuda_status(ps::launch_beam_select(a, logits_dtype, s), "beam selection kernels");
+}
+
+int ps_sample(const void* logits, int64_t row_stride, const float* temperature,
+              const int32_t* top_k, const float* top_p, const float* min_p,
+              const uint32_t* random_bits, int B, int V, int logits_dtype, int32_t* tokens,
+              float* logprobs, void* stream) {
+  if (B < 0 || V <= 0 || row_stride < V) return PS_ERR_ARG;
+  if (logits_dtype != PS_F16 && logits_dtype != PS_BF16 && logits_dtype != PS_F32)
+    return PS_ERR_UNSUPPORTED;
+  if (V > ps::kSampleMaxVocab || B > (1 << 24)) return PS_ERR_UNSUPPORTED;
+  if (B == 0) return PS_OK;
+  if (!logits || !random_bits || !tokens || !logprobs) return PS_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) & (logits_dtype == PS_F32 ? 3u : 1u)) return PS_ERR_ALIGN;
+  DeviceState* ds;
+  const int rc = current_device_state(&ds);
+  if (rc) return rc;
+  ps::SampleParams a = {};
+  a.logits = logits;
+  a.ld = row_stride;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.random = random_bits;
+  a.B = B;
+  a.V = V;
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(7, s);
+  return cuda_status(ps::launch_sample(a, logits_dtype, ds->num_sms, s), "sampling kernel");
+}
+
+int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                        const int32_t* new_lens, int32_t* free_blocks, int free_capacity,
+                        const int32_t* free_count, int B, int T, int num_blocks, int window,
+                        int sinks, int32_t* query_start_loc, int32_t* slot_mapping,
+                        int32_t* positions, int32_t* out_seq_lens, int32_t* out_free_count,
+                        void* stream) {
+  if (B < 0 || T < 0 || max_blocks_per_seq <= 0 || free_capacity < 0 || num_blocks <= 0 ||
+      window < 0 || sinks < 0)
+    return PS_ERR_ARG;
+  if (static_cast<int64_t>(num_blocks) * PS_BLOCK_SIZE > INT32_MAX) return PS_ERR_ARG;
+  if (B > ps::kExtendMaxSeqs || static_cast<int64_t>(B) * max_blocks_per_seq > INT32_MAX ||
+      T > INT32_MAX - (1 << 20))
+    return PS_ERR_UNSUPPORTED;
+  if (!free_count || !out_free_count || !query_start_loc) return PS_ERR_ARG;
+  if (B > 0 && (!block_tables || !seq_lens || !new_lens || !out_seq_lens)) return PS_ERR_ARG;
+  if (free_capacity > 0 && !free_blocks) return PS_ERR_ARG;
+  if (T > 0 && (!slot_mapping || !positions)) return PS_ERR_ARG;
+  DeviceState* ds;
+  const int rc = current_device_state(&ds);
+  if (rc) return rc;
+  ps::ExtendParams a = {};
+  a.tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.qsl = query_start_loc;
+  a.slots = slot_mapping;
+  a.positions = positions;
+  a.out_lens = out_seq_lens;
+  a.out_count = out_free_count;
+  a.max_blocks = max_blocks_per_seq;
+  a.free_capacity = free_capacity;
+  a.B = B;
+  a.T = T;
+  a.num_blocks = num_blocks;
+  a.window = window;
+  a.sinks = sinks;
+  a.err = ds->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Timed tm(0, s);
+  return cuda_status(ps::launch_extend(a, s), "sequence extension kernel");
 }
 
 size_t ps_spec_accept_workspace_size(int B, int k, int V) {
@@ -847,23 +962,13 @@ int ps_paged_attention(const void* q, const void* k_pool, const void* v_pool,
                            dtype == PS_BF16, static_cast<cudaStream_t>(stream));
 }
 
-int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_pool,
-                              const int32_t* block_tables, int max_blocks_per_seq,
-                              const int32_t* seq_lens, const int32_t* query_start_loc, int B,
-                              int T, int H_q, int H_kv, int D, int num_blocks, float scale,
-                              float softcap, const float* distance_slopes, int window,
-                              const int32_t* prefix_lens, const int32_t* key_starts, void* out,
-                              void* workspace, size_t workspace_bytes, int dtype, void* stream) {
-  // (the tile kernel takes a row's maximum on the raw scores)
-  if (!(scale > 0.f) || !std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap) ||
-      window < 0)
-    return PS_ERR_ARG;
-  int rc = check_attention(q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens,
-                           query_start_loc, B, T, H_q, H_kv, D, num_blocks, out, workspace,
-                           workspace_bytes, dtype);
-  if (rc) return rc;
-  if (T == 0) return PS_OK;
-  ps::MaskedAttnParams p{};
+namespace {
+// The masked attention's parameters but for the masks. PS_OK or the status to return.
+int masked_params(ps::MaskedAttnParams& p, const void* q, const int32_t* block_tables,
+                  int max_blocks_per_seq, const int32_t* seq_lens,
+                  const int32_t* query_start_loc, int B, int T, int H_q, int H_kv, int D,
+                  int num_blocks, float scale, float softcap, void* out, void* workspace,
+                  size_t workspace_bytes) {
   p.q = q;
   p.out = out;
   p.block_tables = block_tables;
@@ -889,15 +994,73 @@ int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_p
   // A cap of 2^100 times the scale is none: up to raw scores of 2^88 tanh(y) is y to the last
   // bit of fp32, and scale / cap soon has no bits left.
   if (softcap > 0.f && p.cap_y < 0x1p-100f) p.cap_log2 = 0.f;
+  p.tpt = ps::tile_tokens(p.G);
+  return ps::layout_workspace(p, static_cast<uint8_t*>(workspace), workspace_bytes, false)
+             ? PS_OK
+             : PS_ERR_WORKSPACE;
+}
+
+// (the tile kernel takes a row's maximum on the raw scores)
+bool scores_ok(float scale, float softcap) {
+  return scale > 0.f && std::isfinite(scale) && softcap >= 0.f && std::isfinite(softcap);
+}
+}  // namespace
+
+int ps_paged_attention_masked(const void* q, const void* k_pool, const void* v_pool,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* seq_lens, const int32_t* query_start_loc, int B,
+                              int T, int H_q, int H_kv, int D, int num_blocks, float scale,
+                              float softcap, const float* distance_slopes, int window,
+                              const int32_t* prefix_lens, const int32_t* key_starts, void* out,
+                              void* workspace, size_t workspace_bytes, int dtype, void* stream) {
+  if (!scores_ok(scale, softcap) || window < 0) return PS_ERR_ARG;
+  int rc = check_attention(q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens,
+                           query_start_loc, B, T, H_q, H_kv, D, num_blocks, out, workspace,
+                           workspace_bytes, dtype);
+  if (rc) return rc;
+  if (T == 0) return PS_OK;
+  ps::MaskedAttnParams p{};
+  if ((rc = masked_params(p, q, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, B, T,
+                          H_q, H_kv, D, num_blocks, scale, softcap, out, workspace,
+                          workspace_bytes)))
+    return rc;
   p.slopes = distance_slopes;
   p.window = window;
   p.prefix = prefix_lens;
   p.starts = key_starts;
-  p.tpt = ps::tile_tokens(p.G);
-  if (!ps::layout_workspace(p, static_cast<uint8_t*>(workspace), workspace_bytes, false))
-    return PS_ERR_WORKSPACE;
   return ps::run_masked_attention(p, k_pool, v_pool, dtype == PS_BF16,
                                   static_cast<cudaStream_t>(stream));
+}
+
+int ps_paged_attention_streaming(const void* q, const void* k_pool, const void* v_pool,
+                                 const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* seq_lens, const int32_t* query_start_loc, int B,
+                                 int T, int H_q, int H_kv, int D, int num_blocks, float scale,
+                                 float softcap, int window, int sinks, void* out,
+                                 void* workspace, size_t workspace_bytes, int dtype,
+                                 void* stream) {
+  if (!scores_ok(scale, softcap) || window < 0 || sinks < 0) return PS_ERR_ARG;
+  int rc = check_attention(q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens,
+                           query_start_loc, B, T, H_q, H_kv, D, num_blocks, out, workspace,
+                           workspace_bytes, dtype);
+  if (rc) return rc;
+  if (T == 0) return PS_OK;
+  ps::StreamAttnParams p{};
+  if ((rc = masked_params(p, q, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, B, T,
+                          H_q, H_kv, D, num_blocks, scale, softcap, out, workspace,
+                          workspace_bytes)))
+    return rc;
+  p.window = window;
+  p.sinks = sinks;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // one interval of keys a row: the masked attention as it is
+  if (window == 0 || sinks == 0)
+    return ps::run_masked_attention(static_cast<const ps::MaskedAttnParams&>(p), k_pool, v_pool,
+                                    dtype == PS_BF16, s);
+  // (the table's end bounds every position: from there on more sinks are the same)
+  const int64_t most = static_cast<int64_t>(max_blocks_per_seq) * PS_BLOCK_SIZE;
+  if (sinks > most) p.sinks = static_cast<int>(most);
+  return ps::run_masked_attention(p, k_pool, v_pool, dtype == PS_BF16, s);
 }
 
 namespace {

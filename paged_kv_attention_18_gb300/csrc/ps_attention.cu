@@ -30,6 +30,10 @@ struct SeqInfo {
   // Masked attention only (both 0 for the causal mask alone, and folded away): the first
   // page any row of the sequence sees, and the length of its bidirectional prefix.
   int page0, pre;
+  // Streams: the sinks' pages (counted ahead of the window's, so that a sequence's pages are
+  // page0 .. pages - 1 with the window's from page0 + sink_pages on as they are), and the
+  // position of the first row.
+  int sink_pages;
 };
 
 // Packed rows of a split-kernel item.
@@ -50,8 +54,13 @@ __device__ __forceinline__ SeqInfo seq_info(const Params& p, const int* qsl, con
   s.L = lens[b];
   s.pages = (s.L + kBlockSize - 1) / kBlockSize;
   s.valid = p.sequence_ok(s.tok0, qsl[b + 1], s.L);
-  s.page0 = s.pre = 0;
-  if constexpr (Params::kMasked) {
+  s.page0 = s.pre = s.sink_pages = 0;
+  if constexpr (Params::kSinks) {
+    if (s.valid && s.n > 0) {
+      s.sink_pages = (min(p.sinks, s.L) + kBlockSize - 1) / kBlockSize;
+      s.page0 = min(p.window_lo(s.L - s.n) / kBlockSize, s.pages) - s.sink_pages;
+    }
+  } else if constexpr (Params::kMasked) {
     if (s.valid && s.n > 0) {
       // the rows' lower bounds do not fall from one row to the next: the first row's holds
       s.pre = p.prefix_len(b, s.L);
@@ -90,6 +99,7 @@ __device__ __forceinline__ int split_page(const SeqInfo& s, int ns, int k) {
 // The first token that sees a key at or after page `page`: those of the prefix are seen
 // by all.
 __device__ __forceinline__ int first_token_at(const SeqInfo& s, int page) {
+  if (s.sink_pages > 0 && page < s.page0 + s.sink_pages) page -= s.page0;  // one of the sinks'
   const int f = page * kBlockSize - (s.L - s.n);
   return f > 0 && page * kBlockSize >= s.pre ? f : 0;
 }
@@ -276,9 +286,29 @@ __device__ __forceinline__ void store_item(WorkItem* dst_item, const WorkItem& i
 // rows are held by keeps one page at least (with every key of it masked), so that their
 // partial results are written. pad[1], pad[2]: the keys [lo, hi) that some row of the item
 // sees; pad[3]: the prefix.
+// Streams: the item's pages, as the sequence counts them, in their two runs.
 template <class Params>
-__device__ __forceinline__ void mask_item(const Params& p, const SeqInfo& s, WorkItem& it,
+__device__ __forceinline__ void mask_item(const Params& p, const SeqInfo& s, int ns, WorkItem& it,
                                           int i_first, int i_last) {
+  if constexpr (Params::kSinks) {
+    const int from = split_page(s, ns, it.split), to = split_page(s, ns, it.split + 1);
+    const int last = s.L - s.n + i_last, end = last / kBlockSize + 1;  // behind the last row's page
+    const int first = s.page0 + s.sink_pages;  // the sequence's first page of the window
+    const int lo = p.window_lo(s.L - s.n + i_first);
+    it.pad[3] = min(max(from - s.page0, 0), s.sink_pages);
+    it.pad[4] = max(min(min(max(to - s.page0, 0), s.sink_pages), end), it.pad[3]);
+    const int b = max(from, first), e = min(max(to, first), end);
+    it.page_begin = max(b, lo / kBlockSize);
+    it.page_end = e;
+    if (it.page_end <= it.page_begin) {
+      // no page of the window: one all the same if rows are held here and there is none of the
+      // sinks' either
+      it.page_begin = e > b && it.pad[4] == it.pad[3] ? e - 1 : e;
+    }
+    it.pad[1] = lo;
+    it.pad[2] = last + 1;
+    return;
+  }
   const int lo = p.row_lo(s.tok0 + i_first, s.L - s.n + i_first);
   if (it.page_end > it.page_begin)
     it.page_begin = min(max(it.page_begin, lo / kBlockSize), it.page_end - 1);
@@ -566,7 +596,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int concurre
         it.n_query = s.n;
         it.tok0 = s.tok0;
         it.pad[0] = it.pad[1] = it.pad[2] = it.pad[3] = it.pad[4] = 0;
-        if constexpr (Params::kMasked) mask_item(p, s, it, it.row0 / p.G, i_last);
+        if constexpr (Params::kMasked) mask_item(p, s, ns, it, it.row0 / p.G, i_last);
         store_item(p.items + first + local, it);
       }
     } else {
@@ -614,7 +644,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int concurre
         it.tok0 = s.tok0;
         it.pad[0] = nb * p.G;
         it.pad[1] = it.pad[2] = it.pad[3] = it.pad[4] = 0;
-        if constexpr (Params::kMasked) mask_item(p, s, it, qa, i_last);
+        if constexpr (Params::kMasked) mask_item(p, s, ns, it, qa, i_last);
         store_item(p.tile_items + pos, it);
       }
     }
@@ -1257,6 +1287,11 @@ cudaError_t launch_plan(const AttnParams& p, int concurrency, int tile_ctas, int
 }
 
 cudaError_t launch_plan_masked(const MaskedAttnParams& p, int concurrency, int tile_ctas,
+                               int num_sms, cudaStream_t stream) {
+  return launch_plan_t(p, concurrency, tile_ctas, num_sms, stream, nullptr);
+}
+
+cudaError_t launch_plan_masked(const StreamAttnParams& p, int concurrency, int tile_ctas,
                                int num_sms, cudaStream_t stream) {
   return launch_plan_t(p, concurrency, tile_ctas, num_sms, stream, nullptr);
 }

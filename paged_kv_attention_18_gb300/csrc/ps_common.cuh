@@ -29,6 +29,8 @@ enum DevError : int {
   kDevWaitTimeout = 4,    // an mbarrier wait ran out of iterations
   kDevPlanOverflow = 5,   // the work plan did not fit the workspace
   kDevBadToken = 6,       // a draft token id outside the vocabulary
+  kDevNoBlocks = 7,       // a step needs more blocks than are free
+  kDevBadAxis = 8,        // a frequency's axis outside [0, num_axes)
 };
 
 // Programmatic dependent launch: let the next kernel on the stream start launching, and

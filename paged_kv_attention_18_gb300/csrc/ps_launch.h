@@ -14,6 +14,7 @@ struct WorkItem;
 // Everything the planner, the attention kernels and the combine kernel read.
 struct AttnParams {
   static constexpr bool kMasked = false;  // the causal mask alone (see MaskedAttnParams)
+  static constexpr bool kSinks = false;
   const void* q;                 // [T, H_q, D]
   void* out;                     // [T, H_q, D]
   const int32_t* block_tables;   // [B, max_blocks]
@@ -77,6 +78,7 @@ struct AttnParams {
 // distance as the fields below say.
 struct MaskedAttnParams : AttnParams {
   static constexpr bool kMasked = true;
+  static constexpr bool kSinks = false;  // (see StreamAttnParams)
   float cap_log2;         // cap * log2(e); 0: scores are not capped
   float cap_arg;          // 2 * log2(e) * scale / cap (the tanh's exponent per raw score)
   float cap_y;            // scale / cap (its argument per raw score)
@@ -110,6 +112,22 @@ struct MaskedAttnParams : AttnParams {
   }
 };
 
+// Masked attention of streams: a row sees the window before it and the first `sinks` keys of
+// its sequence, those up to its own position. An item then reads two runs of pages, the sinks'
+// first: [pad[3], pad[4]), with the keys below `sinks`, and [page_begin, page_end), with the keys
+// from `sinks` on; pad[1], pad[2] bound the latter (there is no prefix, nor documents). A page
+// that holds the last sinks and the window's first keys is read in both.
+struct StreamAttnParams : MaskedAttnParams {
+  static constexpr bool kSinks = true;
+  int sinks;              // > 0
+
+  // the first key behind the sinks that the row at position `pos` sees
+  __device__ __forceinline__ int window_lo(int pos) const {
+    const int lo = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
+    return lo > sinks ? lo : sinks;
+  }
+};
+
 // Raise `kern`'s dynamic shared-memory limit to `bytes` once per device: the setting lasts
 // for the process, and repeating it on every launch only costs host time.
 template <typename Kern>
@@ -139,6 +157,27 @@ inline cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = pdl ? attr : nullptr;
   cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
+// Launch `kern` as clusters of `cluster` CTAs, programmatically dependent as above.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, unsigned cluster,
+                                  unsigned threads, size_t smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
@@ -196,7 +235,9 @@ struct RotaryParams {
   const uint16_t *q, *k, *v;      // [T, heads, D], token strides below
   uint16_t* q_out;                // may be q
   int64_t q_stride, k_stride, v_stride, qo_stride;
-  const int32_t* pos;             // [T]
+  const int32_t* pos;             // [T], or [num_axes, T] with axes
+  const int32_t* axes;            // [rot / 2] axis of each frequency, or null (one axis)
+  int num_axes;
   const int32_t* slots;           // [T]
   uint16_t *k_pool, *v_pool;      // [num_slots, H_kv, D]
   const double* inv_freq;         // [rot / 2] radians per position
@@ -241,6 +282,42 @@ struct ForkParams {
 };
 cudaError_t launch_fork(const ForkParams& p, int num_sms, cudaStream_t stream);
 
+// A step's blocks, slots, positions and offsets from lengths and numbers of new tokens.
+constexpr int kExtendMaxSeqs = 8192;  // sequences at most (their sums lie in shared memory)
+struct ExtendParams {
+  int32_t* tables;                // [B, max_blocks]
+  const int32_t* seq_lens;        // [B]
+  const int32_t* new_lens;        // [B]; negative: the sequence ends
+  int32_t* free_blocks;           // [free_capacity], a stack of free_count entries
+  const int32_t* free_count;      // [1]
+  int32_t* qsl;                   // [B + 1]
+  int32_t* slots;                 // [T]
+  int32_t* positions;             // [T]
+  int32_t* out_lens;              // [B], may be seq_lens
+  int32_t* out_count;             // [1], may be free_count
+  int max_blocks, free_capacity, B, T, num_blocks, window, sinks;
+  int* err;
+};
+cudaError_t launch_extend(const ExtendParams& p, cudaStream_t stream);
+
+// A token of every row by temperature, top-k, top-p and min-p.
+constexpr int kSampleMaxVocab = 3 << 17;  // a cluster's shared memory holds a row of fp32
+struct SampleParams {
+  const void* logits;             // [B, V], rows `ld` elements apart
+  int64_t ld;
+  const float* temperature;       // [B] or null
+  const int32_t* top_k;           // [B] or null
+  const float* top_p;             // [B] or null
+  const float* min_p;             // [B] or null
+  const uint32_t* random;         // [B]
+  int B, V;
+  int slice, scale;               // set by the launcher: logits of a CTA; see Row
+  int32_t* tokens;                // [B]
+  float* logprobs;                // [B]
+};
+// dtype: 0 fp16, 1 bf16, 2 fp32
+cudaError_t launch_sample(SampleParams p, int dtype, int num_sms, cudaStream_t stream);
+
 // Speculative acceptance (rejection rule or greedy) of every sequence's k drafts.
 struct SpecParams {
   const float* p;          // [B, k + 1, V] target probabilities of the verify rows
@@ -277,6 +354,8 @@ cudaError_t launch_plan(const AttnParams& p, int concurrency, int tile_ctas, int
                         cudaStream_t stream, const CopySegments* pre = nullptr);
 cudaError_t launch_plan_masked(const MaskedAttnParams& p, int concurrency, int tile_ctas,
                                int num_sms, cudaStream_t stream);
+cudaError_t launch_plan_masked(const StreamAttnParams& p, int concurrency, int tile_ctas,
+                               int num_sms, cudaStream_t stream);
 
 // The split and tile kernels with a mask, capped scores and a distance bias, launched as
 // their causal forms are.
@@ -285,6 +364,9 @@ constexpr int masked_split_warps(int D, bool narrow) { return narrow && D == 64 
 // p.direct: the split kernel's direct mode, about a CTA for each group of rows of a
 // (sequence, KV head).
 cudaError_t launch_masked_split(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, int ctas, cudaStream_t stream,
+                                bool pdl);
+cudaError_t launch_masked_split(const StreamAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int ctas, cudaStream_t stream,
                                 bool pdl);
 // (the tile kernel is one per kind of score, each in a file of its own)
@@ -306,8 +388,22 @@ inline cudaError_t launch_masked_tile(const MaskedAttnParams& p, bool bf16, cons
                          : (p.slopes ? launch_masked_tile_bias : launch_masked_tile_plain);
   return f(p, bf16, kmap, vmap, qmap, ctas, stream, direct);
 }
-int run_masked_attention(const MaskedAttnParams& p, const void* k_pool, const void* v_pool,
-                         bool bf16, cudaStream_t s);
+using StreamTileLaunch = cudaError_t(const StreamAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                                     const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
+                                     cudaStream_t stream, bool direct);
+StreamTileLaunch launch_stream_tile_plain, launch_stream_tile_cap, launch_stream_tile_large_cap;
+inline cudaError_t launch_masked_tile(const StreamAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                                      const CUtensorMap& vmap, const CUtensorMap& qmap, int ctas,
+                                      cudaStream_t stream, bool direct) {
+  StreamTileLaunch* const f = p.cap_log2 > kLargeCapLog2 ? launch_stream_tile_large_cap
+                              : p.cap_log2 > 0.f         ? launch_stream_tile_cap
+                                                         : launch_stream_tile_plain;
+  return f(p, bf16, kmap, vmap, qmap, ctas, stream, direct);
+}
+// Params: MaskedAttnParams or StreamAttnParams.
+template <class Params>
+int run_masked_attention(const Params& p, const void* k_pool, const void* v_pool, bool bf16,
+                         cudaStream_t s);
 
 // Query tokens per 128-row tile for G query heads per KV head (0 = use the split kernel).
 int tile_tokens(int G);

@@ -106,7 +106,9 @@ static_assert(sizeof(TileBars) <= 512, "barrier block");
 // block table, and query rows inside the packed batch. Every role checks each item the
 // same way and skips one that does not fit, so no role reads or writes outside its
 // buffers on a plan it cannot use.
-__device__ __forceinline__ bool tile_item_ok(const WorkItem& w, const MaskedAttnParams& p) {
+template <class Params>
+__device__ __forceinline__ bool tile_item_ok(const WorkItem& w, const Params& p) {
+  if (Params::kSinks && (w.pad[3] < 0 || w.pad[4] > p.max_blocks)) return false;
   if (w.seq < 0 || w.seq >= p.B || w.kv < 0 || w.kv >= p.H_kv) return false;
   if (w.page_begin < 0 || w.page_end > p.max_blocks) return false;
   if (w.tok0 < 0 || w.row0 < 0 || w.nrows <= 0 || w.pad[0] < 0) return false;
@@ -114,17 +116,43 @@ __device__ __forceinline__ bool tile_item_ok(const WorkItem& w, const MaskedAttn
   return w.tok0 + last_row / p.G < p.T;
 }
 
+// The key tiles of an item: those of its run of pages, or of its two runs, the sinks' first,
+// each run's last tile filled up with zeros.
+template <class Params>
+struct ItemTiles {
+  int pb, pe;                 // the window's pages (all of them without sinks)
+  int sb = 0, sinks = 0, nt;  // the sinks' first page, their tiles; key tiles in all
+  __device__ __forceinline__ explicit ItemTiles(const WorkItem& w)
+      : pb(w.page_begin), pe(w.page_end) {
+    nt = pe > pb ? (pe - pb + kPagesPerTile - 1) / kPagesPerTile : 0;
+    if constexpr (Params::kSinks) {
+      sb = w.pad[3];
+      sinks = w.pad[4] > sb ? (w.pad[4] - sb + kPagesPerTile - 1) / kPagesPerTile : 0;
+      nt += sinks;
+    }
+  }
+  __device__ __forceinline__ bool in_sinks(int j) const { return Params::kSinks && j < sinks; }
+  // first page of tile j, and one past the last page of its run
+  __device__ __forceinline__ int first(int j) const {
+    return in_sinks(j) ? sb + j * kPagesPerTile : pb + (j - sinks) * kPagesPerTile;
+  }
+  __device__ __forceinline__ int end(int j, const WorkItem& w) const {
+    return in_sinks(j) ? w.pad[4] : pe;
+  }
+};
+
 }  // namespace
 
 // kDirect: no plan. Each CTA derives its items from seq_lens and qsl (every sequence
 // unsplit, its query-tile pairs longest first).
 // kCap: 0 none, 1 up to kLargeCapLog2, 2 beyond (the exact form of small scores in every tile; as
 // a branch inside it made the kernel larger and its other caps 1.5 % slower).
-template <bool kBF16, int D, bool kDirect, int kCap, bool kBias>
+template <class Params, bool kBF16, int D, bool kDirect, int kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
     masked_tile_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap,
-                       const __grid_constant__ CUtensorMap qmap, const MaskedAttnParams p) {
+                       const __grid_constant__ CUtensorMap qmap, const Params p) {
+  static_assert(!(Params::kSinks && kBias), "a stream's tiles go in order");
   using L = TileSmem<D>;
   constexpr int kHalves = D / 64;
   constexpr bool kDuo = kCap > 0 || kBias;
@@ -263,7 +291,7 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
           d_n = n;
           d_L = L;
           d_t0 = q0;
-          d_pre = p.prefix_len(lane, L);
+          if constexpr (!Params::kSinks) d_pre = p.prefix_len(lane, L);
           d_pairs = ((n + p.tpt - 1) / p.tpt + p.tile_step - 1) / p.tile_step;
         }
       }
@@ -296,13 +324,16 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
       const int pre = __shfl_sync(0xffffffffu, d_pre, b);
       const int key_end = max(L - n + i_last + 1, pre);  // one past the last key (at most L)
       const int pe = (key_end + kBlockSize - 1) / kBlockSize;
-      const int key_lo = p.row_lo(t0 + qa_, L - n + qa_);
+      int key_lo;
+      if constexpr (Params::kSinks) key_lo = p.window_lo(L - n + qa_);
+      else key_lo = p.row_lo(t0 + qa_, L - n + qa_);
       int f = 0;  // seq, kv, row0, nrows, page_begin, page_end, split 0, nsplit 1, L, n, t0
       f = lane == 0 ? b : f;
       f = lane == 1 ? kv : f;
       f = lane == 2 ? qa_ * p.G : f;
       f = lane == 3 ? na * p.G : f;
-      f = lane == 4 ? min(key_lo / kBlockSize, pe - 1) : f;  // one page at least
+      // (one page at least, the sinks' included)
+      f = lane == 4 ? min(key_lo / kBlockSize, Params::kSinks ? pe : pe - 1) : f;
       f = lane == 5 ? pe : f;
       f = lane == 7 ? 1 : f;
       f = lane == 8 ? L : f;
@@ -311,7 +342,9 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
       f = lane == 11 ? nb * p.G : f;  // rows of query tile B
       f = lane == 12 ? key_lo : f;    // pad[1..3], as the plan has them
       f = lane == 13 ? key_end : f;
-      f = lane == 14 ? pre : f;
+      f = lane == 14 && !Params::kSinks ? pre : f;
+      if constexpr (Params::kSinks)  // (lane 14: the sinks' first page, 0)
+        f = lane == 15 ? (min(p.sinks, key_end) + kBlockSize - 1) / kBlockSize : f;
       return f;
     };
     for (int it = 0;; ++it) {
@@ -357,10 +390,10 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
       }
       if (idx < 0) break;
       const WorkItem& w = items[it % (2 * kItemRing)];
-      const int pb = w.page_begin, pe = w.page_end;
-      if (pe <= pb || !tile_item_ok(w, p)) continue;
+      const ItemTiles<Params> tiles(w);
+      const int nt = tiles.nt;
+      if (nt == 0 || !tile_item_ok(w, p)) continue;
       const int seq = w.seq, kv = w.kv;
-      const int nt = (pe - pb + kPagesPerTile - 1) / kPagesPerTile;
       // query tiles (K warp): whole tokens x the G heads of this KV head. Each tile has its
       // own buffer, refilled as soon as that tile's last S of the previous item has read
       // it. They are loaded after the item's first K tile, whose stage frees earlier.
@@ -388,8 +421,9 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
       bool ok = true;
       const int pp = lane / kHalves, h = lane % kHalves;
       for (int j = 0; j < nt; ++j) {
-        const int first = pb + tile_at(j, nt) * kPagesPerTile;
-        if (first < bt_base || first - bt_base + kPagesPerTile > 32) {
+        const int first = tiles.first(tile_at(j, nt)), pe = tiles.end(tile_at(j, nt), w);
+        if (first < bt_base || first - bt_base + kPagesPerTile > 32 ||
+            (Params::kSinks && j == tiles.sinks)) {
           bt_base = kBias ? max(first + kPagesPerTile - 32, 0) : first;
           bt_reg = bt_base + lane < pe ? __ldg(bt + bt_base + lane) : -1;
         }
@@ -453,15 +487,14 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         mbar_arrive(&bars->item_empty[slot]);
         if (idx < 0) break;
         const WorkItem& w = items[it % (2 * kItemRing)];
-        const int pb = w.page_begin, pe = w.page_end;
+        const int nt = ItemTiles<Params>(w).nt;
         if (!tile_item_ok(w, p)) {
           record_error(p.err, kDevPlanOverflow);  // a plan this launch cannot use
           continue;
         }
-        if (pe <= pb) continue;
+        if (nt == 0) continue;
         const bool has_b = w.pad[0] > 0;
         const int ng = has_b ? 2 : 1;
-        const int nt = (pe - pb + kPagesPerTile - 1) / kPagesPerTile;
         if (!wait1(&bars->q_full[0], qa & 1)) break;
         const uint32_t g0 = g;
         // S of query tile `grp` against K tile j. Only the item's first K tile is waited
@@ -542,15 +575,15 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
       const int idx = next_item(it);
       if (idx < 0) break;
       const WorkItem& w = items[it % (2 * kItemRing)];
-      const int pb = w.page_begin, pe = w.page_end;
-      if (pe <= pb || !tile_item_ok(w, p)) continue;
-      const int nt = (pe - pb + kPagesPerTile - 1) / kPagesPerTile;
+      const ItemTiles<Params> tiles(w);
+      const int nt = tiles.nt;
+      if (nt == 0 || !tile_item_ok(w, p)) continue;
       // Where some row of the item sees nothing, a key from the item's first token on (`own`,
       // behind the prefix) may be seen by none.
       const int pos0 = w.ctx_len - w.n_query, i0 = w.row0 / p.G;
       const int i1 = i0 + (w.pad[0] > 0 ? p.tpt + w.pad[0] / p.G : w.nrows / p.G);
       int own = 0x7fffffff;
-      if (p.starts != nullptr) {
+      if (!Params::kSinks && p.starts != nullptr) {
         bool empty = false;
 #pragma unroll 1
         for (int i = i0 + lane; i < i1; i += 32) empty |= __ldg(p.starts + w.tok0 + i) > pos0 + i;
@@ -565,16 +598,25 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         // rows are zeroed, four at a time (this code runs once or twice an item, so its size
         // counts: with loops unrolled, 6 chunks of documents took 31.1 us in place of 30.5, and
         // the 777 us with a bias above 788)
-        const int kb = (pb + tile_at(j, nt) * kPagesPerTile) * kBlockSize;
-        const int ke = min(kb + kKeys, pe * kBlockSize);
-        if (kb < w.pad[1] || ke > w.pad[2] || ke > own) {
+        const int at = tile_at(j, nt);
+        const int kb = tiles.first(at) * kBlockSize;
+        const int ke = min(kb + kKeys, tiles.end(at, w) * kBlockSize);
+        int lo = w.pad[1], hi = w.pad[2];  // the keys that some row sees
+        if constexpr (Params::kSinks) {
+          if (tiles.in_sinks(at)) {
+            lo = 0;
+            hi = min(hi, p.sinks);
+          }
+        }
+        if (kb < lo || ke > hi || ke > own) {
           uint8_t* v = smem + L::kOffV + (gv % kVStages) * L::kK + (lane & 7) * 16;
 #pragma unroll 1
           for (int k = 0; k < kKeys; k += 32) {
             const int key = kb + k + lane;
             uint32_t dead = __ballot_sync(
-                0xffffffffu, key < ke && (key < w.pad[1] || key >= w.pad[2] ||
-                                          p.key_unseen(key, own, w.pad[2], w.tok0 - pos0)));
+                0xffffffffu, key < ke && (key < lo || key >= hi ||
+                                          (!Params::kSinks &&
+                                           p.key_unseen(key, own, hi, w.tok0 - pos0))));
             while (dead != 0) {
               const int four = (__ffs(dead) - 1) & ~3, r = four + (lane >> 3);
               if (dead >> r & 1u) {
@@ -609,9 +651,9 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         const int idx = next_item(it);
         if (idx < 0) break;
         const WorkItem& w = items[it % (2 * kItemRing)];
-        const int pb = w.page_begin, pe = w.page_end;
-        if (pe <= pb || !tile_item_ok(w, p)) continue;
-        const int nt = (pe - pb + kPagesPerTile - 1) / kPagesPerTile;
+        const ItemTiles<Params> tiles(w);
+        [[maybe_unused]] const int pb = tiles.pb, pe = tiles.pe, nt = tiles.nt;
+        if (nt == 0 || !tile_item_ok(w, p)) continue;
         const int nrows = grp == 0 ? w.nrows : w.pad[0];
         if (nrows == 0) continue;  // no query tile B in this item
         // this thread's query row
@@ -622,8 +664,12 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         const int head = w.kv * p.G + R - qtok * p.G;
         const int pos = valid ? w.ctx_len - w.n_query + qtok : -1;
         // the row's keys: [key_lo, key_hi] within the item
-        const int key_hi = min(max(pos, w.pad[3] - 1), pe * kBlockSize - 1);
-        const int key_lo = valid ? p.row_lo(tok, pos) : 0;
+        // (streams: [key_lo, key_hi] of the window's run)
+        const int key_hi =
+            min(Params::kSinks ? pos : max(pos, w.pad[3] - 1), pe * kBlockSize - 1);
+        int key_lo = 0;
+        if constexpr (Params::kSinks) key_lo = valid ? p.window_lo(pos) : 0;
+        else key_lo = valid ? p.row_lo(tok, pos) : 0;
         // the row's split count and partial base, fetched now so that the epilogue's
         // stores do not wait on them
         // (both loads are issued at once; nothing waits for them before the epilogue)
@@ -635,8 +681,14 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         for (int j = 0; j < nt; ++j) {
           // visible columns: c <= lim (a row past the tile's rows is computed unmasked and
           // not written)
-          const int tile0 = pb * kBlockSize + j * kKeys;  // the tile's first key
-          const int lim = valid ? key_hi - tile0 : kKeys, low = valid ? key_lo - tile0 : 0;
+          const int tile0 = tiles.first(j) * kBlockSize;  // the tile's first key
+          int lim = valid ? key_hi - tile0 : kKeys, low = valid ? key_lo - tile0 : 0;
+          if constexpr (Params::kSinks) {
+            if (tiles.in_sinks(j) && valid) {
+              lim = min(min(pos, p.sinks - 1), w.pad[4] * kBlockSize - 1) - tile0;
+              low = 0;
+            }
+          }
           if (!wait(&bars->s_full[grp], sc & 1)) { ok = false; break; }
           ++sc;
           tc_fence_after();
@@ -908,9 +960,9 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         const int idx = next_item(it);
         if (idx < 0) break;
         const WorkItem& w = items[it % (2 * kItemRing)];
-        const int pb = w.page_begin, pe = w.page_end;
-        if (pe <= pb || !tile_item_ok(w, p)) continue;
-        const int nt = (pe - pb + kPagesPerTile - 1) / kPagesPerTile;
+        const ItemTiles<Params> tiles(w);
+        [[maybe_unused]] const int pb = tiles.pb, pe = tiles.pe, nt = tiles.nt;
+        if (nt == 0 || !tile_item_ok(w, p)) continue;
         const int nrows = grp == 0 ? w.nrows : w.pad[0];
         if (nrows == 0) continue;  // no query tile B in this item
         // this thread's query row
@@ -923,17 +975,31 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         // the row's keys within the item, [key_lo, key_hi], relative to the warp's columns (a
         // row past the tile's rows is computed unmasked and not written)
         const int col0 = pb * kBlockSize + 64 * half;
+        // (streams: of the window's run, whose first tile is tile `tiles.sinks`)
         const int key_hi =
-            valid ? min(max(pos, w.pad[3] - 1), pe * kBlockSize - 1) - col0 : (1 << 30);
-        const int key_lo = valid ? p.row_lo(tok, pos) - col0 : -(1 << 30);
+            valid ? min(Params::kSinks ? pos : max(pos, w.pad[3] - 1), pe * kBlockSize - 1) - col0
+                  : (1 << 30);
+        int key_lo = -(1 << 30);
+        if (valid) {
+          if constexpr (Params::kSinks) key_lo = p.window_lo(pos) - col0;
+          else key_lo = p.row_lo(tok, pos) - col0;
+        }
         const float slope = kBias && valid ? -kLog2e * __ldg(p.slopes + head) : 0.f;
         const float first_dist = static_cast<float>(pos - col0);  // of the item's first column
         // m_ref: the reference max (log2 units) that P, O and l are currently taken against;
         // m_next: the reference from the next tile on, when this one's P summed to over 2^8
         float m_ref = m_fixed, m_next = m_fixed, l = 0.f;
         for (int j = 0; j < nt; ++j) {
-          const int t0 = tile_at(j, nt) * kKeys;  // the tile's first key, from the item's
-          const int lim = key_hi - t0, low = key_lo - t0;  // visible: low <= c <= lim
+          // the tile's first key, from the item's
+          const int t0 = (tile_at(j, nt) - (Params::kSinks ? tiles.sinks : 0)) * kKeys;
+          int lim = key_hi - t0, low = key_lo - t0;  // visible: low <= c <= lim
+          if constexpr (Params::kSinks) {
+            if (tiles.in_sinks(j) && valid) {
+              const int c0 = tiles.first(j) * kBlockSize + 64 * half;
+              lim = min(min(pos, p.sinks - 1), w.pad[4] * kBlockSize - 1) - c0;
+              low = -c0;
+            }
+          }
           if (!wait(&bars->s_full[grp], sc & 1)) { ok = false; break; }
           ++sc;
           tc_fence_after();
@@ -1174,12 +1240,12 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
   if (!kDirect && p.after_split && blockIdx.x == 0 && threadIdx.x == 0) pdl_wait();
 }
 
-template <bool kBF16, int D, bool kDirect, int kCap, bool kBias>
-static cudaError_t launch_masked_tile_t(const MaskedAttnParams& p, const CUtensorMap& kmap,
+template <bool kBF16, int D, bool kDirect, int kCap, bool kBias, class Params>
+static cudaError_t launch_masked_tile_t(const Params& p, const CUtensorMap& kmap,
                                         const CUtensorMap& vmap, const CUtensorMap& qmap,
                                         int ctas, cudaStream_t stream) {
   constexpr int smem = TileSmem<D>::kBytes;
-  auto kern = masked_tile_kernel<kBF16, D, kDirect, kCap, kBias>;
+  auto kern = masked_tile_kernel<Params, kBF16, D, kDirect, kCap, kBias>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_limit(kern, smem, done);
   if (e != cudaSuccess) return e;
@@ -1187,8 +1253,8 @@ static cudaError_t launch_masked_tile_t(const MaskedAttnParams& p, const CUtenso
 }
 
 // The instantiations of one (cap, bias) pair: one per type, head size and mode.
-template <int kCap, bool kBias>
-static cudaError_t launch_masked_tile_kind(const MaskedAttnParams& p, bool bf16,
+template <int kCap, bool kBias, class Params>
+static cudaError_t launch_masked_tile_kind(const Params& p, bool bf16,
                                            const CUtensorMap& kmap, const CUtensorMap& vmap,
                                            const CUtensorMap& qmap, int ctas,
                                            cudaStream_t stream, bool direct) {

@@ -3,6 +3,8 @@
 // passed through, with the frequencies given as a table (any scaling for long contexts is
 // in the table) and a magnitude on the cosine and sine:
 //     (x, y) -> (x c - y s, y c + x s),  c = m cos(pos f_i),  s = m sin(pos f_i).
+// With several axes (time, height, width of images and video) pos is that of the frequency's
+// axis.
 //
 // Angle: each frequency is held as a 64-bit fixed-point fraction of a turn; pos * F_i
 // wrapping modulo 2^64 is the angle modulo one turn (exact but for F_i's own rounding, so
@@ -69,17 +71,27 @@ __device__ __forceinline__ void turn_unit(uint4& a, uint4& b, const float* c, co
 // units each. (Whole passes of 8 tokens dealt to the CTAs left some with half as many again:
 // 8192 tokens of 32 + 8 + 8 heads took 36.6 us, equal
 // shares take 34.2: 5.9 TB/s.)
-template <bool kBF16, int D, bool kInter>
+template <bool kBF16, int D, bool kInter, bool kAxes>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     rotary_kernel(const RotaryParams p) {
   constexpr int kRowUnits = D / 16, kRowsPerRound = kThreads / kRowUnits;
   __shared__ unsigned long long turns[D / 2];
+  __shared__ int64_t first[kAxes ? D / 2 : 1];  // the frequency's axis: its first position
   __shared__ float cs[2][kMaxPassTokens][D / 2], sn[2][kMaxPassTokens][D / 2];
   const int half = p.rot / 2, rot_units = p.rot / 16;
   pdl_wait();
   for (int i = threadIdx.x; i < half; i += kThreads) {
     const double t = p.inv_freq[i] * kInvTwoPi;
     turns[i] = __double2ull_rn((t - floor(t)) * kTwoTo64);
+    if constexpr (kAxes) {
+      const int a = p.axes[i];
+      const bool ok = a >= 0 && a < p.num_axes;
+      if (!ok) {  // an axis that is none: no turn
+        turns[i] = 0;
+        if (blockIdx.x == 0) record_error(p.err, kDevBadAxis);
+      }
+      first[i] = ok ? static_cast<int64_t>(a) * p.T : 0;
+    }
   }
   const int heads = p.H_q + 2 * p.H_kv;
   const int un = threadIdx.x % kRowUnits, row0 = threadIdx.x / kRowUnits;
@@ -142,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           const int ux = x / half, i = x - ux * half, t = t0 + ux;
           if (t >= t_hi) continue;
           const unsigned long long ph =
-              static_cast<unsigned long long>(static_cast<long long>(p.pos[t])) * turns[i];
+              static_cast<unsigned long long>(
+                  static_cast<long long>(p.pos[kAxes ? first[i] + t : t])) * turns[i];
           float s, c;
           sincosf(static_cast<float>(static_cast<int32_t>(ph >> 32)) * kTurnToRad, &s, &c);
           cs[buf][ux][i] = c * p.magnitude;
@@ -167,25 +180,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
-template <bool kBF16, int D>
+template <bool kBF16, int D, bool kAxes>
 cudaError_t launch_t(const RotaryParams& p, bool inter, int num_sms, cudaStream_t stream) {
   const int ctas = num_sms * kCtasPerSm;
   const dim3 grid(static_cast<unsigned>(p.T < ctas ? p.T : ctas));
-  return inter ? launch_kernel(rotary_kernel<kBF16, D, true>, grid, dim3(kThreads), 0, stream,
-                               true, p)
-               : launch_kernel(rotary_kernel<kBF16, D, false>, grid, dim3(kThreads), 0, stream,
-                               true, p);
+  return inter ? launch_kernel(rotary_kernel<kBF16, D, true, kAxes>, grid, dim3(kThreads), 0,
+                               stream, true, p)
+               : launch_kernel(rotary_kernel<kBF16, D, false, kAxes>, grid, dim3(kThreads), 0,
+                               stream, true, p);
+}
+
+template <int D, bool kAxes>
+cudaError_t launch_d(const RotaryParams& p, bool inter, bool bf16, int num_sms,
+                     cudaStream_t stream) {
+  return bf16 ? launch_t<true, D, kAxes>(p, inter, num_sms, stream)
+              : launch_t<false, D, kAxes>(p, inter, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryParams& p, int D, bool interleaved, bool bf16, int num_sms,
                           cudaStream_t stream) {
-  if (D == 128)
-    return bf16 ? launch_t<true, 128>(p, interleaved, num_sms, stream)
-                : launch_t<false, 128>(p, interleaved, num_sms, stream);
-  return bf16 ? launch_t<true, 64>(p, interleaved, num_sms, stream)
-              : launch_t<false, 64>(p, interleaved, num_sms, stream);
+  if (p.axes != nullptr)
+    return D == 128 ? launch_d<128, true>(p, interleaved, bf16, num_sms, stream)
+                    : launch_d<64, true>(p, interleaved, bf16, num_sms, stream);
+  return D == 128 ? launch_d<128, false>(p, interleaved, bf16, num_sms, stream)
+                  : launch_d<64, false>(p, interleaved, bf16, num_sms, stream);
 }
 
 }  // namespace ps

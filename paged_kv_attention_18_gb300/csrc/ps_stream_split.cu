@@ -1,0 +1,12 @@
+// The masked split kernel for streams: a window and the sequence's first keys.
+#include "ps_masked_split.cuh"
+
+namespace ps {
+
+cudaError_t launch_masked_split(const StreamAttnParams& p, bool bf16, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, int ctas, cudaStream_t stream,
+                                bool pdl) {
+  return launch_split_any(p, bf16, kmap, vmap, ctas, stream, pdl);
+}
+
+}  // namespace ps

@@ -18,6 +18,22 @@ import math
 import torch
 
 
+def axes(sections, interleaved: bool = False, device=None) -> torch.Tensor:
+    """int32 [sum(sections)]: the axis of every frequency of
+    :func:`binding.rotary_axes_reshape_and_cache`, sections[a] of them on axis a: one section
+    behind another, or (interleaved) the axes in turns as long as each has frequencies left."""
+    left = [int(n) for n in sections]
+    if not left or any(n < 0 for n in left) or sum(left) == 0:
+        raise ValueError("sections must be counts, one at least above 0")
+    if not interleaved:
+        table = [a for a, n in enumerate(left) for _ in range(n)]
+    else:
+        table = []
+        for turn in range(max(left)):
+            table += [a for a, n in enumerate(left) if n > turn]
+    return torch.tensor(table, dtype=torch.int32, device=device)
+
+
 def frequencies(rotary_dim: int, theta: float = 10000.0, factor: float = 1.0,
                 theta_factor: float = 1.0, original_len: int | None = None, low: float = 1.0,
                 high: float = 4.0, device=None) -> torch.Tensor:
