@@ -792,6 +792,7 @@ int ps_sample(const void* logits, int64_t row_stride, const float* temperature,
   a.V = V;
   a.tokens = tokens;
   a.logprobs = logprobs;
+  a.err = ds->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Timed tm(7, s);
   return cuda_status(ps::launch_sample(a, logits_dtype, ds->num_sms, s), "sampling kernel");

@@ -314,6 +314,7 @@ struct SampleParams {
   int slice, scale;               // set by the launcher: logits of a CTA; see Row
   int32_t* tokens;                // [B]
   float* logprobs;                // [B]
+  int* err;
 };
 // dtype: 0 fp16, 1 bf16, 2 fp32
 cudaError_t launch_sample(SampleParams p, int dtype, int num_sms, cudaStream_t stream);

@@ -47,13 +47,14 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kList = 2048;           // places that a row's list holds
+constexpr int kShort = kThreads;      // places that sort in a fraction of the time
 constexpr int kMaxTopK = 1024;        // k up to which the threads' maxima bound it
 constexpr int kMaxCluster = 8;
 constexpr int kSmemLimit = 232448;    // of a CTA
 constexpr int kSmemTwo = 113 * 1024;  // of each of two on an SM
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, a float's low bits are its integer
 constexpr int kMagicBits = 0x4b400000;
-constexpr double kLog2eD = 1.4426950408889634073599246810018921;
+constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.9259629911266175e-08f;
 
 // 2^31 * 2^(j / 64), rounded
 __constant__ uint32_t kExp2Table[64] = {
@@ -115,6 +116,16 @@ __device__ __forceinline__ float element(const uint4& v, int e) {
   return fmaxf(x + 0.f, -INFINITY);
 }
 
+// Elements e and e + 1 as they are, for their weights (NaN and -inf weigh nothing, -0 as 0).
+template <int kType>
+__device__ __forceinline__ float2 pair(const uint4& v, int e) {
+  const uint32_t* w = &v.x;
+  if constexpr (kType == 2) return make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+  else if constexpr (kType == 1)
+    return make_float2(__uint_as_float(w[e / 2] << 16), __uint_as_float(w[e / 2] & 0xffff0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w[e / 2]));
+}
+
 // The largest element of a vector (NaN counts as -inf).
 template <int kType>
 __device__ __forceinline__ float vector_max(const uint4& v) {
@@ -136,7 +147,8 @@ struct Row {
   float max;      // the row's largest logit (times s)
   float c, c_lo;  // log2(e) / T (over s) as two floats
   float s;        // 1, or 1/4 where differences would overflow beside T
-  int scale;      // the largest weight is 2^scale
+  float limit;    // from this y on (scale + 2) a weight rounds to 0; the largest is 2^scale
+  uint32_t down;  // 60 - scale, and what kMagicBits adds to an exponent
 };
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
@@ -153,10 +165,9 @@ __device__ __forceinline__ Below below(float2 x, const Row& r) {
   b.t = ffma2(b.y, both(-64.f), both(kMagic));
   return b;
 }
-constexpr float kNothing = 100.f;  // y from which a weight is 0 whatever the scale
 // Counting bin: 32 a factor of two, 64 factors; the last one takes the rest. Never falls as x does.
-__device__ __forceinline__ int bin_of(float y, float t) {
-  return y < 63.9f ? (kMagicBits - static_cast<int>(__float_as_uint(t))) >> 1 : kBins - 1;
+__device__ __forceinline__ int bin_of(float t) {  // y below 63.9
+  return (kMagicBits - static_cast<int>(__float_as_uint(t))) >> 1;
 }
 
 // The weights of two logits.
@@ -182,11 +193,15 @@ __device__ __forceinline__ void weights(float2 x, const Below& b, const Row& r,
   const float2 f = ffma2(q, both(536870912.f), both(kMagic));
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int mi = static_cast<int>(__float_as_uint(e ? b.t.y : b.t.x)) - kMagicBits;
-    const uint32_t fi = __float_as_uint(e ? f.y : f.x) - kMagicBits + (1u << 29);
-    const uint64_t p = static_cast<uint64_t>(table[mi & 63]) * fi;  // 2^60 times 2^(frac)
-    const int down = 60 - r.scale - (mi >> 6);
-    w[e] = (e ? b.y.y : b.y.x) < kNothing && down < 63 ? (p + (1ull << (down - 1))) >> down : 0ull;
+    const uint32_t bits = __float_as_uint(e ? b.t.y : b.t.x);  // (kMagicBits is a multiple of 64)
+    uint32_t fi = __float_as_uint(e ? f.y : f.x) - (kMagicBits - (1u << 29));
+    // from here on a weight rounds to 0 (and not a number: -inf, NaN): 0 whatever the shift
+    if (!((e ? b.y.y : b.y.x) < r.limit)) fi = 0;
+    const uint32_t down = r.down - (bits >> 6);  // 63 at most
+    uint64_t half, p;
+    asm("shl.b64 %0, %1, %2;" : "=l"(half) : "l"(1ull), "r"(down - 1));
+    asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(p) : "r"(table[bits & 63]), "r"(fi), "l"(half));
+    asm("shr.b64 %0, %1, %2;" : "=l"(w[e]) : "l"(p), "r"(down));
   }
 }
 template <int kType>
@@ -195,6 +210,16 @@ __device__ __forceinline__ uint64_t weight(float x, const Row& r, const uint32_t
   const float2 xx = both(x * r.s);
   weights<kType>(xx, below(xx, r), r, table, w);
   return w[0];
+}
+
+// A copy of whole 16-byte words, global to shared, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // What the CTAs of a cluster show one another.
@@ -206,7 +231,10 @@ struct alignas(16) Shared {
   unsigned long long total, found[2];
   uint32_t table[64];
   float max, edge[2];
-  int listed, state, at;
+  double fall;     // T ln(min_p)
+  uint32_t least;  // the key of min-p's border
+  int listed, state, at, guess[2];
+  uint64_t arrived[kWarps];  // barriers of the warps' copies
 };
 static_assert(sizeof(Shared) % 16 == 0, "the slice behind it is read in 16-byte words");
 
@@ -237,20 +265,46 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, unsigned long long* sh
   return v;
 }
 
-// A bitonic sort, falling, of kPer * kThreads values: element j * kThreads + tid in v[j] of thread
-// tid. Only the first `size` (a power of two, 32 at least) take part.
-template <int kPer>
+// The threads that settle a list: a warp, or the block. Element j * kSize + i in v[j] of thread i.
+struct WarpGroup {
+  static constexpr int kSize = 32;
+  __device__ static int self() { return threadIdx.x & 31; }
+  __device__ static void sync() { __syncwarp(); }
+  __device__ static int count(bool x) { return __popc(__ballot_sync(0xffffffffu, x)); }
+  __device__ static uint64_t scan(uint64_t v, unsigned long long*) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (self() >= o) v += y;
+    }
+    return v;
+  }
+};
+struct BlockGroup {
+  static constexpr int kSize = kThreads;
+  __device__ static int self() { return threadIdx.x; }
+  __device__ static void sync() { __syncthreads(); }
+  __device__ static int count(bool x) { return __syncthreads_count(x); }
+  __device__ static uint64_t scan(uint64_t v, unsigned long long* sh) { return block_scan(v, sh); }
+};
+
+// A bitonic sort, falling, of the first `size` values (a power of two, 32 at least).
+template <class Group, int kPer>
 __device__ __forceinline__ void sort_falling(uint64_t* v, int size, unsigned long long* sh) {
-  const int tid = threadIdx.x;
+  constexpr int kSize = Group::kSize;
+  const int me = Group::self();
+#pragma unroll 1
   for (int k = 2; k <= size; k <<= 1) {
+#pragma unroll 1
     for (int s = k >> 1; s > 0; s >>= 1) {
-      if (s >= kThreads) {
-        const int js = s / kThreads;
+      if (s >= kSize) {
+        const int js = s / kSize;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          const int o = j ^ js;
-          if (o > j && o < kPer) {
-            const bool up = ((j * kThreads + tid) & k) == 0;
+#pragma unroll
+          for (int o = j + 1; o < kPer; ++o) {
+            if ((j ^ o) != js) continue;
+            const bool up = ((j * kSize + me) & k) == 0;
             if ((v[j] < v[o]) == up) {
               const uint64_t y = v[j];
               v[j] = v[o];
@@ -262,19 +316,19 @@ __device__ __forceinline__ void sort_falling(uint64_t* v, int size, unsigned lon
       }
       uint64_t other[kPer];
       if (s >= 32) {
-        __syncthreads();
+        Group::sync();
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sh[j * kThreads + tid] = v[j];
-        __syncthreads();
+        for (int j = 0; j < kPer; ++j) sh[j * kSize + me] = v[j];
+        Group::sync();
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) other[j] = sh[j * kThreads + (tid ^ s)];
+        for (int j = 0; j < kPer; ++j) other[j] = sh[j * kSize + (me ^ s)];
       } else {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) other[j] = __shfl_xor_sync(0xffffffffu, v[j], s);
       }
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int i = j * kThreads + tid;
+        const int i = j * kSize + me;
         const bool larger = ((i & k) == 0) == ((i & s) == 0);
         if (larger == (v[j] < other[j])) v[j] = other[j];
       }
@@ -379,35 +433,32 @@ struct Sampler {
   }
   // The first place that min-p keeps.
   __device__ __forceinline__ uint64_t min_place() const {
-    if (!(min_p > 0.f)) return place(kLowestKey, kIdxMask);
-    const double least =
-        min_p < 1.f ? peak + static_cast<double>(T) * log(static_cast<double>(min_p)) : peak;
-    const uint32_t key = key_of(__double2float_ru(least) + 0.f);
-    return place(key > kLowestKey ? key : kLowestKey, kIdxMask);
+    return place(min_p > 0.f ? sh.least : kLowestKey, kIdxMask);
   }
 
   // The list of n places, all that may be kept, decides: top-k, top-p of the sum of those, min-p,
-  // the draw. (First CTA.)
-  template <int kPer>
+  // the draw. (First CTA; the warps of the group.)
+  template <class Group, int kPer>
   __device__ __forceinline__ void decide(int n, uint64_t all, bool by_all) const {
+    constexpr int kSize = Group::kSize;
+    const int me = Group::self();
     uint64_t v[kPer], upto[kPer];
     int size = 32;
     while (size < n) size <<= 1;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = j * kThreads + tid < n ? sh.list[j * kThreads + tid] : 0;
-    sort_falling<kPer>(v, size, sh.list);
+    for (int j = 0; j < kPer; ++j) v[j] = j * kSize + me < n ? sh.list[j * kSize + me] : 0;
+    sort_falling<Group, kPer>(v, size, sh.list);
     const int nk = k > 0 && k < n ? k : n;
     auto scan = [&](int m, auto weight_of) {
       uint64_t carry = 0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        if (j * kThreads < size) {  // (uniform)
-          const int i = j * kThreads + tid;
-          upto[j] = carry + block_scan(i < m ? weight_of(v[j]) : 0, sh.warp);
+        if (j * kSize < m) {  // (uniform)
+          upto[j] = carry + Group::scan(j * kSize + me < m ? weight_of(v[j]) : 0, sh.warp);
           if (kPer > 1) {
-            __syncthreads();
-            if (tid == kThreads - 1) sh.total = upto[j];
-            __syncthreads();
+            Group::sync();
+            if (me == kSize - 1) sh.total = upto[j];
+            Group::sync();
             carry = sh.total;
           }
         }
@@ -417,19 +468,18 @@ struct Sampler {
       int c = 0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        c += __syncthreads_count(j * kThreads + tid < m && pred(j));
+        if (j * kSize < m) c += Group::count(j * kSize + me < m && pred(j));
       return c;
     };
     auto show = [&](int i) {  // the sum up to i, to every thread
-      __syncthreads();
+      Group::sync();
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
-        if (j * kThreads + tid == i) sh.total = upto[j];
-      __syncthreads();
+        if (j * kSize + me == i) sh.total = upto[j];
+      Group::sync();
       return static_cast<uint64_t>(sh.total);
     };
-    auto w_of = [&](uint64_t at) { return weight<kType>(logit_at(at), r, sh.table); };
-    scan(n, w_of);
+    scan(nk, [&](uint64_t at) { return weight<kType>(logit_at(at), r, sh.table); });
     int m = nk;
     if (top_p < 1.f) {
       const uint64_t target = share_of(by_all ? all : show(nk - 1));
@@ -443,33 +493,47 @@ struct Sampler {
     // the kept ones in the vocabulary's order: the index (as a place has it) before the key
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      v[j] = j * kThreads + tid < m
+      v[j] = j * kSize + me < m
                  ? (v[j] & kIdxMask) << 32 | static_cast<uint32_t>(v[j] >> kIdxBits)
                  : 0;
-    size = 32;
-    while (size < m) size <<= 1;
+    int at = 0;
     if (m > 1) {
-      sort_falling<kPer>(v, size, sh.list);
+      size = 32;
+      while (size < m) size <<= 1;
+      sort_falling<Group, kPer>(v, size, sh.list);
       scan(m, [&](uint64_t u) {
         return weight<kType>(of_key(static_cast<uint32_t>(u)), r, sh.table);
       });
+      at = count(m, [&](int j) { return upto[j] <= goal; });
     }
-    const int at = m > 1 ? count(m, [&](int j) { return upto[j] <= goal; }) : 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (j * kThreads + tid == at)
+      if (j * kSize + me == at)
         finish(static_cast<int>(kIdxMask - (v[j] >> 32)), of_key(static_cast<uint32_t>(v[j])), z);
   }
   __device__ void decide(int n, uint64_t all, bool by_all) const {
-    if (n <= kThreads) decide<1>(n, all, by_all);
-    else decide<kList / kThreads>(n, all, by_all);
+    if (n <= 128) {
+      if (warp == 0) decide<WarpGroup, 4>(n, all, by_all);
+    } else if (n <= kThreads) {
+      decide<BlockGroup, 1>(n, all, by_all);
+    } else {
+      decide<BlockGroup, kList / kThreads>(n, all, by_all);
+    }
   }
 
   // top_p's share of a sum, rounded up: a place is kept while the sum before it is less.
+  // (top_p is 24 bits and a power of two: the product is exact.)
   __device__ __forceinline__ uint64_t share_of(uint64_t z) const {
-    const double goal = ceil(static_cast<double>(top_p) * static_cast<double>(z));
-    const uint64_t t = goal < 1.0 ? 1 : static_cast<uint64_t>(goal);
-    return t < z ? t : z;
+    const uint32_t bits = __float_as_uint(top_p);
+    const uint64_t m = (bits & 0x7fffffu) | 0x800000u;
+    const int down = 150 - static_cast<int>(bits >> 23);  // 24 at least
+    const uint64_t lo = z * m, hi = __umul64hi(z, m);
+    if (down >= 64 + 24) return 1;
+    if (down >= 64) {
+      const uint64_t part = hi & ((1ull << (down - 64)) - 1);
+      return (hi >> (down - 64)) + ((part | lo) != 0 ? 1 : 0);
+    }
+    return (hi << (64 - down) | lo >> down) + ((lo & ((1ull << down) - 1)) != 0 ? 1 : 0);
   }
 
   // Every warp's kept weights are in sh.sums: the draw among the places from `cut` on. The row's
@@ -612,13 +676,15 @@ struct Sampler {
     uint64_t y = 0;
     if ((cut & kIdxMask) == 0 && r.s == 1.f) {  // (every token of the least logit)
       const float edge = logit_at(cut);
+      const bool all = cut <= place(kLowestKey, kIdxMask);
       each_vector([&](const uint4& w, int) {
+        if (!all && vector_max<kType>(w) < edge) return;
 #pragma unroll
         for (int e = 0; e < kVec; e += 2) {
-          const float2 v = make_float2(element<kType>(w, e), element<kType>(w, e + 1));
+          const float2 v = pair<kType>(w, e);
           uint64_t we[2];
           weights<kType>(v, below(v, r), r, sh.table, we);
-          y += (v.x >= edge ? we[0] : 0) + (v.y >= edge ? we[1] : 0);
+          y += (all || v.x >= edge ? we[0] : 0) + (all || v.y >= edge ? we[1] : 0);
         }
       });
     } else {
@@ -703,7 +769,7 @@ struct Sampler {
       bool in = key >= hi;
       if (!in) {
         const Below at = below(both(of_key(key)), r);
-        in = bin_of(at.y.x, at.t.x) <= b;
+        in = at.y.x < 63.9f && bin_of(at.t.x) <= b;
       }
       const int f = __ffs(__ballot_sync(0xffffffffu, in)) - 1;  // the first key in (none: hi)
       const uint32_t was = lo;
@@ -719,20 +785,23 @@ struct Sampler {
 
   // ---- top-p without a small k
   __device__ bool by_nucleus() const {
-    // the sum of all weights, and counts by bin
+    // The sum of all weights, and counts by bin; of the logits that may be kept: those under
+    // (1 - top_p) / V of the largest weigh less than 1 - top_p of it together, so the border lies
+    // above them.
+    const float past = fminf(log2f(static_cast<float>(p.V)) - log2f(1.f - top_p) + 1.f, 63.9f);
     for (int i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
     __syncthreads();
     uint64_t y = 0;
     each_vector([&](const uint4& w, int) {
 #pragma unroll
       for (int e = 0; e < kVec; e += 2) {
-        const float2 v = make_float2(element<kType>(w, e), element<kType>(w, e + 1));
+        const float2 v = pair<kType>(w, e);
         const Below b = below(v, r);
         uint64_t we[2];
         weights<kType>(v, b, r, sh.table, we);
         y += we[0] + we[1];
-        if (b.y.x < 63.9f) atomicAdd(&sh.count[bin_of(b.y.x, b.t.x)], 1u);
-        if (b.y.y < 63.9f) atomicAdd(&sh.count[bin_of(b.y.y, b.t.y)], 1u);
+        if (b.y.x < past) atomicAdd(&sh.count[bin_of(b.t.x)], 1u);
+        if (b.y.y < past) atomicAdd(&sh.count[bin_of(b.t.y)], 1u);
       }
     });
     y = block_sum(y, sh.warp);
@@ -759,21 +828,28 @@ struct Sampler {
     const uint64_t upto = block_scan(own, sh.warp);
     __syncthreads();
     if (tid == kThreads - 1) sh.total = upto;
+    if (tid < 2) sh.guess[tid] = 0;
     __syncthreads();
-    const uint64_t want = share_of(sh.total);
-    if (tid == 0) sh.at = 0;
-    __syncthreads();
-    if (upto - own < want && upto >= want) {
-      float part = static_cast<float>(want - (upto - own)) * 0x1p-40f;
-      int i = 0;
-      for (; i < 3; ++i) {
-        part -= mass[i];
-        if (part <= 0.f) break;
+    // The border by the counted masses, of their own sum (what a middle weight is off by cancels)
+    // and of the exact one (some are left out): between the two, but for the bins' unevenness.
+    const uint64_t goal = (target >> (p.scale - 40)) + 1;
+    const uint64_t wants[2] = {share_of(sh.total), goal < sh.total ? goal : sh.total};
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint64_t want = wants[g];
+      if (upto - own < want && upto >= want) {
+        float part = static_cast<float>(want - (upto - own)) * 0x1p-40f;
+        int i = 0;
+        for (; i < 3; ++i) {
+          part -= mass[i];
+          if (part <= 0.f) break;
+        }
+        sh.guess[g] = 4 * tid + i;
       }
-      sh.at = 4 * tid + i;
     }
     __syncthreads();
-    int mid = min(sh.at, kBins - 2);
+    const int mid = min(sh.guess[0], kBins - 2);
+    const int far = min(max(sh.guess[0], sh.guess[1]), kBins - 2);
     // merged counts up to each bin, for the window's choice
     {
       uint32_t c = static_cast<uint32_t>(upto_n) - sum_n;
@@ -783,12 +859,14 @@ struct Sampler {
     __syncthreads();
     auto upto_bin = [&](int b) { return b < 0 ? 0u : sh.count[min(b, kBins - 1)]; };
     // everything down to a bin past the border, or the bins around it
-    int b1 = min(mid + 1, kBins - 2), b0 = 0;
-    if (upto_bin(b1) > kList) {
+    int b1 = min(far + 1, kBins - 2), b0 = 0;
+    if (upto_bin(b1) > kShort) {
+      b1 = min(mid + 1, kBins - 2);
       b0 = max(mid - 1, 0);
-      if (upto_bin(b1) - upto_bin(b0 - 1) > kList) b0 = b1 = mid;
+      if (upto_bin(b1) - upto_bin(b0 - 1) > kShort) b0 = b1 = mid;
     }
-    for (int round = 0; round < kBins; ++round) {
+    int least = 0, most = kBins - 2;  // the border's bin lies between
+    while (least <= most) {
       if (upto_bin(b1) - upto_bin(b0 - 1) > kList) return false;
       if (warp == 0) {
         const float e = edge_of(b1);
@@ -802,20 +880,20 @@ struct Sampler {
       const float low = sh.edge[0], high = sh.edge[1];
       if (b0 == 0) {
         if (by_list_round(low, all, target)) return true;
+        least = b1 + 1;  // not all of the nucleus is in the list: on by what lacks
+        b0 = step(least, 1, *at_first(&sh.found[0]));
       } else {
         y = 0;
         each_vector([&](const uint4& w, int at) {
           if (vector_max<kType>(w) >= low) {
 #pragma unroll
             for (int e = 0; e < kVec; e += 2) {
-              const float2 v = make_float2(element<kType>(w, e), element<kType>(w, e + 1));
-              if (fmaxf(v.x, v.y) >= high) {
-                uint64_t we[2];
-                weights<kType>(v, below(v, r), r, sh.table, we);
-                y += (v.x >= high ? we[0] : 0) + (v.y >= high ? we[1] : 0);
-              }
-              if (v.x >= low && v.x < high) append(place(key_of(v.x), at + e));
-              if (v.y >= low && v.y < high) append(place(key_of(v.y), at + e + 1));
+              const float2 v = pair<kType>(w, e);
+              uint64_t we[2];
+              weights<kType>(v, below(v, r), r, sh.table, we);
+              y += (v.x >= high ? we[0] : 0) + (v.y >= high ? we[1] : 0);
+              if (v.x >= low && v.x < high) append(place(key_of(v.x + 0.f), at + e));
+              if (v.y >= low && v.y < high) append(place(key_of(v.y + 0.f), at + e + 1));
             }
           }
         });
@@ -834,17 +912,37 @@ struct Sampler {
           if (rank == 0) draw(sh.found[1]);
           return true;
         }
-        // the border lies in another bin
-        if (state < 0) b1 = b0 - 1;
-        else b0 = b1 + 1;
+        // the border lies in another bin: so far on by the masses between
+        if (state < 0) most = b0 - 1;
+        else least = b1 + 1;
+        b0 = step(state < 0 ? most : least, state < 0 ? -1 : 1, *at_first(&sh.found[0]));
       }
-      if (b0 == 0 && b1 < kBins - 2 && upto_bin(b1 + 1) <= kList) ++b1;
-      else if (b0 == 0) b0 = b1 = b1 + 1;
-      else b0 = b1 = *at_first(&sh.state) < 0 ? b1 : b0;
+      b0 = b1 = min(max(b0, least), most);
       cluster.sync();  // (the state has been read, the list is empty again)
-      if (b1 > kBins - 2) return false;
     }
     return false;
+  }
+  // The bin, from `bin` on by `by`, where the counted masses reach `gap` (of 2^scale). The merged
+  // counts up to each bin are in sh.count.
+  __device__ int step(int bin, int by, uint64_t gap) const {
+    const float want = static_cast<float>(gap) * exp2f(-static_cast<float>(p.scale));
+    float sum = 0.f;
+    for (; bin >= 0 && bin <= kBins - 2; bin += 32 * by) {
+      const int b = bin + by * lane;
+      float m = 0.f;
+      if (b >= 0 && b <= kBins - 2)
+        m = static_cast<float>(sh.count[b] - (b > 0 ? sh.count[b - 1] : 0)) *
+            fast_exp2(-(2 * b + 0.5f) / 64.f);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, m, o);
+        if (lane >= o) m += y;
+      }
+      const unsigned has = __ballot_sync(0xffffffffu, sum + m >= want);
+      if (has) return min(max(bin + by * (__ffs(has) - 1), 0), kBins - 2);
+      sum += __shfl_sync(0xffffffffu, m, 31);
+    }
+    return bin;
   }
   // a window that begins at the maximum: the whole nucleus in the list
   __device__ bool by_list_round(float low, uint64_t all, uint64_t target) const {
@@ -861,6 +959,7 @@ struct Sampler {
       __syncthreads();
       if (tid == 0) {
         sh.state = ok ? 0 : 1;
+        sh.found[0] = target - y;
         sh.listed = 0;
       }
     }
@@ -873,35 +972,46 @@ struct Sampler {
   __device__ void border(uint64_t target) const {
     const int n = min(sh.listed, kList);
     const uint64_t above = block_sum(tid < ctas * kWarps ? sh.sums[tid] : 0, sh.warp);
-    if (n <= kThreads) border_t<1>(n, above, target);
-    else border_t<kList / kThreads>(n, above, target);
+    if (n <= 128) {
+      if (warp == 0) border_t<WarpGroup, 4>(n, above, target);
+    } else if (n <= kThreads) {
+      border_t<BlockGroup, 1>(n, above, target);
+    } else {
+      border_t<BlockGroup, kList / kThreads>(n, above, target);
+    }
+    __syncthreads();
   }
-  template <int kPer>
+  template <class Group, int kPer>
   __device__ __forceinline__ void border_t(int n, uint64_t above, uint64_t target) const {
-    uint64_t v[kPer], upto[kPer];
+    constexpr int kSize = Group::kSize;
+    const int me = Group::self();
+    uint64_t v[kPer];
     int size = 32;
     while (size < n) size <<= 1;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = j * kThreads + tid < n ? sh.list[j * kThreads + tid] : 0;
-    sort_falling<kPer>(v, size, sh.list);
+    for (int j = 0; j < kPer; ++j) v[j] = j * kSize + me < n ? sh.list[j * kSize + me] : 0;
+    sort_falling<Group, kPer>(v, size, sh.list);
     uint64_t sum = above;
-    int kept = 0;
+    int kept = 0;  // those whose sum with what is before them is below the target, and one more
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const bool in = j * kThreads + tid < n;
-      upto[j] = sum + block_scan(in ? weight<kType>(logit_at(v[j]), r, sh.table) : 0, sh.warp);
-      __syncthreads();
-      if (tid == kThreads - 1) sh.total = upto[j];
-      kept += __syncthreads_count(in && upto[j] < target);
+      if (j * kSize >= n) continue;  // (uniform)
+      const bool in = j * kSize + me < n;
+      const uint64_t upto =
+          sum + Group::scan(in ? weight<kType>(logit_at(v[j]), r, sh.table) : 0, sh.warp);
+      Group::sync();
+      if (me == kSize - 1) sh.total = upto;
+      Group::sync();
+      kept += Group::count(in && upto < target);
       sum = sh.total;
     }
-    __syncthreads();
+    Group::sync();
     const bool ok = above < target && sum >= target;
     if (ok) {
       ++kept;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int i = j * kThreads + tid;
+        const int i = j * kSize + me;
         if (i == kept - 1) sh.found[1] = v[j];
         if (i < kept) {
           const int token = token_at(v[j]), q = token / p.slice;
@@ -912,12 +1022,12 @@ struct Sampler {
         }
       }
     }
-    __syncthreads();
-    if (tid == 0) {
+    Group::sync();
+    if (me == 0) {
       sh.state = !ok ? (above >= target ? -1 : 1) : min_place() > sh.found[1] ? 2 : 0;
+      if (!ok) sh.found[0] = above >= target ? above - target : target - sum;
       sh.listed = 0;
     }
-    __syncthreads();
   }
 };
 
@@ -937,6 +1047,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (s.tid < 64) sh.table[s.tid] = kExp2Table[s.tid];
   for (int i = s.tid; i < kBins; i += kThreads) sh.count[i] = 0;
   if (s.tid == 0) sh.listed = 0;
+  if (s.lane == 0) {
+    mbar_init(&sh.arrived[s.warp], 1);
+    fence_barrier_init();
+  }
   __syncthreads();
   pdl_wait();
   s.T = p.temperature ? p.temperature[s.row] : 1.f;
@@ -946,25 +1060,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   s.greedy = !(s.T >= 0x1p-100f);
   if (s.k >= p.V || s.k < 0) s.k = 0;
 
-  // ---- the slice, and the maximum
+  // min-p's border below the maximum: one thread's work while the others load
+  const bool bordered = s.min_p > 0.f && !s.greedy;
+  if (bordered && s.tid == kThreads - 1)
+    sh.fall = s.min_p < 1.f ? static_cast<double>(s.T) * log(static_cast<double>(s.min_p)) : 0.0;
+
+  // ---- the slice, and the maximum: a copy a warp of the words that lie in the slice whole, the
+  // others word by word
   const typename S::Slice slice = s.slice_of(s.rank);
   s.first = slice.first;
   s.t0 = min(s.warp * slice.per_warp, slice.tiles);
   s.t1 = min(s.t0 + slice.per_warp, slice.tiles);
-  float mx = -INFINITY;
-  constexpr int kAhead = 4;
-  for (int t = s.t0; t < s.t1; t += kAhead) {
-    uint4 w[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (t + u < s.t1) w[u] = s.load(s.first + ((t + u) * 32 + s.lane) * S::kVec, slice);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (t + u < s.t1) {
-        s.data[(t + u) * 32 + s.lane] = w[u];
-        mx = fmaxf(mx, vector_max<kType>(w[u]));
-      }
+  const int whole0 = (slice.lo - slice.first + S::kVec - 1) / S::kVec;  // whole words
+  const int whole1 = max((slice.hi - slice.first) / S::kVec, whole0);
+  const int a = min(max(s.t0 * 32, whole0), whole1), b = max(min(s.t1 * 32, whole1), a);
+  if (s.lane == 0 && b > a) {
+    mbar_arrive_expect_tx(&sh.arrived[s.warp], 16 * (b - a));
+    bulk_load(s.data + a, s.x + s.first + a * S::kVec, 16 * (b - a), &sh.arrived[s.warp]);
   }
+  if (s.t1 * 32 > whole1 || s.t0 * 32 < whole0)
+    for (int v = s.t0 * 32 + s.lane; v < s.t1 * 32; v += 32)
+      if (v < whole0 || v >= whole1) s.data[v] = s.load(s.first + v * S::kVec, slice);
+  float mx = -INFINITY;
+  if (b > a && !mbar_wait(&sh.arrived[s.warp], 0)) record_error(p.err, kDevWaitTimeout);
+  __syncwarp();
+  for (int t = s.t0; t < s.t1; ++t)
+    mx = fmaxf(mx, vector_max<kType>(s.data[t * 32 + s.lane]));
   mx += 0.f;
   if (s.k > 0 && mx > -INFINITY) atomicAdd(&sh.count[key_of(mx) >> 21], 1u);
 #pragma unroll
@@ -996,16 +1117,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const bool far = s.T >= 0x1p100f;
   s.r.s = far ? 0.25f : 1.f;
   s.r.max = s.peak * s.r.s;
-  const double c = kLog2eD / (static_cast<double>(s.T) * s.r.s);
-  s.r.c = static_cast<float>(c);
-  s.r.c_lo = static_cast<float>(c - s.r.c);
-  s.r.scale = p.scale;
+  // log2(e) / T to 2^-45 in two floats (fp64 by every thread costs microseconds here)
+  const float Ts = s.T * s.r.s;
+  s.r.c = kLog2eHi / Ts;
+  s.r.c_lo = s.r.c > 0.f ? (fmaf(-s.r.c, Ts, kLog2eHi) + kLog2eLo) / Ts : 0.f;
+  s.r.limit = static_cast<float>(p.scale + 2);
+  s.r.down = 60 - p.scale + (kMagicBits >> 6);
+  if (bordered) {
+    if (s.tid == kThreads - 1) {
+      const uint32_t key = key_of(__double2float_ru(s.peak + sh.fall) + 0.f);
+      sh.least = key > kLowestKey ? key : kLowestKey;
+    }
+    __syncthreads();
+  }
   bool done = false;
   if (!far) {
     if (s.k > 0 && s.k <= kMaxTopK) {
       done = s.by_list(s.bound_of_k(), 0, false);
     } else if (s.k == 0 && s.top_p < 1.f) {
-      done = p.V <= kList ? s.by_list(-FLT_MAX, 0, false) : s.by_nucleus();
+      done = p.V <= kShort ? s.by_list(-FLT_MAX, 0, false) : s.by_nucleus();
     } else if (s.k == 0) {
       s.sum_and_draw(s.min_place());
       done = true;
