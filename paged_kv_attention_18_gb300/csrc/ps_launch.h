@@ -311,7 +311,7 @@ struct SampleParams {
   const float* min_p;             // [B] or null
   const uint32_t* random;         // [B]
   int B, V;
-  int slice, scale;               // set by the launcher: logits of a CTA; see Row
+  int slice;                      // logits of a CTA (set by the launcher)
   int32_t* tokens;                // [B]
   float* logprobs;                // [B]
   int* err;

@@ -10,22 +10,20 @@
 // The token is a decision between neighbours whose borders lie as close as the smallest
 // weight, so sums must not depend on an order and weights need more bits than fp32 has:
 // with 2^17 tokens an error of 2^-24 in each border would change one draw in hundreds.
-// A weight is a 64-bit fixed-point number (2^scale for the largest; scale leaves room for V of
-// them), from exp2 in two floats: the difference x - max and its product with log2(e) / T are
-// each kept as a sum of two floats, 2^(j/64) comes from a table, the rest (at most 2^(1/128))
-// from three terms of its series, all within about 2^-30. Integer sums are exact in any order.
+// A weight is a whole number of 2^-42 of the largest, from exp2 in two floats (see weights):
+// within 2^-29 of itself before that rounding. Sums of whole numbers are exact in any order.
 //
 // A cluster takes a row, a slice of it in each CTA's shared memory, read from memory once; the
 // first CTA decides, the others leave as soon as it has what it needs of them. By what the row
 // asks for:
 //   - the largest logit alone: its first place;
-//   - top-k: the k-th largest of the threads' maxima bounds the k-th logit from below; the few
-//     logits from the bound on are listed, and the list, sorted, decides everything;
-//   - top-p without it: one pass takes the sum of all weights and counts the logits by weight
-//     (32 bins a factor of two). The border's bin follows from the counts with each bin's middle
-//     weight; a second pass sums the weights above that bin exactly and lists those around it.
-//     The list, sorted, has the border, which the exact sums confirm, or a next bin is tried. A
-//     nucleus that fits the list is listed whole;
+//   - top-k: the k-th largest of the maxima of parts of the row bounds the k-th logit from below;
+//     the few logits from the bound on are listed, and the list decides everything;
+//   - top-p without it: a first pass counts the logits by weight (80 bins or so a factor of two), each
+//     bin with its middle weight, to guess the border's bin; a second one sums all weights and
+//     those above that bin exactly, and lists the logits around it. The list, in order, has the
+//     border if the sums say so; else a next bin is tried. A nucleus that fits the list is listed
+//     whole;
 //   - none of these: the sum of all weights (from min-p's border on), by warps; the word's point
 //     lies in one warp's logits, which the first CTA reads again;
 //   - what fits none (a list that overflows, as with equal logits everywhere; k beyond 1024; T
@@ -43,32 +41,49 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kPerThread = kBins / kThreads;  // bins of a thread
+constexpr int kFine = 512;            // second digit of the maxima's keys
 constexpr int kList = 2048;           // places that a row's list holds
-constexpr int kShort = kThreads;      // places that sort in a fraction of the time
-constexpr int kMaxTopK = 1024;        // k up to which the threads' maxima bound it
+constexpr int kCounted = 256;         // places that are put in order by counting
+constexpr int kShort = 512;           // places that sort in a fraction of the time
+constexpr int kMaxTopK = 1024;        // k up to which the parts' maxima bound it
+constexpr int kFineTopK = 128;        // k from which they do so by two digits
 constexpr int kMaxCluster = 8;
+constexpr int kSums = kMaxCluster * kWarps;
 constexpr int kSmemLimit = 232448;    // of a CTA
 constexpr int kSmemTwo = 113 * 1024;  // of each of two on an SM
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, a float's low bits are its integer
-constexpr int kMagicBits = 0x4b400000;
+constexpr uint32_t kMagicBits = 0x4b400000u;
 constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.9259629911266175e-08f;
+constexpr float kFarthest = 62.f;     // y from which a weight counts as this one's, 0
 
-// 2^31 * 2^(j / 64), rounded
-__constant__ uint32_t kExp2Table[64] = {
-    0x80000000u, 0x8164d1f4u, 0x82cd8699u, 0x843a28c4u, 0x85aac368u, 0x871f6197u,
-    0x88980e81u, 0x8a14d575u, 0x8b95c1e4u, 0x8d1adf5bu, 0x8ea4398bu, 0x9031dc43u,
-    0x91c3d374u, 0x935a2b2fu, 0x94f4efa9u, 0x96942d37u, 0x9837f052u, 0x99e04593u,
-    0x9b8d39bau, 0x9d3ed9a7u, 0x9ef53261u, 0xa0b05110u, 0xa2704303u, 0xa43515aeu,
-    0xa5fed6aau, 0xa7cd93b5u, 0xa9a15ab5u, 0xab7a39b6u, 0xad583eeau, 0xaf3b78adu,
-    0xb123f582u, 0xb311c413u, 0xb504f334u, 0xb6fd91e3u, 0xb8fbaf47u, 0xbaff5ab2u,
-    0xbd08a39fu, 0xbf1799b6u, 0xc12c4ccau, 0xc346ccdau, 0xc5672a11u, 0xc78d74c9u,
-    0xc9b9bd86u, 0xcbec14ffu, 0xce248c15u, 0xd06333dbu, 0xd2a81d92u, 0xd4f35aacu,
-    0xd744fccbu, 0xd99d15c2u, 0xdbfbb798u, 0xde60f482u, 0xe0ccdeecu, 0xe33f8973u,
-    0xe5b906e7u, 0xe8396a50u, 0xeac0c6e8u, 0xed4f301fu, 0xefe4b99cu, 0xf281773cu,
-    0xf5257d15u, 0xf7d0df73u, 0xfa83b2dbu, 0xfd3e0c0du};
+// 2^(j / 64) / (1 + j / 64) as two floats, the first of 17 bits
+__constant__ float2 kExp2Table[64] = {
+    {1.0f, 0.000000000e+00f}, {0.9953384399414062f, -1.296752089e-06f}, {0.9909286499023438f, 1.918489488e-06f},
+    {0.9867706298828125f, -5.961908869e-07f}, {0.98284912109375f, -3.208220960e-06f}, {0.9791488647460938f, 2.861970358e-07f},
+    {0.9756698608398438f, 1.362636112e-06f}, {0.9724044799804688f, -3.805937752e-07f}, {0.9693374633789062f, 2.743434607e-06f},
+    {0.9664688110351562f, 3.590768983e-06f}, {0.9637908935546875f, 3.045987796e-06f}, {0.9612960815429688f, 2.366336048e-06f},
+    {0.9589767456054688f, 3.157347464e-06f}, {0.9568328857421875f, -2.790280291e-07f}, {0.9548492431640625f, 1.923012405e-06f},
+    {0.953033447265625f, -2.973017217e-06f}, {0.9513626098632812f, 3.082138846e-06f}, {0.9498519897460938f, 2.425128400e-07f},
+    {0.948486328125f, -5.837500225e-07f}, {0.947265625f, -3.524869499e-06f}, {0.9461746215820312f, 2.759045401e-06f},
+    {0.9452285766601562f, -7.125474326e-07f}, {0.9444122314453125f, -2.216791017e-06f}, {0.9437179565429688f, 2.515055257e-06f},
+    {0.9431533813476562f, 2.658398444e-06f}, {0.9427108764648438f, 2.803732741e-06f}, {0.9423904418945312f, 5.990795415e-08f},
+    {0.9421844482421875f, -6.950618285e-07f}, {0.9420928955078125f, -2.080247441e-06f}, {0.942108154296875f, 1.040008215e-06f},
+    {0.9422378540039062f, -1.338624315e-06f}, {0.9424667358398438f, 3.780396582e-06f}, {0.94281005859375f, -1.017011641e-06f},
+    {0.9432525634765625f, -2.525774562e-06f}, {0.9437942504882812f, -2.703074642e-06f}, {0.9444351196289062f, -3.414299954e-06f},
+    {0.9451675415039062f, 1.191897354e-06f}, {0.9459991455078125f, 1.791231171e-06f}, {0.946929931640625f, -3.231974233e-06f},
+    {0.9479446411132812f, -1.590972545e-07f}, {0.9490509033203125f, 1.912315383e-06f}, {0.9502487182617188f, 1.582835580e-06f},
+    {0.9515380859375f, -2.481344154e-06f}, {0.9529037475585938f, 3.707449878e-06f}, {0.9543609619140625f, 3.679240990e-06f},
+    {0.9559097290039062f, -3.719839924e-06f}, {0.9575271606445312f, 3.299372338e-06f}, {0.9592361450195312f, 8.021958706e-07f},
+    {0.9610214233398438f, 3.051235808e-06f}, {0.962890625f, 1.469141466e-06f}, {0.9648361206054688f, 2.783603577e-06f},
+    {0.9668655395507812f, -1.492094157e-06f}, {0.968963623046875f, 3.086124707e-06f}, {0.9711456298828125f, 4.856872238e-07f},
+    {0.9734039306640625f, -2.398458946e-06f}, {0.9757308959960938f, 1.366457923e-06f}, {0.9781341552734375f, 3.490811650e-06f},
+    {0.9806137084960938f, 3.349399321e-06f}, {0.9831695556640625f, 3.507544477e-07f}, {0.9857940673828125f, 1.565312800e-06f},
+    {0.988494873046875f, -1.163938691e-06f}, {0.9912643432617188f, -7.049936812e-07f}, {0.9941024780273438f, 2.473934728e-06f},
+    {0.9970169067382812f, 3.034099905e-07f},};
 
 // A token's place in the order, larger first: its logit's bits made to ascend, then the index
 // made to descend.
@@ -105,18 +120,7 @@ struct Elem<2> {
   static constexpr uint32_t kNone = 0xff800000u;
 };
 
-// Element e of a 16-byte vector; NaN counts as -inf, -0 as 0.
-template <int kType>
-__device__ __forceinline__ float element(const uint4& v, int e) {
-  const uint32_t* w = &v.x;
-  float x;
-  if constexpr (kType == 2) x = __uint_as_float(w[e]);
-  else if constexpr (kType == 1) x = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-  else x = __half2float(__ushort_as_half(static_cast<unsigned short>(w[e / 2] >> (e & 1) * 16)));
-  return fmaxf(x + 0.f, -INFINITY);
-}
-
-// Elements e and e + 1 as they are, for their weights (NaN and -inf weigh nothing, -0 as 0).
+// Elements e and e + 1 of a 16-byte vector as they are.
 template <int kType>
 __device__ __forceinline__ float2 pair(const uint4& v, int e) {
   const uint32_t* w = &v.x;
@@ -124,6 +128,12 @@ __device__ __forceinline__ float2 pair(const uint4& v, int e) {
   else if constexpr (kType == 1)
     return make_float2(__uint_as_float(w[e / 2] << 16), __uint_as_float(w[e / 2] & 0xffff0000u));
   else return __half22float2(*reinterpret_cast<const __half2*>(&w[e / 2]));
+}
+// Element e; NaN counts as -inf, -0 as 0.
+template <int kType>
+__device__ __forceinline__ float element(const uint4& v, int e) {
+  const float2 x = pair<kType>(v, e & ~1);
+  return fmaxf((e & 1 ? x.y : x.x) + 0.f, -INFINITY);
 }
 
 // The largest element of a vector (NaN counts as -inf).
@@ -145,71 +155,82 @@ __device__ __forceinline__ float vector_max(const uint4& v) {
 
 struct Row {
   float max;      // the row's largest logit (times s)
+  float far;      // the difference whose y is kFarthest: larger ones count as it
   float c, c_lo;  // log2(e) / T (over s) as two floats
   float s;        // 1, or 1/4 where differences would overflow beside T
-  float limit;    // from this y on (scale + 2) a weight rounds to 0; the largest is 2^scale
-  uint32_t down;  // 60 - scale, and what kMagicBits adds to an exponent
 };
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Where two logits lie below the maximum: y = (max - x) log2(e) / T >= 0, as a float, and -64 y
-// rounded to a whole number (as kMagic holds it; of no use from y = 2^16 on).
+// Where two logits (times s) lie below the maximum: y = (max - x) log2(e) / T >= 0 as a float, and
+// -64 y rounded to a whole number (as kMagic holds it).
 struct Below {
-  float2 d, y, t;
+  float2 x, d0, d, y, t;
 };
 __device__ __forceinline__ Below below(float2 x, const Row& r) {
   Below b;
-  b.d = ffma2(x, both(-1.f), both(r.max));
+  b.x = x;
+  b.d0 = ffma2(x, both(-1.f), both(r.max));
+  b.d = make_float2(fminf(b.d0.x, r.far), fminf(b.d0.y, r.far));  // (NaN, -inf: the farthest)
   b.y = fmul2(b.d, both(r.c));
   b.t = ffma2(b.y, both(-64.f), both(kMagic));
   return b;
 }
-// Counting bin: 32 a factor of two, 64 factors; the last one takes the rest. Never falls as x does.
-__device__ __forceinline__ int bin_of(float t) {  // y below 63.9
-  return (kMagicBits - static_cast<int>(__float_as_uint(t))) >> 1;
+// Counting bin, `per` to a factor of two. Never falls as x does.
+__device__ __forceinline__ int bin_of(float y, float per) {
+  return static_cast<int>(__float_as_uint(fmaf(y, per, kMagic)) - kMagicBits);
 }
 
-// The weights of two logits.
+// The weights of two logits, in two parts each: hi (units of 2^-20 of the largest) and lo (of
+// 2^-42), as kMagic holds them.
+struct Parts {
+  uint32_t hi[2], lo[2];
+};
 template <int kType>
-__device__ __forceinline__ void weights(float2 x, const Below& b, const Row& r,
-                                        const uint32_t* table, uint64_t* w) {
-  // -y = zh + zl: what the product and, in fp32, the difference were rounded by is kept. (The
-  // differences of two 16-bit values are exact but for logits thousands of times smaller than
-  // the maximum, whose error is 2^-24 of the difference and random.)
+__device__ __forceinline__ Parts weights(const Below& b, const Row& r, const float2* table) {
+  // -y = -64 y rounded / 64 + s; s keeps what the product and, in fp32, the difference were
+  // rounded by. (The differences of two 16-bit values are exact but for logits thousands of times
+  // smaller than the maximum, whose error is 2^-24 of the difference and random.)
   float2 zl = ffma2(b.d, both(-r.c), b.y);
   zl = ffma2(b.d, both(-r.c_lo), zl);
   if constexpr (kType == 2) {
-    const float2 q = ffma2(both(r.max), both(-1.f), b.d);
-    const float2 e1 = ffma2(ffma2(q, both(-1.f), b.d), both(-1.f), both(r.max));
-    const float2 err = ffma2(ffma2(x, both(1.f), q), both(-1.f), e1);
+    const float2 q = ffma2(both(r.max), both(-1.f), b.d0);
+    const float2 e1 = ffma2(ffma2(q, both(-1.f), b.d0), both(-1.f), both(r.max));
+    float2 err = ffma2(ffma2(b.x, both(1.f), q), both(-1.f), e1);
+    err = make_float2(b.d0.x < r.far ? err.x : 0.f, b.d0.y < r.far ? err.y : 0.f);
     zl = ffma2(err, both(-r.c), zl);
   }
   const float2 m = ffma2(both(kMagic), both(-1.f), b.t);
   const float2 s = ffma2(ffma2(m, both(1.f / 64.f), b.y), both(-1.f), zl);
+  // 2^s = 1 + q, |s| at most 1/128 and a little: the series' next term is under 2^-34
   float2 q = ffma2(s, both(0.05550410866f), both(0.2402265070f));
-  q = ffma2(s, q, both(0.6931471806f));
-  q = fmul2(s, q);
-  const float2 f = ffma2(q, both(536870912.f), both(kMagic));
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const uint32_t bits = __float_as_uint(e ? b.t.y : b.t.x);  // (kMagicBits is a multiple of 64)
-    uint32_t fi = __float_as_uint(e ? f.y : f.x) - (kMagicBits - (1u << 29));
-    // from here on a weight rounds to 0 (and not a number: -inf, NaN): 0 whatever the shift
-    if (!((e ? b.y.y : b.y.x) < r.limit)) fi = 0;
-    const uint32_t down = r.down - (bits >> 6);  // 63 at most
-    uint64_t half, p;
-    asm("shl.b64 %0, %1, %2;" : "=l"(half) : "l"(1ull), "r"(down - 1));
-    asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(p) : "r"(table[bits & 63]), "r"(fi), "l"(half));
-    asm("shr.b64 %0, %1, %2;" : "=l"(w[e]) : "l"(p), "r"(down));
-  }
+  q = fmul2(s, ffma2(s, q, both(0.6931471806f)));
+  // 2^(-64 y rounded / 64) = f (hi + lo): f = 2^n (1 + j / 64) from the bits of t, hi and lo by
+  // table; f hi is exact
+  const uint32_t tx = __float_as_uint(b.t.x), ty = __float_as_uint(b.t.y);
+  const float2 cx = table[tx & 63], cy = table[ty & 63];  // (kMagicBits is a multiple of 64)
+  // (by one value each, where a packed operation would want its operands brought together)
+  const float2 f = make_float2(__uint_as_float((tx << 17) + 0x3f800000u),
+                               __uint_as_float((ty << 17) + 0x3f800000u));
+  const float2 wh = make_float2(f.x * cx.x, f.y * cy.x);
+  const float2 wl = fmul2(f, make_float2(fmaf(cx.x, q.x, cx.y), fmaf(cy.x, q.y, cy.y)));
+  // their sum as two floats, and those as whole numbers: each remainder is exact
+  const float2 hi = ffma2(wh, both(1.f), wl);
+  const float2 lo = ffma2(ffma2(wh, both(-1.f), hi), both(-1.f), wl);
+  const float2 a = ffma2(hi, both(0x1p20f), both(kMagic));
+  const float2 am = ffma2(both(kMagic), both(-1.f), a);
+  const float2 rest = ffma2(ffma2(am, both(-0x1p-20f), hi), both(1.f), lo);
+  const float2 l = ffma2(rest, both(0x1p42f), both(kMagic));
+  return {{__float_as_uint(a.x), __float_as_uint(a.y)}, {__float_as_uint(l.x), __float_as_uint(l.y)}};
+}
+__device__ __forceinline__ uint64_t whole(uint32_t hi, uint32_t lo) {
+  return static_cast<uint64_t>((static_cast<int64_t>(static_cast<int32_t>(hi)) << 22) +
+                               static_cast<int32_t>(lo));
 }
 template <int kType>
-__device__ __forceinline__ uint64_t weight(float x, const Row& r, const uint32_t* table) {
-  uint64_t w[2];
-  const float2 xx = both(x * r.s);
-  weights<kType>(xx, below(xx, r), r, table, w);
-  return w[0];
+__device__ __forceinline__ uint64_t weight(float x, const Row& r, const float2* table) {
+  const Parts w = weights<kType>(below(both(x * r.s), r), r, table);
+  return whole(w.hi[0] - kMagicBits, w.lo[0] - kMagicBits);
 }
 
 // A copy of whole 16-byte words, global to shared, counted on `bar`.
@@ -225,15 +246,16 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // What the CTAs of a cluster show one another.
 struct alignas(16) Shared {
   uint32_t count[kBins];
-  unsigned long long list[kList];                  // places, in any order; or masses of bins
-  unsigned long long sums[kMaxCluster * kWarps];   // (first CTA) every warp's kept weights
+  unsigned long long list[kList];          // places, in any order; or masses of bins
+  uint32_t fine[kFine];
+  unsigned long long kept[kSums], all[kSums];  // (first CTA) every warp's sums
   unsigned long long warp[kWarps];
   unsigned long long total, found[2];
-  uint32_t table[64];
-  float max, edge[2];
+  float2 table[64];
   double fall;     // T ln(min_p)
+  float max, edge[2];
   uint32_t least;  // the key of min-p's border
-  int listed, state, at, guess[2];
+  int listed, state, at, digit[2];
   uint64_t arrived[kWarps];  // barriers of the warps' copies
 };
 static_assert(sizeof(Shared) % 16 == 0, "the slice behind it is read in 16-byte words");
@@ -265,46 +287,23 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, unsigned long long* sh
   return v;
 }
 
-// The threads that settle a list: a warp, or the block. Element j * kSize + i in v[j] of thread i.
-struct WarpGroup {
-  static constexpr int kSize = 32;
-  __device__ static int self() { return threadIdx.x & 31; }
-  __device__ static void sync() { __syncwarp(); }
-  __device__ static int count(bool x) { return __popc(__ballot_sync(0xffffffffu, x)); }
-  __device__ static uint64_t scan(uint64_t v, unsigned long long*) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, v, o);
-      if (self() >= o) v += y;
-    }
-    return v;
-  }
-};
-struct BlockGroup {
-  static constexpr int kSize = kThreads;
-  __device__ static int self() { return threadIdx.x; }
-  __device__ static void sync() { __syncthreads(); }
-  __device__ static int count(bool x) { return __syncthreads_count(x); }
-  __device__ static uint64_t scan(uint64_t v, unsigned long long* sh) { return block_scan(v, sh); }
-};
-
-// A bitonic sort, falling, of the first `size` values (a power of two, 32 at least).
-template <class Group, int kPer>
+// A bitonic sort, falling, of the first `size` values (a power of two, 32 at least): element
+// j * kThreads + tid in v[j] of thread tid.
+template <int kPer>
 __device__ __forceinline__ void sort_falling(uint64_t* v, int size, unsigned long long* sh) {
-  constexpr int kSize = Group::kSize;
-  const int me = Group::self();
+  const int me = threadIdx.x;
 #pragma unroll 1
   for (int k = 2; k <= size; k <<= 1) {
 #pragma unroll 1
     for (int s = k >> 1; s > 0; s >>= 1) {
-      if (s >= kSize) {
-        const int js = s / kSize;
+      if (s >= kThreads) {
+        const int js = s / kThreads;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
 #pragma unroll
           for (int o = j + 1; o < kPer; ++o) {
             if ((j ^ o) != js) continue;
-            const bool up = ((j * kSize + me) & k) == 0;
+            const bool up = ((j * kThreads + me) & k) == 0;
             if ((v[j] < v[o]) == up) {
               const uint64_t y = v[j];
               v[j] = v[o];
@@ -316,19 +315,19 @@ __device__ __forceinline__ void sort_falling(uint64_t* v, int size, unsigned lon
       }
       uint64_t other[kPer];
       if (s >= 32) {
-        Group::sync();
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sh[j * kSize + me] = v[j];
-        Group::sync();
+        for (int j = 0; j < kPer; ++j) sh[j * kThreads + me] = v[j];
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) other[j] = sh[j * kSize + (me ^ s)];
+        for (int j = 0; j < kPer; ++j) other[j] = sh[j * kThreads + (me ^ s)];
       } else {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) other[j] = __shfl_xor_sync(0xffffffffu, v[j], s);
       }
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int i = j * kSize + me;
+        const int i = j * kThreads + me;
         const bool larger = ((i & k) == 0) == ((i & s) == 0);
         if (larger == (v[j] < other[j])) v[j] = other[j];
       }
@@ -394,6 +393,9 @@ struct Sampler {
   }
   template <class V>
   __device__ __forceinline__ V* at_first(V* v) const { return cluster.map_shared_rank(v, 0); }
+  __device__ __forceinline__ uint64_t weight_at(uint64_t at) const {
+    return weight<kType>(logit_at(at), r, sh.table);
+  }
 
   __device__ __forceinline__ void append(uint64_t at) const {
     const int i = atomicAdd(&sh.listed, 1);
@@ -426,7 +428,7 @@ struct Sampler {
   __device__ __forceinline__ void finish(int token, float logit, uint64_t z) const {
     p.tokens[row] = token;
     const double lw = greedy ? 0.0 : (static_cast<double>(logit) - peak) / T;
-    p.logprobs[row] = static_cast<float>(lw - log(ldexp(static_cast<double>(z), -p.scale)));
+    p.logprobs[row] = static_cast<float>(lw - log(static_cast<double>(z) * 0x1p-42));
   }
   __device__ __forceinline__ uint64_t point(uint64_t z) const {
     return __umul64hi(static_cast<uint64_t>(p.random[row]) << 32, z);
@@ -435,94 +437,8 @@ struct Sampler {
   __device__ __forceinline__ uint64_t min_place() const {
     return place(min_p > 0.f ? sh.least : kLowestKey, kIdxMask);
   }
-
-  // The list of n places, all that may be kept, decides: top-k, top-p of the sum of those, min-p,
-  // the draw. (First CTA; the warps of the group.)
-  template <class Group, int kPer>
-  __device__ __forceinline__ void decide(int n, uint64_t all, bool by_all) const {
-    constexpr int kSize = Group::kSize;
-    const int me = Group::self();
-    uint64_t v[kPer], upto[kPer];
-    int size = 32;
-    while (size < n) size <<= 1;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = j * kSize + me < n ? sh.list[j * kSize + me] : 0;
-    sort_falling<Group, kPer>(v, size, sh.list);
-    const int nk = k > 0 && k < n ? k : n;
-    auto scan = [&](int m, auto weight_of) {
-      uint64_t carry = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if (j * kSize < m) {  // (uniform)
-          upto[j] = carry + Group::scan(j * kSize + me < m ? weight_of(v[j]) : 0, sh.warp);
-          if (kPer > 1) {
-            Group::sync();
-            if (me == kSize - 1) sh.total = upto[j];
-            Group::sync();
-            carry = sh.total;
-          }
-        }
-      }
-    };
-    auto count = [&](int m, auto pred) {  // of the first m
-      int c = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j * kSize < m) c += Group::count(j * kSize + me < m && pred(j));
-      return c;
-    };
-    auto show = [&](int i) {  // the sum up to i, to every thread
-      Group::sync();
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j * kSize + me == i) sh.total = upto[j];
-      Group::sync();
-      return static_cast<uint64_t>(sh.total);
-    };
-    scan(nk, [&](uint64_t at) { return weight<kType>(logit_at(at), r, sh.table); });
-    int m = nk;
-    if (top_p < 1.f) {
-      const uint64_t target = share_of(by_all ? all : show(nk - 1));
-      m = min(m, count(nk, [&](int j) { return upto[j] < target; }) + 1);
-    }
-    if (min_p > 0.f) {
-      const uint64_t least = min_place();
-      m = min(m, count(m, [&](int j) { return v[j] >= least; }));
-    }
-    const uint64_t z = show(m - 1), goal = point(z);
-    // the kept ones in the vocabulary's order: the index (as a place has it) before the key
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      v[j] = j * kSize + me < m
-                 ? (v[j] & kIdxMask) << 32 | static_cast<uint32_t>(v[j] >> kIdxBits)
-                 : 0;
-    int at = 0;
-    if (m > 1) {
-      size = 32;
-      while (size < m) size <<= 1;
-      sort_falling<Group, kPer>(v, size, sh.list);
-      scan(m, [&](uint64_t u) {
-        return weight<kType>(of_key(static_cast<uint32_t>(u)), r, sh.table);
-      });
-      at = count(m, [&](int j) { return upto[j] <= goal; });
-    }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (j * kSize + me == at)
-        finish(static_cast<int>(kIdxMask - (v[j] >> 32)), of_key(static_cast<uint32_t>(v[j])), z);
-  }
-  __device__ void decide(int n, uint64_t all, bool by_all) const {
-    if (n <= 128) {
-      if (warp == 0) decide<WarpGroup, 4>(n, all, by_all);
-    } else if (n <= kThreads) {
-      decide<BlockGroup, 1>(n, all, by_all);
-    } else {
-      decide<BlockGroup, kList / kThreads>(n, all, by_all);
-    }
-  }
-
-  // top_p's share of a sum, rounded up: a place is kept while the sum before it is less.
-  // (top_p is 24 bits and a power of two: the product is exact.)
+  // top_p's share of a sum, rounded up: a place is kept while the sum before it is less. (top_p is
+  // 24 bits and a power of two: the product is exact.)
   __device__ __forceinline__ uint64_t share_of(uint64_t z) const {
     const uint32_t bits = __float_as_uint(top_p);
     const uint64_t m = (bits & 0x7fffffu) | 0x800000u;
@@ -536,16 +452,155 @@ struct Sampler {
     return (hi << (64 - down) | lo >> down) + ((lo & ((1ull << down) - 1)) != 0 ? 1 : 0);
   }
 
-  // Every warp's kept weights are in sh.sums: the draw among the places from `cut` on. The row's
-  // logits of the warp that the point lies in are read again. (First CTA.)
+  // ---- the list of n places, all that may be kept, decides: top-k, top-p of the sum of those (or
+  // of `all`), min-p, the draw. (First CTA.)
+
+  // A few: each compares itself with the others, `parts` threads for a place, thread by thread a
+  // part of the others. Sums of the weights in sh.list + kCounted over the places that `counts`,
+  // and their number.
+  struct Counted {
+    uint64_t sum;
+    int n;
+  };
+  template <class Counts>
+  __device__ __forceinline__ Counted compare(int n, int i, int part, int parts, Counts counts) const {
+    Counted c{0, 0};
+    const unsigned long long *at = sh.list, *w = sh.list + kCounted;
+    if (i < n) {
+#pragma unroll 4
+      for (int j = part; j < n; j += parts) {
+        if (counts(at[j])) {
+          c.sum += w[j];
+          ++c.n;
+        }
+      }
+    }
+    for (int o = parts >> 1; o; o >>= 1) {
+      c.sum += __shfl_xor_sync(0xffffffffu, c.sum, o);
+      c.n += __shfl_xor_sync(0xffffffffu, c.n, o);
+    }
+    return c;
+  }
+  __device__ __forceinline__ int parts_of(int n) const {
+    return n <= 32 ? 8 : n <= 64 ? 4 : n <= 128 ? 2 : 1;
+  }
+  __device__ __forceinline__ void weigh(int n) const {
+    for (int i = tid; i < n; i += kThreads) sh.list[kCounted + i] = weight_at(sh.list[i]);
+    __syncthreads();
+  }
+  __device__ __forceinline__ void decide_few(int n, uint64_t all, bool by_all) const {
+    weigh(n);
+    const int parts = parts_of(n), i = tid / parts, part = tid % parts;
+    const uint64_t own = i < n ? sh.list[i] : 0, w = i < n ? sh.list[kCounted + i] : 0;
+    const Counted before = compare(n, i, part, parts, [&](uint64_t at) { return at > own; });
+    const int nk = k > 0 && k < n ? k : n;
+    auto show = [&](int rank_of) {  // the sum up to the place of a rank, to every thread
+      if (i < n && part == 0 && before.n == rank_of) sh.total = before.sum + w;
+      __syncthreads();
+      const uint64_t y = sh.total;
+      __syncthreads();
+      return y;
+    };
+    bool keep = i < n && before.n < nk;
+    if (top_p < 1.f) {
+      const uint64_t target = share_of(by_all ? all : show(nk - 1));
+      keep = keep && before.sum < target;
+    }
+    if (min_p > 0.f) keep = keep && own >= min_place();
+    const int m = __syncthreads_count(keep && part == 0);
+    const uint64_t z = show(m - 1), goal = point(z);
+    // in the vocabulary's order (a place's index falls): sums of the kept weights before
+    if (i < n && part == 0 && !keep) sh.list[kCounted + i] = 0;
+    __syncthreads();
+    const Counted left = compare(n, i, part, parts, [&](uint64_t at) {
+      return (at & kIdxMask) > (own & kIdxMask);
+    });
+    if (keep && part == 0 && left.sum <= goal && goal < left.sum + w)
+      finish(token_at(own), logit_at(own), z);
+  }
+  // More: sorted by their places, then by their indexes.
+  template <int kPer>
+  __device__ __forceinline__ void decide_sorted(int n, uint64_t all, bool by_all) const {
+    uint64_t v[kPer], upto[kPer];
+    int size = 32;
+    while (size < n) size <<= 1;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v[j] = j * kThreads + tid < n ? sh.list[j * kThreads + tid] : 0;
+    sort_falling<kPer>(v, size, sh.list);
+    const int nk = k > 0 && k < n ? k : n;
+    auto scan = [&](int m, auto weight_of) {
+      uint64_t carry = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (j * kThreads < m) {  // (uniform)
+          upto[j] = carry + block_scan(j * kThreads + tid < m ? weight_of(v[j]) : 0, sh.warp);
+          __syncthreads();
+          if (tid == kThreads - 1) sh.total = upto[j];
+          __syncthreads();
+          carry = sh.total;
+        }
+      }
+    };
+    auto count = [&](int m, auto pred) {  // of the first m
+      int c = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j * kThreads < m) c += __syncthreads_count(j * kThreads + tid < m && pred(j));
+      return c;
+    };
+    auto show = [&](int i) {  // the sum up to i, to every thread
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j * kThreads + tid == i) sh.total = upto[j];
+      __syncthreads();
+      return static_cast<uint64_t>(sh.total);
+    };
+    scan(nk, [&](uint64_t at) { return weight_at(at); });
+    int m = nk;
+    if (top_p < 1.f) {
+      const uint64_t target = share_of(by_all ? all : show(nk - 1));
+      m = min(m, count(nk, [&](int j) { return upto[j] < target; }) + 1);
+    }
+    if (min_p > 0.f) {
+      const uint64_t least = min_place();
+      m = min(m, count(m, [&](int j) { return v[j] >= least; }));
+    }
+    const uint64_t z = show(m - 1), goal = point(z);
+    // the kept ones in the vocabulary's order: the index (as a place has it) before the key
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      v[j] = j * kThreads + tid < m
+                 ? (v[j] & kIdxMask) << 32 | static_cast<uint32_t>(v[j] >> kIdxBits)
+                 : 0;
+    size = 32;
+    while (size < m) size <<= 1;
+    sort_falling<kPer>(v, size, sh.list);
+    scan(m, [&](uint64_t u) {
+      return weight<kType>(of_key(static_cast<uint32_t>(u)), r, sh.table);
+    });
+    const int at = count(m, [&](int j) { return upto[j] <= goal; });
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (j * kThreads + tid == at)
+        finish(static_cast<int>(kIdxMask - (v[j] >> 32)), of_key(static_cast<uint32_t>(v[j])), z);
+  }
+  __device__ void decide(int n, uint64_t all, bool by_all) const {
+    if (n <= kCounted) decide_few(n, all, by_all);
+    else if (n <= kShort) decide_sorted<kShort / kThreads>(n, all, by_all);
+    else decide_sorted<kList / kThreads>(n, all, by_all);
+  }
+
+  // ---- Every warp's kept weights are in sh.kept: the draw among the places from `cut` on. The
+  // row's logits of the warp that the point lies in are read again. (First CTA.)
   __device__ void draw(uint64_t cut) const {
     const int n = ctas * kWarps;
-    const uint64_t upto = block_scan(tid < n ? sh.sums[tid] : 0, sh.warp);
+    const uint64_t own = tid < n ? sh.kept[tid] : 0;
+    const uint64_t upto = block_scan(own, sh.warp);
     __syncthreads();
     if (tid == n - 1) sh.total = upto;
     __syncthreads();
     const uint64_t z = sh.total, goal = point(z);
-    const uint64_t own = tid < n ? sh.sums[tid] : 0;
     if (tid < n && goal < upto && goal >= upto - own) {
       sh.at = tid;
       sh.found[0] = upto - own;
@@ -586,10 +641,10 @@ struct Sampler {
     }
   }
   // A warp's sum to the first CTA. (The cluster meets behind it.)
-  __device__ __forceinline__ void send_sum(uint64_t y) const {
+  __device__ __forceinline__ void send_sum(uint64_t y, unsigned long long* sums) const {
 #pragma unroll
     for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (lane == 0) at_first(sh.sums)[rank * kWarps + warp] = y;
+    if (lane == 0) at_first(sums)[rank * kWarps + warp] = y;
   }
 
   // ---- the digit by digit search: places from `cut` on, up to which the sum (of 1 each, or of
@@ -613,11 +668,11 @@ struct Sampler {
         else atomicAdd(&sh.count[d], 1u);
       });
       cluster.sync();
-      // four digits a thread, the highest first
-      uint64_t sum[4], all = 0;
+      // some digits a thread, the highest first
+      uint64_t sum[kPerThread], all = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = bins - 1 - (4 * tid + i);
+      for (int i = 0; i < kPerThread; ++i) {
+        const int d = bins - 1 - (kPerThread * tid + i);
         sum[i] = 0;
         for (int q = 0; d >= 0 && q < ctas; ++q)
           sum[i] += by_mass ? *cluster.map_shared_rank(&sh.list[d], q)
@@ -626,9 +681,9 @@ struct Sampler {
       }
       uint64_t before = block_scan(all, sh.warp) - all;
       if (before < target && before + all >= target) {
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kPerThread; ++i) {
           if (before + sum[i] >= target) {
-            sh.found[0] = bins - 1 - (4 * tid + i);
+            sh.found[0] = bins - 1 - (kPerThread * tid + i);
             sh.found[1] = before;
             break;
           }
@@ -676,23 +731,44 @@ struct Sampler {
     uint64_t y = 0;
     if ((cut & kIdxMask) == 0 && r.s == 1.f) {  // (every token of the least logit)
       const float edge = logit_at(cut);
-      const bool all = cut <= place(kLowestKey, kIdxMask);
-      each_vector([&](const uint4& w, int) {
-        if (!all && vector_max<kType>(w) < edge) return;
+      uint32_t hi = 0, lo = 0, n = 0;
+      if (cut <= place(kLowestKey, kIdxMask)) {  // (what is no token weighs nothing)
+        each_vector([&](const uint4& w, int) {
 #pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-          const float2 v = pair<kType>(w, e);
-          uint64_t we[2];
-          weights<kType>(v, below(v, r), r, sh.table, we);
-          y += (all || v.x >= edge ? we[0] : 0) + (all || v.y >= edge ? we[1] : 0);
-        }
-      });
+          for (int e = 0; e < kVec; e += 2) {
+            const Parts a = weights<kType>(below(pair<kType>(w, e), r), r, sh.table);
+            hi += a.hi[0] + a.hi[1];
+            lo += a.lo[0] + a.lo[1];
+          }
+          n += kVec;
+        });
+      } else {
+        each_vector([&](const uint4& w, int) {
+          if (vector_max<kType>(w) < edge) return;
+#pragma unroll
+          for (int e = 0; e < kVec; e += 2) {
+            const float2 v = pair<kType>(w, e);
+            const Parts a = weights<kType>(below(v, r), r, sh.table);
+            if (v.x >= edge) {
+              hi += a.hi[0];
+              lo += a.lo[0];
+              ++n;
+            }
+            if (v.y >= edge) {
+              hi += a.hi[1];
+              lo += a.lo[1];
+              ++n;
+            }
+          }
+        });
+      }
+      y = whole(hi - n * kMagicBits, lo - n * kMagicBits);
     } else {
       each([&](float v, int at) {
         if (place(key_of(v), at) >= cut) y += weight<kType>(v, r, sh.table);
       });
     }
-    send_sum(y);
+    send_sum(y, sh.kept);
     cluster.sync();
     if (rank == 0) draw(cut);
   }
@@ -708,11 +784,11 @@ struct Sampler {
       }
     });
     at = __reduce_min_sync(0xffffffffu, at);
-    if (lane == 0) at_first(sh.sums)[rank * kWarps + warp] = static_cast<unsigned>(at);
+    if (lane == 0) at_first(sh.kept)[rank * kWarps + warp] = static_cast<unsigned>(at);
     cluster.sync();
     if (rank == 0 && warp == 0) {
       int v = 0x7fffffff;
-      for (int i = lane; i < ctas * kWarps; i += 32) v = min(v, static_cast<int>(sh.sums[i]));
+      for (int i = lane; i < ctas * kWarps; i += 32) v = min(v, static_cast<int>(sh.kept[i]));
       v = __reduce_min_sync(0xffffffffu, v);
       if (lane == 0) {
         p.tokens[row] = v;
@@ -721,33 +797,61 @@ struct Sampler {
     }
   }
 
-  // ---- top-k by the threads' maxima, counted in sh.count by their keys' first 11 bits
-  __device__ float bound_of_k() const {
-    if (warp == 0) {
-      int top = static_cast<int>(key_of(peak + 0.f) >> 21), sum = 0, found = -1;
-      for (; top >= 0 && found < 0; top -= 32) {
-        const int bin = top - lane;
-        int n = 0;
-        for (int q = 0; bin >= 0 && q < ctas; ++q) n += *cluster.map_shared_rank(&sh.count[bin], q);
+  // ---- top-k by the maxima of parts of the row (two of each thread)
+
+  // The digit, from `top` down, at which the counts of all CTAs reach `want`: in sh.digit[0], what
+  // is still wanted of it in sh.digit[1]; -1 if they do not. (A warp.)
+  __device__ __forceinline__ void digit_of(const uint32_t* counts, int top, int want) const {
+    int found = -1;
+    for (; top >= 0 && found < 0; top -= 32) {
+      const int bin = top - lane;
+      int n = 0;
+      if (bin >= 0) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, n, o);
-          if (lane >= o) n += y;
-        }
-        const unsigned has = __ballot_sync(0xffffffffu, sum + n >= k);
-        if (has) found = top - (__ffs(has) - 1);
-        sum += __shfl_sync(0xffffffffu, n, 31);
+        for (int q = 0; q < kMaxCluster; ++q)
+          if (q < ctas) n += *cluster.map_shared_rank(&counts[bin], q);
       }
-      if (lane == 0) {
-        const uint32_t key = found > 0 ? static_cast<uint32_t>(found) << 21 : 0u;
-        sh.edge[0] = of_key(key > kLowestKey ? key : kLowestKey);
+      int upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const unsigned has = __ballot_sync(0xffffffffu, upto >= want);
+      if (has) {
+        const int l = __ffs(has) - 1;
+        found = top - l;
+        want -= __shfl_sync(0xffffffffu, upto - n, l);
+      } else {
+        want -= __shfl_sync(0xffffffffu, upto, 31);
       }
     }
+    if (lane == 0) {
+      sh.digit[0] = found;
+      sh.digit[1] = want;
+    }
+  }
+  __device__ float bound_of_k(const float* maxima) const {
+    if (warp == 0) digit_of(sh.count, static_cast<int>(key_of(peak + 0.f) >> 21), k);
     __syncthreads();
-    return sh.edge[0];
+    const int d = sh.digit[0];
+    uint32_t key = d > 0 ? static_cast<uint32_t>(d) << 21 : 0u;
+    if (k >= kFineTopK && d > 0) {  // and by the next digit
+      const int want = sh.digit[1];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t km = key_of(maxima[i]);
+        if (km >> 21 == static_cast<uint32_t>(d)) atomicAdd(&sh.fine[(km >> 12) & (kFine - 1)], 1u);
+      }
+      cluster.sync();
+      if (warp == 0) digit_of(sh.fine, kFine - 1, want);
+      __syncthreads();
+      key |= static_cast<uint32_t>(sh.digit[0]) << 12;  // (it is found: the first digit was)
+    }
+    return of_key(key > kLowestKey ? key : kLowestKey);
   }
   // The row by a list of all logits from `edge` on; false if they are too many.
-  __device__ bool by_list(float edge, uint64_t all, bool by_all) const {
+  __device__ bool by_list(float edge) const {
     list_from(edge);
     send_list();
     cluster.sync();
@@ -756,21 +860,17 @@ struct Sampler {
       cluster.sync();  // (the count has been read)
       return false;
     }
-    if (rank == 0) decide(n, all, by_all);
+    if (rank == 0) decide(n, 0, false);
     return true;
   }
 
   // The least logit whose bin is at most b (bins rise as logits fall). A warp does it.
-  __device__ float edge_of(int b) const {
+  __device__ float edge_of(int b, float per) const {
     uint32_t lo = kLowestKey, hi = key_of(peak + 0.f);  // hi: a key in a bin at most b
     while (hi > lo) {
       const uint32_t step = (hi - lo) / 32 + 1;
       const uint32_t key = lo + step * lane;
-      bool in = key >= hi;
-      if (!in) {
-        const Below at = below(both(of_key(key)), r);
-        in = at.y.x < 63.9f && bin_of(at.t.x) <= b;
-      }
+      const bool in = key >= hi || bin_of(below(both(of_key(key)), r).y.x, per) <= b;
       const int f = __ffs(__ballot_sync(0xffffffffu, in)) - 1;  // the first key in (none: hi)
       const uint32_t was = lo;
       if (f >= 0) {
@@ -785,248 +885,241 @@ struct Sampler {
 
   // ---- top-p without a small k
   __device__ bool by_nucleus() const {
-    // The sum of all weights, and counts by bin; of the logits that may be kept: those under
-    // (1 - top_p) / V of the largest weigh less than 1 - top_p of it together, so the border lies
-    // above them.
-    const float past = fminf(log2f(static_cast<float>(p.V)) - log2f(1.f - top_p) + 1.f, 63.9f);
+    // Counts by bin, of the logits that may be kept: those under (1 - top_p) / V of the largest
+    // weigh less than 1 - top_p of it together, so the border lies above them.
+    const float past =
+        fminf(log2f(static_cast<float>(p.V)) - log2f(1.f - top_p) + 1.f, kFarthest - 0.5f);
+    const float per = (kBins - 2) / past;
     for (int i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
     __syncthreads();
-    uint64_t y = 0;
     each_vector([&](const uint4& w, int) {
 #pragma unroll
       for (int e = 0; e < kVec; e += 2) {
-        const float2 v = pair<kType>(w, e);
-        const Below b = below(v, r);
-        uint64_t we[2];
-        weights<kType>(v, b, r, sh.table, we);
-        y += we[0] + we[1];
-        if (b.y.x < past) atomicAdd(&sh.count[bin_of(b.t.x)], 1u);
-        if (b.y.y < past) atomicAdd(&sh.count[bin_of(b.t.y)], 1u);
+        const Below b = below(pair<kType>(w, e), r);
+        if (b.y.x < past) atomicAdd(&sh.count[bin_of(b.y.x, per)], 1u);
+        if (b.y.y < past) atomicAdd(&sh.count[bin_of(b.y.y, per)], 1u);
       }
     });
-    y = block_sum(y, sh.warp);
-    if (tid == 0) sh.total = y;
     cluster.sync();
-    uint64_t all = 0;
-    for (int q = 0; q < ctas; ++q) all += *cluster.map_shared_rank(&sh.total, q);
-    const uint64_t target = share_of(all);
-    // the bin of the border, each bin's logits counted with its middle weight; four bins a thread
-    uint32_t n[4], sum_n = 0;
-    float mass[4], sum = 0.f;
+    // the bins of a thread, the counts of all CTAs
+    uint32_t n[kPerThread], sum_n = 0;
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPerThread; ++i) {
       n[i] = 0;
-      for (int q = 0; q < ctas; ++q) n[i] += *cluster.map_shared_rank(&sh.count[4 * tid + i], q);
-      mass[i] = static_cast<float>(n[i]) * fast_exp2(-(2 * (4 * tid + i) + 0.5f) / 64.f);
-      sum += mass[i];
+      for (int q = 0; q < ctas; ++q) n[i] += *cluster.map_shared_rank(&sh.count[kPerThread * tid + i], q);
+      sum += mass_of(n[i], kPerThread * tid + i, per);
       sum_n += n[i];
     }
-    cluster.sync();  // (the sums and counts have been read)
-    // (sums of masses in units of 2^-40: they take part in no decision)
-    const uint64_t upto_n = block_scan(sum_n, sh.warp);
-    const uint64_t own = __float2ull_rn(sum * 1099511627776.f);
+    // (sums of masses in units of 2^-40 of the largest weight: they take part in no decision)
+    const uint64_t own = __float2ull_rn(sum * 0x1p40f);
     const uint64_t upto = block_scan(own, sh.warp);
+    const uint32_t upto_n = static_cast<uint32_t>(block_scan(sum_n, sh.warp));
     __syncthreads();
-    if (tid == kThreads - 1) sh.total = upto;
-    if (tid < 2) sh.guess[tid] = 0;
-    __syncthreads();
-    // The border by the counted masses, of their own sum (what a middle weight is off by cancels)
-    // and of the exact one (some are left out): between the two, but for the bins' unevenness.
-    const uint64_t goal = (target >> (p.scale - 40)) + 1;
-    const uint64_t wants[2] = {share_of(sh.total), goal < sh.total ? goal : sh.total};
+    if (tid == kThreads - 1) {
+      sh.total = upto;
+      sh.at = static_cast<int>(upto_n);
+    }
+    if (tid < 2) sh.digit[tid] = 0;
+    cluster.sync();  // (the counts have been read: they become sums)
+    {
+      uint32_t c = upto_n - sum_n;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) sh.count[kPerThread * tid + i] = c += n[i];
+    }
+    // The border by the counted masses, of their own sum, and with as much as the others may
+    // weigh: it lies between the two but for the bins' unevenness.
+    const uint64_t rest = static_cast<uint64_t>(
+        static_cast<float>(p.V - sh.at) * fast_exp2(40.f - past));
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const uint64_t want = wants[g];
+      const uint64_t with = share_of(sh.total + (g ? rest : 0));
+      const uint64_t want = with < sh.total ? with : sh.total;
       if (upto - own < want && upto >= want) {
         float part = static_cast<float>(want - (upto - own)) * 0x1p-40f;
         int i = 0;
-        for (; i < 3; ++i) {
-          part -= mass[i];
+        for (; i < kPerThread - 1; ++i) {
+          part -= mass_of(n[i], kPerThread * tid + i, per);
           if (part <= 0.f) break;
         }
-        sh.guess[g] = 4 * tid + i;
+        sh.digit[g] = kPerThread * tid + i;
       }
     }
     __syncthreads();
-    const int mid = min(sh.guess[0], kBins - 2);
-    const int far = min(max(sh.guess[0], sh.guess[1]), kBins - 2);
-    // merged counts up to each bin, for the window's choice
-    {
-      uint32_t c = static_cast<uint32_t>(upto_n) - sum_n;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sh.count[4 * tid + i] = c += n[i];
-    }
-    __syncthreads();
-    auto upto_bin = [&](int b) { return b < 0 ? 0u : sh.count[min(b, kBins - 1)]; };
+    const int mid = min(sh.digit[0], kBins - 2);
+    const int far = min(max(sh.digit[0], sh.digit[1]), kBins - 2);
+    auto upto_bin = [&](int b) { return b < 0 ? 0u : sh.count[b]; };
     // everything down to a bin past the border, or the bins around it
     int b1 = min(far + 1, kBins - 2), b0 = 0;
-    if (upto_bin(b1) > kShort) {
+    if (upto_bin(b1) > kCounted) {
       b1 = min(mid + 1, kBins - 2);
       b0 = max(mid - 1, 0);
-      if (upto_bin(b1) - upto_bin(b0 - 1) > kShort) b0 = b1 = mid;
+      if (upto_bin(b1) - upto_bin(b0 - 1) > kCounted) b0 = mid;
+      if (upto_bin(b1) - upto_bin(b0 - 1) > kCounted) b1 = mid;
     }
     int least = 0, most = kBins - 2;  // the border's bin lies between
     while (least <= most) {
       if (upto_bin(b1) - upto_bin(b0 - 1) > kList) return false;
       if (warp == 0) {
-        const float e = edge_of(b1);
+        const float e = edge_of(b1, per);
         if (lane == 0) sh.edge[0] = e;
       } else if (warp == 1) {
-        const float e = b0 > 0 ? edge_of(b0 - 1) : INFINITY;
+        const float e = b0 > 0 ? edge_of(b0 - 1, per) : INFINITY;
         if (lane == 0) sh.edge[1] = e;
       }
       if (tid == 0 && rank != 0) sh.listed = 0;
       __syncthreads();
       const float low = sh.edge[0], high = sh.edge[1];
-      if (b0 == 0) {
-        if (by_list_round(low, all, target)) return true;
-        least = b1 + 1;  // not all of the nucleus is in the list: on by what lacks
-        b0 = step(least, 1, *at_first(&sh.found[0]));
-      } else {
-        y = 0;
-        each_vector([&](const uint4& w, int at) {
-          if (vector_max<kType>(w) >= low) {
+      // the sums of all weights and of those above the window; the window listed
+      uint32_t hi = 0, lo = 0, num = 0, hi_up = 0, lo_up = 0;
+      each_vector([&](const uint4& w, int at) {
+        const float top = vector_max<kType>(w);
 #pragma unroll
-            for (int e = 0; e < kVec; e += 2) {
-              const float2 v = pair<kType>(w, e);
-              uint64_t we[2];
-              weights<kType>(v, below(v, r), r, sh.table, we);
-              y += (v.x >= high ? we[0] : 0) + (v.y >= high ? we[1] : 0);
-              if (v.x >= low && v.x < high) append(place(key_of(v.x + 0.f), at + e));
-              if (v.y >= low && v.y < high) append(place(key_of(v.y + 0.f), at + e + 1));
-            }
+        for (int e = 0; e < kVec; e += 2) {
+          const float2 v = pair<kType>(w, e);
+          const Parts a = weights<kType>(below(v, r), r, sh.table);
+          hi += a.hi[0] + a.hi[1];
+          lo += a.lo[0] + a.lo[1];
+          if (v.x >= high) {
+            hi_up += a.hi[0] - kMagicBits;
+            lo_up += a.lo[0] - kMagicBits;
           }
-        });
-        send_sum(y);
-        send_list();
-        cluster.sync();
-        if (rank == 0) border(target);
-        cluster.sync();
-        const int state = *at_first(&sh.state);
-        if (state == 2) {  // min-p's border is the higher one
-          cluster.sync();
-          sum_and_draw(min_place());
-          return true;
+          if (v.y >= high) {
+            hi_up += a.hi[1] - kMagicBits;
+            lo_up += a.lo[1] - kMagicBits;
+          }
         }
-        if (state == 0) {
-          if (rank == 0) draw(sh.found[1]);
-          return true;
+        num += kVec;
+        if (top >= low) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            const float y = element<kType>(w, e);
+            if (y >= low && y < high) append(place(key_of(y), at + e));
+          }
         }
-        // the border lies in another bin: so far on by the masses between
-        if (state < 0) most = b0 - 1;
-        else least = b1 + 1;
-        b0 = step(state < 0 ? most : least, state < 0 ? -1 : 1, *at_first(&sh.found[0]));
+      });
+      send_sum(whole(hi - num * kMagicBits, lo - num * kMagicBits), sh.all);
+      send_sum(whole(hi_up, lo_up), sh.kept);
+      send_list();
+      cluster.sync();
+      if (rank == 0) border(b0 == 0);
+      cluster.sync();
+      const int state = *at_first(&sh.state);
+      if (state == kDone) return true;
+      if (state == kMinP) {  // min-p's border is the higher one
+        cluster.sync();
+        sum_and_draw(min_place());
+        return true;
       }
+      if (state == kHere) {
+        if (rank == 0) draw(sh.found[1]);
+        return true;
+      }
+      // the border lies in another bin: so far on by the masses between
+      if (state == kAbove) most = b0 - 1;
+      else least = b1 + 1;
+      b0 = step(state == kAbove ? most : least, state == kAbove ? -1 : 1, *at_first(&sh.found[0]),
+                per);
       b0 = b1 = min(max(b0, least), most);
       cluster.sync();  // (the state has been read, the list is empty again)
     }
     return false;
   }
-  // The bin, from `bin` on by `by`, where the counted masses reach `gap` (of 2^scale). The merged
-  // counts up to each bin are in sh.count.
-  __device__ int step(int bin, int by, uint64_t gap) const {
-    const float want = static_cast<float>(gap) * exp2f(-static_cast<float>(p.scale));
+  // A bin's counted mass, of the largest weight.
+  __device__ __forceinline__ static float mass_of(uint32_t n, int b, float per) {
+    return static_cast<float>(n) * fast_exp2(-static_cast<float>(b) / per);
+  }
+  // The bin, from `bin` on by `by`, where the counted masses reach `gap`. The counts up to each bin
+  // are in sh.count.
+  __device__ int step(int bin, int by, uint64_t gap, float per) const {
+    const float want = static_cast<float>(gap) * 0x1p-42f;
     float sum = 0.f;
-    for (; bin >= 0 && bin <= kBins - 2; bin += 32 * by) {
+    for (; bin >= 0 && bin < (kBins - 1); bin += 32 * by) {
       const int b = bin + by * lane;
       float m = 0.f;
-      if (b >= 0 && b <= kBins - 2)
-        m = static_cast<float>(sh.count[b] - (b > 0 ? sh.count[b - 1] : 0)) *
-            fast_exp2(-(2 * b + 0.5f) / 64.f);
+      if (b >= 0 && b < (kBins - 1)) m = mass_of(sh.count[b] - (b > 0 ? sh.count[b - 1] : 0), b, per);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float y = __shfl_up_sync(0xffffffffu, m, o);
         if (lane >= o) m += y;
       }
       const unsigned has = __ballot_sync(0xffffffffu, sum + m >= want);
-      if (has) return min(max(bin + by * (__ffs(has) - 1), 0), kBins - 2);
+      if (has) return bin + by * (__ffs(has) - 1);
       sum += __shfl_sync(0xffffffffu, m, 31);
     }
     return bin;
   }
-  // a window that begins at the maximum: the whole nucleus in the list
-  __device__ bool by_list_round(float low, uint64_t all, uint64_t target) const {
-    list_from(low);
-    send_list();
-    cluster.sync();
-    if (rank == 0) {
-      const int n = sh.listed;
-      uint64_t y = 0;
-      for (int i = tid; i < n; i += kThreads) y += weight<kType>(logit_at(sh.list[i]), r, sh.table);
-      y = block_sum(y, sh.warp);
-      const bool ok = y >= target;
-      if (ok) decide(n, all, true);
+  // What the first CTA found of a window: the row is done; the border is here (the cut in
+  // sh.found[1], the kept of the list added to sh.kept); min-p's is higher; it is above or below (by
+  // sh.found[0]).
+  static constexpr int kDone = 0, kHere = 1, kMinP = 2, kAbove = 3, kBelow = 4;
+  __device__ void border(bool whole_list) const {
+    const int n = min(sh.listed, kList), sums = ctas * kWarps;
+    const uint64_t all = block_sum(tid < sums ? sh.all[tid] : 0, sh.warp);
+    const uint64_t above = block_sum(tid < sums ? sh.kept[tid] : 0, sh.warp);
+    uint64_t y = 0;
+    for (int i = tid; i < n; i += kThreads) y += weight_at(sh.list[i]);
+    const uint64_t upto = above + block_sum(y, sh.warp);
+    const uint64_t target = share_of(all);
+    int state = above >= target ? kAbove : upto < target ? kBelow : kHere;
+    if (state == kHere && whole_list) {
+      decide(n, all, true);
+      state = kDone;
+    } else if (state == kHere) {
+      if (n <= kCounted) border_few(n, above, target);
+      else if (n <= kShort) border_sorted<kShort / kThreads>(n, above, target);
+      else border_sorted<kList / kThreads>(n, above, target);
       __syncthreads();
-      if (tid == 0) {
-        sh.state = ok ? 0 : 1;
-        sh.found[0] = target - y;
-        sh.listed = 0;
-      }
+      if (min_place() > sh.found[1]) state = kMinP;
     }
-    cluster.sync();
-    return *at_first(&sh.state) == 0;
-  }
-  // The border of `target` in the list, the weights above the list's in sh.sums: sh.state 0 if it
-  // is there (the cut in sh.found[1], the kept of the list added to sh.sums), -1 above, 1 below;
-  // 2 if min-p's is higher. (First CTA.)
-  __device__ void border(uint64_t target) const {
-    const int n = min(sh.listed, kList);
-    const uint64_t above = block_sum(tid < ctas * kWarps ? sh.sums[tid] : 0, sh.warp);
-    if (n <= 128) {
-      if (warp == 0) border_t<WarpGroup, 4>(n, above, target);
-    } else if (n <= kThreads) {
-      border_t<BlockGroup, 1>(n, above, target);
-    } else {
-      border_t<BlockGroup, kList / kThreads>(n, above, target);
+    __syncthreads();
+    if (tid == 0) {
+      sh.state = state;
+      if (state >= kAbove) sh.found[0] = state == kAbove ? above - target : target - upto;
+      sh.listed = 0;
     }
     __syncthreads();
   }
-  template <class Group, int kPer>
-  __device__ __forceinline__ void border_t(int n, uint64_t above, uint64_t target) const {
-    constexpr int kSize = Group::kSize;
-    const int me = Group::self();
+  // A kept place of the list counts to the warp that its logit lies in.
+  __device__ __forceinline__ void add_kept(uint64_t at, uint64_t w) const {
+    const int token = token_at(at), q = token / p.slice;
+    const Slice s = slice_of(q);
+    const int t = (token - s.first) / kTile / s.per_warp;
+    atomicAdd(&sh.kept[q * kWarps + t], static_cast<unsigned long long>(w));
+  }
+  __device__ __forceinline__ void border_few(int n, uint64_t above, uint64_t target) const {
+    weigh(n);
+    const int parts = parts_of(n), i = tid / parts, part = tid % parts;
+    const uint64_t own = i < n ? sh.list[i] : 0, w = i < n ? sh.list[kCounted + i] : 0;
+    const uint64_t before =
+        above + compare(n, i, part, parts, [&](uint64_t at) { return at > own; }).sum;
+    if (i < n && part == 0 && before < target) {
+      add_kept(own, w);
+      if (before + w >= target) sh.found[1] = own;
+    }
+  }
+  template <int kPer>
+  __device__ __forceinline__ void border_sorted(int n, uint64_t above, uint64_t target) const {
     uint64_t v[kPer];
     int size = 32;
     while (size < n) size <<= 1;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = j * kSize + me < n ? sh.list[j * kSize + me] : 0;
-    sort_falling<Group, kPer>(v, size, sh.list);
+    for (int j = 0; j < kPer; ++j) v[j] = j * kThreads + tid < n ? sh.list[j * kThreads + tid] : 0;
+    sort_falling<kPer>(v, size, sh.list);
     uint64_t sum = above;
-    int kept = 0;  // those whose sum with what is before them is below the target, and one more
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      if (j * kSize >= n) continue;  // (uniform)
-      const bool in = j * kSize + me < n;
-      const uint64_t upto =
-          sum + Group::scan(in ? weight<kType>(logit_at(v[j]), r, sh.table) : 0, sh.warp);
-      Group::sync();
-      if (me == kSize - 1) sh.total = upto;
-      Group::sync();
-      kept += Group::count(in && upto < target);
-      sum = sh.total;
-    }
-    Group::sync();
-    const bool ok = above < target && sum >= target;
-    if (ok) {
-      ++kept;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = j * kSize + me;
-        if (i == kept - 1) sh.found[1] = v[j];
-        if (i < kept) {
-          const int token = token_at(v[j]), q = token / p.slice;
-          const Slice s = slice_of(q);
-          const int w = (token - s.first) / kTile / s.per_warp;
-          atomicAdd(&sh.sums[q * kWarps + w],
-                    static_cast<unsigned long long>(weight<kType>(logit_at(v[j]), r, sh.table)));
-        }
+      if (j * kThreads >= n) continue;  // (uniform)
+      const bool in = j * kThreads + tid < n;
+      const uint64_t w = in ? weight_at(v[j]) : 0, upto = sum + block_scan(w, sh.warp);
+      if (in && upto - w < target) {
+        add_kept(v[j], w);
+        if (upto >= target) sh.found[1] = v[j];
       }
-    }
-    Group::sync();
-    if (me == 0) {
-      sh.state = !ok ? (above >= target ? -1 : 1) : min_place() > sh.found[1] ? 2 : 0;
-      if (!ok) sh.found[0] = above >= target ? above - target : target - sum;
-      sh.listed = 0;
+      __syncthreads();
+      if (tid == kThreads - 1) sh.total = upto;
+      __syncthreads();
+      sum = sh.total;
     }
   }
 };
@@ -1044,29 +1137,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   s.lane = s.tid & 31;
   s.warp = s.tid >> 5;
   s.x = static_cast<const typename S::Bits*>(p.logits) + s.row * p.ld;
-  if (s.tid < 64) sh.table[s.tid] = kExp2Table[s.tid];
-  for (int i = s.tid; i < kBins; i += kThreads) sh.count[i] = 0;
-  if (s.tid == 0) sh.listed = 0;
   if (s.lane == 0) {
     mbar_init(&sh.arrived[s.warp], 1);
     fence_barrier_init();
   }
-  __syncthreads();
+  __syncwarp();
   pdl_wait();
-  s.T = p.temperature ? p.temperature[s.row] : 1.f;
-  s.k = p.top_k ? p.top_k[s.row] : 0;
-  s.top_p = p.top_p ? p.top_p[s.row] : 1.f;
-  s.min_p = p.min_p ? p.min_p[s.row] : 0.f;
-  s.greedy = !(s.T >= 0x1p-100f);
-  if (s.k >= p.V || s.k < 0) s.k = 0;
 
-  // min-p's border below the maximum: one thread's work while the others load
-  const bool bordered = s.min_p > 0.f && !s.greedy;
-  if (bordered && s.tid == kThreads - 1)
-    sh.fall = s.min_p < 1.f ? static_cast<double>(s.T) * log(static_cast<double>(s.min_p)) : 0.0;
-
-  // ---- the slice, and the maximum: a copy a warp of the words that lie in the slice whole, the
-  // others word by word
+  // ---- the slice: a copy a warp of the words that lie in it whole, the others word by word
   const typename S::Slice slice = s.slice_of(s.rank);
   s.first = slice.first;
   s.t0 = min(s.warp * slice.per_warp, slice.tiles);
@@ -1081,20 +1159,47 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   if (s.t1 * 32 > whole1 || s.t0 * 32 < whole0)
     for (int v = s.t0 * 32 + s.lane; v < s.t1 * 32; v += 32)
       if (v < whole0 || v >= whole1) s.data[v] = s.load(s.first + v * S::kVec, slice);
-  float mx = -INFINITY;
+  // beside the copies: what the row asks for, and shared memory made ready
+  s.T = p.temperature ? p.temperature[s.row] : 1.f;
+  s.k = p.top_k ? p.top_k[s.row] : 0;
+  s.top_p = p.top_p ? p.top_p[s.row] : 1.f;
+  s.min_p = p.min_p ? p.min_p[s.row] : 0.f;
+  s.greedy = !(s.T >= 0x1p-100f);
+  if (s.k >= p.V || s.k < 0) s.k = 0;
+  if (s.tid < 64) sh.table[s.tid] = kExp2Table[s.tid];
+  if (s.k > 0) {
+    for (int i = s.tid; i < kBins; i += kThreads) sh.count[i] = 0;
+    for (int i = s.tid; i < kFine; i += kThreads) sh.fine[i] = 0;
+  }
+  if (s.tid == 0) sh.listed = 0;
+  const bool bordered = s.min_p > 0.f && !s.greedy;
+  if (bordered && s.tid == kThreads - 1)  // (fp64 by every thread would cost microseconds)
+    sh.fall = s.min_p < 1.f ? static_cast<double>(s.T) * log(static_cast<double>(s.min_p)) : 0.0;
+  __syncthreads();
+
+  // ---- the maximum
+  float mx[2] = {-INFINITY, -INFINITY};
   if (b > a && !mbar_wait(&sh.arrived[s.warp], 0)) record_error(p.err, kDevWaitTimeout);
   __syncwarp();
-  for (int t = s.t0; t < s.t1; ++t)
-    mx = fmaxf(mx, vector_max<kType>(s.data[t * 32 + s.lane]));
-  mx += 0.f;
-  if (s.k > 0 && mx > -INFINITY) atomicAdd(&sh.count[key_of(mx) >> 21], 1u);
+  for (int t = s.t0; t < s.t1; t += 2) {
+    mx[0] = fmaxf(mx[0], vector_max<kType>(s.data[t * 32 + s.lane]));
+    if (t + 1 < s.t1) mx[1] = fmaxf(mx[1], vector_max<kType>(s.data[(t + 1) * 32 + s.lane]));
+  }
+  const float maxima[2] = {mx[0] + 0.f, mx[1] + 0.f};
+  if (s.k > 0) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (s.lane == 0) sh.warp[s.warp] = __float_as_uint(mx);
+    for (int i = 0; i < 2; ++i)
+      if (maxima[i] > -INFINITY) atomicAdd(&sh.count[key_of(maxima[i]) >> 21], 1u);
+  }
+  float top = fmaxf(maxima[0], maxima[1]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (s.lane == 0) sh.warp[s.warp] = __float_as_uint(top);
   __syncthreads();
   if (s.tid == 0) {
-    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, __uint_as_float(static_cast<uint32_t>(sh.warp[w])));
-    sh.max = mx;
+    for (int w = 1; w < kWarps; ++w)
+      top = fmaxf(top, __uint_as_float(static_cast<uint32_t>(sh.warp[w])));
+    sh.max = top;
   }
   s.cluster.sync();
   s.peak = -INFINITY;
@@ -1117,12 +1222,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const bool far = s.T >= 0x1p100f;
   s.r.s = far ? 0.25f : 1.f;
   s.r.max = s.peak * s.r.s;
-  // log2(e) / T to 2^-45 in two floats (fp64 by every thread costs microseconds here)
+  // log2(e) / T to 2^-45 in two floats
   const float Ts = s.T * s.r.s;
   s.r.c = kLog2eHi / Ts;
   s.r.c_lo = s.r.c > 0.f ? (fmaf(-s.r.c, Ts, kLog2eHi) + kLog2eLo) / Ts : 0.f;
-  s.r.limit = static_cast<float>(p.scale + 2);
-  s.r.down = 60 - p.scale + (kMagicBits >> 6);
+  s.r.far = fminf(kFarthest / s.r.c, FLT_MAX);
   if (bordered) {
     if (s.tid == kThreads - 1) {
       const uint32_t key = key_of(__double2float_ru(s.peak + sh.fall) + 0.f);
@@ -1133,9 +1237,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   bool done = false;
   if (!far) {
     if (s.k > 0 && s.k <= kMaxTopK) {
-      done = s.by_list(s.bound_of_k(), 0, false);
+      done = s.by_list(s.bound_of_k(maxima));
     } else if (s.k == 0 && s.top_p < 1.f) {
-      done = p.V <= kShort ? s.by_list(-FLT_MAX, 0, false) : s.by_nucleus();
+      done = p.V <= kCounted ? s.by_list(-FLT_MAX) : s.by_nucleus();
     } else if (s.k == 0) {
       s.sum_and_draw(s.min_place());
       done = true;
@@ -1176,10 +1280,6 @@ cudaError_t launch_sample(SampleParams p, int dtype, int num_sms, cudaStream_t s
          slice(cluster * 2) >= 4 * kThreads * word)
     cluster *= 2;
   p.slice = slice(cluster);
-  // the sum of V weights stays below 2^62
-  p.scale = 62;
-  while (p.scale > 0 && (static_cast<int64_t>(p.V) - 1) >> (62 - p.scale) != 0) --p.scale;
-  if (p.scale > 58) p.scale = 58;  // (a weight is made with 60 bits)
   switch (dtype) {
     case 0: return launch_t<0>(p, cluster, stream);
     case 1: return launch_t<1>(p, cluster, stream);

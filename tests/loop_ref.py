@@ -49,9 +49,11 @@ def draw(x, T, k, p, m, word, shift=0.0, p_shift=0.0):
 
 def check_draws(x, tokens, logprobs, bits, T=None, k=None, p=None, m=None):
     """Every row's token and log probability. Weights are off by 2^-29 of themselves and rounded to
-    2^-58 of the largest times their number, so a border between tokens lies within
-    2^-28 of the sum of where it is in 64 bits: there either neighbour is right, elsewhere one.
-    The log probability is a double rounded once (2^-24), with the sum's 2^-29."""
+    multiples of 2^-42 of the largest, so V of them add up to within 2^-29 + V 2^-43 of the sum
+    (which is no less than the largest), and a border between tokens, a ratio of two such sums, lies
+    within twice that of where it is in 64 bits: there either neighbour is right, elsewhere one.
+    The log probability is a double rounded once (2^-24 of it), off by the sum's error and by its
+    own weight's: 2^-29, and 2^-43 of the largest, which is 2^-43 / w of it."""
     x64 = x.double().cpu().numpy()
     tokens, logprobs = tokens.tolist(), logprobs.double().tolist()
     bits = [b & 0xffffffff for b in bits.tolist()]
@@ -59,7 +61,8 @@ def check_draws(x, tokens, logprobs, bits, T=None, k=None, p=None, m=None):
     def at(t, b):
         return None if t is None else t[b].item()
 
-    eps = 2.0 ** -28
+    V = x.shape[1]
+    eps = 2.0 ** -28 + V * 2.0 ** -42
     for b in range(x.shape[0]):
         args = (at(T, b), at(k, b), at(p, b), at(m, b), bits[b])
         want = draw(x64[b], *args)
@@ -71,7 +74,8 @@ def check_draws(x, tokens, logprobs, bits, T=None, k=None, p=None, m=None):
         if want[1] == -math.inf:
             assert logprobs[b] == -math.inf
         else:
-            tol = 2.0 ** -24 * abs(want[1]) + 2.0 ** -27
+            # (the weight is at least its share of the sum, of the largest)
+            tol = 2.0 ** -24 * abs(want[1]) + eps + 2.0 ** -43 * math.exp(-want[1])
             assert abs(logprobs[b] - want[1]) <= tol, (b, args, logprobs[b], want)
 
 
