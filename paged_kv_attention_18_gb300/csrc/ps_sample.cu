@@ -17,17 +17,17 @@
 // first CTA decides, the others leave as soon as it has what it needs of them. By what the row
 // asks for:
 //   - the largest logit alone: its first place;
-//   - top-k: the k-th largest of the maxima of parts of the row bounds the k-th logit from below;
-//     the few logits from the bound on are listed, and the list decides everything;
+//   - a small top-k: the k-th largest of the maxima of parts of the row bounds the k-th logit from
+//     below; the few logits from the bound on are listed, and the list decides everything;
 //   - top-p without it: a first pass counts the logits by weight (80 bins or so a factor of two), each
 //     bin with its middle weight, to guess the border's bin; a second one sums all weights and
 //     those above that bin exactly, and lists the logits around it. The list, in order, has the
 //     border if the sums say so; else a next bin is tried. A nucleus that fits the list is listed
-//     whole;
+//     whole. A large top-k the same way, its bin by the counts, top-p of it by another pass;
 //   - none of these: the sum of all weights (from min-p's border on), by warps; the word's point
 //     lies in one warp's logits, which the first CTA reads again;
-//   - what fits none (a list that overflows, as with equal logits everywhere; k beyond 1024; T
-//     beyond 2^100): the border digit by digit, by histograms of places and exact weights.
+//   - what fits none (a list that overflows, as with equal logits everywhere; T beyond 2^100): the
+//     border digit by digit, by histograms of places and exact weights.
 #include <cooperative_groups.h>
 
 #include <cfloat>
@@ -49,8 +49,8 @@ constexpr int kFine = 512;            // second digit of the maxima's keys
 constexpr int kList = 2048;           // places that a row's list holds
 constexpr int kCounted = 256;         // places that are put in order by counting
 constexpr int kShort = 512;           // places that sort in a fraction of the time
-constexpr int kMaxTopK = 1024;        // k up to which the parts' maxima bound it
-constexpr int kFineTopK = 128;        // k from which they do so by two digits
+constexpr int kMaxTopK = 128;         // k up to which the parts' maxima bound it
+constexpr int kFineTopK = 32;         // k from which they do so by two digits
 constexpr int kMaxCluster = 8;
 constexpr int kSums = kMaxCluster * kWarps;
 constexpr int kSmemLimit = 232448;    // of a CTA
@@ -585,7 +585,7 @@ struct Sampler {
       if (j * kThreads + tid == at)
         finish(static_cast<int>(kIdxMask - (v[j] >> 32)), of_key(static_cast<uint32_t>(v[j])), z);
   }
-  __device__ void decide(int n, uint64_t all, bool by_all) const {
+  __device__ __forceinline__ void decide(int n, uint64_t all, bool by_all) const {
     if (n <= kCounted) decide_few(n, all, by_all);
     else if (n <= kShort) decide_sorted<kShort / kThreads>(n, all, by_all);
     else decide_sorted<kList / kThreads>(n, all, by_all);
@@ -593,7 +593,7 @@ struct Sampler {
 
   // ---- Every warp's kept weights are in sh.kept: the draw among the places from `cut` on. The
   // row's logits of the warp that the point lies in are read again. (First CTA.)
-  __device__ void draw(uint64_t cut) const {
+  __device__ __forceinline__ void draw(uint64_t cut) const {
     const int n = ctas * kWarps;
     const uint64_t own = tid < n ? sh.kept[tid] : 0;
     const uint64_t upto = block_scan(own, sh.warp);
@@ -707,7 +707,7 @@ struct Sampler {
     for (int q = 0; q < ctas; ++q) y += *cluster.map_shared_rank(&sh.total, q);
     return y;
   }
-  __device__ void general() const {
+  __device__ __noinline__ uint64_t general() const {
     uint64_t cut = place(kLowestKey, kIdxMask);
     if (k > 0 && k < p.V) {
       uint64_t n = 0;
@@ -722,12 +722,11 @@ struct Sampler {
       cut = search(true, share_of(cluster_sum(z)), cut);
     }
     const uint64_t least = min_place();
-    cut = least > cut ? least : cut;
     cluster.sync();
-    sum_and_draw(cut);
+    return least > cut ? least : cut;
   }
-  // The sum of the weights from `cut` on by warps, and the draw; the row is done.
-  __device__ void sum_and_draw(uint64_t cut) const {
+  // The sum of the weights from `cut` on by warps, for the draw. (The cluster meets in it.)
+  __device__ __forceinline__ void sum_from(uint64_t cut) const {
     uint64_t y = 0;
     if ((cut & kIdxMask) == 0 && r.s == 1.f) {  // (every token of the least logit)
       const float edge = logit_at(cut);
@@ -770,11 +769,14 @@ struct Sampler {
     }
     send_sum(y, sh.kept);
     cluster.sync();
-    if (rank == 0) draw(cut);
   }
 
+  // What a row still needs: nothing; the draw from `cut` on (the sums are there); the sums first;
+  // the digit by digit search.
+  static constexpr int kDone = 0, kDraw = 1, kSum = 2, kSearch = 3;
+
   // ---- the row's first largest logit
-  __device__ void take_first() const {
+  __device__ __forceinline__ void take_first() const {
     int at = 0x7fffffff;
     each_vector([&](const uint4& w, int v) {
       if (vector_max<kType>(w) >= peak) {
@@ -831,7 +833,7 @@ struct Sampler {
       sh.digit[1] = want;
     }
   }
-  __device__ float bound_of_k(const float* maxima) const {
+  __device__ __forceinline__ float bound_of_k(const float* maxima) const {
     if (warp == 0) digit_of(sh.count, static_cast<int>(key_of(peak + 0.f) >> 21), k);
     __syncthreads();
     const int d = sh.digit[0];
@@ -851,7 +853,7 @@ struct Sampler {
     return of_key(key > kLowestKey ? key : kLowestKey);
   }
   // The row by a list of all logits from `edge` on; false if they are too many.
-  __device__ bool by_list(float edge) const {
+  __device__ __forceinline__ bool by_list(float edge) const {
     list_from(edge);
     send_list();
     cluster.sync();
@@ -865,7 +867,7 @@ struct Sampler {
   }
 
   // The least logit whose bin is at most b (bins rise as logits fall). A warp does it.
-  __device__ float edge_of(int b, float per) const {
+  __device__ __forceinline__ float edge_of(int b, float per) const {
     uint32_t lo = kLowestKey, hi = key_of(peak + 0.f);  // hi: a key in a bin at most b
     while (hi > lo) {
       const uint32_t step = (hi - lo) / 32 + 1;
@@ -883,161 +885,36 @@ struct Sampler {
     return of_key(hi);
   }
 
-  // ---- top-p without a small k
-  __device__ bool by_nucleus() const {
-    // Counts by bin, of the logits that may be kept: those under (1 - top_p) / V of the largest
-    // weigh less than 1 - top_p of it together, so the border lies above them.
-    const float past =
-        fminf(log2f(static_cast<float>(p.V)) - log2f(1.f - top_p) + 1.f, kFarthest - 0.5f);
-    const float per = (kBins - 2) / past;
-    for (int i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
-    __syncthreads();
-    each_vector([&](const uint4& w, int) {
+  // ---- top-p without a small k, or a large k
+
+  // The counts of all CTAs, merged: CTA q has bins q * width and on, in sh.count up to each of them
+  // within its slice.
+  struct Bins {
+    float per;                       // bins to a factor of two
+    int width;
+    uint32_t count[kMaxCluster];     // before slice q
+  };
+  __device__ __forceinline__ uint32_t upto_bin(const Bins& g, int b) const {
+    if (b < 0) return 0;
+    const int q = b / g.width;
+    uint32_t before = 0;
 #pragma unroll
-      for (int e = 0; e < kVec; e += 2) {
-        const Below b = below(pair<kType>(w, e), r);
-        if (b.y.x < past) atomicAdd(&sh.count[bin_of(b.y.x, per)], 1u);
-        if (b.y.y < past) atomicAdd(&sh.count[bin_of(b.y.y, per)], 1u);
-      }
-    });
-    cluster.sync();
-    // the bins of a thread, the counts of all CTAs
-    uint32_t n[kPerThread], sum_n = 0;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      n[i] = 0;
-      for (int q = 0; q < ctas; ++q) n[i] += *cluster.map_shared_rank(&sh.count[kPerThread * tid + i], q);
-      sum += mass_of(n[i], kPerThread * tid + i, per);
-      sum_n += n[i];
-    }
-    // (sums of masses in units of 2^-40 of the largest weight: they take part in no decision)
-    const uint64_t own = __float2ull_rn(sum * 0x1p40f);
-    const uint64_t upto = block_scan(own, sh.warp);
-    const uint32_t upto_n = static_cast<uint32_t>(block_scan(sum_n, sh.warp));
-    __syncthreads();
-    if (tid == kThreads - 1) {
-      sh.total = upto;
-      sh.at = static_cast<int>(upto_n);
-    }
-    if (tid < 2) sh.digit[tid] = 0;
-    cluster.sync();  // (the counts have been read: they become sums)
-    {
-      uint32_t c = upto_n - sum_n;
-#pragma unroll
-      for (int i = 0; i < kPerThread; ++i) sh.count[kPerThread * tid + i] = c += n[i];
-    }
-    // The border by the counted masses, of their own sum, and with as much as the others may
-    // weigh: it lies between the two but for the bins' unevenness.
-    const uint64_t rest = static_cast<uint64_t>(
-        static_cast<float>(p.V - sh.at) * fast_exp2(40.f - past));
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const uint64_t with = share_of(sh.total + (g ? rest : 0));
-      const uint64_t want = with < sh.total ? with : sh.total;
-      if (upto - own < want && upto >= want) {
-        float part = static_cast<float>(want - (upto - own)) * 0x1p-40f;
-        int i = 0;
-        for (; i < kPerThread - 1; ++i) {
-          part -= mass_of(n[i], kPerThread * tid + i, per);
-          if (part <= 0.f) break;
-        }
-        sh.digit[g] = kPerThread * tid + i;
-      }
-    }
-    __syncthreads();
-    const int mid = min(sh.digit[0], kBins - 2);
-    const int far = min(max(sh.digit[0], sh.digit[1]), kBins - 2);
-    auto upto_bin = [&](int b) { return b < 0 ? 0u : sh.count[b]; };
-    // everything down to a bin past the border, or the bins around it
-    int b1 = min(far + 1, kBins - 2), b0 = 0;
-    if (upto_bin(b1) > kCounted) {
-      b1 = min(mid + 1, kBins - 2);
-      b0 = max(mid - 1, 0);
-      if (upto_bin(b1) - upto_bin(b0 - 1) > kCounted) b0 = mid;
-      if (upto_bin(b1) - upto_bin(b0 - 1) > kCounted) b1 = mid;
-    }
-    int least = 0, most = kBins - 2;  // the border's bin lies between
-    while (least <= most) {
-      if (upto_bin(b1) - upto_bin(b0 - 1) > kList) return false;
-      if (warp == 0) {
-        const float e = edge_of(b1, per);
-        if (lane == 0) sh.edge[0] = e;
-      } else if (warp == 1) {
-        const float e = b0 > 0 ? edge_of(b0 - 1, per) : INFINITY;
-        if (lane == 0) sh.edge[1] = e;
-      }
-      if (tid == 0 && rank != 0) sh.listed = 0;
-      __syncthreads();
-      const float low = sh.edge[0], high = sh.edge[1];
-      // the sums of all weights and of those above the window; the window listed
-      uint32_t hi = 0, lo = 0, num = 0, hi_up = 0, lo_up = 0;
-      each_vector([&](const uint4& w, int at) {
-        const float top = vector_max<kType>(w);
-#pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-          const float2 v = pair<kType>(w, e);
-          const Parts a = weights<kType>(below(v, r), r, sh.table);
-          hi += a.hi[0] + a.hi[1];
-          lo += a.lo[0] + a.lo[1];
-          if (v.x >= high) {
-            hi_up += a.hi[0] - kMagicBits;
-            lo_up += a.lo[0] - kMagicBits;
-          }
-          if (v.y >= high) {
-            hi_up += a.hi[1] - kMagicBits;
-            lo_up += a.lo[1] - kMagicBits;
-          }
-        }
-        num += kVec;
-        if (top >= low) {
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            const float y = element<kType>(w, e);
-            if (y >= low && y < high) append(place(key_of(y), at + e));
-          }
-        }
-      });
-      send_sum(whole(hi - num * kMagicBits, lo - num * kMagicBits), sh.all);
-      send_sum(whole(hi_up, lo_up), sh.kept);
-      send_list();
-      cluster.sync();
-      if (rank == 0) border(b0 == 0);
-      cluster.sync();
-      const int state = *at_first(&sh.state);
-      if (state == kDone) return true;
-      if (state == kMinP) {  // min-p's border is the higher one
-        cluster.sync();
-        sum_and_draw(min_place());
-        return true;
-      }
-      if (state == kHere) {
-        if (rank == 0) draw(sh.found[1]);
-        return true;
-      }
-      // the border lies in another bin: so far on by the masses between
-      if (state == kAbove) most = b0 - 1;
-      else least = b1 + 1;
-      b0 = step(state == kAbove ? most : least, state == kAbove ? -1 : 1, *at_first(&sh.found[0]),
-                per);
-      b0 = b1 = min(max(b0, least), most);
-      cluster.sync();  // (the state has been read, the list is empty again)
-    }
-    return false;
+    for (int i = 0; i < kMaxCluster; ++i)
+      if (i == q) before = g.count[i];
+    return before + *cluster.map_shared_rank(&sh.count[b], q);
   }
   // A bin's counted mass, of the largest weight.
   __device__ __forceinline__ static float mass_of(uint32_t n, int b, float per) {
     return static_cast<float>(n) * fast_exp2(-static_cast<float>(b) / per);
   }
-  // The bin, from `bin` on by `by`, where the counted masses reach `gap`. The counts up to each bin
-  // are in sh.count.
-  __device__ int step(int bin, int by, uint64_t gap, float per) const {
+  // The bin, from `bin` on by `by`, where the counted masses reach `gap`. (Every warp.)
+  __device__ __forceinline__ int step(const Bins& g, int bin, int by, uint64_t gap) const {
     const float want = static_cast<float>(gap) * 0x1p-42f;
     float sum = 0.f;
-    for (; bin >= 0 && bin < (kBins - 1); bin += 32 * by) {
+    for (; bin >= 0 && bin < kBins - 1; bin += 32 * by) {
       const int b = bin + by * lane;
       float m = 0.f;
-      if (b >= 0 && b < (kBins - 1)) m = mass_of(sh.count[b] - (b > 0 ? sh.count[b - 1] : 0), b, per);
+      if (b >= 0 && b < kBins - 1) m = mass_of(upto_bin(g, b) - upto_bin(g, b - 1), b, g.per);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float y = __shfl_up_sync(0xffffffffu, m, o);
@@ -1049,36 +926,265 @@ struct Sampler {
     }
     return bin;
   }
-  // What the first CTA found of a window: the row is done; the border is here (the cut in
-  // sh.found[1], the kept of the list added to sh.kept); min-p's is higher; it is above or below (by
-  // sh.found[0]).
-  static constexpr int kDone = 0, kHere = 1, kMinP = 2, kAbove = 3, kBelow = 4;
-  __device__ void border(bool whole_list) const {
+
+  __device__ __forceinline__ int by_border(uint64_t* cut) const {
+    // Counts by bin, of the logits that may be kept: without a k those under (1 - top_p) / V of the
+    // largest weigh less than 1 - top_p of it together, so the border lies above them.
+    const float past =
+        k > 0 ? kFarthest - 0.5f
+              : fminf(log2f(static_cast<float>(p.V)) - log2f(1.f - top_p) + 1.f, kFarthest - 0.5f);
+    Bins g;
+    g.per = (kBins - 2) / past;
+    g.width = kBins / ctas;
+    for (int i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
+    if (tid < 2) sh.digit[tid] = -1;
+    __syncthreads();
+    each_vector([&](const uint4& w, int) {
+#pragma unroll
+      for (int e = 0; e < kVec; e += 2) {
+        const Below b = below(pair<kType>(w, e), r);
+        if (b.y.x < past) atomicAdd(&sh.count[bin_of(b.y.x, g.per)], 1u);
+        if (b.y.y < past) atomicAdd(&sh.count[bin_of(b.y.y, g.per)], 1u);
+      }
+    });
+    cluster.sync();
+    // a slice of the bins each (a thread some neighbours), the counts of all CTAs
+    const int mine = g.width / kThreads, bin0 = rank * g.width + tid * mine;
+    uint32_t n[kPerThread], sum_n = 0;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      n[i] = 0;
+      if (i < mine) {
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+          if (q < ctas) n[i] += *cluster.map_shared_rank(&sh.count[bin0 + i], q);
+        sum += mass_of(n[i], bin0 + i, g.per);
+        sum_n += n[i];
+      }
+    }
+    // (sums of masses in units of 2^-40 of the largest weight: they take part in no decision)
+    const uint64_t own = __float2ull_rn(sum * 0x1p40f);
+    uint64_t upto = block_scan(own, sh.warp);
+    uint32_t upto_n = static_cast<uint32_t>(block_scan(sum_n, sh.warp));
+    if (tid == kThreads - 1) {
+      sh.total = upto;
+      sh.at = static_cast<int>(upto_n);
+    }
+    cluster.sync();  // (the counts have been read)
+    {
+      uint32_t c = upto_n - sum_n;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i)
+        if (i < mine) sh.count[bin0 + i] = c += n[i];
+    }
+    uint64_t mass = 0, before_mass = 0;
+    uint32_t all_n = 0, before_n = 0;
+#pragma unroll
+    for (int q = 0; q < kMaxCluster; ++q) {
+      g.count[q] = all_n;
+      if (q < ctas) {
+        if (q == rank) {
+          before_mass = mass;
+          before_n = all_n;
+        }
+        mass += *cluster.map_shared_rank(&sh.total, q);
+        all_n += *cluster.map_shared_rank(&sh.at, q);
+      }
+    }
+    upto += before_mass;
+    upto_n += before_n;
+    const bool by_count = k > 0 && static_cast<uint32_t>(k) < all_n;
+    if (by_count) {
+      // the k-th's bin
+      if (upto_n - sum_n < static_cast<uint32_t>(k) && upto_n >= static_cast<uint32_t>(k)) {
+        uint32_t c = upto_n - sum_n;
+        int i = 0;
+        for (; i < mine - 1; ++i)
+          if ((c += n[i]) >= static_cast<uint32_t>(k)) break;
+        at_first(sh.digit)[0] = bin0 + i;
+      }
+    } else if (top_p < 1.f) {
+      // The border by the counted masses, of their own sum, and with as much as the others may
+      // weigh: it lies between the two but for the bins' unevenness.
+      const uint64_t rest = static_cast<uint64_t>(
+          static_cast<float>(static_cast<uint32_t>(p.V) - all_n) * fast_exp2(40.f - past));
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const uint64_t with = share_of(mass + (f ? rest : 0));
+        const uint64_t want = with < mass ? with : mass;
+        if (upto - own < want && upto >= want) {
+          float part = static_cast<float>(want - (upto - own)) * 0x1p-40f;
+          int i = 0;
+          for (; i < mine - 1; ++i) {
+            part -= mass_of(n[i], bin0 + i, g.per);
+            if (part <= 0.f) break;
+          }
+          at_first(sh.digit)[f] = bin0 + i;
+        }
+      }
+    }
+    cluster.sync();
+    if (!by_count && !(top_p < 1.f)) {  // (what is behind the k-th weighs nothing)
+      *cut = min_place();
+      return kSum;
+    }
+    // By count: the k-th's bin. By mass, with the target known or the share of all weights (0):
+    // everything down to a bin past the border, or the bins around it; then where its sums say.
+    int kind = by_count ? kCount : kMass, mid = *at_first(&sh.digit[0]);
+    int far = by_count ? mid : *at_first(&sh.digit[1]), least = 0, most = kBins - 2, by = 0;
+    uint64_t target = 0, gap = 0;
+    while (least <= most) {  // the border's bin lies between
+      int b0, b1;
+      if (kind == kCount) {
+        b0 = b1 = mid;
+      } else if (by == 0) {
+        mid = min(max(mid, 0), kBins - 2);
+        far = min(max(mid, far), kBins - 2);
+        b0 = 0;
+        b1 = min(far + 1, kBins - 2);
+        if (upto_bin(g, b1) > kCounted) {
+          b1 = min(mid + 1, kBins - 2);
+          b0 = max(mid - 1, 0);
+          const uint32_t end = upto_bin(g, b1);
+          if (end - upto_bin(g, b0 - 1) > kCounted) b0 = mid;
+          if (end - upto_bin(g, b0 - 1) > kCounted) b1 = mid;
+        }
+      } else {
+        b0 = b1 = min(max(mid, least), most);
+      }
+      const int state = window(g, b0, b1, kind, target);
+      if (state == kFull) return kSearch;
+      if (state == kSettled) return kDone;
+      if (state == kMinP) {
+        *cut = min_place();
+        cluster.sync();  // (the state has been read)
+        return kSum;
+      }
+      if (state == kHere) {
+        *cut = sh.found[1];  // (the first CTA's)
+        return kDraw;
+      }
+      gap = *at_first(&sh.found[0]);
+      int from = 0;
+      if (state == kNext) {  // top-p of the first k: its border lies above theirs
+        kind = kMass;
+        target = gap;
+        by = 1;
+      } else {  // the border lies in another bin: so far on by the masses between
+        by = state == kAbove ? -1 : 1;
+        if (state == kAbove) most = from = b0 - 1;
+        else least = from = b1 + 1;
+      }
+      mid = far = step(g, from, by, gap);
+      if (state == kNext) by = 0;
+    }
+    return kSearch;
+  }
+  // The pass over the row for a window of bins: the sums of all weights and of those above the
+  // window; the window listed, and settled by the first CTA (see settle).
+  static constexpr int kSettled = 0, kHere = 1, kMinP = 2, kAbove = 3, kBelow = 4, kNext = 5,
+                       kFull = 6;
+  static constexpr int kMass = 0, kCount = 1;
+  __device__ __forceinline__ int window(const Bins& g, int b0, int b1, int kind, uint64_t target) const {
+    const uint32_t before = upto_bin(g, b0 - 1);
+    if (upto_bin(g, b1) - before > kList) return kFull;
+    if (warp == 0) {
+      const float e = edge_of(b1, g.per);
+      if (lane == 0) sh.edge[0] = e;
+    } else if (warp == 1) {
+      const float e = b0 > 0 ? edge_of(b0 - 1, g.per) : INFINITY;
+      if (lane == 0) sh.edge[1] = e;
+    }
+    if (tid == 0) sh.listed = 0;
+    cluster.sync();  // (and what the first CTA said of the last window has been read)
+    const float low = sh.edge[0], high = sh.edge[1];
+    uint32_t hi = 0, lo = 0, num = 0, hi_up = 0, lo_up = 0;
+    each_vector([&](const uint4& w, int at) {
+      const float top = vector_max<kType>(w);
+#pragma unroll
+      for (int e = 0; e < kVec; e += 2) {
+        const float2 v = pair<kType>(w, e);
+        const Parts a = weights<kType>(below(v, r), r, sh.table);
+        hi += a.hi[0] + a.hi[1];
+        lo += a.lo[0] + a.lo[1];
+        if (v.x >= high) {
+          hi_up += a.hi[0] - kMagicBits;
+          lo_up += a.lo[0] - kMagicBits;
+        }
+        if (v.y >= high) {
+          hi_up += a.hi[1] - kMagicBits;
+          lo_up += a.lo[1] - kMagicBits;
+        }
+      }
+      num += kVec;
+      if (top >= low) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const float y = element<kType>(w, e);
+          if (y >= low && y < high) append(place(key_of(y), at + e));
+        }
+      }
+    });
+    send_sum(whole(hi - num * kMagicBits, lo - num * kMagicBits), sh.all);
+    send_sum(whole(hi_up, lo_up), sh.kept);
+    send_list();
+    cluster.sync();
+    if (rank == 0) settle(kind, target, static_cast<uint32_t>(k) - before, b0 == 0);
+    cluster.sync();
+    return *at_first(&sh.state);
+  }
+  // What the first CTA finds of a window. By count: the list's first `need` places are kept; by
+  // mass: the border of the target. The row is done; the border is here (the cut in
+  // sh.found[1], the kept of the list added to sh.kept); min-p's is higher; it is above or below, by
+  // sh.found[0]; top-p of the kept is next, its target in sh.found[0].
+  __device__ __forceinline__ void settle(int kind, uint64_t target, uint32_t need, bool from_top) const {
     const int n = min(sh.listed, kList), sums = ctas * kWarps;
     const uint64_t all = block_sum(tid < sums ? sh.all[tid] : 0, sh.warp);
     const uint64_t above = block_sum(tid < sums ? sh.kept[tid] : 0, sh.warp);
-    uint64_t y = 0;
-    for (int i = tid; i < n; i += kThreads) y += weight_at(sh.list[i]);
-    const uint64_t upto = above + block_sum(y, sh.warp);
-    const uint64_t target = share_of(all);
-    int state = above >= target ? kAbove : upto < target ? kBelow : kHere;
-    if (state == kHere && whole_list) {
-      decide(n, all, true);
-      state = kDone;
-    } else if (state == kHere) {
-      if (n <= kCounted) border_few(n, above, target);
-      else if (n <= kShort) border_sorted<kShort / kThreads>(n, above, target);
-      else border_sorted<kList / kThreads>(n, above, target);
+    uint64_t found = 0;
+    int state = kHere;
+    if (kind == kCount) {
+      ordered(n, [&](uint64_t at, uint64_t w, uint32_t before_n, uint64_t before) {
+        if (before_n < need) add_kept(at, w);
+        if (before_n == need - 1) {
+          sh.found[1] = at;
+          sh.total = above + before + w;
+        }
+      });
       __syncthreads();
-      if (min_place() > sh.found[1]) state = kMinP;
+      if (top_p < 1.f) {
+        found = share_of(sh.total);
+        state = kNext;
+      }
+    } else {
+      uint64_t y = 0;
+      for (int i = tid; i < n; i += kThreads) y += weight_at(sh.list[i]);
+      const uint64_t upto = above + block_sum(y, sh.warp), goal = target ? target : share_of(all);
+      if (above >= goal) {
+        state = kAbove;
+        found = above - goal;
+      } else if (upto < goal) {
+        state = kBelow;
+        found = goal - upto;
+      } else if (from_top && k == 0) {
+        decide(n, all, true);
+        state = kSettled;
+      } else {
+        ordered(n, [&](uint64_t at, uint64_t w, uint32_t, uint64_t before) {
+          before += above;
+          if (before < goal) add_kept(at, w);
+          if (before < goal && before + w >= goal) sh.found[1] = at;
+        });
+        __syncthreads();
+      }
     }
+    if (state == kHere && min_place() > sh.found[1]) state = kMinP;
     __syncthreads();
     if (tid == 0) {
       sh.state = state;
-      if (state >= kAbove) sh.found[0] = state == kAbove ? above - target : target - upto;
-      sh.listed = 0;
+      sh.found[0] = found;
     }
-    __syncthreads();
   }
   // A kept place of the list counts to the warp that its logit lies in.
   __device__ __forceinline__ void add_kept(uint64_t at, uint64_t w) const {
@@ -1087,39 +1193,40 @@ struct Sampler {
     const int t = (token - s.first) / kTile / s.per_warp;
     atomicAdd(&sh.kept[q * kWarps + t], static_cast<unsigned long long>(w));
   }
-  __device__ __forceinline__ void border_few(int n, uint64_t above, uint64_t target) const {
-    weigh(n);
-    const int parts = parts_of(n), i = tid / parts, part = tid % parts;
-    const uint64_t own = i < n ? sh.list[i] : 0, w = i < n ? sh.list[kCounted + i] : 0;
-    const uint64_t before =
-        above + compare(n, i, part, parts, [&](uint64_t at) { return at > own; }).sum;
-    if (i < n && part == 0 && before < target) {
-      add_kept(own, w);
-      if (before + w >= target) sh.found[1] = own;
+  // Every place of the list, its weight, how many are before it and what they weigh, to one thread.
+  template <class F>
+  __device__ __forceinline__ void ordered(int n, F f) const {
+    if (n <= kCounted) {
+      weigh(n);
+      const int parts = parts_of(n), i = tid / parts, part = tid % parts;
+      const uint64_t own = i < n ? sh.list[i] : 0, w = i < n ? sh.list[kCounted + i] : 0;
+      const Counted c = compare(n, i, part, parts, [&](uint64_t at) { return at > own; });
+      if (i < n && part == 0) f(own, w, static_cast<uint32_t>(c.n), c.sum);
+    } else if (n <= kShort) {
+      ordered_sorted<kShort / kThreads>(n, f);
+    } else {
+      ordered_sorted<kList / kThreads>(n, f);
     }
   }
-  template <int kPer>
-  __device__ __forceinline__ void border_sorted(int n, uint64_t above, uint64_t target) const {
+  template <int kPer, class F>
+  __device__ __forceinline__ void ordered_sorted(int n, F f) const {
     uint64_t v[kPer];
     int size = 32;
     while (size < n) size <<= 1;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) v[j] = j * kThreads + tid < n ? sh.list[j * kThreads + tid] : 0;
     sort_falling<kPer>(v, size, sh.list);
-    uint64_t sum = above;
+    uint64_t sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (j * kThreads >= n) continue;  // (uniform)
       const bool in = j * kThreads + tid < n;
       const uint64_t w = in ? weight_at(v[j]) : 0, upto = sum + block_scan(w, sh.warp);
-      if (in && upto - w < target) {
-        add_kept(v[j], w);
-        if (upto >= target) sh.found[1] = v[j];
-      }
       __syncthreads();
-      if (tid == kThreads - 1) sh.total = upto;
+      if (tid == kThreads - 1) sh.found[0] = upto;
       __syncthreads();
-      sum = sh.total;
+      sum = sh.found[0];
+      if (in) f(v[j], w, static_cast<uint32_t>(j * kThreads + tid), upto - w);
     }
   }
 };
@@ -1234,21 +1341,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     __syncthreads();
   }
-  bool done = false;
+  int todo = S::kSearch;
+  uint64_t cut = 0;
   if (!far) {
-    if (s.k > 0 && s.k <= kMaxTopK) {
-      done = s.by_list(s.bound_of_k(maxima));
-    } else if (s.k == 0 && s.top_p < 1.f) {
-      done = p.V <= kCounted ? s.by_list(-FLT_MAX) : s.by_nucleus();
-    } else if (s.k == 0) {
-      s.sum_and_draw(s.min_place());
-      done = true;
+    const bool filtered = s.k > 0 || s.top_p < 1.f, tiny = p.V <= kCounted;
+    if (!filtered) {
+      todo = S::kSum;
+      cut = s.min_place();
+    } else if (tiny || (s.k > 0 && s.k <= kMaxTopK)) {
+      if (s.by_list(tiny ? -FLT_MAX : s.bound_of_k(maxima))) todo = S::kDone;
     }
+    if (todo == S::kSearch) todo = s.by_border(&cut);
   }
-  if (!done) {
+  if (todo == S::kSearch) {
     s.cluster.sync();
-    s.general();
+    const S other = s;  // (that its address is taken there must not cost the rest its registers)
+    cut = other.general();
+    todo = S::kSum;
   }
+  if (todo == S::kSum) s.sum_from(cut);
+  if (todo != S::kDone && s.rank == 0) s.draw(cut);
   if (s.rank == 0) s.cluster.sync();  // (waits for the threads that have not left)
 }
 
