@@ -45,12 +45,12 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kPerThread = kBins / kThreads;  // bins of a thread
-constexpr int kFine = 512;            // second digit of the maxima's keys
+constexpr int kFine = 128;            // second digit of the maxima's keys
 constexpr int kList = 2048;           // places that a row's list holds
 constexpr int kCounted = 256;         // places that are put in order by counting
 constexpr int kShort = 512;           // places that sort in a fraction of the time
 constexpr int kMaxTopK = 128;         // k up to which the parts' maxima bound it
-constexpr int kFineTopK = 32;         // k from which they do so by two digits
+constexpr int kFineTopK = 64;         // k from which they do so by two digits
 constexpr int kMaxCluster = 8;
 constexpr int kSums = kMaxCluster * kWarps;
 constexpr int kSmemLimit = 232448;    // of a CTA
@@ -152,6 +152,44 @@ __device__ __forceinline__ float vector_max(const uint4& v) {
     return fmax3(f.x, f.y, -INFINITY);
   }
 }
+
+// Whether some element of a vector is in [low, high): two at a time for 16-bit types, against the
+// bounds rounded up to the type (a value of it is no less than a bound if no less than that).
+template <int kType>
+struct Between {
+  float low, high;
+  uint32_t low2, high2;
+  __device__ __forceinline__ Between(float a, float b) : low(a), high(b) {
+    if constexpr (kType == 1) {
+      const __nv_bfloat162 l = __bfloat162bfloat162(__float2bfloat16_ru(a)),
+                           h = __bfloat162bfloat162(__float2bfloat16_ru(b));
+      low2 = *reinterpret_cast<const uint32_t*>(&l);
+      high2 = *reinterpret_cast<const uint32_t*>(&h);
+    } else if constexpr (kType == 0) {
+      const __half2 l = __half2half2(__float2half_ru(a)), h = __half2half2(__float2half_ru(b));
+      low2 = *reinterpret_cast<const uint32_t*>(&l);
+      high2 = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  __device__ __forceinline__ bool any(const uint4& v) const {
+    const uint32_t* w = &v.x;
+    uint32_t in = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kType == 2) {
+        const float y = __uint_as_float(w[i]);
+        in |= y >= low && y < high;
+      } else if constexpr (kType == 1) {
+        auto h = [](const uint32_t& x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+        in |= __hge2_mask(h(w[i]), h(low2)) & __hlt2_mask(h(w[i]), h(high2));
+      } else {
+        auto h = [](const uint32_t& x) { return *reinterpret_cast<const __half2*>(&x); };
+        in |= __hge2_mask(h(w[i]), h(low2)) & __hlt2_mask(h(w[i]), h(high2));
+      }
+    }
+    return in != 0;
+  }
+};
 
 struct Row {
   float max;      // the row's largest logit (times s)
@@ -802,18 +840,24 @@ struct Sampler {
   // ---- top-k by the maxima of parts of the row (two of each thread)
 
   // The digit, from `top` down, at which the counts of all CTAs reach `want`: in sh.digit[0], what
-  // is still wanted of it in sh.digit[1]; -1 if they do not. (A warp.)
+  // is still wanted of it in sh.digit[1]; -1 if they do not. (A warp, kEach digits a lane.)
+  template <int kEach>
   __device__ __forceinline__ void digit_of(const uint32_t* counts, int top, int want) const {
     int found = -1;
-    for (; top >= 0 && found < 0; top -= 32) {
-      const int bin = top - lane;
-      int n = 0;
-      if (bin >= 0) {
+    for (; top >= 0 && found < 0; top -= 32 * kEach) {
+      int n[kEach], sum = 0;
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q)
-          if (q < ctas) n += *cluster.map_shared_rank(&counts[bin], q);
+      for (int i = 0; i < kEach; ++i) {
+        const int bin = top - kEach * lane - i;
+        n[i] = 0;
+        if (bin >= 0) {
+#pragma unroll
+          for (int q = 0; q < kMaxCluster; ++q)
+            if (q < ctas) n[i] += *cluster.map_shared_rank(&counts[bin], q);
+        }
+        sum += n[i];
       }
-      int upto = n;
+      int upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -822,8 +866,16 @@ struct Sampler {
       const unsigned has = __ballot_sync(0xffffffffu, upto >= want);
       if (has) {
         const int l = __ffs(has) - 1;
-        found = top - l;
-        want -= __shfl_sync(0xffffffffu, upto - n, l);
+        int at = top - kEach * lane, left = want - (upto - sum);
+#pragma unroll
+        for (int i = 0; i < kEach - 1; ++i) {
+          if (left > n[i] && at == top - kEach * lane - i) {
+            left -= n[i];
+            --at;
+          }
+        }
+        found = __shfl_sync(0xffffffffu, at, l);
+        want = __shfl_sync(0xffffffffu, left, l);
       } else {
         want -= __shfl_sync(0xffffffffu, upto, 31);
       }
@@ -834,7 +886,7 @@ struct Sampler {
     }
   }
   __device__ __forceinline__ float bound_of_k(const float* maxima) const {
-    if (warp == 0) digit_of(sh.count, static_cast<int>(key_of(peak + 0.f) >> 21), k);
+    if (warp == 0) digit_of<1>(sh.count, static_cast<int>(key_of(peak + 0.f) >> 21), k);
     __syncthreads();
     const int d = sh.digit[0];
     uint32_t key = d > 0 ? static_cast<uint32_t>(d) << 21 : 0u;
@@ -843,12 +895,12 @@ struct Sampler {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t km = key_of(maxima[i]);
-        if (km >> 21 == static_cast<uint32_t>(d)) atomicAdd(&sh.fine[(km >> 12) & (kFine - 1)], 1u);
+        if (km >> 21 == static_cast<uint32_t>(d)) atomicAdd(&sh.fine[(km >> 14) & (kFine - 1)], 1u);
       }
       cluster.sync();
-      if (warp == 0) digit_of(sh.fine, kFine - 1, want);
+      if (warp == 0) digit_of<kFine / 32>(sh.fine, kFine - 1, want);
       __syncthreads();
-      key |= static_cast<uint32_t>(sh.digit[0]) << 12;  // (it is found: the first digit was)
+      key |= static_cast<uint32_t>(sh.digit[0]) << 14;  // (it is found: the first digit was)
     }
     return of_key(key > kLowestKey ? key : kLowestKey);
   }
@@ -942,9 +994,10 @@ struct Sampler {
     each_vector([&](const uint4& w, int) {
 #pragma unroll
       for (int e = 0; e < kVec; e += 2) {
-        const Below b = below(pair<kType>(w, e), r);
-        if (b.y.x < past) atomicAdd(&sh.count[bin_of(b.y.x, g.per)], 1u);
-        if (b.y.y < past) atomicAdd(&sh.count[bin_of(b.y.y, g.per)], 1u);
+        // (as below has it, where it counts)
+        const float2 y = fmul2(ffma2(pair<kType>(w, e), both(-1.f), both(r.max)), both(r.c));
+        if (y.x < past) atomicAdd(&sh.count[bin_of(y.x, g.per)], 1u);
+        if (y.y < past) atomicAdd(&sh.count[bin_of(y.y, g.per)], 1u);
       }
     });
     cluster.sync();
@@ -1099,9 +1152,9 @@ struct Sampler {
     if (tid == 0) sh.listed = 0;
     cluster.sync();  // (and what the first CTA said of the last window has been read)
     const float low = sh.edge[0], high = sh.edge[1];
+    const Between<kType> inside(low, high);
     uint32_t hi = 0, lo = 0, num = 0, hi_up = 0, lo_up = 0;
     each_vector([&](const uint4& w, int at) {
-      const float top = vector_max<kType>(w);
 #pragma unroll
       for (int e = 0; e < kVec; e += 2) {
         const float2 v = pair<kType>(w, e);
@@ -1118,7 +1171,7 @@ struct Sampler {
         }
       }
       num += kVec;
-      if (top >= low) {
+      if (inside.any(w)) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
           const float y = element<kType>(w, e);
