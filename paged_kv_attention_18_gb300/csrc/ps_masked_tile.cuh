@@ -108,7 +108,7 @@ static_assert(sizeof(TileBars) <= 512, "barrier block");
 // buffers on a plan it cannot use.
 template <class Params>
 __device__ __forceinline__ bool tile_item_ok(const WorkItem& w, const Params& p) {
-  if (Params::kSinks && (w.pad[3] < 0 || w.pad[4] > p.max_blocks)) return false;
+  if (Params::kSinks && (w.pad[3] < 0 || w.pad[4] < w.pad[3] || w.pad[4] > p.max_blocks)) return false;
   if (w.seq < 0 || w.seq >= p.B || w.kv < 0 || w.kv >= p.H_kv) return false;
   if (w.page_begin < 0 || w.page_end > p.max_blocks) return false;
   if (w.tok0 < 0 || w.row0 < 0 || w.nrows <= 0 || w.pad[0] < 0) return false;
@@ -116,29 +116,40 @@ __device__ __forceinline__ bool tile_item_ok(const WorkItem& w, const Params& p)
   return w.tok0 + last_row / p.G < p.T;
 }
 
-// The key tiles of an item: those of its run of pages, or of its two runs, the sinks' first,
-// each run's last tile filled up with zeros.
+// The key tiles of an item: its run of pages, or its two runs one behind the other, the sinks'
+// first, eight pages a tile (the last one's rest is filled with zeros). Columns are counted from
+// the window's first key, so those of the sinks' pages lie before it.
 template <class Params>
 struct ItemTiles {
-  int pb, pe;                 // the window's pages (all of them without sinks)
-  int sb = 0, sinks = 0, nt;  // the sinks' first page, their tiles; key tiles in all
+  int pb, pe, nt;      // the window's pages (all of them without sinks); key tiles
+  int sb = 0, sp = 0;  // the sinks' first page, their number
   __device__ __forceinline__ explicit ItemTiles(const WorkItem& w)
       : pb(w.page_begin), pe(w.page_end) {
-    nt = pe > pb ? (pe - pb + kPagesPerTile - 1) / kPagesPerTile : 0;
     if constexpr (Params::kSinks) {
       sb = w.pad[3];
-      sinks = w.pad[4] > sb ? (w.pad[4] - sb + kPagesPerTile - 1) / kPagesPerTile : 0;
-      nt += sinks;
+      sp = w.pad[4] - sb;
     }
+    const int n = sp + pe - pb;
+    nt = n > 0 ? (n + kPagesPerTile - 1) / kPagesPerTile : 0;
   }
-  __device__ __forceinline__ bool in_sinks(int j) const { return Params::kSinks && j < sinks; }
-  // first page of tile j, and one past the last page of its run
-  __device__ __forceinline__ int first(int j) const {
-    return in_sinks(j) ? sb + j * kPagesPerTile : pb + (j - sinks) * kPagesPerTile;
+  // key of tile j's first column, as if all of its pages were the window's
+  __device__ __forceinline__ int key0(int j) const {
+    return (pb - sp + j * kPagesPerTile) * kBlockSize;
   }
-  __device__ __forceinline__ int end(int j, const WorkItem& w) const {
-    return in_sinks(j) ? w.pad[4] : pe;
+  // columns of tile j that hold sinks' pages (0 or less: none), and the key of its first
+  __device__ __forceinline__ int sink_cols(int j) const {
+    return Params::kSinks ? (sp - j * kPagesPerTile) * kBlockSize : 0;
   }
+  __device__ __forceinline__ int sink_key0(int j) const {
+    return (sb + j * kPagesPerTile) * kBlockSize;
+  }
+  // columns, from the item's first, of sinks that the row at position `pos` sees
+  __device__ __forceinline__ int sunk(const Params& p, int pos) const {
+    if constexpr (Params::kSinks) return min(sp * kBlockSize, min(p.sinks, pos + 1) - sb * kBlockSize);
+    else return 0;
+  }
+  // page i of the item
+  __device__ __forceinline__ int page(int i) const { return i < sp ? sb + i : pb + i - sp; }
 };
 
 }  // namespace
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
       const ItemTiles<Params> tiles(w);
       const int nt = tiles.nt;
       if (nt == 0 || !tile_item_ok(w, p)) continue;
-      const int seq = w.seq, kv = w.kv;
+      const int seq = w.seq, kv = w.kv, pages = tiles.sp + tiles.pe - tiles.pb;
       // query tiles (K warp): whole tokens x the G heads of this KV head. Each tile has its
       // own buffer, refilled as soon as that tile's last S of the previous item has read
       // it. They are loaded after the item's first K tile, whose stage frees earlier.
@@ -421,11 +432,10 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
       bool ok = true;
       const int pp = lane / kHalves, h = lane % kHalves;
       for (int j = 0; j < nt; ++j) {
-        const int first = tiles.first(tile_at(j, nt)), pe = tiles.end(tile_at(j, nt), w);
-        if (first < bt_base || first - bt_base + kPagesPerTile > 32 ||
-            (Params::kSinks && j == tiles.sinks)) {
+        const int first = tile_at(j, nt) * kPagesPerTile;  // of the item's pages
+        if (first < bt_base || first - bt_base + kPagesPerTile > 32) {
           bt_base = kBias ? max(first + kPagesPerTile - 32, 0) : first;
-          bt_reg = bt_base + lane < pe ? __ldg(bt + bt_base + lane) : -1;
+          bt_reg = bt_base + lane < pages ? __ldg(bt + tiles.page(bt_base + lane)) : -1;
         }
         const uint32_t st = g % n_stages;
         uint64_t* empty = is_k ? &bars->k_empty[st] : &bars->v_empty[st];
@@ -437,7 +447,7 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         __syncwarp();
         if (lane < kPagesPerTile * kHalves) {
           int row;
-          if (first + pp >= pe) {
+          if (first + pp >= pages) {
             row = p.num_blocks * kBlockSize;  // past the pool: zero fill, no HBM read
           } else if (blk < 0 || blk >= p.num_blocks) {
             record_error(p.err, kDevBadBlockId);
@@ -598,25 +608,27 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         // rows are zeroed, four at a time (this code runs once or twice an item, so its size
         // counts: with loops unrolled, 6 chunks of documents took 31.1 us in place of 30.5, and
         // the 777 us with a bias above 788)
-        const int at = tile_at(j, nt);
-        const int kb = tiles.first(at) * kBlockSize;
-        const int ke = min(kb + kKeys, tiles.end(at, w) * kBlockSize);
-        int lo = w.pad[1], hi = w.pad[2];  // the keys that some row sees
-        if constexpr (Params::kSinks) {
-          if (tiles.in_sinks(at)) {
-            lo = 0;
-            hi = min(hi, p.sinks);
-          }
-        }
-        if (kb < lo || ke > hi || ke > own) {
+        const int at = tile_at(j, nt), kb = tiles.key0(at), ke = min(kb + kKeys, tiles.pe * kBlockSize);
+        const int sink_cols = tiles.sink_cols(at);
+        // (a tile's sinks, but for those of pages that hold sinks alone, end inside it)
+        bool part = kb < w.pad[1] || ke > w.pad[2] || ke > own;
+        if constexpr (Params::kSinks)
+          part = sink_cols > 0
+                     ? kb + max(sink_cols, 0) < w.pad[1] || ke > w.pad[2] ||
+                           tiles.sink_key0(at) + min(sink_cols, kKeys) > min(p.sinks, w.pad[2])
+                     : part;
+        if (part) {
           uint8_t* v = smem + L::kOffV + (gv % kVStages) * L::kK + (lane & 7) * 16;
 #pragma unroll 1
           for (int k = 0; k < kKeys; k += 32) {
             const int key = kb + k + lane;
-            uint32_t dead = __ballot_sync(
-                0xffffffffu, key < ke && (key < lo || key >= hi ||
-                                          (!Params::kSinks &&
-                                           p.key_unseen(key, own, hi, w.tok0 - pos0))));
+            bool unseen = key < ke && (key < w.pad[1] || key >= w.pad[2] ||
+                                       (!Params::kSinks &&
+                                        p.key_unseen(key, own, w.pad[2], w.tok0 - pos0)));
+            if constexpr (Params::kSinks)
+              if (k + lane < sink_cols)
+                unseen = tiles.sink_key0(at) + k + lane >= min(p.sinks, w.pad[2]);
+            uint32_t dead = __ballot_sync(0xffffffffu, unseen);
             while (dead != 0) {
               const int four = (__ffs(dead) - 1) & ~3, r = four + (lane >> 3);
               if (dead >> r & 1u) {
@@ -652,7 +664,7 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         if (idx < 0) break;
         const WorkItem& w = items[it % (2 * kItemRing)];
         const ItemTiles<Params> tiles(w);
-        [[maybe_unused]] const int pb = tiles.pb, pe = tiles.pe, nt = tiles.nt;
+        const int pe = tiles.pe, nt = tiles.nt;
         if (nt == 0 || !tile_item_ok(w, p)) continue;
         const int nrows = grp == 0 ? w.nrows : w.pad[0];
         if (nrows == 0) continue;  // no query tile B in this item
@@ -670,6 +682,9 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         int key_lo = 0;
         if constexpr (Params::kSinks) key_lo = valid ? p.window_lo(pos) : 0;
         else key_lo = valid ? p.row_lo(tok, pos) : 0;
+        // as columns of the item's tiles
+        const int lim0 = key_hi - tiles.key0(0), low0 = key_lo - tiles.key0(0);
+        const int sunk0 = Params::kSinks && valid ? tiles.sunk(p, pos) : 0;
         // the row's split count and partial base, fetched now so that the epilogue's
         // stores do not wait on them
         // (both loads are issued at once; nothing waits for them before the epilogue)
@@ -681,14 +696,9 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         for (int j = 0; j < nt; ++j) {
           // visible columns: c <= lim (a row past the tile's rows is computed unmasked and
           // not written)
-          const int tile0 = tiles.first(j) * kBlockSize;  // the tile's first key
-          int lim = valid ? key_hi - tile0 : kKeys, low = valid ? key_lo - tile0 : 0;
-          if constexpr (Params::kSinks) {
-            if (tiles.in_sinks(j) && valid) {
-              lim = min(min(pos, p.sinks - 1), w.pad[4] * kBlockSize - 1) - tile0;
-              low = 0;
-            }
-          }
+          // (streams: and those below `sunk`, of the sinks)
+          const int lim = valid ? lim0 - j * kKeys : kKeys, low = valid ? low0 - j * kKeys : 0;
+          [[maybe_unused]] const int sunk = sunk0 - j * kKeys;
           if (!wait(&bars->s_full[grp], sc & 1)) { ok = false; break; }
           ++sc;
           tc_fence_after();
@@ -714,7 +724,8 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
           }
           // P = 2^(s*scale*log2e - m_ref) as 16-bit pairs written over S; half h of P lands
           // on columns 32h..32h+31, which the loads of halves <= h have already read
-          const bool full = __all_sync(0xffffffffu, lim >= kKeys - 1 && low <= 0);
+          const bool full =
+              __all_sync(0xffffffffu, lim >= kKeys - 1 && low <= (Params::kSinks ? max(sunk, 0) : 0));
           // l holds the earlier tiles' sum; this tile's halves are summed apart, so that a
           // reference moved in half 1 can re-sum the half-0 P it re-rounds
           float l_half0 = 0.f, l_h = 0.f;
@@ -727,7 +738,9 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
             if (!full) {
 #pragma unroll
               for (int e = 0; e < 64; ++e)
-                if (64 * h + e > lim || 64 * h + e < low) v[e] = __float_as_uint(-INFINITY);
+                if ((64 * h + e > lim || 64 * h + e < low) &&
+                    !(Params::kSinks && 64 * h + e < sunk))
+                  v[e] = __float_as_uint(-INFINITY);
             }
             // P is taken against the row's reference without the half's max; the max (and a move
             // of the reference) is taken only when there is no reference yet, or when the half's
@@ -961,7 +974,7 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         if (idx < 0) break;
         const WorkItem& w = items[it % (2 * kItemRing)];
         const ItemTiles<Params> tiles(w);
-        [[maybe_unused]] const int pb = tiles.pb, pe = tiles.pe, nt = tiles.nt;
+        const int pe = tiles.pe, nt = tiles.nt;
         if (nt == 0 || !tile_item_ok(w, p)) continue;
         const int nrows = grp == 0 ? w.nrows : w.pad[0];
         if (nrows == 0) continue;  // no query tile B in this item
@@ -974,8 +987,7 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         const int pos = valid ? w.ctx_len - w.n_query + qtok : -1;
         // the row's keys within the item, [key_lo, key_hi], relative to the warp's columns (a
         // row past the tile's rows is computed unmasked and not written)
-        const int col0 = pb * kBlockSize + 64 * half;
-        // (streams: of the window's run, whose first tile is tile `tiles.sinks`)
+        const int col0 = tiles.key0(0) + 64 * half;
         const int key_hi =
             valid ? min(Params::kSinks ? pos : max(pos, w.pad[3] - 1), pe * kBlockSize - 1) - col0
                   : (1 << 30);
@@ -984,22 +996,17 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
           if constexpr (Params::kSinks) key_lo = p.window_lo(pos) - col0;
           else key_lo = p.row_lo(tok, pos) - col0;
         }
+        const int sunk0 = Params::kSinks && valid ? tiles.sunk(p, pos) - 64 * half : 0;
         const float slope = kBias && valid ? -kLog2e * __ldg(p.slopes + head) : 0.f;
         const float first_dist = static_cast<float>(pos - col0);  // of the item's first column
         // m_ref: the reference max (log2 units) that P, O and l are currently taken against;
         // m_next: the reference from the next tile on, when this one's P summed to over 2^8
         float m_ref = m_fixed, m_next = m_fixed, l = 0.f;
         for (int j = 0; j < nt; ++j) {
-          // the tile's first key, from the item's
-          const int t0 = (tile_at(j, nt) - (Params::kSinks ? tiles.sinks : 0)) * kKeys;
-          int lim = key_hi - t0, low = key_lo - t0;  // visible: low <= c <= lim
-          if constexpr (Params::kSinks) {
-            if (tiles.in_sinks(j) && valid) {
-              const int c0 = tiles.first(j) * kBlockSize + 64 * half;
-              lim = min(min(pos, p.sinks - 1), w.pad[4] * kBlockSize - 1) - c0;
-              low = -c0;
-            }
-          }
+          const int t0 = tile_at(j, nt) * kKeys;  // the tile's first key, from the item's
+          // visible: low <= c <= lim (streams: and those below `sunk`, of the sinks)
+          const int lim = key_hi - t0, low = key_lo - t0;
+          [[maybe_unused]] const int sunk = sunk0 - t0;
           if (!wait(&bars->s_full[grp], sc & 1)) { ok = false; break; }
           ++sc;
           tc_fence_after();
@@ -1023,7 +1030,8 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
             l *= alpha;
             m_ref = fmaxf(m_ref, m_next);
           }
-          const bool full = __all_sync(0xffffffffu, lim >= 63 && low <= 0);
+          const bool full =
+              __all_sync(0xffffffffu, lim >= 63 && low <= (Params::kSinks ? max(sunk, 0) : 0));
           // every column visible, and (with a bias) none past the row's own position
           const bool one_sign =
               full && (!kBias || __all_sync(0xffffffffu, !valid || first_dist - t0 >= 63.f));
@@ -1055,10 +1063,11 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
                     fmaf(slope, fabsf(d0 - static_cast<float>(e)), __uint_as_float(v[e])));
             }
             if (!full) {
-              const int hi = lim - 32 * h, lo = low - 32 * h;
+              const int hi = lim - 32 * h, lo = low - 32 * h, to = sunk - 32 * h;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (e > hi || e < lo) v[e] = __float_as_uint(-INFINITY);
+                if ((e > hi || e < lo) && !(Params::kSinks && e < to))
+                  v[e] = __float_as_uint(-INFINITY);
             }
           };
           // P of 32 columns against the reference, 16-bit pairs; the row sum adds the values the
@@ -1118,7 +1127,8 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
           uint32_t top = 0;  // exponent of the larger of the row's half sums
           // (a row without a reference asks for one only once it sees a key: lim and low are
           // those of the warp's half of the tile)
-          const bool sees = lim + 64 * half >= 0 && low + 64 * half <= kKeys - 1;
+          const bool sees = (lim + 64 * half >= 0 && low + 64 * half <= kKeys - 1) ||
+                            (Params::kSinks && sunk + 64 * half > 0);
           bool redo = !fixed && __any_sync(0xffffffffu, m_ref == -INFINITY && sees);
           if (fixed) {
             take(0);
