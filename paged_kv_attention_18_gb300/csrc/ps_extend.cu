@@ -28,38 +28,42 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;            // of the cluster (the portable size)
 constexpr int kPerCta = 4 * kThreads;  // tokens and sequences that ask for another CTA
 
+// Tokens and blocks, as sums that stop at a cap each (one more than there is room for): 32 bits
+// hold them whatever is asked for, and sums of sums are the same in any grouping.
 struct Two {
-  long long x, y;
+  unsigned x, y;
 };
+__device__ __forceinline__ Two add(Two a, Two b, Two cap) {
+  return Two{min(a.x + b.x, cap.x), min(a.y + b.y, cap.y)};
+}
 
-// Exclusive sums over the block, and the totals.
-__device__ Two block_exscan(Two v, Two* sh, Two& total) {
+// Sums over the threads before this one, and over all.
+__device__ __forceinline__ Two block_exscan(Two v, Two cap, Two* sh, Two& total) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  auto up = [&](Two s, int o) {
+    return Two{__shfl_up_sync(0xffffffffu, s.x, o), __shfl_up_sync(0xffffffffu, s.y, o)};
+  };
   Two s = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, s.x, o), b = __shfl_up_sync(0xffffffffu, s.y, o);
-    if (lane >= o) {
-      s.x += a;
-      s.y += b;
-    }
+    const Two y = up(s, o);
+    if (lane >= o) s = add(s, y, cap);
   }
+  Two before = up(s, 1);
+  if (lane == 0) before = Two{0, 0};
+  __syncthreads();
   if (lane == 31) sh[wid] = s;
   __syncthreads();
-  Two before{0, 0}, all{0, 0};
+  Two w = lane < kWarps ? sh[lane] : Two{0, 0};
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const Two t = sh[w];
-    if (w < wid) {
-      before.x += t.x;
-      before.y += t.y;
-    }
-    all.x += t.x;
-    all.y += t.y;
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const Two y = up(w, o);
+    if (lane >= o) w = add(w, y, cap);
   }
-  __syncthreads();
-  total = all;
-  return Two{before.x + s.x - v.x, before.y + s.y - v.y};
+  total = Two{__shfl_sync(0xffffffffu, w.x, kWarps - 1), __shfl_sync(0xffffffffu, w.y, kWarps - 1)};
+  const Two base{__shfl_sync(0xffffffffu, w.x, (wid + 31) & 31),
+                 __shfl_sync(0xffffffffu, w.y, (wid + 31) & 31)};
+  return wid > 0 ? add(base, before, cap) : before;
 }
 
 // The largest b in [0, n) with at[b] <= x (at rises, at[0] <= x).
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
   int* s_tok = s_len + p.B + 1;     // [B + 1] first packed token
   int* s_blk = s_tok + p.B + 1;     // [B + 1] first new block
   int* s_ret = s_blk + p.B + 1;     // [B + 1] first block given back
-  uint8_t* s_end = reinterpret_cast<uint8_t*>(s_ret + p.B + 1);  // [B] 1: ends; 2: left out
+  uint8_t* s_end = reinterpret_cast<uint8_t*>(s_ret + p.B + 1);  // [B] 1: ends; 2: bad; 4: goes without
   const int tid = threadIdx.x, warp = tid >> 5;
   pdl_wait();
 
@@ -125,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
     if (rank == 0 && tid == 0) record_error(p.err, kDevBadBlockId);
     count = 0;
   }
-  // what each sequence asks for; the blocks given back
+  // what each sequence asks for, and the blocks it gives back
   for (int b = tid; b < p.B; b += kThreads) {
     const int n = p.new_lens[b], L = p.seq_lens[b];
     const int64_t room = static_cast<int64_t>(p.max_blocks) * kBlockSize;
@@ -139,10 +143,13 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
     s_ret[b] = 0;
   }
   __syncthreads();
+  // (a thread's sequences are neighbours)
+  const int share = (p.B + kThreads - 1) / kThreads;
+  const int b_lo = min(tid * share, p.B), b_hi = min(b_lo + share, p.B);
   int gave = 0;
   {
     bool any = p.window > 0;
-    for (int b = tid; !any && b < p.B; b += kThreads) any = s_end[b] == 1;
+    for (int b = b_lo; !any && b < b_hi; ++b) any = s_end[b] == 1;
     if (__syncthreads_or(any)) {
       for (int b = warp; b < p.B; b += kWarps) {
         const int n =
@@ -150,43 +157,73 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
         if ((tid & 31) == 0) s_ret[b] = n;
       }
       __syncthreads();
-      long long run = 0;
-      for (int base = 0; base < p.B; base += kThreads) {
-        const int b = base + tid;
-        Two total;
-        const Two e = block_exscan(Two{b < p.B ? s_ret[b] : 0, 0}, sh, total);
-        if (b < p.B) s_ret[b] = static_cast<int>(run + e.x);
-        run += total.x;
+      const Two cap{0x7fffffffu, 0};  // (at most every entry of the tables once)
+      Two sum{0, 0}, total;
+      for (int b = b_lo; b < b_hi; ++b) sum.x += s_ret[b];
+      unsigned at = block_exscan(sum, cap, sh, total).x;
+      for (int b = b_lo; b < b_hi; ++b) {
+        const int n = s_ret[b];
+        s_ret[b] = static_cast<int>(at);
+        at += n;
       }
-      gave = static_cast<int>(run);  // (at most every entry of the tables once)
+      gave = static_cast<int>(total.x);
     }
   }
   if (gave > p.free_capacity - count) {  // more than the stack holds: blocks given back twice
     if (rank == 0 && tid == 0) record_error(p.err, kDevBadBlockId);
   }
   const int have = min(gave, p.free_capacity - count) + count;
-  // who is served: what is asked for up to and with it is there
-  long long run_tok = 0, run_blk = 0, at_tok = 0, at_blk = 0;
-  for (int base = 0; base < p.B; base += kThreads) {
-    const int b = base + tid;
-    const Two want{b < p.B ? s_tok[b] : 0, b < p.B ? s_blk[b] : 0};
-    Two total, given;
-    const Two e = block_exscan(want, sh, total);
-    const bool room = run_tok + e.x + want.x <= p.T;
-    const bool blocks = want.y == 0 || run_blk + e.y + want.y <= have;
-    const bool ok = room && blocks;
-    if (!ok && rank == 0) record_error(p.err, room ? kDevNoBlocks : kDevBadSequence);
-    const Two g = block_exscan(ok ? want : Two{0, 0}, sh, given);
-    if (b < p.B) {
-      s_tok[b] = static_cast<int>(at_tok + g.x);
-      s_blk[b] = static_cast<int>(at_blk + g.y);
+  // Who is served: what is asked for up to and with it is there. Blocks run out for every sequence
+  // behind the first that goes without, but for those that need none; so do tokens. So a served
+  // sequence's blocks lie behind those of all before it, and only its tokens' place wants a sum of
+  // its own, if some sequence goes without.
+  const Two cap{static_cast<unsigned>(p.T) + 1, static_cast<unsigned>(have) + 1};
+  int tokens, blocks;
+  {
+    Two sum{0, 0}, total;
+    for (int b = b_lo; b < b_hi; ++b)
+      sum = add(sum, Two{static_cast<unsigned>(s_tok[b]), static_cast<unsigned>(s_blk[b])}, cap);
+    Two at = block_exscan(sum, cap, sh, total);
+    unsigned last = 0, kept = 0;  // blocks up to the thread's last served one; tokens
+    bool all = true;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const Two want{static_cast<unsigned>(s_tok[b]), static_cast<unsigned>(s_blk[b])};
+      const Two end = add(at, want, cap);
+      const bool room = end.x < cap.x, there = want.y == 0 || end.y < cap.y;
+      const bool ok = (room && there) || (want.x == 0 && want.y == 0);
+      if (ok) {
+        if (want.y != 0) last = end.y;
+        kept += want.x;
+        s_tok[b] = static_cast<int>(at.x);
+      } else {
+        if (rank == 0) record_error(p.err, room ? kDevNoBlocks : kDevBadSequence);
+        all = false;
+        s_end[b] = 4;
+      }
+      s_blk[b] = static_cast<int>(at.y);
+      at = end;
     }
-    run_tok += total.x;
-    run_blk += total.y;
-    at_tok += given.x;
-    at_blk += given.y;
+    tokens = static_cast<int>(total.x);
+    blocks = static_cast<int>(total.y);
+    if (!__syncthreads_and(all)) {
+      // tokens of the served; blocks up to the last of them
+      Two sums;
+      unsigned to = block_exscan(Two{kept, 0}, cap, sh, sums).x;
+      tokens = static_cast<int>(sums.x);
+      __syncthreads();
+      last = __reduce_max_sync(0xffffffffu, last);
+      if ((tid & 31) == 0) sh[warp].x = last;
+      __syncthreads();
+      blocks = 0;
+      for (int w = 0; w < kWarps; ++w) blocks = max(blocks, static_cast<int>(sh[w].x));
+      for (int b = b_lo; b < b_hi; ++b) {
+        const int n = s_end[b] == 0 ? p.new_lens[b] : 0;
+        s_tok[b] = static_cast<int>(to);
+        to += n;
+        s_blk[b] = min(s_blk[b], blocks);
+      }
+    }
   }
-  const int tokens = static_cast<int>(at_tok), blocks = static_cast<int>(at_blk);
   if (tid == 0) {
     s_tok[p.B] = tokens;
     s_blk[p.B] = blocks;
@@ -215,37 +252,44 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
     p.out_lens[b] = s_end[b] == 1 ? 0 : s_len[b] + (s_tok[b + 1] - s_tok[b]);
   }
   if (me == 0) *p.out_count = have - blocks;
-  auto fresh = [&](int nth) {  // the nth new block, or -1
-    const int id = p.free_blocks[have - 1 - nth];
-    const bool ok = id >= 0 && id < p.num_blocks;
-    if (!ok) record_error(p.err, kDevBadBlockId);
-    return ok ? id : -1;
-  };
   for (int i = me; i < blocks; i += stride) {
     const int b = last_le(s_blk, p.B, i);
     const int page = pages_of(s_len[b]) + i - s_blk[b];
-    p.tables[static_cast<int64_t>(b) * p.max_blocks + page] = fresh(i);
+    const int id = p.free_blocks[have - 1 - i];
+    const bool ok = id >= 0 && id < p.num_blocks;
+    if (!ok) record_error(p.err, kDevBadBlockId);
+    p.tables[static_cast<int64_t>(b) * p.max_blocks + page] = ok ? id : -1;
   }
-  for (int t = me; t < p.T; t += stride) {
-    int slot = -1, pos = 0;
-    if (t < tokens) {
-      const int b = last_le(s_tok, p.B, t), L = s_len[b];
-      pos = L + t - s_tok[b];
-      const int page = pos / kBlockSize, had = pages_of(L);
-      int id;
-      if (page >= had) {
-        id = fresh(s_blk[b] + page - had);
-      } else {
-        id = p.tables[static_cast<int64_t>(b) * p.max_blocks + page];
-        if (id < 0 || id >= p.num_blocks) {
-          record_error(p.err, kDevBadBlockId);
-          id = -1;
-        }
+  // A thread's tokens lie a stride apart, a few at a time: it looks for the first one's sequence by
+  // bisection, and their blocks' loads are all on their way before the first is used.
+  constexpr int kAhead = 4;
+  for (int base = me; base < p.T; base += kAhead * stride) {
+    int pos[kAhead], slot[kAhead];
+    const int32_t* from[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = base + u * stride;
+      pos[u] = 0;
+      from[u] = nullptr;
+      if (t < tokens) {
+        const int b = last_le(s_tok, p.B, t), L = s_len[b];
+        pos[u] = L + t - s_tok[b];
+        const int page = pos[u] / kBlockSize, had = pages_of(L);
+        from[u] = page >= had ? p.free_blocks + have - 1 - (s_blk[b] + page - had)
+                              : p.tables + static_cast<int64_t>(b) * p.max_blocks + page;
       }
-      if (id >= 0) slot = id * kBlockSize + pos % kBlockSize;
     }
-    p.slots[t] = slot;
-    p.positions[t] = pos;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) slot[u] = from[u] != nullptr ? *from[u] : -1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = base + u * stride;
+      if (t >= p.T) break;
+      const bool ok = slot[u] >= 0 && slot[u] < p.num_blocks;
+      if (!ok && from[u] != nullptr) record_error(p.err, kDevBadBlockId);
+      p.slots[t] = ok ? slot[u] * kBlockSize + pos[u] % kBlockSize : -1;
+      p.positions[t] = pos[u];
+    }
   }
 }
 
