@@ -31,6 +31,7 @@
 #include <cooperative_groups.h>
 
 #include <cfloat>
+#include <utility>
 
 #include "ps_common.cuh"
 #include "ps_launch.h"
@@ -288,7 +289,7 @@ struct alignas(16) Shared {
   uint32_t fine[kFine];
   unsigned long long kept[kSums], all[kSums];  // (first CTA) every warp's sums
   unsigned long long warp[kWarps];
-  unsigned long long total, found[2];
+  unsigned long long total, found[2], fold[kWarps][3];
   float2 table[64];
   double fall;     // T ln(min_p)
   float max, edge[2];
@@ -648,33 +649,80 @@ struct Sampler {
     uint64_t before = sh.found[0];
     const Slice s = slice_of(q);
     const int a = min(w * s.per_warp, s.tiles), b = min(a + s.per_warp, s.tiles);
-    auto kept = [&](const uint4& v, int at, int e) -> uint64_t {
-      const float y = element<kType>(v, e);
-      return place(key_of(y), at + e) >= cut ? weight<kType>(y, r, sh.table) : 0;
-    };
-    for (int base = a; base < b; base += kWarps) {  // a tile a warp
-      const int t = base + warp, at = s.first + (t * 32 + lane) * kVec;
-      uint4 v = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
-      if (t < b) v = load(at, s);
-      uint64_t some = 0;
+    // elements e and e + 1 of a vector at token `at`
+    auto kept = [&](const uint4& v, int at, int e, uint64_t* we) {
+      const float2 y = make_float2(element<kType>(v, e), element<kType>(v, e + 1));
+      we[0] = place(key_of(y.x), at + e) >= cut;
+      we[1] = place(key_of(y.y), at + e + 1) >= cut;
+      const Parts g = weights<kType>(below(make_float2(y.x * r.s, y.y * r.s), r), r, sh.table);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) some += kept(v, at, e);
-      const uint64_t end = before + block_scan(some, sh.warp);
-      __syncthreads();
-      if (tid == kThreads - 1) sh.total = end;
-      __syncthreads();
-      if (goal >= end - some && goal < end) {
-        uint64_t y = end - some;
-        for (int e = 0; e < kVec; ++e) {
-          const uint64_t we = kept(v, at, e);
-          if (goal < y + we) {
-            finish(at + e, element<kType>(v, e), z);
-            break;
+      for (int i = 0; i < 2; ++i)
+        we[i] = we[i] ? whole(g.hi[i] - kMagicBits, g.lo[i] - kMagicBits) : 0;
+    };
+    // some neighbouring tiles a warp, all on their way before the first is weighed
+    constexpr int kAhead = 4;
+    for (int base = a; base < b; base += kWarps * kAhead) {  // (once, but for the longest rows)
+      const int each = min((b - base + kWarps - 1) / kWarps, kAhead);
+      const int t0 = base + warp * each, t1 = min(t0 + each, b);
+      uint4 v[kAhead];
+      uint64_t some[kAhead], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        v[i] = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+        if (t0 + i < t1) v[i] = load(s.first + ((t0 + i) * 32 + lane) * kVec, s);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        some[i] = 0;
+        if (t0 + i < t1) {
+#pragma unroll
+          for (int e = 0; e < kVec; e += 2) {
+            uint64_t we[2];
+            kept(v[i], s.first + ((t0 + i) * 32 + lane) * kVec, e, we);
+            some[i] += we[0] + we[1];
           }
-          y += we;
+        }
+        sum += some[i];
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      __syncthreads();
+      if (lane == 0) sh.warp[warp] = sum;
+      __syncthreads();
+      uint64_t at = before;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        at += i < warp ? sh.warp[i] : 0;
+        before += sh.warp[i];
+      }
+      if (goal >= at && goal < at + sum) {  // one warp
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          uint64_t upto = some[i];
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+          }
+          const uint64_t end = at + upto;
+          if (goal >= end - some[i] && goal < end) {  // one lane of one tile
+            const int token = s.first + ((t0 + i) * 32 + lane) * kVec;
+            uint64_t y = end - some[i];
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2) {
+              uint64_t we[2];
+              kept(v[i], token, e, we);
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                if (goal >= y && goal < y + we[f])
+                  finish(token + e + f, element<kType>(v[i], e + f), z);
+                y += we[f];
+              }
+            }
+          }
+          at += __shfl_sync(0xffffffffu, upto, 31);
         }
       }
-      before = sh.total;
       if (goal < before) break;  // (uniform)
     }
   }
@@ -914,7 +962,13 @@ struct Sampler {
       cluster.sync();  // (the count has been read)
       return false;
     }
-    if (rank == 0) decide(n, 0, false);
+    // the first CTA stays until the others have read the count (its wait ends for those that have
+    // left, too)
+    auto read = cluster.barrier_arrive();
+    if (rank == 0) {
+      decide(n, 0, false);
+      cluster.barrier_wait(std::move(read));
+    }
     return true;
   }
 
@@ -939,34 +993,21 @@ struct Sampler {
 
   // ---- top-p without a small k, or a large k
 
-  // The counts of all CTAs, merged: CTA q has bins q * width and on, in sh.count up to each of them
-  // within its slice.
-  struct Bins {
-    float per;                       // bins to a factor of two
-    int width;
-    uint32_t count[kMaxCluster];     // before slice q
-  };
-  __device__ __forceinline__ uint32_t upto_bin(const Bins& g, int b) const {
-    if (b < 0) return 0;
-    const int q = b / g.width;
-    uint32_t before = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxCluster; ++i)
-      if (i == q) before = g.count[i];
-    return before + *cluster.map_shared_rank(&sh.count[b], q);
-  }
   // A bin's counted mass, of the largest weight.
   __device__ __forceinline__ static float mass_of(uint32_t n, int b, float per) {
     return static_cast<float>(n) * fast_exp2(-static_cast<float>(b) / per);
   }
-  // The bin, from `bin` on by `by`, where the counted masses reach `gap`. (Every warp.)
-  __device__ __forceinline__ int step(const Bins& g, int bin, int by, uint64_t gap) const {
+  // The counts up to bin b, in the first CTA.
+  __device__ __forceinline__ uint32_t upto_bin(int b) const { return b < 0 ? 0u : sh.count[b]; }
+  // The bin, from `bin` on by `by`, where the counted masses reach `gap`. (Every warp of the first
+  // CTA.)
+  __device__ __forceinline__ int step(int bin, int by, uint64_t gap, float per) const {
     const float want = static_cast<float>(gap) * 0x1p-42f;
     float sum = 0.f;
     for (; bin >= 0 && bin < kBins - 1; bin += 32 * by) {
       const int b = bin + by * lane;
       float m = 0.f;
-      if (b >= 0 && b < kBins - 1) m = mass_of(upto_bin(g, b) - upto_bin(g, b - 1), b, g.per);
+      if (b >= 0 && b < kBins - 1) m = mass_of(upto_bin(b) - upto_bin(b - 1), b, per);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float y = __shfl_up_sync(0xffffffffu, m, o);
@@ -978,179 +1019,163 @@ struct Sampler {
     }
     return bin;
   }
+  // The first CTA's choice of a window, bins b0 .. b1, told to all: its bounds as logits.
+  __device__ __forceinline__ void choose(int b0, int b1, float per) const {
+    __syncthreads();
+    if (warp == 0) {
+      const float e = edge_of(b1, per);
+      if (lane < ctas) cluster.map_shared_rank(sh.edge, lane)[0] = e;
+    } else if (warp == 1) {
+      const float e = b0 > 0 ? edge_of(b0 - 1, per) : INFINITY;
+      if (lane < ctas) cluster.map_shared_rank(sh.edge, lane)[1] = e;
+    }
+  }
 
+  // What the first CTA says: the row is done; the draw is next; min-p's border is the one; another
+  // window; the row is for the digit search.
+  static constexpr int kSettled = 0, kHere = 1, kMinP = 2, kAgain = 3, kFull = 4;
+  static constexpr int kMass = 0, kCount = 1;
   __device__ __forceinline__ int by_border(uint64_t* cut) const {
     // Counts by bin, of the logits that may be kept: without a k those under (1 - top_p) / V of the
     // largest weigh less than 1 - top_p of it together, so the border lies above them.
     const float past =
         k > 0 ? kFarthest - 0.5f
               : fminf(log2f(static_cast<float>(p.V)) - log2f(1.f - top_p) + 1.f, kFarthest - 0.5f);
-    Bins g;
-    g.per = (kBins - 2) / past;
-    g.width = kBins / ctas;
+    const float per = (kBins - 2) / past;
     for (int i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
-    if (tid < 2) sh.digit[tid] = -1;
     __syncthreads();
     each_vector([&](const uint4& w, int) {
 #pragma unroll
       for (int e = 0; e < kVec; e += 2) {
         // (as below has it, where it counts)
         const float2 y = fmul2(ffma2(pair<kType>(w, e), both(-1.f), both(r.max)), both(r.c));
-        if (y.x < past) atomicAdd(&sh.count[bin_of(y.x, g.per)], 1u);
-        if (y.y < past) atomicAdd(&sh.count[bin_of(y.y, g.per)], 1u);
+        if (y.x < past) atomicAdd(&sh.count[bin_of(y.x, per)], 1u);
+        if (y.y < past) atomicAdd(&sh.count[bin_of(y.y, per)], 1u);
       }
     });
+    cluster.sync();  // (the first CTA's counts are all there)
+    if (rank != 0) {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) {
+        const uint32_t n = sh.count[i * kThreads + tid];
+        if (n != 0) atomicAdd(at_first(&sh.count[i * kThreads + tid]), n);
+      }
+    }
     cluster.sync();
-    // a slice of the bins each (a thread some neighbours), the counts of all CTAs
-    const int mine = g.width / kThreads, bin0 = rank * g.width + tid * mine;
-    uint32_t n[kPerThread], sum_n = 0;
-    float sum = 0.f;
+    // The first CTA looks for the border's window; the others do as it says. By count: the k-th's
+    // bin. By mass, with the target known or the share of all weights (0): everything down to a bin
+    // past the border, or the bins around it; then where its sums say.
+    int kind = kMass, least = 0, most = kBins - 2, b0 = 0, b1 = 0;
+    uint64_t target = 0;
+    auto around = [&](int from, int to) {
+      from = min(max(from, least), most);
+      to = min(max(to, from), most);
+      b0 = max(from - 1, least);
+      b1 = min(to + 1, most);
+      if (least == 0 && k == 0 && upto_bin(b1) <= kCounted) b0 = 0;
+      else if (upto_bin(b1) - upto_bin(b0 - 1) > kCounted / 2) {
+        b0 = from;
+        b1 = upto_bin(to) - upto_bin(from - 1) > kCounted ? (from + to) / 2 : to;
+        if (upto_bin(b1) - upto_bin(b0 - 1) > kCounted) b0 = b1;
+      }
+    };
+    int state = kAgain;
+    if (rank == 0) {
+      uint32_t n[kPerThread], sum_n = 0;
+      float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      n[i] = 0;
-      if (i < mine) {
-#pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q)
-          if (q < ctas) n[i] += *cluster.map_shared_rank(&sh.count[bin0 + i], q);
-        sum += mass_of(n[i], bin0 + i, g.per);
+      for (int i = 0; i < kPerThread; ++i) {
+        n[i] = sh.count[kPerThread * tid + i];
+        sum += mass_of(n[i], kPerThread * tid + i, per);
         sum_n += n[i];
       }
-    }
-    // (sums of masses in units of 2^-40 of the largest weight: they take part in no decision)
-    const uint64_t own = __float2ull_rn(sum * 0x1p40f);
-    uint64_t upto = block_scan(own, sh.warp);
-    uint32_t upto_n = static_cast<uint32_t>(block_scan(sum_n, sh.warp));
-    if (tid == kThreads - 1) {
-      sh.total = upto;
-      sh.at = static_cast<int>(upto_n);
-    }
-    cluster.sync();  // (the counts have been read)
-    {
+      // (masses in units of 2^-40 of the largest weight)
+      const uint64_t own = __float2ull_rn(sum * 0x1p40f);
+      const uint64_t upto = block_scan(own, sh.warp);
+      const uint32_t upto_n = static_cast<uint32_t>(block_scan(sum_n, sh.warp));
+      if (tid == kThreads - 1) {
+        sh.total = upto;
+        sh.at = static_cast<int>(upto_n);
+      }
+      if (tid < 2) sh.digit[tid] = 0;
+      __syncthreads();
+      const bool by_count = k > 0 && k < sh.at;
       uint32_t c = upto_n - sum_n;
-#pragma unroll
-      for (int i = 0; i < kPerThread; ++i)
-        if (i < mine) sh.count[bin0 + i] = c += n[i];
-    }
-    uint64_t mass = 0, before_mass = 0;
-    uint32_t all_n = 0, before_n = 0;
-#pragma unroll
-    for (int q = 0; q < kMaxCluster; ++q) {
-      g.count[q] = all_n;
-      if (q < ctas) {
-        if (q == rank) {
-          before_mass = mass;
-          before_n = all_n;
-        }
-        mass += *cluster.map_shared_rank(&sh.total, q);
-        all_n += *cluster.map_shared_rank(&sh.at, q);
-      }
-    }
-    upto += before_mass;
-    upto_n += before_n;
-    const bool by_count = k > 0 && static_cast<uint32_t>(k) < all_n;
-    if (by_count) {
-      // the k-th's bin
-      if (upto_n - sum_n < static_cast<uint32_t>(k) && upto_n >= static_cast<uint32_t>(k)) {
-        uint32_t c = upto_n - sum_n;
-        int i = 0;
-        for (; i < mine - 1; ++i)
-          if ((c += n[i]) >= static_cast<uint32_t>(k)) break;
-        at_first(sh.digit)[0] = bin0 + i;
-      }
-    } else if (top_p < 1.f) {
-      // The border by the counted masses, of their own sum, and with as much as the others may
-      // weigh: it lies between the two but for the bins' unevenness.
-      const uint64_t rest = static_cast<uint64_t>(
-          static_cast<float>(static_cast<uint32_t>(p.V) - all_n) * fast_exp2(40.f - past));
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const uint64_t with = share_of(mass + (f ? rest : 0));
-        const uint64_t want = with < mass ? with : mass;
-        if (upto - own < want && upto >= want) {
-          float part = static_cast<float>(want - (upto - own)) * 0x1p-40f;
+      if (by_count) {
+        kind = kCount;
+        if (c < static_cast<uint32_t>(k) && upto_n >= static_cast<uint32_t>(k)) {
           int i = 0;
-          for (; i < mine - 1; ++i) {
-            part -= mass_of(n[i], bin0 + i, g.per);
-            if (part <= 0.f) break;
-          }
-          at_first(sh.digit)[f] = bin0 + i;
+          for (uint32_t at = c; i < kPerThread - 1; ++i)
+            if ((at += n[i]) >= static_cast<uint32_t>(k)) break;
+          sh.digit[0] = kPerThread * tid + i;
         }
-      }
-    }
-    cluster.sync();
-    if (!by_count && !(top_p < 1.f)) {  // (what is behind the k-th weighs nothing)
-      *cut = min_place();
-      return kSum;
-    }
-    // By count: the k-th's bin. By mass, with the target known or the share of all weights (0):
-    // everything down to a bin past the border, or the bins around it; then where its sums say.
-    int kind = by_count ? kCount : kMass, mid = *at_first(&sh.digit[0]);
-    int far = by_count ? mid : *at_first(&sh.digit[1]), least = 0, most = kBins - 2, by = 0;
-    uint64_t target = 0, gap = 0;
-    while (least <= most) {  // the border's bin lies between
-      int b0, b1;
-      if (kind == kCount) {
-        b0 = b1 = mid;
-      } else if (by == 0) {
-        mid = min(max(mid, 0), kBins - 2);
-        far = min(max(mid, far), kBins - 2);
-        b0 = 0;
-        b1 = min(far + 1, kBins - 2);
-        if (upto_bin(g, b1) > kCounted) {
-          b1 = min(mid + 1, kBins - 2);
-          b0 = max(mid - 1, 0);
-          const uint32_t end = upto_bin(g, b1);
-          if (end - upto_bin(g, b0 - 1) > kCounted) b0 = mid;
-          if (end - upto_bin(g, b0 - 1) > kCounted) b1 = mid;
+      } else if (top_p < 1.f) {
+        // the share of the counted masses, and with as much as the others may weigh: the border
+        // lies between the two but for the bins' unevenness
+        const uint64_t rest = static_cast<uint64_t>(
+            static_cast<float>(p.V - sh.at) * fast_exp2(40.f - past));
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const uint64_t share = share_of(sh.total + (f ? rest : 0));
+          const uint64_t want = share < sh.total ? share : sh.total;
+          if (upto - own < want && upto >= want) {
+            float part = static_cast<float>(want - (upto - own)) * 0x1p-40f;
+            int i = 0;
+            for (; i < kPerThread - 1; ++i) {
+              part -= mass_of(n[i], kPerThread * tid + i, per);
+              if (part <= 0.f) break;
+            }
+            sh.digit[f] = kPerThread * tid + i;
+          }
         }
       } else {
-        b0 = b1 = min(max(mid, least), most);
+        state = kMinP;  // (what is behind the k-th weighs nothing)
       }
-      const int state = window(g, b0, b1, kind, target);
-      if (state == kFull) return kSearch;
-      if (state == kSettled) return kDone;
-      if (state == kMinP) {
-        *cut = min_place();
-        cluster.sync();  // (the state has been read)
-        return kSum;
-      }
-      if (state == kHere) {
-        *cut = sh.found[1];  // (the first CTA's)
-        return kDraw;
-      }
-      gap = *at_first(&sh.found[0]);
-      int from = 0;
-      if (state == kNext) {  // top-p of the first k: its border lies above theirs
-        kind = kMass;
-        target = gap;
-        by = 1;
-      } else {  // the border lies in another bin: so far on by the masses between
-        by = state == kAbove ? -1 : 1;
-        if (state == kAbove) most = from = b0 - 1;
-        else least = from = b1 + 1;
-      }
-      mid = far = step(g, from, by, gap);
-      if (state == kNext) by = 0;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) sh.count[kPerThread * tid + i] = c += n[i];
+      __syncthreads();
+      if (kind == kCount) b0 = b1 = sh.digit[0];
+      else around(sh.digit[0], sh.digit[1]);
     }
-    return kSearch;
+    while (true) {
+      if (rank == 0) {
+        const uint32_t in = upto_bin(b1) - upto_bin(b0 - 1);
+        if (state == kAgain && (least > most || in > kList)) state = kFull;
+        if (state == kAgain) choose(b0, b1, per);
+        if (tid < ctas) *cluster.map_shared_rank(&sh.state, tid) = state;
+      }
+      if (tid == 0) sh.listed = 0;
+      cluster.sync();
+      state = sh.state;
+      if (state != kAgain) break;
+      window();
+      if (rank == 0) {
+        uint64_t gap = 0;
+        const int found = settle(kind, target, static_cast<uint32_t>(k) - upto_bin(b0 - 1),
+                                 b0 == 0, &gap);
+        if (found <= kMinP) {
+          state = found;
+        } else if (found == kNext) {  // top-p of the first k: its border lies above theirs
+          kind = kMass;
+          target = gap;
+          const int mid = step(0, 1, gap, per);
+          around(mid, mid);
+        } else {  // the border lies in another bin: so far on by the masses between
+          if (found == kAbove) most = b0 - 1;
+          else least = b1 + 1;
+          const int mid = step(found == kAbove ? most : least, found == kAbove ? -1 : 1, gap, per);
+          b0 = b1 = min(max(mid, least), most);
+        }
+      }
+    }
+    if (state == kFull) return kSearch;
+    if (state == kSettled) return kDone;
+    *cut = state == kMinP ? min_place() : sh.found[1];  // (the latter the first CTA's)
+    return state == kMinP ? kSum : kDraw;
   }
-  // The pass over the row for a window of bins: the sums of all weights and of those above the
-  // window; the window listed, and settled by the first CTA (see settle).
-  static constexpr int kSettled = 0, kHere = 1, kMinP = 2, kAbove = 3, kBelow = 4, kNext = 5,
-                       kFull = 6;
-  static constexpr int kMass = 0, kCount = 1;
-  __device__ __forceinline__ int window(const Bins& g, int b0, int b1, int kind, uint64_t target) const {
-    const uint32_t before = upto_bin(g, b0 - 1);
-    if (upto_bin(g, b1) - before > kList) return kFull;
-    if (warp == 0) {
-      const float e = edge_of(b1, g.per);
-      if (lane == 0) sh.edge[0] = e;
-    } else if (warp == 1) {
-      const float e = b0 > 0 ? edge_of(b0 - 1, g.per) : INFINITY;
-      if (lane == 0) sh.edge[1] = e;
-    }
-    if (tid == 0) sh.listed = 0;
-    cluster.sync();  // (and what the first CTA said of the last window has been read)
+  // The pass over the row for a window: the sums of all weights and of those above it, the logits
+  // inside listed, all for the first CTA.
+  __device__ __forceinline__ void window() const {
     const float low = sh.edge[0], high = sh.edge[1];
     const Between<kType> inside(low, high);
     uint32_t hi = 0, lo = 0, num = 0, hi_up = 0, lo_up = 0;
@@ -1183,20 +1208,43 @@ struct Sampler {
     send_sum(whole(hi_up, lo_up), sh.kept);
     send_list();
     cluster.sync();
-    if (rank == 0) settle(kind, target, static_cast<uint32_t>(k) - before, b0 == 0);
-    cluster.sync();
-    return *at_first(&sh.state);
   }
   // What the first CTA finds of a window. By count: the list's first `need` places are kept; by
-  // mass: the border of the target. The row is done; the border is here (the cut in
-  // sh.found[1], the kept of the list added to sh.kept); min-p's is higher; it is above or below, by
-  // sh.found[0]; top-p of the kept is next, its target in sh.found[0].
-  __device__ __forceinline__ void settle(int kind, uint64_t target, uint32_t need, bool from_top) const {
+  // mass: the border of the target. The row is done; the border is here (the cut in sh.found[1], the
+  // kept of the list added to sh.kept); min-p's is higher; it is above or below, by *gap; top-p of
+  // the kept is next, its target in *gap.
+  static constexpr int kAbove = 5, kBelow = 6, kNext = 7;
+  __device__ __forceinline__ int settle(int kind, uint64_t target, uint32_t need, bool from_top,
+                                        uint64_t* gap) const {
     const int n = min(sh.listed, kList), sums = ctas * kWarps;
-    const uint64_t all = block_sum(tid < sums ? sh.all[tid] : 0, sh.warp);
-    const uint64_t above = block_sum(tid < sums ? sh.kept[tid] : 0, sh.warp);
-    uint64_t found = 0;
-    int state = kHere;
+    const bool few = n <= kCounted;
+    uint64_t w = 0, inside = 0;  // (few: one place a thread at most)
+    for (int i = tid; i < n; i += kThreads) {
+      w = weight_at(sh.list[i]);
+      inside += w;
+      if (few) sh.list[kCounted + i] = w;
+    }
+    uint64_t all = tid < sums ? sh.all[tid] : 0, above = tid < sums ? sh.kept[tid] : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      above += __shfl_xor_sync(0xffffffffu, above, o);
+      inside += __shfl_xor_sync(0xffffffffu, inside, o);
+    }
+    __syncthreads();
+    if (lane == 0) {
+      sh.fold[warp][0] = all;
+      sh.fold[warp][1] = above;
+      sh.fold[warp][2] = inside;
+    }
+    __syncthreads();
+    all = above = inside = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      all += sh.fold[i][0];
+      above += sh.fold[i][1];
+      inside += sh.fold[i][2];
+    }
     if (kind == kCount) {
       ordered(n, [&](uint64_t at, uint64_t w, uint32_t before_n, uint64_t before) {
         if (before_n < need) add_kept(at, w);
@@ -1207,37 +1255,31 @@ struct Sampler {
       });
       __syncthreads();
       if (top_p < 1.f) {
-        found = share_of(sh.total);
-        state = kNext;
+        *gap = share_of(sh.total);
+        return kNext;
       }
     } else {
-      uint64_t y = 0;
-      for (int i = tid; i < n; i += kThreads) y += weight_at(sh.list[i]);
-      const uint64_t upto = above + block_sum(y, sh.warp), goal = target ? target : share_of(all);
+      const uint64_t upto = above + inside, goal = target ? target : share_of(all);
       if (above >= goal) {
-        state = kAbove;
-        found = above - goal;
-      } else if (upto < goal) {
-        state = kBelow;
-        found = goal - upto;
-      } else if (from_top && k == 0) {
-        decide(n, all, true);
-        state = kSettled;
-      } else {
-        ordered(n, [&](uint64_t at, uint64_t w, uint32_t, uint64_t before) {
-          before += above;
-          if (before < goal) add_kept(at, w);
-          if (before < goal && before + w >= goal) sh.found[1] = at;
-        });
-        __syncthreads();
+        *gap = above - goal;
+        return kAbove;
       }
+      if (upto < goal) {
+        *gap = goal - upto;
+        return kBelow;
+      }
+      if (from_top && k == 0) {
+        decide(n, all, true);
+        return kSettled;
+      }
+      ordered(n, [&](uint64_t at, uint64_t w, uint32_t, uint64_t before) {
+        before += above;
+        if (before < goal) add_kept(at, w);
+        if (before < goal && before + w >= goal) sh.found[1] = at;
+      });
+      __syncthreads();
     }
-    if (state == kHere && min_place() > sh.found[1]) state = kMinP;
-    __syncthreads();
-    if (tid == 0) {
-      sh.state = state;
-      sh.found[0] = found;
-    }
+    return min_place() > sh.found[1] ? kMinP : kHere;
   }
   // A kept place of the list counts to the warp that its logit lies in.
   __device__ __forceinline__ void add_kept(uint64_t at, uint64_t w) const {
@@ -1247,10 +1289,10 @@ struct Sampler {
     atomicAdd(&sh.kept[q * kWarps + t], static_cast<unsigned long long>(w));
   }
   // Every place of the list, its weight, how many are before it and what they weigh, to one thread.
+  // (The first CTA; the weights of kCounted places or fewer behind them.)
   template <class F>
   __device__ __forceinline__ void ordered(int n, F f) const {
-    if (n <= kCounted) {
-      weigh(n);
+    if (n <= kCounted) {  // (weighed already)
       const int parts = parts_of(n), i = tid / parts, part = tid % parts;
       const uint64_t own = i < n ? sh.list[i] : 0, w = i < n ? sh.list[kCounted + i] : 0;
       const Counted c = compare(n, i, part, parts, [&](uint64_t at) { return at > own; });
@@ -1365,8 +1407,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   s.peak = -INFINITY;
   for (int q = 0; q < s.ctas; ++q) s.peak = fmaxf(s.peak, *s.cluster.map_shared_rank(&sh.max, q));
 
-  // ---- the row by what it asks for (the same in every thread of the cluster); the first CTA
-  // stays until the others, which may look at its shared memory, have left
+  // ---- the row by what it asks for (the same in every thread of the cluster). A CTA leaves when no
+  // other looks at its shared memory any more.
   if (!(fabsf(s.peak) < INFINITY)) {  // no token
     if (s.rank == 0 && s.tid == 0) {
       p.tokens[s.row] = -1;
@@ -1414,7 +1456,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   }
   if (todo == S::kSum) s.sum_from(cut);
   if (todo != S::kDone && s.rank == 0) s.draw(cut);
-  if (s.rank == 0) s.cluster.sync();  // (waits for the threads that have not left)
 }
 
 int smem_bytes(int slice, int size) {
