@@ -232,7 +232,8 @@ int ps_rotary_axes_reshape_and_cache(const void* q, int64_t q_stride, const void
  *     that end at or before L_b - window + 1 and begin at or behind `sinks`, from the last one
  *     down to the first whose entry is negative already.
  * Their entries become -1. Such a block must not be in another sequence's table (nor twice in
- * one): what sequences share (prefixes, forks) is for the caller to count and to give back.
+ * one): what sequences share (prefixes, forks) is for the caller to count and to give back. A
+ * caller that takes tokens back (drafts not accepted) passes a window larger by as many.
  *
  *   block_tables  int32 [B, max_blocks_per_seq], updated in place.
  *   seq_lens, new_lens  int32 [B]. (An empty place of a batch: length 0, 0 new tokens.)
@@ -243,7 +244,8 @@ int ps_rotary_axes_reshape_and_cache(const void* q, int64_t q_stride, const void
  *                 most T).
  *   slot_mapping, positions  int32 [T], written: each packed token's pool slot and position; -1
  *                 and 0 from query_start_loc[B] on.
- *   out_seq_lens  int32 [B], written: the lengths after the step; may be seq_lens.
+ *   out_seq_lens  int32 [B], written: the lengths after the step; may be seq_lens (not new_lens:
+ *                 PS_ERR_ARG).
  *   out_free_count int32 [1], written; may be free_count.
  * Entries of pages that a sequence holds already, and those past its new ones, are left as they
  * were. A sequence is left out of the step (no tokens, its length as it was) where
@@ -280,13 +282,14 @@ int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int
  * log probability 0. A logit of -inf or NaN is no token; a row without any, or with one of +inf,
  * gives token -1 and log probability -inf. Finite logits are served whatever their size. A NaN
  * in top_p or min_p is no filter.
- * Weights are off by 2^-29 of themselves at most, and those below 2^(log2(V) - 62) of the
- * largest (2^-58 if that is more) are rounded to multiples of that; their sums are exact. So a
- * draw or a border of top_p is decided as in exact arithmetic but for R or top_p within about
- * 2^-30 of a border between two tokens. min_p's border is exact but for fp64's rounding.
+ * Weights are off by 2^-29 of themselves at most, then rounded to multiples of 2^-42 of the
+ * largest; their sums are exact. So a draw or a border of top_p is decided as in exact arithmetic
+ * but for R or top_p within 2^-28 + V 2^-42 of a border between two tokens (usually thousands of
+ * times less: roundings go either way). min_p's border is exact but for fp64's rounding. The same
+ * row gives the same token in any batch.
  *
  *   logits        [B, V] of logits_dtype (PS_F16, PS_BF16 or PS_F32), rows row_stride ELEMENTS
- *                 apart (at least V), aligned to an element. Read once.
+ *                 apart (at least V), aligned to an element. Nothing outside the rows is read.
  *   temperature   float [B] or NULL (1).     top_k  int32 [B] or NULL.
  *   top_p, min_p  float [B] or NULL.         random_bits  uint32 [B].
  *   tokens        int32 [B], logprobs float [B], written.

@@ -812,7 +812,9 @@ int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int
       T > INT32_MAX - (1 << 20))
     return PS_ERR_UNSUPPORTED;
   if (!free_count || !out_free_count || !query_start_loc) return PS_ERR_ARG;
-  if (B > 0 && (!block_tables || !seq_lens || !new_lens || !out_seq_lens)) return PS_ERR_ARG;
+  if (B > 0 && (!block_tables || !seq_lens || !new_lens || !out_seq_lens ||
+                out_seq_lens == new_lens))
+    return PS_ERR_ARG;
   if (free_capacity > 0 && !free_blocks) return PS_ERR_ARG;
   if (T > 0 && (!slot_mapping || !positions)) return PS_ERR_ARG;
   DeviceState* ds;

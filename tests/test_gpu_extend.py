@@ -151,6 +151,23 @@ def test_bad_blocks():
     c.step([-1, 1], error=1)
 
 
+def test_everything_at_once():
+    """Sequences that end, grow under a window, are bad, go without and do not fit, together."""
+    g = torch.Generator().manual_seed(21)
+
+    def ints(lo, hi, n):
+        return torch.randint(lo, hi, (n,), generator=g).tolist()
+
+    for B in (7, 130, 900):
+        c = Cache(ints(0, 400, B), 30, B // 2 + 3, B)
+        for step in range(12):
+            news = ints(-1, 6, B)
+            for b in ints(0, B, 3):
+                news[b] = (-1, 100, 600)[b % 3]
+            T = max(sum(max(n, 0) for n in news) - (step % 4) * 5, 0)
+            c.step(news, T=T, window=(0, 33, 100)[step % 3], sinks=step % 20)
+
+
 def test_an_empty_batch():
     z = torch.zeros(0, dtype=torch.int32, device="cuda")
     qsl, slots, pos = i32([5]), i32([5, 5]), i32([5, 5])

@@ -148,6 +148,76 @@ def test_views(dt, V, pad, at):
     run(x, bits, top_k=i32(0, 40, 3, 0, 500), top_p=f32(0.9, 1.0, 0.8, 1.0, 0.95))
 
 
+def shapes_of_rows(B, V, dt, seed):
+    """Rows of very different distributions: flat, steep, in steps, one token, two levels a hair
+    apart, geometric, a heavy tail."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = torch.randn(B, V, generator=g, device="cuda")
+    i = torch.arange(V, device="cuda").float()
+    x[0::8] *= 1e-3
+    x[1::8] *= 12.0
+    x[2::8] = torch.floor(x[2::8] * 3.0)
+    x[3::8, 5] = 40.0
+    x[4::8] = (i % 2) * 0.004
+    x[5::8] = -i * 0.01
+    x[6::8] = -torch.log(i + 1.0) * 1.01
+    return x.to(dt)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("B,V", [(64, 20011), (16, 151936), (150, 2000)])
+def test_borders(dt, B, V):
+    """Shares, counts and temperatures all over their ranges: the border's bin is not always the one
+    that the counts point at."""
+    x, bits = shapes_of_rows(B, V, dt, B), words(B, V)
+    g = torch.Generator().manual_seed(B)
+    for _ in range(3):
+        p = torch.rand(B, generator=g)
+        p[::3] = 1.0 - 10.0 ** (-5.0 * p[::3])
+        k = (V * torch.rand(B, generator=g) ** 3).int() + 2
+        T = 0.05 + 3.0 * torch.rand(B, generator=g) ** 2
+        m = torch.rand(B, generator=g) ** 8
+        p, k, T, m = p.cuda(), k.cuda(), T.cuda(), m.cuda()
+        run(x, bits, top_p=p)
+        run(x, bits, top_p=p, temperature=T)
+        run(x, bits, top_k=k)
+        run(x, bits, top_k=k, top_p=p, temperature=T)
+        run(x, bits, top_p=p, min_p=m, temperature=T)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("k", [40, 63, 64, 65, 127, 128, 129, 200])
+def test_small_and_large_k(dt, k):
+    """Around the counts at which a list gives way to bins; rows masked by the least finite value to
+    fewer tokens than k."""
+    x = logits(12, 30000, dt, k)
+    x[1, 50:] = torch.finfo(dt).min
+    x[2, 100:] = -math.inf
+    x[3] = x[3].round()
+    x[4] = 1.0
+    ks = torch.full((12,), k, dtype=torch.int32, device="cuda")
+    bits = words(12, k)
+    run(x, bits, top_k=ks)
+    run(x, bits, top_k=ks, top_p=torch.full((12,), 0.7, device="cuda"))
+
+
+def test_calls_at_once():
+    """Calls that overlap on two streams share nothing."""
+    xs = [logits(40, 151936, torch.bfloat16, 30 + i) for i in range(2)]
+    bits, p = words(40, 31), torch.full((40,), 0.93, device="cuda")
+    want = [binding.sample(x, bits, top_p=p) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            got[i].append(binding.sample(xs[i], bits, top_p=p, stream=st))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for tok, lp in got[i]:
+            assert torch.equal(tok, want[i][0]) and torch.equal(lp, want[i][1])
+
+
 def test_large_vocabularies():
     for dt, V in ((torch.float32, 393216), (torch.bfloat16, 393211), (torch.float16, 262208)):
         x, bits = logits(3, V, dt, 11), words(3, 12)

@@ -32,9 +32,10 @@ def test_sample_refuses(lib):
 
 def test_extend_refuses(lib):
     f = caller(lib.ps_extend_sequences, (
-        ("bt", FAKE), ("mb", 8), ("sl", FAKE), ("nl", FAKE), ("free", FAKE), ("cap", 64),
+        ("bt", FAKE), ("mb", 8), ("sl", FAKE), ("nl", FAKE + 64), ("free", FAKE), ("cap", 64),
         ("count", FAKE), ("B", 2), ("T", 5), ("nb", 64), ("window", 0), ("sinks", 0),
         ("qsl", FAKE), ("slots", FAKE), ("pos", FAKE), ("ol", FAKE), ("oc", FAKE), ("s", None)))
+    assert f(ol=2 * FAKE, nl=2 * FAKE) == -1  # the numbers are read while lengths are written
     assert f(B=-1) == -1 and f(T=-1) == -1 and f(mb=0) == -1 and f(cap=-1) == -1
     assert f(nb=0) == -1 and f(nb=1 << 28) == -1 and f(window=-1) == -1 and f(sinks=-1) == -1
     assert f(B=8193) == -2 and f(B=8192, mb=1 << 18) == -2 and f(T=2 ** 31 - 1) == -2
