@@ -86,6 +86,29 @@ __constant__ float2 kExp2Table[64] = {
     {0.988494873046875f, -1.163938691e-06f}, {0.9912643432617188f, -7.049936812e-07f}, {0.9941024780273438f, 2.473934728e-06f},
     {0.9970169067382812f, 3.034099905e-07f},};
 
+// 1 / (1 + (2 j + 1) / 64), rounded, and minus its logarithm as two floats
+struct LogEntry {
+  float c, hi, lo;
+};
+__constant__ LogEntry kLogTable[32] = {
+    {9.846153855e-01f, 1.550418604e-02f, -4.370104834e-10f}, {9.552238584e-01f, 4.580955952e-02f, -2.097004514e-10f},
+    {9.275362492e-01f, 7.522340119e-02f, 1.422285845e-09f}, {9.014084339e-01f, 1.037968099e-01f, 2.396367327e-09f},
+    {8.767123222e-01f, 1.315763593e-01f, 5.967296879e-09f}, {8.533333540e-01f, 1.586050093e-01f, -3.355146161e-09f},
+    {8.311688304e-01f, 1.849223375e-01f, 1.893291079e-09f}, {8.101266026e-01f, 2.105647475e-01f, -3.491095413e-09f},
+    {7.901234627e-01f, 2.355660647e-01f, -8.531991225e-10f}, {7.710843086e-01f, 2.599575520e-01f, 9.733652995e-09f},
+    {7.529411912e-01f, 2.837681472e-01f, 6.342722347e-09f}, {7.356321812e-01f, 3.070250452e-01f, -6.136276820e-09f},
+    {7.191011310e-01f, 3.297532797e-01f, -3.558054518e-09f}, {7.032967210e-01f, 3.519763947e-01f, 3.358148648e-09f},
+    {6.881720424e-01f, 3.737164140e-01f, -3.249855274e-09f}, {6.736842394e-01f, 3.949937522e-01f, 1.315889708e-08f},
+    {6.597937942e-01f, 4.158279300e-01f, -4.096246009e-09f}, {6.464646459e-01f, 4.362367690e-01f, -1.254712112e-09f},
+    {6.336633563e-01f, 4.562374353e-01f, 1.397318972e-08f}, {6.213592291e-01f, 4.758459032e-01f, -7.601449248e-09f},
+    {6.095238328e-01f, 4.950772226e-01f, 6.027948363e-09f}, {5.981308222e-01f, 5.139457583e-01f, 2.442445890e-08f},
+    {5.871559381e-01f, 5.324648619e-01f, -2.015950074e-08f}, {5.765765905e-01f, 5.506470799e-01f, 1.379366488e-08f},
+    {5.663716793e-01f, 5.685047507e-01f, -1.165064845e-08f}, {5.565217137e-01f, 5.860490799e-01f, 1.074336620e-08f},
+    {5.470085740e-01f, 6.032907963e-01f, 5.798082015e-09f}, {5.378151536e-01f, 6.202403307e-01f, 2.783301056e-08f},
+    {5.289255977e-01f, 6.369075179e-01f, -1.376341796e-08f}, {5.203251839e-01f, 6.533012986e-01f, 1.064733279e-08f},
+    {5.120000243e-01f, 6.694306135e-01f, -7.072582076e-09f}, {5.039370060e-01f, 6.853039861e-01f, 2.075166883e-08f},
+};
+
 // A token's place in the order, larger first: its logit's bits made to ascend, then the index
 // made to descend.
 constexpr int kIdxBits = 20;
@@ -419,9 +442,19 @@ struct Sampler {
     memcpy(&w, part, 16);
     return w;
   }
+  // (the next vector is on its way while f has one)
   template <class F>
   __device__ __forceinline__ void each_vector(F f) const {
-    for (int t = t0; t < t1; ++t) f(data[t * 32 + lane], first + (t * 32 + lane) * kVec);
+    const uint4* v = data + t0 * 32 + lane;
+    uint4 next = make_uint4(0, 0, 0, 0);
+    if (t0 < t1) next = *v;
+    int at = first + (t0 * 32 + lane) * kVec;
+    for (int t = t0; t < t1; ++t, at += kTile) {
+      const uint4 w = next;
+      v += 32;
+      if (t + 1 < t1) next = *v;
+      f(w, at);
+    }
   }
   template <class F>
   __device__ __forceinline__ void each(F f) const {
@@ -442,15 +475,26 @@ struct Sampler {
   }
   // Every logit from `edge` on, listed in the CTA.
   __device__ __forceinline__ void list_from(float edge) const {
-    each_vector([&](const uint4& w, int at) {
-      if (vector_max<kType>(w) >= edge) {
+    constexpr int kAhead = 4;
+    for (int t = t0; t < t1; t += kAhead) {
+      float top[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        top[i] = t + i < t1 ? vector_max<kType>(data[(t + i) * 32 + lane]) : -INFINITY;
+      if (fmax3(fmaxf(top[0], top[1]), top[2], top[3]) < edge) continue;
+#pragma unroll 1
+      for (int i = 0; i < kAhead; ++i) {
+        if (t + i >= t1) break;
+        const uint4 w = data[(t + i) * 32 + lane];
+        if (vector_max<kType>(w) < edge) continue;
+        const int at = first + ((t + i) * 32 + lane) * kVec;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
           const float y = element<kType>(w, e);
           if (y >= edge) append(place(key_of(y), at + e));
         }
       }
-    });
+    }
   }
   // The CTA's list joined to the first CTA's. (The cluster meets behind it.)
   __device__ __forceinline__ void send_list() const {
@@ -464,10 +508,41 @@ struct Sampler {
       dst[sh.at + i] = sh.list[i];
   }
 
+  // The row's results: -(peak - x) / T - ln(z / 2^42), by pairs of floats (one thread's fp64 would
+  // cost a microsecond at the end of every row): within 2^-35, and rounded.
   __device__ __forceinline__ void finish(int token, float logit, uint64_t z) const {
     p.tokens[row] = token;
-    const double lw = greedy ? 0.0 : (static_cast<double>(logit) - peak) / T;
-    p.logprobs[row] = static_cast<float>(lw - log(static_cast<double>(z) * 0x1p-42));
+    if (r.s != 1.f) {  // (T beyond 2^100)
+      p.logprobs[row] = static_cast<float>((static_cast<double>(logit) - peak) / T -
+                                           log(static_cast<double>(z) * 0x1p-42));
+      return;
+    }
+    auto two = [](float a, float b, float* err) {  // their sum, and what it was rounded by
+      const float s = a + b, t = s - a;
+      *err += (a - (s - t)) + (b - t);
+      return s;
+    };
+    // (peak - x) / T: q and a remainder
+    float lo = 0.f, de = 0.f;
+    const float d = two(peak, -logit, &de), q = d / T;
+    lo += (fmaf(-q, T, d) + de) / T;
+    // ln z = e ln 2 - ln c + ln(m c), m in [1, 2) as 24 bits and the rest, c near 1 / m by table
+    const int e = 63 - __clzll(static_cast<long long>(z));
+    const uint64_t bits = z << (63 - e);
+    const float mh = static_cast<float>(static_cast<uint32_t>(bits >> 40)) * 0x1p-23f;
+    const float ml = static_cast<float>(static_cast<uint32_t>(bits >> 8)) * 0x1p-55f;
+    const LogEntry g = kLogTable[(bits >> 58) & 31];
+    const float pr = mh * g.c, pe = fmaf(mh, g.c, -pr) + ml * g.c;
+    const float rh = pr - 1.f, s = rh + pe;  // |s| under 1 / 64: five terms of the series
+    const float series = s * s * fmaf(s, fmaf(s, fmaf(s, 0.2f, -0.25f), 1.f / 3.f), -0.5f);
+    const float n = static_cast<float>(e - 42);
+    constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654299957767878e-09f;
+    const float a = n * kLn2Hi;
+    lo += fmaf(n, kLn2Hi, -a) + n * kLn2Lo + g.lo + pe + series;
+    float sum = two(a, g.hi, &lo);
+    sum = two(sum, rh, &lo);
+    sum = two(sum, q, &lo);
+    p.logprobs[row] = -(sum + lo);
   }
   __device__ __forceinline__ uint64_t point(uint64_t z) const {
     return __umul64hi(static_cast<uint64_t>(p.random[row]) << 32, z);
@@ -1383,9 +1458,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   float mx[2] = {-INFINITY, -INFINITY};
   if (b > a && !mbar_wait(&sh.arrived[s.warp], 0)) record_error(p.err, kDevWaitTimeout);
   __syncwarp();
-  for (int t = s.t0; t < s.t1; t += 2) {
-    mx[0] = fmaxf(mx[0], vector_max<kType>(s.data[t * 32 + s.lane]));
-    if (t + 1 < s.t1) mx[1] = fmaxf(mx[1], vector_max<kType>(s.data[(t + 1) * 32 + s.lane]));
+  for (int t = s.t0; t < s.t1; t += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t + i < s.t1) mx[i & 1] = fmaxf(mx[i & 1], vector_max<kType>(s.data[(t + i) * 32 + s.lane]));
   }
   const float maxima[2] = {mx[0] + 0.f, mx[1] + 0.f};
   if (s.k > 0) {
