@@ -282,11 +282,13 @@ int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int
  * log probability 0. A logit of -inf or NaN is no token; a row without any, or with one of +inf,
  * gives token -1 and log probability -inf. Finite logits are served whatever their size. A NaN
  * in top_p or min_p is no filter.
- * Weights are off by 2^-29 of themselves at most, then rounded to multiples of 2^-42 of the
- * largest; their sums are exact. So a draw or a border of top_p is decided as in exact arithmetic
- * but for R or top_p within 2^-28 + V 2^-42 of a border between two tokens (usually thousands of
- * times less: roundings go either way). min_p's border is exact but for fp64's rounding. The same
- * row gives the same token in any batch.
+ * Weights are off by 2^-29 of themselves at most (16-bit logits: and by 2^-24 (max x - x_v) / T
+ * where that difference has more than 24 bits, one of the two being 2^13 (fp16) or 2^16 (bf16)
+ * times smaller than the other), then rounded to multiples of 2^-42 of the largest; their sums
+ * are exact. So a draw or a border of top_p is decided as in exact arithmetic but for R or top_p
+ * within 2^-28 + V 2^-42 of a border between two tokens (usually thousands of times less:
+ * roundings go either way). min_p's border is exact but for fp64's rounding. The same row gives
+ * the same token in any batch.
  *
  *   logits        [B, V] of logits_dtype (PS_F16, PS_BF16 or PS_F32), rows row_stride ELEMENTS
  *                 apart (at least V), aligned to an element. Nothing outside the rows is read.
@@ -650,13 +652,13 @@ const char* ps_status_string(int status);
  * around the next n launches of each kernel kind (host memory only; events are created
  * here, not in the timed calls). ps_profile_end() waits for the recorded events and
  * stops recording. ps_profile_read(kind, &ms, &launches) then gives the summed device
- * time and the launch count of one kind: 0 slot mapping (and sequence extension), 1 KV scatter as its own launch
- * (ps_reshape_and_cache, or the step's scatter ahead of the tile kernel's direct mode),
+ * time and the launch count of one kind: 0 slot mapping (and sequence extension), 1 KV scatter as
+ * its own launch (ps_reshape_and_cache, or the step's scatter ahead of the tile kernel's direct
+ * mode),
  * 2 planner (carrying the step's KV scatter when there is one), 3 split attention (decode
  * and verify rows), 4 split combine, 5 tile attention (prefill rows, tcgen05), 6 block
- * copy (and sequence forks), 7 speculative acceptance (and beam selection and
- * sampling), 8 rotary KV scatter (any form). The masked and streaming attention's kernels count under
- * 2 to 5.
+ * copy (and sequence forks), 7 speculative acceptance (and beam selection and sampling),
+ * 8 rotary KV scatter (any form). The masked and streaming attention's kernels count under 2 to 5.
  */
 int ps_profile_begin(int max_launches_per_kind);
 int ps_profile_end(void);

@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
   int* s_tok = s_len + p.B + 1;     // [B + 1] first packed token
   int* s_blk = s_tok + p.B + 1;     // [B + 1] first new block
   int* s_ret = s_blk + p.B + 1;     // [B + 1] first block given back
-  uint8_t* s_end = reinterpret_cast<uint8_t*>(s_ret + p.B + 1);  // [B] 1: ends; 2: bad; 4: goes without
+  // [B] 1: the sequence ends; 2: it is bad; 4: it goes without
+  uint8_t* s_end = reinterpret_cast<uint8_t*>(s_ret + p.B + 1);
   const int tid = threadIdx.x, warp = tid >> 5;
   pdl_wait();
 

@@ -1,6 +1,6 @@
 // Masked paged attention, chunks of new tokens: the tcgen05 tile kernel with a mask that is
 // an interval of keys per row, scores capped by a tanh, and a bias that falls with the
-// distance (see ps_masked_split.cu for the formulas).
+// distance (see ps_masked_split.cuh for the formulas).
 //
 // One work item is a pair of query tiles A and B of one sequence and one KV head (up to 128
 // packed rows each) over one split of the context; both share each tile of 128 keys:
@@ -108,7 +108,8 @@ static_assert(sizeof(TileBars) <= 512, "barrier block");
 // buffers on a plan it cannot use.
 template <class Params>
 __device__ __forceinline__ bool tile_item_ok(const WorkItem& w, const Params& p) {
-  if (Params::kSinks && (w.pad[3] < 0 || w.pad[4] < w.pad[3] || w.pad[4] > p.max_blocks)) return false;
+  if (Params::kSinks && (w.pad[3] < 0 || w.pad[4] < w.pad[3] || w.pad[4] > p.max_blocks))
+    return false;
   if (w.seq < 0 || w.seq >= p.B || w.kv < 0 || w.kv >= p.H_kv) return false;
   if (w.page_begin < 0 || w.page_end > p.max_blocks) return false;
   if (w.tok0 < 0 || w.row0 < 0 || w.nrows <= 0 || w.pad[0] < 0) return false;
@@ -145,8 +146,10 @@ struct ItemTiles {
   }
   // columns, from the item's first, of sinks that the row at position `pos` sees
   __device__ __forceinline__ int sunk(const Params& p, int pos) const {
-    if constexpr (Params::kSinks) return min(sp * kBlockSize, min(p.sinks, pos + 1) - sb * kBlockSize);
-    else return 0;
+    if constexpr (Params::kSinks)
+      return min(sp * kBlockSize, min(p.sinks, pos + 1) - sb * kBlockSize);
+    else
+      return 0;
   }
   // page i of the item
   __device__ __forceinline__ int page(int i) const { return i < sp ? sb + i : pb + i - sp; }
@@ -608,7 +611,8 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
         // rows are zeroed, four at a time (this code runs once or twice an item, so its size
         // counts: with loops unrolled, 6 chunks of documents took 31.1 us in place of 30.5, and
         // the 777 us with a bias above 788)
-        const int at = tile_at(j, nt), kb = tiles.key0(at), ke = min(kb + kKeys, tiles.pe * kBlockSize);
+        const int at = tile_at(j, nt), kb = tiles.key0(at);
+        const int ke = min(kb + kKeys, tiles.pe * kBlockSize);
         const int sink_cols = tiles.sink_cols(at);
         // (a tile's sinks, but for those of pages that hold sinks alone, end inside it)
         bool part = kb < w.pad[1] || ke > w.pad[2] || ke > own;

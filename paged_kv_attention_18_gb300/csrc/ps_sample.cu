@@ -19,8 +19,8 @@
 //   - the largest logit alone: its first place;
 //   - a small top-k: the k-th largest of the maxima of parts of the row bounds the k-th logit from
 //     below; the few logits from the bound on are listed, and the list decides everything;
-//   - top-p without it: a first pass counts the logits by weight (80 bins or so a factor of two), each
-//     bin with its middle weight, to guess the border's bin; a second one sums all weights and
+//   - top-p without it: a first pass counts the logits by weight (80 bins or so a factor of two),
+//     each bin with its middle weight, to guess the border's bin; a second one sums all weights and
 //     those above that bin exactly, and lists the logits around it. The list, in order, has the
 //     border if the sums say so; else a next bin is tried. A nucleus that fits the list is listed
 //     whole. A large top-k the same way, its bin by the counts, top-p of it by another pass;
@@ -54,6 +54,7 @@ constexpr int kMaxTopK = 128;         // k up to which the parts' maxima bound i
 constexpr int kFineTopK = 64;         // k from which they do so by two digits
 constexpr int kMaxCluster = 8;
 constexpr int kSums = kMaxCluster * kWarps;
+constexpr int kMinWords = 4;          // of a thread's share of a slice, where CTAs are to spare
 constexpr int kSmemLimit = 232448;    // of a CTA
 constexpr int kSmemTwo = 113 * 1024;  // of each of two on an SM
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, a float's low bits are its integer
@@ -63,50 +64,77 @@ constexpr float kFarthest = 62.f;     // y from which a weight counts as this on
 
 // 2^(j / 64) / (1 + j / 64) as two floats, the first of 17 bits
 __constant__ float2 kExp2Table[64] = {
-    {1.0f, 0.000000000e+00f}, {0.9953384399414062f, -1.296752089e-06f}, {0.9909286499023438f, 1.918489488e-06f},
-    {0.9867706298828125f, -5.961908869e-07f}, {0.98284912109375f, -3.208220960e-06f}, {0.9791488647460938f, 2.861970358e-07f},
-    {0.9756698608398438f, 1.362636112e-06f}, {0.9724044799804688f, -3.805937752e-07f}, {0.9693374633789062f, 2.743434607e-06f},
-    {0.9664688110351562f, 3.590768983e-06f}, {0.9637908935546875f, 3.045987796e-06f}, {0.9612960815429688f, 2.366336048e-06f},
-    {0.9589767456054688f, 3.157347464e-06f}, {0.9568328857421875f, -2.790280291e-07f}, {0.9548492431640625f, 1.923012405e-06f},
-    {0.953033447265625f, -2.973017217e-06f}, {0.9513626098632812f, 3.082138846e-06f}, {0.9498519897460938f, 2.425128400e-07f},
-    {0.948486328125f, -5.837500225e-07f}, {0.947265625f, -3.524869499e-06f}, {0.9461746215820312f, 2.759045401e-06f},
-    {0.9452285766601562f, -7.125474326e-07f}, {0.9444122314453125f, -2.216791017e-06f}, {0.9437179565429688f, 2.515055257e-06f},
-    {0.9431533813476562f, 2.658398444e-06f}, {0.9427108764648438f, 2.803732741e-06f}, {0.9423904418945312f, 5.990795415e-08f},
-    {0.9421844482421875f, -6.950618285e-07f}, {0.9420928955078125f, -2.080247441e-06f}, {0.942108154296875f, 1.040008215e-06f},
-    {0.9422378540039062f, -1.338624315e-06f}, {0.9424667358398438f, 3.780396582e-06f}, {0.94281005859375f, -1.017011641e-06f},
-    {0.9432525634765625f, -2.525774562e-06f}, {0.9437942504882812f, -2.703074642e-06f}, {0.9444351196289062f, -3.414299954e-06f},
-    {0.9451675415039062f, 1.191897354e-06f}, {0.9459991455078125f, 1.791231171e-06f}, {0.946929931640625f, -3.231974233e-06f},
-    {0.9479446411132812f, -1.590972545e-07f}, {0.9490509033203125f, 1.912315383e-06f}, {0.9502487182617188f, 1.582835580e-06f},
-    {0.9515380859375f, -2.481344154e-06f}, {0.9529037475585938f, 3.707449878e-06f}, {0.9543609619140625f, 3.679240990e-06f},
-    {0.9559097290039062f, -3.719839924e-06f}, {0.9575271606445312f, 3.299372338e-06f}, {0.9592361450195312f, 8.021958706e-07f},
-    {0.9610214233398438f, 3.051235808e-06f}, {0.962890625f, 1.469141466e-06f}, {0.9648361206054688f, 2.783603577e-06f},
-    {0.9668655395507812f, -1.492094157e-06f}, {0.968963623046875f, 3.086124707e-06f}, {0.9711456298828125f, 4.856872238e-07f},
-    {0.9734039306640625f, -2.398458946e-06f}, {0.9757308959960938f, 1.366457923e-06f}, {0.9781341552734375f, 3.490811650e-06f},
-    {0.9806137084960938f, 3.349399321e-06f}, {0.9831695556640625f, 3.507544477e-07f}, {0.9857940673828125f, 1.565312800e-06f},
-    {0.988494873046875f, -1.163938691e-06f}, {0.9912643432617188f, -7.049936812e-07f}, {0.9941024780273438f, 2.473934728e-06f},
-    {0.9970169067382812f, 3.034099905e-07f},};
+    {1.0f, 0.000000000e+00f}, {0.9953384399414062f, -1.296752089e-06f},
+    {0.9909286499023438f, 1.918489488e-06f}, {0.9867706298828125f, -5.961908869e-07f},
+    {0.98284912109375f, -3.208220960e-06f}, {0.9791488647460938f, 2.861970358e-07f},
+    {0.9756698608398438f, 1.362636112e-06f}, {0.9724044799804688f, -3.805937752e-07f},
+    {0.9693374633789062f, 2.743434607e-06f}, {0.9664688110351562f, 3.590768983e-06f},
+    {0.9637908935546875f, 3.045987796e-06f}, {0.9612960815429688f, 2.366336048e-06f},
+    {0.9589767456054688f, 3.157347464e-06f}, {0.9568328857421875f, -2.790280291e-07f},
+    {0.9548492431640625f, 1.923012405e-06f}, {0.953033447265625f, -2.973017217e-06f},
+    {0.9513626098632812f, 3.082138846e-06f}, {0.9498519897460938f, 2.425128400e-07f},
+    {0.948486328125f, -5.837500225e-07f}, {0.947265625f, -3.524869499e-06f},
+    {0.9461746215820312f, 2.759045401e-06f}, {0.9452285766601562f, -7.125474326e-07f},
+    {0.9444122314453125f, -2.216791017e-06f}, {0.9437179565429688f, 2.515055257e-06f},
+    {0.9431533813476562f, 2.658398444e-06f}, {0.9427108764648438f, 2.803732741e-06f},
+    {0.9423904418945312f, 5.990795415e-08f}, {0.9421844482421875f, -6.950618285e-07f},
+    {0.9420928955078125f, -2.080247441e-06f}, {0.942108154296875f, 1.040008215e-06f},
+    {0.9422378540039062f, -1.338624315e-06f}, {0.9424667358398438f, 3.780396582e-06f},
+    {0.94281005859375f, -1.017011641e-06f}, {0.9432525634765625f, -2.525774562e-06f},
+    {0.9437942504882812f, -2.703074642e-06f}, {0.9444351196289062f, -3.414299954e-06f},
+    {0.9451675415039062f, 1.191897354e-06f}, {0.9459991455078125f, 1.791231171e-06f},
+    {0.946929931640625f, -3.231974233e-06f}, {0.9479446411132812f, -1.590972545e-07f},
+    {0.9490509033203125f, 1.912315383e-06f}, {0.9502487182617188f, 1.582835580e-06f},
+    {0.9515380859375f, -2.481344154e-06f}, {0.9529037475585938f, 3.707449878e-06f},
+    {0.9543609619140625f, 3.679240990e-06f}, {0.9559097290039062f, -3.719839924e-06f},
+    {0.9575271606445312f, 3.299372338e-06f}, {0.9592361450195312f, 8.021958706e-07f},
+    {0.9610214233398438f, 3.051235808e-06f}, {0.962890625f, 1.469141466e-06f},
+    {0.9648361206054688f, 2.783603577e-06f}, {0.9668655395507812f, -1.492094157e-06f},
+    {0.968963623046875f, 3.086124707e-06f}, {0.9711456298828125f, 4.856872238e-07f},
+    {0.9734039306640625f, -2.398458946e-06f}, {0.9757308959960938f, 1.366457923e-06f},
+    {0.9781341552734375f, 3.490811650e-06f}, {0.9806137084960938f, 3.349399321e-06f},
+    {0.9831695556640625f, 3.507544477e-07f}, {0.9857940673828125f, 1.565312800e-06f},
+    {0.988494873046875f, -1.163938691e-06f}, {0.9912643432617188f, -7.049936812e-07f},
+    {0.9941024780273438f, 2.473934728e-06f}, {0.9970169067382812f, 3.034099905e-07f},
+};
 
 // 1 / (1 + (2 j + 1) / 64), rounded, and minus its logarithm as two floats
 struct LogEntry {
   float c, hi, lo;
 };
 __constant__ LogEntry kLogTable[32] = {
-    {9.846153855e-01f, 1.550418604e-02f, -4.370104834e-10f}, {9.552238584e-01f, 4.580955952e-02f, -2.097004514e-10f},
-    {9.275362492e-01f, 7.522340119e-02f, 1.422285845e-09f}, {9.014084339e-01f, 1.037968099e-01f, 2.396367327e-09f},
-    {8.767123222e-01f, 1.315763593e-01f, 5.967296879e-09f}, {8.533333540e-01f, 1.586050093e-01f, -3.355146161e-09f},
-    {8.311688304e-01f, 1.849223375e-01f, 1.893291079e-09f}, {8.101266026e-01f, 2.105647475e-01f, -3.491095413e-09f},
-    {7.901234627e-01f, 2.355660647e-01f, -8.531991225e-10f}, {7.710843086e-01f, 2.599575520e-01f, 9.733652995e-09f},
-    {7.529411912e-01f, 2.837681472e-01f, 6.342722347e-09f}, {7.356321812e-01f, 3.070250452e-01f, -6.136276820e-09f},
-    {7.191011310e-01f, 3.297532797e-01f, -3.558054518e-09f}, {7.032967210e-01f, 3.519763947e-01f, 3.358148648e-09f},
-    {6.881720424e-01f, 3.737164140e-01f, -3.249855274e-09f}, {6.736842394e-01f, 3.949937522e-01f, 1.315889708e-08f},
-    {6.597937942e-01f, 4.158279300e-01f, -4.096246009e-09f}, {6.464646459e-01f, 4.362367690e-01f, -1.254712112e-09f},
-    {6.336633563e-01f, 4.562374353e-01f, 1.397318972e-08f}, {6.213592291e-01f, 4.758459032e-01f, -7.601449248e-09f},
-    {6.095238328e-01f, 4.950772226e-01f, 6.027948363e-09f}, {5.981308222e-01f, 5.139457583e-01f, 2.442445890e-08f},
-    {5.871559381e-01f, 5.324648619e-01f, -2.015950074e-08f}, {5.765765905e-01f, 5.506470799e-01f, 1.379366488e-08f},
-    {5.663716793e-01f, 5.685047507e-01f, -1.165064845e-08f}, {5.565217137e-01f, 5.860490799e-01f, 1.074336620e-08f},
-    {5.470085740e-01f, 6.032907963e-01f, 5.798082015e-09f}, {5.378151536e-01f, 6.202403307e-01f, 2.783301056e-08f},
-    {5.289255977e-01f, 6.369075179e-01f, -1.376341796e-08f}, {5.203251839e-01f, 6.533012986e-01f, 1.064733279e-08f},
-    {5.120000243e-01f, 6.694306135e-01f, -7.072582076e-09f}, {5.039370060e-01f, 6.853039861e-01f, 2.075166883e-08f},
+    {9.846153855e-01f, 1.550418604e-02f, -4.370104834e-10f},
+    {9.552238584e-01f, 4.580955952e-02f, -2.097004514e-10f},
+    {9.275362492e-01f, 7.522340119e-02f, 1.422285845e-09f},
+    {9.014084339e-01f, 1.037968099e-01f, 2.396367327e-09f},
+    {8.767123222e-01f, 1.315763593e-01f, 5.967296879e-09f},
+    {8.533333540e-01f, 1.586050093e-01f, -3.355146161e-09f},
+    {8.311688304e-01f, 1.849223375e-01f, 1.893291079e-09f},
+    {8.101266026e-01f, 2.105647475e-01f, -3.491095413e-09f},
+    {7.901234627e-01f, 2.355660647e-01f, -8.531991225e-10f},
+    {7.710843086e-01f, 2.599575520e-01f, 9.733652995e-09f},
+    {7.529411912e-01f, 2.837681472e-01f, 6.342722347e-09f},
+    {7.356321812e-01f, 3.070250452e-01f, -6.136276820e-09f},
+    {7.191011310e-01f, 3.297532797e-01f, -3.558054518e-09f},
+    {7.032967210e-01f, 3.519763947e-01f, 3.358148648e-09f},
+    {6.881720424e-01f, 3.737164140e-01f, -3.249855274e-09f},
+    {6.736842394e-01f, 3.949937522e-01f, 1.315889708e-08f},
+    {6.597937942e-01f, 4.158279300e-01f, -4.096246009e-09f},
+    {6.464646459e-01f, 4.362367690e-01f, -1.254712112e-09f},
+    {6.336633563e-01f, 4.562374353e-01f, 1.397318972e-08f},
+    {6.213592291e-01f, 4.758459032e-01f, -7.601449248e-09f},
+    {6.095238328e-01f, 4.950772226e-01f, 6.027948363e-09f},
+    {5.981308222e-01f, 5.139457583e-01f, 2.442445890e-08f},
+    {5.871559381e-01f, 5.324648619e-01f, -2.015950074e-08f},
+    {5.765765905e-01f, 5.506470799e-01f, 1.379366488e-08f},
+    {5.663716793e-01f, 5.685047507e-01f, -1.165064845e-08f},
+    {5.565217137e-01f, 5.860490799e-01f, 1.074336620e-08f},
+    {5.470085740e-01f, 6.032907963e-01f, 5.798082015e-09f},
+    {5.378151536e-01f, 6.202403307e-01f, 2.783301056e-08f},
+    {5.289255977e-01f, 6.369075179e-01f, -1.376341796e-08f},
+    {5.203251839e-01f, 6.533012986e-01f, 1.064733279e-08f},
+    {5.120000243e-01f, 6.694306135e-01f, -7.072582076e-09f},
+    {5.039370060e-01f, 6.853039861e-01f, 2.075166883e-08f},
 };
 
 // A token's place in the order, larger first: its logit's bits made to ascend, then the index
@@ -283,7 +311,8 @@ __device__ __forceinline__ Parts weights(const Below& b, const Row& r, const flo
   const float2 am = ffma2(both(kMagic), both(-1.f), a);
   const float2 rest = ffma2(ffma2(am, both(-0x1p-20f), hi), both(1.f), lo);
   const float2 l = ffma2(rest, both(0x1p42f), both(kMagic));
-  return {{__float_as_uint(a.x), __float_as_uint(a.y)}, {__float_as_uint(l.x), __float_as_uint(l.y)}};
+  return {{__float_as_uint(a.x), __float_as_uint(a.y)},
+          {__float_as_uint(l.x), __float_as_uint(l.y)}};
 }
 __device__ __forceinline__ uint64_t whole(uint32_t hi, uint32_t lo) {
   return static_cast<uint64_t>((static_cast<int64_t>(static_cast<int32_t>(hi)) << 22) +
@@ -299,8 +328,8 @@ __device__ __forceinline__ uint64_t weight(float x, const Row& r, const float2* 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
@@ -577,7 +606,8 @@ struct Sampler {
     int n;
   };
   template <class Counts>
-  __device__ __forceinline__ Counted compare(int n, int i, int part, int parts, Counts counts) const {
+  __device__ __forceinline__ Counted compare(int n, int i, int part, int parts,
+                                             Counts counts) const {
     Counted c{0, 0};
     const unsigned long long *at = sh.list, *w = sh.list + kCounted;
     if (i < n) {
@@ -825,8 +855,11 @@ struct Sampler {
         const uint64_t at = place(key_of(y), v);
         if (at < cut || at >> up != prefix) return;
         const int d = static_cast<int>(at >> shift) & (bins - 1);
-        if (by_mass) atomicAdd(&sh.list[d], static_cast<unsigned long long>(weight<kType>(y, r, sh.table)));
-        else atomicAdd(&sh.count[d], 1u);
+        if (by_mass)
+          atomicAdd(&sh.list[d],
+                    static_cast<unsigned long long>(weight<kType>(y, r, sh.table)));
+        else
+          atomicAdd(&sh.count[d], 1u);
       });
       cluster.sync();
       // some digits a thread, the highest first
@@ -1285,8 +1318,8 @@ struct Sampler {
     cluster.sync();
   }
   // What the first CTA finds of a window. By count: the list's first `need` places are kept; by
-  // mass: the border of the target. The row is done; the border is here (the cut in sh.found[1], the
-  // kept of the list added to sh.kept); min-p's is higher; it is above or below, by *gap; top-p of
+  // mass: the border of the target. The row is done; the border is here (the cut in sh.found[1],
+  // the kept of the list added to sh.kept); min-p's is higher; it is above or below, by *gap; top-p of
   // the kept is next, its target in *gap.
   static constexpr int kAbove = 5, kBelow = 6, kNext = 7;
   __device__ __forceinline__ int settle(int kind, uint64_t target, uint32_t need, bool from_top,
@@ -1461,7 +1494,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   for (int t = s.t0; t < s.t1; t += 4) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (t + i < s.t1) mx[i & 1] = fmaxf(mx[i & 1], vector_max<kType>(s.data[(t + i) * 32 + s.lane]));
+      if (t + i < s.t1)
+        mx[i & 1] = fmaxf(mx[i & 1], vector_max<kType>(s.data[(t + i) * 32 + s.lane]));
   }
   const float maxima[2] = {mx[0] + 0.f, mx[1] + 0.f};
   if (s.k > 0) {
@@ -1483,8 +1517,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   s.peak = -INFINITY;
   for (int q = 0; q < s.ctas; ++q) s.peak = fmaxf(s.peak, *s.cluster.map_shared_rank(&sh.max, q));
 
-  // ---- the row by what it asks for (the same in every thread of the cluster). A CTA leaves when no
-  // other looks at its shared memory any more.
+  // ---- the row by what it asks for (the same in every thread of the cluster). A CTA leaves when
+  // no other looks at its shared memory any more.
   if (!(fabsf(s.peak) < INFINITY)) {  // no token
     if (s.rank == 0 && s.tid == 0) {
       p.tokens[s.row] = -1;
@@ -1555,11 +1589,15 @@ cudaError_t launch_t(const SampleParams& p, int cluster, cudaStream_t stream) {
 cudaError_t launch_sample(SampleParams p, int dtype, int num_sms, cudaStream_t stream) {
   const int size = dtype == 2 ? 4 : 2, word = 16 / size;
   auto slice = [&](int ctas) { return ((p.V + ctas - 1) / ctas + word - 1) / word * word; };
+  // (powers of two: others leave SMs of a GPC without a cluster; 100 rows of 50257 by threes took
+  // 44 us with top-p, by twos 36)
   int cluster = 1;
   while (cluster < kMaxCluster && smem_bytes(slice(cluster), size) > kSmemTwo) cluster *= 2;
-  // few rows: more CTAs for each, while a warp has a few tiles of its slice
-  while (cluster < kMaxCluster && static_cast<int64_t>(p.B) * cluster * 2 <= num_sms &&
-         slice(cluster * 2) >= 4 * kThreads * word)
+  // few rows: more CTAs for each while all of them run at once, two an SM, and a thread has a few
+  // words of its slice
+  const int64_t at_once = (smem_bytes(slice(cluster), size) <= kSmemTwo ? 2 : 1) * num_sms;
+  while (cluster < kMaxCluster && static_cast<int64_t>(p.B) * cluster * 2 <= at_once &&
+         slice(cluster * 2) >= kMinWords * kThreads * word)
     cluster *= 2;
   p.slice = slice(cluster);
   switch (dtype) {

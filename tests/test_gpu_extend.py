@@ -36,7 +36,8 @@ class Cache:
                            for n in (B + 1, T, T))
         outs = {}
         if separate:
-            outs = dict(out_seq_lens=torch.full_like(lens, -7), out_free_count=torch.full_like(count, -7))
+            outs = dict(out_seq_lens=torch.full_like(lens, -7),
+                        out_free_count=torch.full_like(count, -7))
         binding.extend_sequences(bt, lens, i32(news), free, count, self.nb, qsl, slots, pos, window,
                                  sinks, **outs, **kw)
         torch.cuda.synchronize()
@@ -61,7 +62,8 @@ class Cache:
 @pytest.mark.parametrize("lens,news", [
     ([0], [1]), ([15], [1]), ([16], [1]), ([17], [0]), ([0, 0, 0], [0, 0, 0]),
     ([1, 16, 31, 32, 0], [1, 1, 1, 1, 40]), ([100, 7], [5, 200]),
-    ([i % 50 for i in range(600)], [1] * 600), ([3 * i for i in range(70)], [i for i in range(70)])])
+    ([i % 50 for i in range(600)], [1] * 600),
+    ([3 * i for i in range(70)], [i for i in range(70)])])
 def test_steps(lens, news, separate):
     need = sum(-(-(a + b) // 16) for a, b in zip(lens, news))
     c = Cache(lens, max(max(a + 3 * b for a, b in zip(lens, news)) // 16 + 1, 1), 3 * need + 2, 1)

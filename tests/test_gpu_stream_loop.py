@@ -46,8 +46,9 @@ class Loop:
         qkv = self.emb[tokens.long()].view(T, hq + 2 * hkv, d)
         q = torch.empty(T, hq, d, dtype=self.dt, device="cuda")
         at = torch.stack([pos, pos // 5, pos % 5])  # a picture of rows of five, say
-        binding.rotary_axes_reshape_and_cache(qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], at,
-                                              slots, self.k, self.v, self.freq, self.axes, q_out=q)
+        binding.rotary_axes_reshape_and_cache(qkv[:, :hq], qkv[:, hq:hq + hkv],
+                                              qkv[:, hq + hkv:], at, slots, self.k, self.v,
+                                              self.freq, self.axes, q_out=q)
         return q, binding.streaming_paged_attention(q, self.k, self.v, self.bt, self.lens, self.qsl,
                                                     d ** -0.5, self.window, self.sinks,
                                                     workspace=ws)
@@ -85,7 +86,8 @@ def test_streams_past_their_cache(dt, hq, hkv, d):
                             for old, pool in zip(kept[b], (loop.k, loop.v)))
             assert pos[a:e].tolist() == list(range(len(kept[b][0]) - (e - a), len(kept[b][0])))
             if step % 10 == 0 or step < 3:
-                ref, absv, size, tail = S.attend_stream(q[a:e], *kept[b], pos[a:e], d ** -0.5, 45, 5)
+                ref, absv, size, tail = S.attend_stream(q[a:e], *kept[b], pos[a:e], d ** -0.5, 45,
+                                                        5)
                 tol = R.attention_tolerance(ref, absv, size, tail, d, dt)
                 assert ((out[a:e].double() - ref).abs() <= tol).all(), (step, b)
         loop.bits.copy_(words(B, step))

@@ -83,7 +83,8 @@ class Streams:
 DECODES = [(1, 1), (2, 1), (15, 1), (16, 1), (17, 1), (300, 1), (2049, 1), (129, 1)]
 LONG = [(9000, 1), (5, 1), (700, 1), (33, 4), (12000, 2)]
 CHUNKS = [(300, 300), (1, 1), (513, 200), (64, 64), (900, 129), (40, 1)]
-BATCHES = {"decodes": DECODES, "long": LONG, "chunks": CHUNKS, "small_chunks": [(200, 100), (90, 33)],
+BATCHES = {"decodes": DECODES, "long": LONG, "chunks": CHUNKS,
+           "small_chunks": [(200, 100), (90, 33)],
            "one": [(1, 1)], "one_long": [(3000, 1)], "one_chunk": [(1500, 1400)],
            "verify": [(500, 5), (61, 5), (5, 5), (2000, 5)],
            "gaps": [(50, 0), (20, 3), (0, 0), (400, 1), (16, 0)],
