@@ -4,7 +4,8 @@
 // in the table) and a magnitude on the cosine and sine:
 //     (x, y) -> (x c - y s, y c + x s),  c = m cos(pos f_i),  s = m sin(pos f_i).
 // With several axes (time, height, width of images and video) pos is that of the frequency's
-// axis.
+// axis: one more load for a cosine and none for a unit (8192 tokens, 32/8 heads, D 128: 34.6 us,
+// 0.87 of the measured copy peak, as with one axis).
 //
 // Angle: each frequency is held as a 64-bit fixed-point fraction of a turn; pos * F_i
 // wrapping modulo 2^64 is the angle modulo one turn (exact but for F_i's own rounding, so
