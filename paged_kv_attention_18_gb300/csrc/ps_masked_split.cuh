@@ -42,9 +42,11 @@ namespace {
 // pages each in flight hide their dependent steps better than 8 with six (contexts to 8191,
 // 16 heads of 64 elements, each its own: 285 us with 8 warps, 272 with 16). Items of 128
 // elements take 166 registers, and 12 warps with two pages each gained nothing.
-template <int D, bool kNarrow>
+template <int D, bool kNarrow, bool kStreamDirect>
 struct MaskedSplit {
-  static constexpr int kWarps = masked_split_warps(D, kNarrow);
+  static constexpr int kWarps = !kStreamDirect ? masked_split_warps(D, kNarrow)
+                                : kNarrow     ? (D == 128 ? 12 : 16)
+                                              : (D == 128 ? 8 : 12);
   static constexpr int kStages = (D == 128 ? 24 : 48) / kWarps;  // pages in flight per warp
   static constexpr int kRing = kStages + 2;           // item records
   static constexpr int kPage = kBlockSize * D * 2;    // one page of K (or V), one head
@@ -65,10 +67,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // the head's elements as the MMA's 16 rows and the item's 8 rows as its 8 columns: half the
 // MMAs, scores and accumulators of a 16-row item whose upper half would be empty.
 template <class Params, bool kBF16, int D, bool kDirect, bool kNarrow>
-__global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
+__global__ void __launch_bounds__(
+    MaskedSplit<D, kNarrow, kDirect && Params::kSinks>::kWarps * 32, 1)
     masked_split_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const Params p) {
-  using C = MaskedSplit<D, kNarrow>;
+  using C = MaskedSplit<D, kNarrow, kDirect && Params::kSinks>;
   constexpr int kWarps = C::kWarps;
   constexpr int S = C::kStages, kRing = C::kRing, kPage = C::kPage, kStage = C::kStage;
   constexpr int kBoxes = D / 64, kKSteps = D / 16;
@@ -633,6 +636,8 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
       }
       const int key0 = key_base + 2 * t4;
       float mx[2] = {-INFINITY, -INFINITY};
+      // (streams: the reference moves only when some score is more than 2^8 above it, as above)
+      bool up = !Params::kSinks;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -645,15 +650,34 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
           s[nt][e] = x;
           mx[r] = fmaxf(mx[r], x);
         }
-      float alpha[2], m_use[2];
+      if constexpr (Params::kSinks)
+        up = __any_sync(0xffffffffu, mx[0] > m_run[0] + 8.f || mx[1] > m_run[1] + 8.f);
+      float m_use[2] = {m_run[0], m_run[1]};
+      if (up) {
+        float alpha[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        const float m_new = fmaxf(m_run[r], mx[r]);
-        m_use[r] = m_new == -INFINITY ? 0.f : m_new;
-        alpha[r] = fast_exp2(m_run[r] - m_use[r]);
-        m_run[r] = m_new;
+        for (int r = 0; r < 2; ++r) {
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+          const float m_new = fmaxf(m_run[r], mx[r]);
+          m_use[r] = m_new == -INFINITY ? 0.f : m_new;
+          alpha[r] = fast_exp2(m_run[r] - m_use[r]);
+          m_run[r] = m_new;
+          l_run[r] *= alpha[r];
+        }
+        const float2 a0 = make_float2(alpha[0], alpha[0]), a1 = make_float2(alpha[1], alpha[1]);
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          const float2 u = fmul2(make_float2(o[j][0], o[j][1]), a0);
+          const float2 w = fmul2(make_float2(o[j][2], o[j][3]), a1);
+          o[j][0] = u.x;
+          o[j][1] = u.y;
+          o[j][2] = w.x;
+          o[j][3] = w.y;
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) m_use[r] = m_run[r] == -INFINITY ? 0.f : m_run[r];
       }
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
@@ -667,20 +691,10 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
       // the row sums use the rounded P the tensor core multiplies with
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float2 acc = make_float2(l_run[r] * alpha[r], 0.f);
+        float2 acc = make_float2(l_run[r], 0.f);
         add_pair_exact<kBF16>(acc, pa[r]);
         add_pair_exact<kBF16>(acc, pa[2 + r]);
         l_run[r] = acc.x + acc.y;
-      }
-      const float2 a0 = make_float2(alpha[0], alpha[0]), a1 = make_float2(alpha[1], alpha[1]);
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        const float2 u = fmul2(make_float2(o[j][0], o[j][1]), a0);
-        const float2 w = fmul2(make_float2(o[j][2], o[j][3]), a1);
-        o[j][0] = u.x;
-        o[j][1] = u.y;
-        o[j][2] = w.x;
-        o[j][3] = w.y;
       }
       {  // O += P V: the V page is [key][d], read transposed
         const int mi = lane >> 3, rr = lane & 7;
@@ -715,7 +729,10 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
   }
   if constexpr (kDirect) {
     // The warps' shares of the item's pages joined: each leaves its O (not normalised) in its
-    // own stages, which hold no page any more, and its rows' maxima and sums.
+    // own stages, which hold no page any more, and its rows' maxima and sums. (A row of O takes a
+    // few columns more, so that the rows that a store's lanes write lie in other banks.)
+    constexpr int kRowO = D + (kNarrow ? 4 : 8);
+    static_assert(kGroup * kRowO * 4 <= S * kStage, "O of a warp");
     __shared__ float sh_m[kWarps][kGroup], sh_l[kWarps][kGroup];
     const bool worked = g_comp != g_first && !aborted;
 #pragma unroll
@@ -729,7 +746,7 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
         sh_l[warp][row] = worked ? l_run[r] : 0.f;
       }
       if (worked) {
-        float* dst = reinterpret_cast<float*>(tiles) + row * D;
+        float* dst = reinterpret_cast<float*>(tiles) + row * kRowO;
 #pragma unroll
         for (int j = 0; j < kO; ++j) {
           if constexpr (kNarrow) {
@@ -743,18 +760,19 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
       }
     }
     __syncthreads();
-    // threads of a row (of two columns at least: they are stored in pairs), columns of each
-    constexpr int kShare = kWarps * 32 / kGroup, kLanes = kShare < D / 2 ? kShare : D / 2;
-    constexpr int kPer = D / kLanes;
-    static_assert(kPer * kLanes == D && kPer % 2 == 0 && kLanes * kGroup <= kWarps * 32, "join");
-    const int row = threadIdx.x / kLanes, col = (threadIdx.x % kLanes) * kPer;
+    // threads of a row, pairs of columns of each
+    constexpr int kShare = kWarps * 32 / kGroup, kLanes = kShare >= 32 ? 32 : 16;
+    constexpr int kPairs = D / 2 / kLanes;
+    static_assert(kPairs * kLanes * 2 == D && kLanes * kGroup <= kWarps * 32, "join");
+    const int row = threadIdx.x / kLanes, col = 2 * (threadIdx.x % kLanes);
     if (row < dir_rows) {
       float M = -INFINITY;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) M = fmaxf(M, sh_m[k][row]);
-      float acc[kPer], sum = 0.f;
+      float2 acc[kPairs];
+      float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+      for (int e = 0; e < kPairs; ++e) acc[e] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const float m = sh_m[k][row];
@@ -762,9 +780,14 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
         if (sh_l[k][row] == 0.f) continue;
         const float wgt = fast_exp2(m - M);
         sum += wgt * sh_l[k][row];
-        const float* src = reinterpret_cast<const float*>(smem + k * S * kStage) + row * D + col;
+        const float* src =
+            reinterpret_cast<const float*>(smem + k * S * kStage) + row * kRowO + col;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] += wgt * src[e];
+        for (int e = 0; e < kPairs; ++e) {
+          const float2 o2 = *reinterpret_cast<const float2*>(src + 2 * kLanes * e);
+          acc[e].x += wgt * o2.x;
+          acc[e].y += wgt * o2.y;
+        }
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int R = dir_row0 + row, i = R / p.G;
@@ -772,7 +795,8 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
           static_cast<uint16_t*>(p.out) +
           (static_cast<int64_t>(dir_tok0 + i) * p.H_q + dir_kv * p.G + (R - i * p.G)) * D + col);
 #pragma unroll
-      for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack2<kBF16>(acc[e] * inv, acc[e + 1] * inv);
+      for (int e = 0; e < kPairs; ++e)
+        dst[kLanes * e] = pack2<kBF16>(acc[e].x * inv, acc[e].y * inv);
     }
     // the CTA's next item, once the stages that held O have been read
     dir_item += gridDim.x;
@@ -788,7 +812,7 @@ __global__ void __launch_bounds__(MaskedSplit<D, kNarrow>::kWarps * 32, 1)
 template <bool kBF16, int D, bool kDirect, bool kNarrow, class Params>
 cudaError_t launch_split_t(const Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                            int ctas, cudaStream_t stream, bool pdl) {
-  using C = MaskedSplit<D, kNarrow>;
+  using C = MaskedSplit<D, kNarrow, kDirect && Params::kSinks>;
   constexpr int smem = C::kSmem;
   auto kern = masked_split_kernel<Params, kBF16, D, kDirect, kNarrow>;
   static std::atomic<uint64_t> done{0};
