@@ -371,6 +371,9 @@ int encode_pool_map(CUtensorMap* map, const void* pool, int num_blocks, int H_kv
 
 // Direct launch: items per SM, and pages x head size, at most.
 constexpr int kMaskedDirectItems = 2, kMaskedDirectKeys = 128 * 128;
+// Streams: the latter for each CTA of an item, these at most, and the pages for each of a CTA's
+// warps from which there is a second CTA, and for each of all warps from which there are more.
+constexpr int kStreamDirectKeys = 256 * 128, kMaxItemCtas = 8, kMinCtaPages = 3, kMinWarpPages = 2;
 
 // The masked attention's chain: as run_attention's without a scatter. A small batch runs on
 // the split or the tile kernel's direct mode alone; otherwise planner, split kernel, tile
@@ -418,9 +421,29 @@ int run_masked_attention(const Params& p0, const void* k_pool, const void* v_poo
                          (p.sinks + kBlockSize - 1) / kBlockSize;
     if (p.window > 0 && seen < item_pages) item_pages = seen;
   }
+  // Streams: more CTAs for an item, a cluster, while all items' are likely to run at once (a
+  // sequence's last group is half full on average) and their warps have pages to read: a
+  // microsecond for the second CTA, little for the others. us, a CTA an item / clusters:
+  //   12 heads on 2, D 128:  1 sequence, window 250 7.6 / 7.8 by 2 (so not taken), 1000 11.2 /
+  //                          9.4, 4000 22.4 / 10.4 by 8; 16 of 4000 27.9 / 16.5 by 4;
+  //                          4 tokens on average: 4 of 1000 16.3 / 11.7, 18 of 1000 15.8 / 13.1
+  // and so the plan is left later (planned / direct): 18 of 4000 with 4 tokens 42.7 / 23.6 by 2,
+  // 1 of 16000 38 / 17 and of 32000 58 / 26 by 8; also with one CTA an item, 36 of 4000 43 / 28.5,
+  // with 4 tokens 62 / 37, 76 on 4 KV heads 115 / 98. (Not for longer ones, though that was still
+  // faster where all were as long as the window: a single long one among short ones waits for
+  // its one CTA.)
+  int ctas = 1;  // of an item
+  if constexpr (Params::kSinks) {
+    const int warps = stream_direct_warps(p.D, gr == 8);
+    const int64_t likely = p.T <= p.B ? items : p.H_kv * (rows / gr + p.B / 2);
+    if (item_pages >= kMinCtaPages * warps)
+      while (ctas < kMaxItemCtas && likely * ctas * 2 <= num_sms &&
+             item_pages >= kMinWarpPages * warps * ctas)
+        ctas *= 2;
+  }
   if (rows <= 64 * static_cast<int64_t>(p.B) && items <= kMaskedDirectItems * num_sms &&
-      item_pages * p.D <= kMaskedDirectKeys) {
-    p.direct = 1;
+      item_pages * p.D <= (Params::kSinks ? kStreamDirectKeys : kMaskedDirectKeys) * ctas) {
+    p.direct = ctas;
     Timed tm(3, s);
     if ((e = launch_masked_split(p, bf16, kmap, vmap, static_cast<int>(items), s, true)) !=
         cudaSuccess)

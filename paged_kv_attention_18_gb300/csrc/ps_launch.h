@@ -362,8 +362,12 @@ cudaError_t launch_plan_masked(const StreamAttnParams& p, int concurrency, int t
 // their causal forms are.
 // Warps of the masked split kernel's CTA (narrow: its 8-row items).
 constexpr int masked_split_warps(int D, bool narrow) { return narrow && D == 64 ? 16 : 8; }
+// Of a CTA in the direct mode for streams, as many as its registers allow.
+constexpr int stream_direct_warps(int D, bool narrow) {
+  return narrow ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);
+}
 // p.direct: the split kernel's direct mode, about a CTA for each group of rows of a
-// (sequence, KV head).
+// (sequence, KV head); for streams a cluster of p.direct CTAs for each.
 cudaError_t launch_masked_split(const MaskedAttnParams& p, bool bf16, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int ctas, cudaStream_t stream,
                                 bool pdl);

@@ -27,8 +27,13 @@
 // is two runs of pages, the sinks' before the window's, through the same ring one behind the
 // other; on the turn from one to the other only the bounds of the rows' keys change. 128 decodes
 // of 16 heads on 4, D 128, over a window of 4096 and 4 sinks: 174 us, 0.92 of the measured copy
-// peak, as the window alone.
+// peak, as the window alone. Small batches, without a plan: a cluster of up to 8 CTAs for an
+// item, whose warps share its pages out and send their joined rows to the row's CTA. One decode
+// over a window of 4000, 12 heads on 2: 10.4 us with 8 CTAs, 22.4 with one, bound by each warp's
+// chain of steps (about a microsecond a page: the copy's issue, two products, the softmax).
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "ps_common.cuh"
 #include "ps_launch.h"
@@ -44,9 +49,8 @@ namespace {
 // elements take 166 registers, and 12 warps with two pages each gained nothing.
 template <int D, bool kNarrow, bool kStreamDirect>
 struct MaskedSplit {
-  static constexpr int kWarps = !kStreamDirect ? masked_split_warps(D, kNarrow)
-                                : kNarrow     ? (D == 128 ? 12 : 16)
-                                              : (D == 128 ? 8 : 12);
+  static constexpr int kWarps =
+      kStreamDirect ? stream_direct_warps(D, kNarrow) : masked_split_warps(D, kNarrow);
   static constexpr int kStages = (D == 128 ? 24 : 48) / kWarps;  // pages in flight per warp
   static constexpr int kRing = kStages + 2;           // item records
   static constexpr int kPage = kBlockSize * D * 2;    // one page of K (or V), one head
@@ -99,6 +103,14 @@ __global__ void __launch_bounds__(
   const int n_items = kDirect ? 0 : *reinterpret_cast<volatile int*>(p.hdr);
   bool first_fetch = true;
   [[maybe_unused]] bool first_scan = true;
+  // Streams: p.direct CTAs, a cluster, share the pages of an item; row r is the r % p.direct'th's.
+  constexpr bool kClusters = kDirect && Params::kSinks;
+  [[maybe_unused]] const int ctas = kClusters ? p.direct : 1, rank = blockIdx.x % ctas;
+  [[maybe_unused]] __shared__ int sh_stop;  // a CTA of the cluster has given up
+  if constexpr (kClusters) {
+    if (threadIdx.x == 0) sh_stop = 0;
+    if (ctas > 1) cluster_arrive();
+  }
   const bool tile_planned = !kDirect && *reinterpret_cast<volatile int*>(p.hdr + 4) > 0;
   const uint64_t policy = l2_policy_evict_first();
 
@@ -122,7 +134,7 @@ __global__ void __launch_bounds__(
   // (few: the launch has about an item a CTA) to find item idx. The item's record covers every
   // page its rows see; the CTA's warps share the pages out. Lane k returns field k.
   constexpr int kGroup = kNarrow ? 8 : 16;
-  int dir_item = blockIdx.x, dir_items = 0;  // the CTA's item, items in all
+  int dir_item = blockIdx.x / ctas, dir_items = 0;  // the CTA's item, items in all
   auto direct_item = [&](int idx) -> int {
     int b = -1, q0 = 0, n = 0, L = 0, nth = 0, groups = 0;  // the item's sequence, from its lane
     dir_items = 0;
@@ -178,13 +190,14 @@ __global__ void __launch_bounds__(
     const int pe = (hi + kBlockSize - 1) / kBlockSize;
     // (one page at least, the sinks' included)
     const int pb = Params::kSinks ? min(lo / kBlockSize, pe) : min(lo / kBlockSize, pe - 1);
-    const int pages = s1 + pe - pb, share = (pages + kWarps - 1) / kWarps;
+    const int warps = kWarps * ctas, nth_warp = rank * kWarps + warp;
+    const int pages = s1 + pe - pb, share = (pages + warps - 1) / warps;
     // the warp's share of the pages, counted from the window's first with the sinks' before it
-    const int from = pb - s1 + warp * share, to = min(from + share, pe);
+    const int from = pb - s1 + nth_warp * share, to = min(from + share, pe);
     int first = from, end = to;
     if constexpr (Params::kSinks) {
-      s0 = min(warp * share, s1);
-      s1 = min(warp * share + share, s1);
+      s0 = min(nth_warp * share, s1);
+      s1 = min(nth_warp * share + share, s1);
       first = max(from, pb);
       end = max(to, first);
     }
@@ -765,6 +778,21 @@ __global__ void __launch_bounds__(
     constexpr int kPairs = D / 2 / kLanes;
     static_assert(kPairs * kLanes * 2 == D && kLanes * kGroup <= kWarps * 32, "join");
     const int row = threadIdx.x / kLanes, col = 2 * (threadIdx.x % kLanes);
+    auto store_row = [&](int row, int col, const float2 (&acc)[kPairs], float sum) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int R = dir_row0 + row, i = R / p.G;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(
+          static_cast<uint16_t*>(p.out) +
+          (static_cast<int64_t>(dir_tok0 + i) * p.H_q + dir_kv * p.G + (R - i * p.G)) * D + col);
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e)
+        dst[kLanes * e] = pack2<kBF16>(acc[e].x * inv, acc[e].y * inv);
+    };
+    // (clusters: what the CTAs send of this one's rows: O, and maximum and sum)
+    __shared__ float2 sh_o[kClusters ? kGroup * D / 2 : 1], sh_all[kClusters ? kGroup : 1];
+    [[maybe_unused]] const auto cluster = cooperative_groups::this_cluster();
+    if constexpr (kClusters)
+      if (ctas > 1) cluster_wait();  // (every CTA has begun, or read what it was sent before)
     if (row < dir_rows) {
       float M = -INFINITY;
 #pragma unroll
@@ -789,14 +817,52 @@ __global__ void __launch_bounds__(
           acc[e].y += wgt * o2.y;
         }
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int R = dir_row0 + row, i = R / p.G;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(
-          static_cast<uint16_t*>(p.out) +
-          (static_cast<int64_t>(dir_tok0 + i) * p.H_q + dir_kv * p.G + (R - i * p.G)) * D + col);
+      if (ctas == 1) {
+        store_row(row, col, acc, sum);
+      } else if constexpr (kClusters) {  // to the row's CTA
+        const int at = rank * (kGroup / ctas) + row / ctas;
+        float2* dst = cluster.map_shared_rank(sh_o, row % ctas) + (at * D + col) / 2;
 #pragma unroll
-      for (int e = 0; e < kPairs; ++e)
-        dst[kLanes * e] = pack2<kBF16>(acc[e].x * inv, acc[e].y * inv);
+        for (int e = 0; e < kPairs; ++e) dst[kLanes * e] = acc[e];
+        if (col == 0) cluster.map_shared_rank(sh_all, row % ctas)[at] = make_float2(M, sum);
+      }
+    }
+    if constexpr (kClusters) {
+      if (ctas > 1) {
+        if (__syncthreads_or(aborted) && threadIdx.x < ctas)
+          *cluster.map_shared_rank(&sh_stop, threadIdx.x) = 1;
+        cluster_arrive();
+        cluster_wait();
+        if (row < dir_rows && row % ctas == rank) {
+          const int at = row / ctas, step = kGroup / ctas;
+          float M = -INFINITY;
+          for (int c = 0; c < ctas; ++c) M = fmaxf(M, sh_all[at + c * step].x);
+          float2 acc[kPairs];
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) acc[e] = make_float2(0.f, 0.f);
+          for (int c = 0; c < ctas; ++c) {
+            const float2 ms = sh_all[at + c * step];
+            if (ms.y == 0.f) continue;
+            const float wgt = fast_exp2(ms.x - M);
+            sum += wgt * ms.y;
+            const float2* src = sh_o + ((at + c * step) * D + col) / 2;
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+              acc[e].x += wgt * src[kLanes * e].x;
+              acc[e].y += wgt * src[kLanes * e].y;
+            }
+          }
+          store_row(row, col, acc, sum);
+        }
+        dir_item += gridDim.x / ctas;
+        if (dir_item >= dir_items || sh_stop != 0) return;  // (the same in every CTA)
+        fence_proxy_async_smem();
+        cluster_arrive();
+        no_more = have_item = false;
+        first_fetch = true;
+        goto next_item;
+      }
     }
     // the CTA's next item, once the stages that held O have been read
     dir_item += gridDim.x;
@@ -818,6 +884,11 @@ cudaError_t launch_split_t(const Params& p, const CUtensorMap& kmap, const CUten
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_limit(kern, smem, done);
   if (e != cudaSuccess) return e;
+  if constexpr (kDirect && Params::kSinks) {
+    if (p.direct > 1)
+      return launch_cluster(kern, static_cast<unsigned>(ctas) * p.direct, p.direct, C::kWarps * 32,
+                            smem, stream, kmap, vmap, p);
+  }
   return launch_kernel(kern, dim3(ctas), dim3(C::kWarps * 32), smem, stream, pdl, kmap, vmap, p);
 }
 

@@ -138,6 +138,46 @@ def test_split_contexts(window, sinks):
         b.check(b.run())
 
 
+SHARED = [([(3000, 1)], 2500, 4), ([(700, 1)], 600, 20), ([(60, 1), (2100, 1), (0, 0)], 2000, 33),
+          ([(4100, 5)], 4000, 100), ([(1200, 3), (900, 5), (5, 2), (17, 1)], 1000, 4),
+          ([(20000, 1)], 30000, 4), ([(9000, 2), (40, 2)], 8000, 1), ([(1500, 40)], 1400, 17),
+          ([(800 + 37 * i, 1) for i in range(17)], 900, 4),
+          ([(600 + 70 * i, 1 + i % 5) for i in range(9)], 1100, 50)]
+
+
+@pytest.mark.parametrize("case", range(len(SHARED)))
+@pytest.mark.parametrize("hq,hkv,d", HEADS + [(16, 1, 128), (2, 2, 64), (32, 8, 128)])
+def test_an_item_on_several_ctas(case, hq, hkv, d):
+    """Small batches: clusters of CTAs share an item's pages, many with none of a short sequence."""
+    seqs, window, sinks = SHARED[case]
+    for dt in DTS:
+        for cap in (0.0, 30.0):
+            b = Streams(seqs, hq, hkv, d, dt, window, sinks, seed=case, softcap=cap)
+            out = b.run()
+            b.check(out)
+            assert torch.equal(out, b.run())
+
+
+def test_more_items_than_clusters():
+    """Offsets that go back: the sequence is recorded as bad, those around it are served, though
+    together they have more tokens than the batch."""
+    b = Streams([(700, 40), (900, 40), (800, 40)], 4, 1, 128, torch.bfloat16, 600, 9)
+    T = 48  # sequence 0: tokens 0 .. 39, 1: bad, 2: 8 .. 47
+    b.qs[:] = torch.tensor([0, 40, 8, 48], dtype=torch.int32)
+    q = b.q[:T].contiguous()
+    out = torch.full_like(q, 7.0)
+    binding.streaming_paged_attention(q, b.k, b.v, b.bt, b.sl, b.qs, b.scale, 600, 9, out=out)
+    torch.cuda.synchronize()
+    assert binding.device_error() == 3
+    for s, a, e in ((0, 0, 8), (2, 40, 48)):  # (tokens of one sequence alone)
+        L, first = b.seqs[s][0], 0 if s == 0 else 8
+        pos = torch.arange(L - 40 + a - first, L - 40 + e - first, device="cuda")
+        ref, absv, size, tail = S.attend_stream(
+            q[a:e], R.gather(b.k, b.bt[s], L), R.gather(b.v, b.bt[s], L), pos, b.scale, 600, 9)
+        tol = R.attention_tolerance(ref, absv, size, tail, b.d, b.dt)
+        assert not ((out[a:e].double() - ref).abs() > tol).any()
+
+
 def test_without_a_window_or_sinks_it_is_the_masked_attention():
     for window, sinks in ((0, 0), (0, 7), (40, 0)):
         b = Streams(CHUNKS, 12, 2, 128, torch.bfloat16, window, sinks)
