@@ -26,9 +26,10 @@
 // Streams (StreamAttnParams): the sinks' pages and the window's form one run of key tiles
 // (ItemTiles), and a row drops the columns outside its window that are not its sinks'. As a tile
 // of their own, of which 4 keys count, the sinks cost as much as 128 keys more: 4 x 2048 tokens
-// over 8192 keys, 32/8 heads, D 128, bf16, 4 sinks: 239 against 225 us at a window of 2000 (206
-// GFLOP: 0.92 PFLOP/s, 0.47 of the measured burst peak), 92 against 79 at 128. What is left there
-// is the items' own: about 7 of an item's 32 us are Q's load, the first tile's and the epilogue.
+// over 8192 keys, 32/8 heads, D 128, bf16, 4 sinks: 239 against 225 us at a window of 2000, 92
+// against 79 at 128. With masks by words (drop_unseen) these take 212 (206 GFLOP: 0.97 PFLOP/s,
+// 0.49 of the measured burst peak) and 69. What is left is the items' own: 5 or 6 of an item's 30
+// us are its first tile's, with the row's first maximum, and the epilogue.
 #pragma once
 
 #include <type_traits>
@@ -167,6 +168,21 @@ struct ItemTiles {
 // unsplit, its query-tile pairs longest first).
 // kCap: 0 none, 1 up to kLargeCapLog2, 2 beyond (the exact form of small scores in every tile; as
 // a branch inside it made the kernel larger and its other caps 1.5 % slower).
+// 32 columns of scores, those outside [low, lim] dropped (streams: but not those below `sunk`). One
+// word has the columns that are kept, so that a column costs a test of a bit and a select in place
+// of up to three comparisons. (6 chunks of 1000 in documents behind a prefix, 14/2 heads, D 64: 33.4
+// us with those, 29.3.)
+template <class Params>
+__device__ __forceinline__ void drop_unseen(uint32_t* v, int lim, int low, int sunk) {
+  auto from = [](int n) { return __funnelshift_lc(0u, ~0u, max(n, 0)); };  // columns n and on
+  uint32_t kept = from(low) & ~from(lim + 1);
+  if constexpr (Params::kSinks) kept |= ~from(sunk);
+  if (__all_sync(0xffffffffu, kept == ~0u)) return;  // (a warp's rows are few tokens)
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(kept >> e & 1u)) v[e] = __float_as_uint(-INFINITY);
+}
+
 template <class Params, bool kBF16, int D, bool kDirect, int kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
     masked_tile_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -746,11 +762,9 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
             tmem_ld32(tS + 64 * h + 32, v + 32);
             tmem_ld_wait();
             if (!full) {
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if ((64 * h + e > lim || 64 * h + e < low) &&
-                    !(Params::kSinks && 64 * h + e < sunk))
-                  v[e] = __float_as_uint(-INFINITY);
+              drop_unseen<Params>(v, lim - 64 * h, low - 64 * h, sunk - 64 * h);
+              drop_unseen<Params>(v + 32, lim - 64 * h - 32, low - 64 * h - 32,
+                                  sunk - 64 * h - 32);
             }
             // P is taken against the row's reference without the half's max; the max (and a move
             // of the reference) is taken only when there is no reference yet, or when the half's
@@ -1072,12 +1086,13 @@ __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
                 v[e] = __float_as_uint(
                     fmaf(slope, fabsf(d0 - static_cast<float>(e)), __uint_as_float(v[e])));
             }
-            if (!full) {
-              const int hi = lim - 32 * h, lo = low - 32 * h, to = sunk - 32 * h;
+            if constexpr (Params::kSinks) {
+              if (!full) drop_unseen<Params>(v, lim - 32 * h, low - 32 * h, sunk - 32 * h);
+            } else if (!full) {  // (by words: capped chunks of 2048 over 8192 593 us, so 585)
+              const int hi = lim - 32 * h, lo = low - 32 * h;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if ((e > hi || e < lo) && !(Params::kSinks && e < to))
-                  v[e] = __float_as_uint(-INFINITY);
+                if (e > hi || e < lo) v[e] = __float_as_uint(-INFINITY);
             }
           };
           // P of 32 columns against the reference, 16-bit pairs; the row sum adds the values the
