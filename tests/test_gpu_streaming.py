@@ -158,6 +158,36 @@ def test_an_item_on_several_ctas(case, hq, hkv, d):
             assert torch.equal(out, b.run())
 
 
+def test_clusters_captured_and_on_two_streams():
+    """Calls by clusters replayed from one graph, with other queries, while another stream makes
+    its own."""
+    a = Streams([(3000, 1), (40, 1)], 12, 2, 128, torch.bfloat16, 2500, 20, seed=3)
+    b = Streams([(2600, 4)], 14, 2, 64, torch.float16, 2500, 20, seed=4)
+    want_b = b.run()
+    other, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    out = torch.full_like(a.q, float("nan"))
+    call = lambda: binding.streaming_paged_attention(
+        a.q, a.k, a.v, a.bt, a.sl, a.qs, a.scale, a.window, a.sinks, out=out)
+    call()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            call()
+    outs = [torch.empty_like(b.q) for _ in range(8)]
+    for i in range(4):
+        a.q.copy_(torch.randn(a.q.shape, device="cuda").to(a.dt))
+        torch.cuda.synchronize()
+        out.fill_(float("nan"))
+        graph.replay()
+        for o in outs:
+            binding.streaming_paged_attention(b.q, b.k, b.v, b.bt, b.sl, b.qs, b.scale, b.window,
+                                              b.sinks, out=o, stream=other)
+        torch.cuda.synchronize()
+        assert binding.device_error() == 0
+        a.check(out)
+        assert all(torch.equal(o, want_b) for o in outs)
+
+
 def test_more_items_than_clusters():
     """Offsets that go back: the sequence is recorded as bad, those around it are served, though
     together they have more tokens than the batch."""
