@@ -435,7 +435,7 @@ int run_masked_attention(const Params& p0, const void* k_pool, const void* v_poo
   int ctas = 1;  // of an item
   if constexpr (Params::kSinks) {
     const int warps = stream_direct_warps(p.D, gr == 8);
-    const int64_t likely = p.T <= p.B ? items : p.H_kv * (rows / gr + p.B / 2);
+    const int64_t likely = p.T <= p.B ? items : p.H_kv * (rows / gr + (p.B + 1) / 2);
     if (item_pages >= kMinCtaPages * warps)
       while (ctas < kMaxItemCtas && likely * ctas * 2 <= num_sms &&
              item_pages >= kMinWarpPages * warps * ctas)
