@@ -19,6 +19,7 @@
 #include "ps_common.cuh"
 #include "ps_launch.h"
 #include "ps_scatter.cuh"
+#include "ps_split.h"
 
 namespace ps {
 
@@ -93,7 +94,7 @@ __device__ __forceinline__ int seq_splits(const SeqInfo& s, int pps_dec, int pps
 
 // First page of split k of ns.
 __device__ __forceinline__ int split_page(const SeqInfo& s, int ns, int k) {
-  return s.page0 + (k * (s.pages - s.page0)) / ns;
+  return split_start(s.page0, s.pages, ns, k);
 }
 
 // The first token that sees a key at or after page `page`: those of the prefix are seen
