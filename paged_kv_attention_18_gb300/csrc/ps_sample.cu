@@ -255,7 +255,7 @@ struct Row {
   float max;      // the row's largest logit (times s)
   float far;      // the difference whose y is kFarthest: larger ones count as it
   float c, c_lo;  // log2(e) / T (over s) as two floats
-  float s;        // 1, or 1/4 where differences would overflow beside T
+  float s;        // 1, or 2^-64 where T is so large that c_lo would lose its bits
 };
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
@@ -1540,7 +1540,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     return;
   }
   const bool far = s.T >= 0x1p100f;
-  s.r.s = far ? 0.25f : 1.f;
+  // (from T = 2^104 or so the bits of c_lo that count would lie below the least float, 2^-149; those
+  // that a logit below 2^-62 loses by the scale are under 2^-185 of T)
+  s.r.s = far ? 0x1p-64f : 1.f;
   s.r.max = s.peak * s.r.s;
   // log2(e) / T to 2^-45 in two floats
   const float Ts = s.T * s.r.s;
