@@ -232,8 +232,9 @@ int ps_rotary_axes_reshape_and_cache(const void* q, int64_t q_stride, const void
  *     that end at or before L_b - window + 1 and begin at or behind `sinks`, from the last one
  *     down to the first whose entry is negative already.
  * Their entries become -1. Such a block must not be in another sequence's table (nor twice in
- * one): what sequences share (prefixes, forks) is for the caller to count and to give back. A
- * caller that takes tokens back (drafts not accepted) passes a window larger by as many.
+ * one): what sequences share (prefixes, forks) is for the caller to count and to give back.
+ * A length must not be shorter than the step before left it (0 for a new sequence in the place of
+ * one that ended): a caller that takes tokens back calls ps_extend_held_sequences.
  *
  *   block_tables  int32 [B, max_blocks_per_seq], updated in place.
  *   seq_lens, new_lens  int32 [B]. (An empty place of a batch: length 0, 0 new tokens.)
@@ -264,6 +265,27 @@ int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int
                         int sinks, int32_t* query_start_loc, int32_t* slot_mapping,
                         int32_t* positions, int32_t* out_seq_lens, int32_t* out_free_count,
                         void* stream);
+
+/*
+ * ps_extend_held_sequences -- ps_extend_sequences for sequences that take tokens back: drafts that
+ * were not accepted (ps_spec_accept), after which seq_lens[b] is less than the step before left it.
+ *
+ *   held_pages    int32 [B], updated in place: the pages of its table that each sequence holds,
+ *                 H_b >= L_b / 16 (rounded up): that to begin with, and then what the calls leave.
+ * Pages H_b .. (L_b + n_b - 1) / 16 get new blocks; those below H_b keep theirs, also where the
+ * tokens on them were taken back, for the tokens that come next. A sequence that ends gives back
+ * pages H_b - 1 .. 0, and holds 0. A sequence with H_b below its length's pages or above
+ * max_blocks_per_seq is left out (PS_DEV_BAD_SEQUENCE). With a window the caller passes one larger
+ * by as many tokens as it may take back. held_pages is none of the arrays of lengths (PS_ERR_ARG).
+ * All else as for ps_extend_sequences.
+ */
+int ps_extend_held_sequences(int32_t* block_tables, int max_blocks_per_seq,
+                             const int32_t* seq_lens, const int32_t* new_lens,
+                             int32_t* held_pages, int32_t* free_blocks, int free_capacity,
+                             const int32_t* free_count, int B, int T, int num_blocks, int window,
+                             int sinks, int32_t* query_start_loc, int32_t* slot_mapping,
+                             int32_t* positions, int32_t* out_seq_lens, int32_t* out_free_count,
+                             void* stream);
 
 /*
  * ps_sample -- one token of every row of logits, by temperature, top-k, top-p and min-p, from a

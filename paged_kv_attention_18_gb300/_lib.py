@@ -35,6 +35,8 @@ SIGNATURES = {
                                                  _p]),
     "ps_extend_sequences": (c_int, [_p, c_int, _p, _p, _p, c_int, _p, c_int, c_int, c_int, c_int,
                                     c_int, _p, _p, _p, _p, _p, _p]),
+    "ps_extend_held_sequences": (c_int, [_p, c_int, _p, _p, _p, _p, c_int, _p, c_int, c_int,
+                                         c_int, c_int, c_int, _p, _p, _p, _p, _p, _p]),
     "ps_sample": (c_int, [_p, c_i64, _p, _p, _p, _p, _p, c_int, c_int, c_int, _p, _p, _p]),
     "ps_beam_select_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
     "ps_beam_select": (c_int, [_p, c_i64, _p, _p, c_int, c_int, c_int, c_int, c_int, c_int, _p,

@@ -250,7 +250,8 @@ def rotary_axes_reshape_and_cache(q, k, v, positions, slot_mapping_t, k_pool, v_
 
 def extend_sequences(block_tables, seq_lens, new_lens, free_blocks, free_count, num_blocks: int,
                      query_start_loc, slot_mapping_t, positions, window: int = 0, sinks: int = 0,
-                     out_seq_lens=None, out_free_count=None, stream=None) -> None:
+                     out_seq_lens=None, out_free_count=None, stream=None,
+                     held_pages=None) -> None:
     """The blocks, slots, positions and packed offsets of a step, on the device
     (ps_extend_sequences). Sequence b of seq_lens[b] tokens adds new_lens[b] (negative: it ends):
     new pages get blocks from the top of the stack free_blocks [capacity] of free_count [1]
@@ -258,11 +259,14 @@ def extend_sequences(block_tables, seq_lens, new_lens, free_blocks, free_count, 
     end. All int32 CUDA tensors; block_tables [B, max_blocks], free_blocks, seq_lens and
     free_count (the last two unless out_seq_lens, out_free_count are given) are updated in place;
     query_start_loc [B + 1], slot_mapping_t [T] and positions [T] are written, with -1 and 0
-    behind the last token."""
+    behind the last token. A program that takes tokens back between steps, shortening seq_lens by
+    drafts that were not accepted, gives held_pages [B], the pages that each sequence holds
+    (ps_extend_held_sequences; ceil(seq_lens / 16) to begin with), which is kept in place: without
+    it the block of a page that held such tokens alone would be lost."""
     (_native_module or _native()).extend(block_tables, seq_lens, new_lens, free_blocks,
                                          free_count, num_blocks, query_start_loc, slot_mapping_t,
                                          positions, window, sinks, out_seq_lens, out_free_count,
-                                         stream)
+                                         held_pages, stream)
 
 
 def sample(logits, random_bits, temperature=None, top_k=None, top_p=None, min_p=None,

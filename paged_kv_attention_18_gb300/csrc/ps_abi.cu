@@ -821,12 +821,13 @@ int ps_sample(const void* logits, int64_t row_stride, const float* temperature,
   return cuda_status(ps::launch_sample(a, logits_dtype, ds->num_sms, s), "sampling kernel");
 }
 
-int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
-                        const int32_t* new_lens, int32_t* free_blocks, int free_capacity,
-                        const int32_t* free_count, int B, int T, int num_blocks, int window,
-                        int sinks, int32_t* query_start_loc, int32_t* slot_mapping,
-                        int32_t* positions, int32_t* out_seq_lens, int32_t* out_free_count,
-                        void* stream) {
+namespace {
+// Without held pages (null) they are those of the lengths.
+int extend(int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+           const int32_t* new_lens, int32_t* held_pages, int32_t* free_blocks, int free_capacity,
+           const int32_t* free_count, int B, int T, int num_blocks, int window, int sinks,
+           int32_t* query_start_loc, int32_t* slot_mapping, int32_t* positions,
+           int32_t* out_seq_lens, int32_t* out_free_count, void* stream) {
   if (B < 0 || T < 0 || max_blocks_per_seq <= 0 || free_capacity < 0 || num_blocks <= 0 ||
       window < 0 || sinks < 0)
     return PS_ERR_ARG;
@@ -847,6 +848,7 @@ int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int
   a.tables = block_tables;
   a.seq_lens = seq_lens;
   a.new_lens = new_lens;
+  a.held = held_pages;
   a.free_blocks = free_blocks;
   a.free_count = free_count;
   a.qsl = query_start_loc;
@@ -865,6 +867,33 @@ int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Timed tm(0, s);
   return cuda_status(ps::launch_extend(a, s), "sequence extension kernel");
+}
+}  // namespace
+
+int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                        const int32_t* new_lens, int32_t* free_blocks, int free_capacity,
+                        const int32_t* free_count, int B, int T, int num_blocks, int window,
+                        int sinks, int32_t* query_start_loc, int32_t* slot_mapping,
+                        int32_t* positions, int32_t* out_seq_lens, int32_t* out_free_count,
+                        void* stream) {
+  return extend(block_tables, max_blocks_per_seq, seq_lens, new_lens, nullptr, free_blocks,
+                free_capacity, free_count, B, T, num_blocks, window, sinks, query_start_loc,
+                slot_mapping, positions, out_seq_lens, out_free_count, stream);
+}
+
+int ps_extend_held_sequences(int32_t* block_tables, int max_blocks_per_seq,
+                             const int32_t* seq_lens, const int32_t* new_lens,
+                             int32_t* held_pages, int32_t* free_blocks, int free_capacity,
+                             const int32_t* free_count, int B, int T, int num_blocks, int window,
+                             int sinks, int32_t* query_start_loc, int32_t* slot_mapping,
+                             int32_t* positions, int32_t* out_seq_lens, int32_t* out_free_count,
+                             void* stream) {
+  if (B > 0 && (!held_pages || held_pages == seq_lens || held_pages == new_lens ||
+                held_pages == out_seq_lens))
+    return PS_ERR_ARG;
+  return extend(block_tables, max_blocks_per_seq, seq_lens, new_lens, held_pages, free_blocks,
+                free_capacity, free_count, B, T, num_blocks, window, sinks, query_start_loc,
+                slot_mapping, positions, out_seq_lens, out_free_count, stream);
 }
 
 size_t ps_spec_accept_workspace_size(int B, int k, int V) {

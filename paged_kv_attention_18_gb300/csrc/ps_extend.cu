@@ -3,9 +3,12 @@
 // stack of free ones, and what a sliding window has left behind, or a sequence that ends
 // holds, goes back onto it first.
 //
-//     need_b  = ceil((L_b + n_b) / 16) - ceil(L_b / 16)   blocks, in order of (sequence, page)
+//     need_b  = max(ceil((L_b + n_b) / 16) - H_b, 0)      blocks, in order of (sequence, page)
 //     block i = free[count - 1 - i]                        (count: after the returns)
 //     slot    = block(page) * 16 + position % 16
+//
+// H_b: the pages that the sequence holds, ceil(L_b / 16), or more where tokens were taken back
+// (then counted by the caller's array, which the kernel keeps).
 //
 // One cluster: every CTA scans the whole batch (blocks given back, needed, tokens: sums over
 // the sequences) into its own shared memory, all wait for one another, since lengths, count,
@@ -83,15 +86,16 @@ __device__ __forceinline__ int pages_of(int L) {
   return static_cast<int>((static_cast<unsigned>(L) + kBlockSize - 1) / kBlockSize);
 }
 
-// The entries that sequence b of length L gives back, visited by a warp: `take(page, id, nth)`
-// for each, the highest page first. All of them for a sequence that ends; for a window, the pages
-// that no later row sees, from the last one down to the first that is gone already. Returns how
-// many.
+// The entries that sequence b of length L with `had` pages gives back, visited by a warp:
+// `take(page, id, nth)` for each, the highest page first. All of them for a sequence that ends; for
+// a window, the pages that no later row sees, from the last one down to the first that is gone
+// already. Returns how many.
 template <class Take>
-__device__ __forceinline__ int returned(const ExtendParams& p, int b, int L, bool ends, Take take) {
+__device__ __forceinline__ int returned(const ExtendParams& p, int b, int L, int had, bool ends,
+                                        Take take) {
   const int lane = threadIdx.x & 31;
   const int32_t* row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
-  int low = 0, high = pages_of(L);  // [low, high)
+  int low = 0, high = had;  // [low, high)
   if (!ends) {
     if (p.window <= 0) return 0;
     low = pages_of(p.sinks);
@@ -111,6 +115,8 @@ __device__ __forceinline__ int returned(const ExtendParams& p, int b, int L, boo
   return n;
 }
 
+// kHeld: p.held has the sequences' pages.
+template <bool kHeld>
 __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -122,8 +128,13 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
   int* s_tok = s_len + p.B + 1;     // [B + 1] first packed token
   int* s_blk = s_tok + p.B + 1;     // [B + 1] first new block
   int* s_ret = s_blk + p.B + 1;     // [B + 1] first block given back
+  int* s_had = s_ret + p.B + 1;     // [B] pages held before the step (kHeld)
   // [B] 1: the sequence ends; 2: it is bad; 4: it goes without
-  uint8_t* s_end = reinterpret_cast<uint8_t*>(s_ret + p.B + 1);
+  uint8_t* s_end = reinterpret_cast<uint8_t*>(s_had + (kHeld ? p.B : 0));
+  auto had = [&](int b) {
+    if constexpr (kHeld) return s_had[b];
+    else return pages_of(s_len[b]);
+  };
   const int tid = threadIdx.x, warp = tid >> 5;
   pdl_wait();
 
@@ -136,13 +147,19 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
   for (int b = tid; b < p.B; b += kThreads) {
     const int n = p.new_lens[b], L = p.seq_lens[b];
     const int64_t room = static_cast<int64_t>(p.max_blocks) * kBlockSize;
-    const bool ok = L >= 0 && L <= room && (n < 0 || static_cast<int64_t>(L) + n <= room) &&
-                    static_cast<int64_t>(L) + n <= 0x7fffffff - 1024;
+    bool ok = L >= 0 && L <= room && (n < 0 || static_cast<int64_t>(L) + n <= room) &&
+              static_cast<int64_t>(L) + n <= 0x7fffffff - 1024;
+    int pages = pages_of(L);
+    if constexpr (kHeld) {
+      const int held = p.held[b];
+      ok = ok && held >= pages && held <= p.max_blocks;
+      s_had[b] = pages = held;
+    }
     if (!ok && rank == 0) record_error(p.err, kDevBadSequence);
     s_len[b] = L;
     s_end[b] = !ok ? 2 : n < 0 ? 1 : 0;
     s_tok[b] = ok && n > 0 ? n : 0;
-    s_blk[b] = ok && n > 0 ? pages_of(L + n) - pages_of(L) : 0;
+    s_blk[b] = ok && n > 0 ? max(pages_of(L + n) - pages, 0) : 0;
     s_ret[b] = 0;
   }
   __syncthreads();
@@ -156,7 +173,9 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
     if (__syncthreads_or(any)) {
       for (int b = warp; b < p.B; b += kWarps) {
         const int n =
-            s_end[b] == 2 ? 0 : returned(p, b, s_len[b], s_end[b] == 1, [](int, int, int) {});
+            s_end[b] == 2
+                ? 0
+                : returned(p, b, s_len[b], had(b), s_end[b] == 1, [](int, int, int) {});
         if ((tid & 31) == 0) s_ret[b] = n;
       }
       __syncthreads();
@@ -240,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
       if (s_ret[b + 1] == s_ret[b]) continue;
       const int first = count + s_ret[b];
       int32_t* row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
-      returned(p, b, s_len[b], s_end[b] == 1, [&](int page, int id, int nth) {
+      returned(p, b, s_len[b], had(b), s_end[b] == 1, [&](int page, int id, int nth) {
         if (first + nth < p.free_capacity) p.free_blocks[first + nth] = id;
         row[page] = -1;
       });
@@ -252,12 +271,16 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
   for (int b = me; b <= p.B; b += stride) {
     p.qsl[b] = s_tok[b];
     if (b == p.B) break;
-    p.out_lens[b] = s_end[b] == 1 ? 0 : s_len[b] + (s_tok[b + 1] - s_tok[b]);
+    const int L = s_len[b] + (s_tok[b + 1] - s_tok[b]);
+    p.out_lens[b] = s_end[b] == 1 ? 0 : L;
+    if constexpr (kHeld) {
+      if (s_end[b] <= 1) p.held[b] = s_end[b] == 1 ? 0 : max(s_had[b], pages_of(L));
+    }
   }
   if (me == 0) *p.out_count = have - blocks;
   for (int i = me; i < blocks; i += stride) {
     const int b = last_le(s_blk, p.B, i);
-    const int page = pages_of(s_len[b]) + i - s_blk[b];
+    const int page = had(b) + i - s_blk[b];
     const int id = p.free_blocks[have - 1 - i];
     const bool ok = id >= 0 && id < p.num_blocks;
     if (!ok) record_error(p.err, kDevBadBlockId);
@@ -275,11 +298,11 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
       pos[u] = 0;
       from[u] = nullptr;
       if (t < tokens) {
-        const int b = last_le(s_tok, p.B, t), L = s_len[b];
-        pos[u] = L + t - s_tok[b];
-        const int page = pos[u] / kBlockSize, had = pages_of(L);
-        from[u] = page >= had ? p.free_blocks + have - 1 - (s_blk[b] + page - had)
-                              : p.tables + static_cast<int64_t>(b) * p.max_blocks + page;
+        const int b = last_le(s_tok, p.B, t);
+        pos[u] = s_len[b] + t - s_tok[b];
+        const int page = pos[u] / kBlockSize, first = had(b);
+        from[u] = page >= first ? p.free_blocks + have - 1 - (s_blk[b] + page - first)
+                                : p.tables + static_cast<int64_t>(b) * p.max_blocks + page;
       }
     }
 #pragma unroll
@@ -298,15 +321,21 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendParams p) 
 
 }  // namespace
 
-cudaError_t launch_extend(const ExtendParams& p, cudaStream_t stream) {
-  const int smem = 4 * (p.B + 1) * static_cast<int>(sizeof(int)) + p.B;
+template <bool kHeld>
+static cudaError_t launch_extend_t(const ExtendParams& p, cudaStream_t stream) {
+  constexpr int kArrays = kHeld ? 5 : 4;
+  const int smem = kArrays * (p.B + 1) * static_cast<int>(sizeof(int)) + p.B;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e =
-      ensure_smem_limit(extend_kernel, 17 * (kExtendMaxSeqs + 1), done);
+  const cudaError_t e = ensure_smem_limit(extend_kernel<kHeld>,
+                                          (4 * kArrays + 1) * (kExtendMaxSeqs + 1), done);
   if (e != cudaSuccess) return e;
   const int64_t want = (static_cast<int64_t>(p.T) + p.B + kPerCta - 1) / kPerCta;
   const int ctas = static_cast<int>(want < 1 ? 1 : want < kMaxCtas ? want : kMaxCtas);
-  return launch_cluster(extend_kernel, ctas, ctas, kThreads, smem, stream, p);
+  return launch_cluster(extend_kernel<kHeld>, ctas, ctas, kThreads, smem, stream, p);
+}
+
+cudaError_t launch_extend(const ExtendParams& p, cudaStream_t stream) {
+  return p.held != nullptr ? launch_extend_t<true>(p, stream) : launch_extend_t<false>(p, stream);
 }
 
 }  // namespace ps

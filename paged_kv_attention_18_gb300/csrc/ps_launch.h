@@ -288,6 +288,7 @@ struct ExtendParams {
   int32_t* tables;                // [B, max_blocks]
   const int32_t* seq_lens;        // [B]
   const int32_t* new_lens;        // [B]; negative: the sequence ends
+  int32_t* held;                  // [B] pages held, kept by the kernel; null: as the lengths say
   int32_t* free_blocks;           // [free_capacity], a stack of free_count entries
   const int32_t* free_count;      // [1]
   int32_t* qsl;                   // [B + 1]

@@ -372,7 +372,7 @@ PyObject* sample(PyObject* const* a) {
 
 // block_tables, seq_lens, new_lens, free_blocks, free_count, num_blocks, query_start_loc,
 // slot_mapping, positions, window, sinks, out_seq_lens | None, out_free_count | None,
-// stream | None
+// held_pages | None, stream | None
 PyObject* extend(PyObject* const* a) {
   Call c;
   const at::Tensor& bt = c.first(a[0], "block_tables");
@@ -388,20 +388,28 @@ PyObject* extend(PyObject* const* a) {
   const int window = arg_int(a[9], "window"), sinks = arg_int(a[10], "sinks");
   const at::Tensor& ol = c.on(a[11] == Py_None ? a[1] : a[11], "out_seq_lens", at::kInt, 1);
   const at::Tensor& oc = c.on(a[12] == Py_None ? a[4] : a[12], "out_free_count", at::kInt, 1);
+  const at::Tensor* held =
+      a[13] == Py_None ? nullptr : &c.on(a[13], "held_pages", at::kInt, 1);
   const int64_t B = bt.size(0);
+  if (held && held->size(0) != B) refuse("held_pages: one per sequence");
   if (sl.size(0) != B || nl.size(0) != B || ol.size(0) != B || qsl.size(0) != B + 1 ||
       pos.size(0) != slots.size(0) || fc.size(0) != 1 || oc.size(0) != 1)
     refuse("extend_sequences: inconsistent shapes");
-  void* s = arg_stream(a[13], c.dev);
+  void* s = arg_stream(a[14], c.dev);
   const int b = to_int(B, "B"), w = to_int(bt.size(1), "max_blocks");
   const int T = to_int(slots.size(0), "T"), cap = to_int(fb.size(0), "free_capacity");
   auto out = [](const at::Tensor& t) { return static_cast<int32_t*>(t.mutable_data_ptr()); };
   int rc;
   Py_BEGIN_ALLOW_THREADS;
-  rc = ps_extend_sequences(out(bt), w, ints(sl), ints(nl), out(fb), cap, ints(fc), b, T, nb,
-                           window, sinks, out(qsl), out(slots), out(pos), out(ol), out(oc), s);
+  if (held)
+    rc = ps_extend_held_sequences(out(bt), w, ints(sl), ints(nl), out(*held), out(fb), cap,
+                                  ints(fc), b, T, nb, window, sinks, out(qsl), out(slots),
+                                  out(pos), out(ol), out(oc), s);
+  else
+    rc = ps_extend_sequences(out(bt), w, ints(sl), ints(nl), out(fb), cap, ints(fc), b, T, nb,
+                             window, sinks, out(qsl), out(slots), out(pos), out(ol), out(oc), s);
   Py_END_ALLOW_THREADS;
-  check(rc, "ps_extend_sequences");
+  check(rc, held ? "ps_extend_held_sequences" : "ps_extend_sequences");
   return give(Py_None);
 }
 
@@ -542,7 +550,7 @@ PyMethodDef g_methods[] = {method<rotary<false>, 12>("rotary"),
                            method<rotary<true>, 13>("rotary_axes"),
                            method<stream_attend, 14>("stream_attend"),
                            method<sample, 9>("sample"),
-                           method<extend, 14>("extend"),
+                           method<extend, 15>("extend"),
                            method<attend, 16>("attend"),
                            method<select, 10>("select"),
                            method<fork, 9>("fork"),
