@@ -256,8 +256,9 @@ int ps_rotary_axes_reshape_and_cache(const void* q, int64_t q_stride, const void
  *     (PS_DEV_NO_BLOCKS).
  * The host sees who was left out by query_start_loc. A stack entry or table entry outside the
  * pool that is to be used records PS_DEV_BAD_BLOCK_ID (its slots are -1, the new table entry
- * -1), and so does a free_count outside [0, free_capacity] (which counts as 0) and a stack that
- * overflows. B up to 8192 and B * max_blocks_per_seq below 2^31 (PS_ERR_UNSUPPORTED).
+ * -1), as does a table entry of num_blocks or more that is to be given back (it stays as it is,
+ * the blocks around it come back), a free_count outside [0, free_capacity] (which counts as 0)
+ * and a stack that overflows. B up to 8192 and B * max_blocks_per_seq below 2^31 (PS_ERR_UNSUPPORTED).
  */
 int ps_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
                         const int32_t* new_lens, int32_t* free_blocks, int free_capacity,

@@ -89,7 +89,7 @@ __device__ __forceinline__ int pages_of(int L) {
 // The entries that sequence b of length L with `had` pages gives back, visited by a warp:
 // `take(page, id, nth)` for each, the highest page first. All of them for a sequence that ends; for
 // a window, the pages that no later row sees, from the last one down to the first that is gone
-// already. Returns how many.
+// already. An entry that is no block of the pool is recorded and passed over. Returns how many.
 template <class Take>
 __device__ __forceinline__ int returned(const ExtendParams& p, int b, int L, int had, bool ends,
                                         Take take) {
@@ -105,12 +105,14 @@ __device__ __forceinline__ int returned(const ExtendParams& p, int b, int L, int
   for (int top = high - 1; top >= low; top -= 32) {
     const int page = top - lane;
     const int id = page >= low ? row[page] : -1;
-    const bool held = id >= 0 && id < p.num_blocks;
-    unsigned has = __ballot_sync(0xffffffffu, held);
-    if (!ends && ~has != 0u) has &= (1u << (__ffs(~has) - 1)) - 1u;  // up to the first gone
+    unsigned has = __ballot_sync(0xffffffffu, id >= 0);
+    const bool gone = !ends && ~has != 0u;
+    if (gone) has &= (1u << (__ffs(~has) - 1)) - 1u;  // up to the first gone
+    if ((has >> lane) & 1u && id >= p.num_blocks) record_error(p.err, kDevBadBlockId);
+    has &= __ballot_sync(0xffffffffu, id < p.num_blocks);
     if ((has >> lane) & 1u) take(page, id, n + __popc(has & ((1u << lane) - 1u)));
     n += __popc(has);
-    if (!ends && ~has != 0u) break;
+    if (gone) break;
   }
   return n;
 }
