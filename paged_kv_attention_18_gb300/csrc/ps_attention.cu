@@ -32,8 +32,7 @@ struct SeqInfo {
   // page any row of the sequence sees, and the length of its bidirectional prefix.
   int page0, pre;
   // Streams: the sinks' pages (counted ahead of the window's, so that a sequence's pages are
-  // page0 .. pages - 1 with the window's from page0 + sink_pages on as they are), and the
-  // position of the first row.
+  // page0 .. pages - 1 with the window's from page0 + sink_pages on as they are).
   int sink_pages;
 };
 

@@ -162,12 +162,6 @@ struct ItemTiles {
   __device__ __forceinline__ int page(int i) const { return i < sp ? sb + i : pb + i - sp; }
 };
 
-}  // namespace
-
-// kDirect: no plan. Each CTA derives its items from seq_lens and qsl (every sequence
-// unsplit, its query-tile pairs longest first).
-// kCap: 0 none, 1 up to kLargeCapLog2, 2 beyond (the exact form of small scores in every tile; as
-// a branch inside it made the kernel larger and its other caps 1.5 % slower).
 // 32 columns of scores, those outside [low, lim] dropped (streams: but not those below `sunk`). One
 // word has the columns that are kept, so that a column costs a test of a bit and a select in place
 // of up to three comparisons. (6 chunks of 1000 in documents behind a prefix, 14/2 heads, D 64: 33.4
@@ -183,6 +177,12 @@ __device__ __forceinline__ void drop_unseen(uint32_t* v, int lim, int low, int s
     if (!(kept >> e & 1u)) v[e] = __float_as_uint(-INFINITY);
 }
 
+}  // namespace
+
+// kDirect: no plan. Each CTA derives its items from seq_lens and qsl (every sequence
+// unsplit, its query-tile pairs longest first).
+// kCap: 0 none, 1 up to kLargeCapLog2, 2 beyond (the exact form of small scores in every tile; as
+// a branch inside it made the kernel larger and its other caps 1.5 % slower).
 template <class Params, bool kBF16, int D, bool kDirect, int kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads<(kCap > 0 || kBias)>, 1)
     masked_tile_kernel(const __grid_constant__ CUtensorMap kmap,
