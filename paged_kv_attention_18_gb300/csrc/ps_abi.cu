@@ -425,10 +425,10 @@ int run_masked_attention(const Params& p0, const void* k_pool, const void* v_poo
   // sequence's last group is half full on average) and their warps have pages to read: a
   // microsecond for the second CTA, little for the others. us, a CTA an item / clusters:
   //   12 heads on 2, D 128:  1 sequence, window 250 7.6 / 7.8 by 2 (so not taken), 1000 11.2 /
-  //                          9.4, 4000 22.4 / 10.4 by 8; 16 of 4000 27.9 / 16.5 by 4;
+  //                          9.4, 4000 22.4 / 9.8 by 8; 16 of 4000 27.9 / 16.2 by 4;
   //                          4 tokens on average: 4 of 1000 16.3 / 11.7, 18 of 1000 15.8 / 13.1
-  // and so the plan is left later (planned / direct): 18 of 4000 with 4 tokens 42.7 / 23.6 by 2,
-  // 1 of 16000 38 / 17 and of 32000 58 / 26 by 8; also with one CTA an item, 36 of 4000 43 / 28.5,
+  // and so the plan is left later (planned / direct): 18 of 4000 with 4 tokens 42.7 / 21.7 by 2,
+  // 1 of 16000 38 / 17 and of 32000 58 / 25 by 8; also with one CTA an item, 36 of 4000 43 / 28.5,
   // with 4 tokens 62 / 37, 76 on 4 KV heads 115 / 98. (Not for longer ones, though that was still
   // faster where all were as long as the window: a single long one among short ones waits for
   // its one CTA.)

@@ -16,9 +16,11 @@
 // new blocks and the packed tokens, which find their sequence by bisection. A token on a new
 // page takes its block from the stack, not from the table that another thread writes. Nothing
 // here is work: a step is bound by the launch, the loads one behind another (lengths, table or
-// stack) and the barriers. 256 decodes take 3.7 us (of which a call takes 3), 1000 sequences of
-// up to 65 tokens 11.3: 4.9 and 15.5 with sums in 64 bits and a sequence a thread at a time; 1024
-// threads a CTA took 8.9 and 13.8.
+// stack) and the barriers. 256 decodes take 3.6 us (of which a call takes 3), 1000 sequences of
+// up to 65 tokens 11.2: 4.9 and 15.5 with sums in 64 bits and a sequence a thread at a time; 1024
+// threads a CTA took 8.9 and 13.8. Blocks that are given back cost more, twice a warp's look at each
+// sequence's table, one behind the other: 256 decodes under a window of 1000 keys 13.4, 1000 of them
+// 41; 16 sequences of 128 to 256 pages that end among 256, all of one warp, 55 more.
 #include <cooperative_groups.h>
 
 #include "ps_common.cuh"

@@ -29,7 +29,7 @@
 // of 16 heads on 4, D 128, over a window of 4096 and 4 sinks: 174 us, 0.92 of the measured copy
 // peak, as the window alone. Small batches, without a plan: a cluster of up to 8 CTAs for an
 // item, whose warps share its pages out and send their joined rows to the row's CTA. One decode
-// over a window of 4000, 12 heads on 2: 10.4 us with 8 CTAs, 22.4 with one, bound by each warp's
+// over a window of 4000, 12 heads on 2: 9.8 us with 8 CTAs, 22.4 with one, bound by each warp's
 // chain of steps (about a microsecond a page: the copy's issue, two products, the softmax).
 #pragma once
 

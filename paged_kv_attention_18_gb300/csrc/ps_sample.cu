@@ -33,9 +33,10 @@
 // where all are summed (the FMA and ALU pipes at 0.3 each, 1.5 instructions a cycle) and, with
 // two CTAs on an SM, by what a row does one thing behind another: load 3 us, maximum 1, list and
 // decision 8 (top-k) or counts 8, merge and choice 5, exact pass 10, list in order 6, draw 4
-// (top-p). 256 rows of 151936, bf16, us: greedy 26, unfiltered 69, min-p 49, top-k 50 54, top-p
-// 0.9 166; one row 5.2, 11.3, -, 10.9, 27. 512 threads of 64 registers, or clusters of 8 at three
-// CTAs an SM, gave nothing.
+// (top-p). 256 rows of 151936, bf16, us: greedy 25, unfiltered 69, min-p 48, top-k 50 54, top-p
+// 0.9 167; one row 4.3, 12, -, 11.3, 29. 512 threads of 64 registers, or clusters of 8 at three CTAs
+// an SM, gave nothing. What is left is this way's, not a limit: a row in its cluster's shared memory
+// keeps other rows out, and a second read of it would come from the L2 for the most part.
 #include <cooperative_groups.h>
 
 #include <cfloat>
